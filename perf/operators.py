@@ -165,7 +165,8 @@ def _run_own(st):
     if c["op"] == "moe_route":
         return tg.moe_route(st["logits"], c["k"], renormalize=c["renorm"])
     return tg.moe(st["x"], st["logits"], st["gate_up"], st["down"], st["y"], top_k=c["k"],
-                  activation=c["act"], renormalize=c["renorm"])
+                  activation=c["act"], renormalize=c["renorm"],
+                  intermediate=c["I"])
 
 
 # ------------------------------------------------------------------ plain forms

@@ -17,10 +17,11 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional, Tuple
+from typing import Dict, NamedTuple, Optional, Tuple
 
 __all__ = [
-    "gemm", "plan", "TcGemmError", "last_kernel", "dispatch_count", "time_next_gemm", "library_path",
+    "gemm", "w4_quantize", "w4_dequantize", "w4_pack", "w4_gemm", "moe_route", "moe", "W4Weight",
+    "plan", "TcGemmError", "last_kernel", "dispatch_count", "time_next_gemm", "library_path",
     "load_library", "F32", "F16", "BF16", "I8", "I32", "status_name", "DescT",
     "BatchedDescT", "PlanInfoT",
 ]
@@ -75,6 +76,44 @@ class EpilogueT(ctypes.Structure):
                 ("scale_stride", ctypes.c_int64)]
 
 
+class QWeightDescT(ctypes.Structure):
+    """tc_qweight_desc"""
+    _fields_ = [("batch", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int),
+                ("has_zeros", ctypes.c_bool)]
+
+
+class QWeightT(ctypes.Structure):
+    """tc_qweight"""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p)]
+
+
+class QGemmDescT(ctypes.Structure):
+    """tc_qgemm_desc"""
+    _fields_ = [("M", ctypes.c_int32), ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("ldx", ctypes.c_int32), ("ldy", ctypes.c_int32)]
+
+
+class RouteDescT(ctypes.Structure):
+    """tc_route_desc"""
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("ld", ctypes.c_int32), ("renormalize", ctypes.c_bool),
+                ("scale", ctypes.c_float)]
+
+
+class MoeDescT(ctypes.Structure):
+    """tc_moe_desc"""
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("x_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int), ("ldx", ctypes.c_int32), ("ldy", ctypes.c_int32),
+                ("gate", ctypes.c_int), ("group", ctypes.c_int32), ("has_zeros", ctypes.c_bool)]
+
+
+# tc_gate_t
+GATES = {"silu": 0, "gelu_tanh": 1}
+
 # tc_activation_t
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu_tanh": 2}
 
@@ -125,6 +164,26 @@ _SIGNATURES = {
                                             ctypes.POINTER(ctypes.c_int32),
                                             ctypes.POINTER(ctypes.c_int32)]),
     "tc_version": (ctypes.c_char_p, []),
+    "tc_qweight_sizes": (ctypes.c_int, [ctypes.POINTER(QWeightDescT), ctypes.POINTER(ctypes.c_int64),
+                                        ctypes.POINTER(ctypes.c_int64),
+                                        ctypes.POINTER(ctypes.c_int64)]),
+    "tc_quantize_async": (ctypes.c_int, [_VP, ctypes.POINTER(QWeightDescT), _VP, ctypes.c_int,
+                                         ctypes.c_int64, ctypes.c_int64,
+                                         ctypes.POINTER(QWeightT), _VP]),
+    "tc_dequantize_async": (ctypes.c_int, [_VP, ctypes.POINTER(QWeightDescT),
+                                           ctypes.POINTER(QWeightT), _VP, ctypes.c_int,
+                                           ctypes.c_int64, ctypes.c_int64, _VP]),
+    "tc_qweight_pack_async": (ctypes.c_int, [_VP, ctypes.POINTER(QWeightDescT),
+                                             ctypes.POINTER(QWeightT), ctypes.POINTER(QWeightT),
+                                             _VP]),
+    "tc_qgemm_async": (ctypes.c_int, [_VP, ctypes.POINTER(QGemmDescT),
+                                      ctypes.POINTER(QWeightDescT), _VP, ctypes.POINTER(QWeightT),
+                                      _VP, ctypes.POINTER(EpilogueT), _VP]),
+    "tc_moe_route_async": (ctypes.c_int, [_VP, ctypes.POINTER(RouteDescT), _VP, _VP, _VP, _VP]),
+    "tc_moe_workspace": (ctypes.c_int, [ctypes.POINTER(MoeDescT), ctypes.POINTER(ctypes.c_int64)]),
+    "tc_moe_async": (ctypes.c_int, [_VP, ctypes.POINTER(MoeDescT), _VP, ctypes.POINTER(RouteDescT),
+                                    _VP, _VP, _VP, ctypes.POINTER(QWeightT),
+                                    ctypes.POINTER(QWeightT), _VP, _VP, ctypes.c_int64, _VP]),
 }
 
 _lib = None
@@ -348,6 +407,391 @@ def gemm(a, b, c, *, alpha: float = 1.0, beta: float = 0.0, transpose_a: bool = 
     if st != 0:
         _check(st, ctx)
     return c
+
+
+# ------------------------------------------------------------------ weights in 4 bits
+class W4Weight(NamedTuple):
+    """Matrices held in 4 bits with a scale (and zero point) per group of K
+    (the layout is in include/tcgemm.h): codes uint8 [.., ceil(N/16),
+    ceil(K/128), 1024], scales f16 or bf16 [.., ceil(N/16), ceil(K/128), 16,
+    128/group], zeros uint8 of the scales' shape or None.  Contiguous; the
+    leading dims, if any, count matrices.  Functions that take one accept a
+    plain tuple too."""
+    codes: "torch.Tensor"
+    scales: "torch.Tensor"
+    zeros: "Optional[torch.Tensor]" = None
+
+
+def _float_code(t, name: str, types=(F32, F16, BF16)) -> int:
+    code = _dtype_code(t)
+    if code not in types:
+        raise TcGemmError(2, "%s must be one of %s (got %s)"
+                          % (name, "/".join(_NAMES[c] for c in types), _NAMES[code]))
+    return code
+
+
+def _same_device(first, *others) -> int:
+    """The device index all tensors share."""
+    if not first.is_cuda:
+        raise TcGemmError(1, "the operands must be GPU tensors")
+    device = first.get_device()
+    for t in others:
+        if t is not None and (not t.is_cuda or t.get_device() != device):
+            raise TcGemmError(1, "the operands must be on one GPU")
+    return device
+
+
+# Descriptors of the calls seen so far, as _desc_cache, bounded.
+_op_cache: Dict[tuple, tuple] = {}
+
+
+def _cached(key, make):
+    v = _op_cache.get(key)
+    if v is None:
+        v = make()
+        if len(_op_cache) < 4096:
+            _op_cache[key] = v
+    return v
+
+
+def _w4_desc(w, N: int, K: int, lead=()):
+    """tc_qweight_desc of w, checked to hold matrices [N, K], one per index
+    of the leading shape `lead`."""
+    codes, scales, zeros = w
+    import torch
+    nb, kb = (N + 15) // 16, (K + 127) // 128
+    per = int(scales.size(-1)) if scales.dim() else 0
+    if per not in (1, 2, 4):
+        raise TcGemmError(1, "the scales' last dimension must be 128/group: 1, 2 or 4 (got %d)" % per)
+    lead = tuple(lead)
+    if codes.dtype != torch.uint8 or tuple(codes.shape) != lead + (nb, kb, 1024):
+        raise TcGemmError(1, "codes must be uint8 of shape %s (got %s %s)"
+                          % (lead + (nb, kb, 1024), codes.dtype, tuple(codes.shape)))
+    if tuple(scales.shape) != lead + (nb, kb, 16, per):
+        raise TcGemmError(1, "scales must have shape %s (got %s)"
+                          % (lead + (nb, kb, 16, per), tuple(scales.shape)))
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+        raise TcGemmError(1, "zeros must be uint8 of the scales' shape")
+    if not (codes.is_contiguous() and scales.is_contiguous()
+            and (zeros is None or zeros.is_contiguous())):
+        raise TcGemmError(1, "codes, scales and zeros must be contiguous")
+    batch = 1
+    for n in lead:
+        batch *= n
+    return QWeightDescT(batch, N, K, 128 // per, _float_code(scales, "scales", (F16, BF16)),
+                        zeros is not None)
+
+
+def _w4_ptrs(w) -> QWeightT:
+    codes, scales, zeros = w
+    return QWeightT(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr())
+
+
+def _w4_key(w) -> tuple:
+    codes, scales, zeros = w
+    return (codes.shape, codes.dtype, codes.is_contiguous(), scales.shape, scales.dtype,
+            scales.is_contiguous(), None if zeros is None else
+            (zeros.shape, zeros.dtype, zeros.is_contiguous()))
+
+
+def _as_w4(w):
+    """(codes, scales, zeros) of a W4Weight or a tuple of two or three."""
+    if not isinstance(w, (tuple, list)) or len(w) not in (2, 3):
+        raise TcGemmError(1, "the weight must be (codes, scales, zeros or None)")
+    return tuple(w) if len(w) == 3 else (w[0], w[1], None)
+
+
+def _on_stream(device: int, stream):
+    """Context under which torch allocates for the stream a call runs on."""
+    import torch
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+
+
+def _w4_empty(lead, N: int, K: int, group: int, zeros: bool, scale_dtype, device) -> W4Weight:
+    import torch
+    if group not in (32, 64, 128):
+        raise TcGemmError(1, "group must be 32, 64 or 128 (got %r)" % (group,))
+    nb, kb = (N + 15) // 16, (K + 127) // 128
+    shape = (*lead, nb, kb, 16, 128 // group)
+    return W4Weight(torch.empty(*lead, nb, kb, 1024, dtype=torch.uint8, device=device),
+                    torch.empty(shape, dtype=scale_dtype, device=device),
+                    torch.empty(shape, dtype=torch.uint8, device=device) if zeros else None)
+
+
+def _dense_batch(t, name: str):
+    """(leading shape, N, K, row pitch, matrix stride) of a [.., N, K] tensor
+    whose matrices are evenly spaced."""
+    if t.dim() < 2:
+        raise TcGemmError(1, "%s must have at least 2 dimensions" % name)
+    lead, N, K = tuple(t.shape[:-2]), int(t.size(-2)), int(t.size(-1))
+    ld = _ld(t)
+    stride, expect = 0, None
+    for d in range(len(lead) - 1, -1, -1):
+        if lead[d] == 1:
+            continue
+        if expect is None:
+            stride = int(t.stride(d))
+        elif int(t.stride(d)) != expect:
+            raise TcGemmError(1, "the matrices of %s must be evenly spaced" % name)
+        expect = int(t.stride(d)) * lead[d]
+    return lead, N, K, ld, stride
+
+
+def w4_quantize(w, *, group: int = 128, zeros: bool = False, scale_dtype=None, stream=None) -> W4Weight:
+    """w [.., N, K] (f32, f16 or bf16) in 4 bits, with a scale per `group`
+    values of K (32, 64 or 128) and, with zeros, a zero point
+    (tc_quantize_async has the formulas).  scale_dtype: torch.float16 or
+    torch.bfloat16, the type of the activations it will meet; by default w's,
+    bfloat16 for f32."""
+    import torch
+    device = _same_device(w)
+    code = _float_code(w, "w")
+    if scale_dtype is None:
+        scale_dtype = torch.bfloat16 if code == F32 else w.dtype
+    if scale_dtype not in (torch.float16, torch.bfloat16):
+        raise TcGemmError(2, "scale_dtype must be torch.float16 or torch.bfloat16")
+    lead, N, K, ld, stride = _dense_batch(w, "w")
+    if w.numel() == 0:
+        raise TcGemmError(1, "dims must be >= 1 (shape %s)" % (tuple(w.shape),))
+    lib = load_library()
+    ctx, s = _torch_stream(device, stream)
+    with _on_stream(device, stream):
+        out = _w4_empty(lead, N, K, group, zeros, scale_dtype, w.device)
+    d, q = _w4_desc(out, N, K, lead), _w4_ptrs(out)
+    _check(lib.tc_quantize_async(ctx, ctypes.byref(d), w.data_ptr(), code, ld, stride,
+                                 ctypes.byref(q), s), ctx)
+    return out
+
+
+def w4_dequantize(w, out, *, stream=None):
+    """The values a W4Weight stands for into out [.., N, K] (f32, f16 or
+    bf16), rounded once.  Returns out."""
+    w = _as_w4(w)
+    device = _same_device(out, *w)
+    code = _float_code(out, "out")
+    lead, N, K, ld, stride = _dense_batch(out, "out")
+    d, q = _w4_desc(w, N, K, lead), _w4_ptrs(w)
+    ctx, s = _torch_stream(device, stream)
+    _check(load_library().tc_dequantize_async(ctx, ctypes.byref(d), ctypes.byref(q), out.data_ptr(),
+                                              code, ld, stride, s), ctx)
+    return out
+
+
+def w4_pack(codes, scales, zeros=None, *, K: Optional[int] = None, group: int = 128,
+            stream=None) -> W4Weight:
+    """Lay out what another quantizer made: codes uint8 [.., N, ceil(K/2)],
+    two per byte, the even k in the low nibble; scales f16 or bf16 and zeros
+    uint8 [.., N, ceil(K/group)]; all contiguous.  W = scale * (code - zero),
+    zero 8 without zeros.  K: by default twice the codes' last dimension."""
+    import torch
+    device = _same_device(codes, scales, zeros)
+    _float_code(scales, "scales", (F16, BF16))
+    if codes.dim() < 2 or codes.dtype != torch.uint8 or codes.numel() == 0:
+        raise TcGemmError(1, "codes must be uint8 [.., N, ceil(K/2)]")
+    lead, N = tuple(codes.shape[:-2]), int(codes.size(-2))
+    K = 2 * int(codes.size(-1)) if K is None else int(K)
+    if group not in (32, 64, 128):
+        raise TcGemmError(1, "group must be 32, 64 or 128 (got %r)" % (group,))
+    if (K + 1) // 2 != codes.size(-1):
+        raise TcGemmError(1, "K=%d does not fit %d bytes of codes per row" % (K, codes.size(-1)))
+    shape = lead + (N, (K + group - 1) // group)
+    if tuple(scales.shape) != shape:
+        raise TcGemmError(1, "scales must have shape %s (got %s)" % (shape, tuple(scales.shape)))
+    if zeros is not None and (zeros.dtype != torch.uint8 or tuple(zeros.shape) != shape):
+        raise TcGemmError(1, "zeros must be uint8 of the scales' shape")
+    if not all(t is None or t.is_contiguous() for t in (codes, scales, zeros)):
+        raise TcGemmError(1, "codes, scales and zeros must be contiguous")
+    ctx, s = _torch_stream(device, stream)
+    with _on_stream(device, stream):
+        out = _w4_empty(lead, N, K, group, zeros is not None, scales.dtype, codes.device)
+    d, q, src = _w4_desc(out, N, K, lead), _w4_ptrs(out), _w4_ptrs((codes, scales, zeros))
+    _check(load_library().tc_qweight_pack_async(ctx, ctypes.byref(d), ctypes.byref(src),
+                                                ctypes.byref(q), s), ctx)
+    return out
+
+
+def _make_qgemm(x, w, y, alpha, beta):
+    if x.dim() != 2 or y.dim() != 2 or x.size(0) != y.size(0):
+        raise TcGemmError(1, "x must be [M, K] and y [M, N] (got %s and %s)"
+                          % (tuple(x.shape), tuple(y.shape)))
+    wd = _w4_desc(w, int(y.size(1)), int(x.size(1)))
+    g = QGemmDescT(int(x.size(0)), _dtype_code(x), _dtype_code(y), float(alpha), float(beta),
+                   _ld(x), _ld(y))
+    return g, wd, ctypes.byref(g), ctypes.byref(wd)
+
+
+def w4_gemm(x, w, y, *, alpha: float = 1.0, beta: float = 0.0, bias=None,
+            activation: Optional[str] = None, stream=None):
+    """y = activation(alpha * (x @ W^T) + beta * y + bias) for a weight held
+    in 4 bits: x [M, K] of the scales' type, W [N, K] as a W4Weight, y [M, N]
+    of x's type or f32, bias [N] of y's type; activation None, "none", "relu"
+    or "gelu_tanh".  Runs on torch's current stream (or `stream`), needs no
+    workspace.  Returns y."""
+    w = _as_w4(w)
+    device = _same_device(y, x, bias, *w)
+    key = ("w4_gemm", x.shape, x.stride(), x.dtype, y.shape, y.stride(), y.dtype, alpha, beta,
+           _w4_key(w))
+    _, _, g, wd = _cached(key, lambda: _make_qgemm(x, w, y, alpha, beta))
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    q = _w4_ptrs(w)
+    ep = None
+    if bias is not None or activation is not None:
+        ep = ctypes.byref(make_epilogue(y, bias, activation))
+    st = lib.tc_qgemm_async(ctx, g, wd, x.data_ptr(), ctypes.byref(q), y.data_ptr(), ep, s)
+    if st != 0:
+        _check(st, ctx)
+    return y
+
+
+# ------------------------------------------------------------------ mixture of experts
+def _make_route(logits, top_k, renormalize, scale):
+    if logits.dim() != 2:
+        raise TcGemmError(1, "logits must be [T, E] (got %s)" % (tuple(logits.shape),))
+    r = RouteDescT(int(logits.size(0)), int(logits.size(1)), int(top_k), _dtype_code(logits),
+                   _ld(logits), bool(renormalize), float(scale))
+    return r, ctypes.byref(r)
+
+
+def moe_route(logits, top_k: int, *, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """(ids int32 [T, top_k], weights f32 [T, top_k]): the experts with the
+    largest of the router's logits [T, E] (f32, f16 or bf16), the largest
+    first, ties to the lowest index, and scale times their softmax weights,
+    over the chosen ones (renormalize) or over all E.  Experts whose logit is
+    -inf or NaN are never chosen; places left over hold id -1, weight 0."""
+    import torch
+    device = _same_device(logits)
+    if not (isinstance(top_k, int) and top_k >= 1):
+        raise TcGemmError(1, "top_k must be a whole number >= 1 (got %r)" % (top_k,))
+    key = ("route", logits.shape, logits.stride(), logits.dtype, top_k, renormalize, scale)
+    d, r = _cached(key, lambda: _make_route(logits, top_k, renormalize, scale))
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    with _on_stream(device, stream):
+        ids = torch.empty((d.T, d.top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((d.T, d.top_k), dtype=torch.float32, device=logits.device)
+    st = lib.tc_moe_route_async(ctx, r, logits.data_ptr(), ids.data_ptr(), weights.data_ptr(), s)
+    if st != 0:
+        _check(st, ctx)
+    return ids, weights
+
+
+def _make_moe(x, route, gate_up, down, y, top_k, activation, renormalize, scale, intermediate):
+    import torch
+    if activation not in GATES:
+        raise TcGemmError(1, "unknown activation %r" % (activation,))
+    if x.dim() != 2 or x.shape != y.shape:
+        raise TcGemmError(1, "x and y must be [T, H] (got %s and %s)" % (tuple(x.shape), tuple(y.shape)))
+    T, H = int(x.size(0)), int(x.size(1))
+    held = isinstance(gate_up, tuple)
+    if held != isinstance(down, tuple):
+        raise TcGemmError(2, "gate_up and down must both be held in 4 bits or both in 16")
+    if held:
+        if down[0].dim() != 4 or gate_up[0].dim() != 5:
+            raise TcGemmError(1, "gate_up must hold [E, 2] matrices and down [E]")
+        E = int(down[0].size(0))
+        I = 16 * int(gate_up[0].size(2)) if intermediate is None else int(intermediate)
+        up, dn = _w4_desc(gate_up, I, H, (E, 2)), _w4_desc(down, H, I, (E,))
+        if (up.group, up.has_zeros, up.scale_dtype) != (dn.group, dn.has_zeros, dn.scale_dtype):
+            raise TcGemmError(2, "gate_up and down must be held alike")
+        if up.scale_dtype != _dtype_code(x):
+            raise TcGemmError(2, "the scales must have x's dtype %s" % x.dtype)
+        group, zeros = up.group, up.has_zeros
+    else:
+        if down.dim() != 3 or gate_up.dim() not in (3, 4):
+            raise TcGemmError(1, "gate_up must be [E, 2, I, H] or [E, 2 I, H], down [E, H, I]")
+        E, I = int(down.size(0)), int(down.size(2))
+        if (tuple(gate_up.shape) not in ((E, 2, I, H), (E, 2 * I, H)) or int(down.size(1)) != H
+                or intermediate not in (None, I)):
+            raise TcGemmError(1, "shapes of gate_up %s, down %s and x %s do not fit"
+                              % (tuple(gate_up.shape), tuple(down.shape), tuple(x.shape)))
+        if gate_up.dtype != x.dtype or down.dtype != x.dtype:
+            raise TcGemmError(2, "gate_up and down must have x's dtype %s" % x.dtype)
+        if not (gate_up.is_contiguous() and down.is_contiguous()):
+            raise TcGemmError(1, "gate_up and down must be contiguous")
+        group, zeros = 0, False
+    r = rref = None
+    if isinstance(route, tuple):
+        ids, weights = route
+        if top_k is not None and int(top_k) != int(ids.size(-1)):
+            raise TcGemmError(1, "top_k=%d, but ids have %d columns" % (top_k, ids.size(-1)))
+        k = int(ids.size(-1))
+        if (tuple(ids.shape) != (T, k) or weights.shape != ids.shape or ids.dtype != torch.int32
+                or weights.dtype != torch.float32):
+            raise TcGemmError(1, "ids must be int32 and weights float32 [T, top_k]")
+        if not (ids.is_contiguous() and weights.is_contiguous()):
+            raise TcGemmError(1, "ids and weights must be contiguous")
+    else:
+        if top_k is None:
+            raise TcGemmError(1, "top_k must be given with logits")
+        k = int(top_k)
+        if tuple(route.shape) != (T, E):
+            raise TcGemmError(1, "logits must be [T, E] = %s (got %s)" % ((T, E), tuple(route.shape)))
+        r, rref = _make_route(route, k, renormalize, scale)
+    d = MoeDescT(T, H, I, E, k, _dtype_code(x), _dtype_code(y), _ld(x), _ld(y), GATES[activation],
+                 group, zeros)
+    need = ctypes.c_int64()
+    st = load_library().tc_moe_workspace(ctypes.byref(d), ctypes.byref(need))
+    # (a descriptor the library refuses is refused again, with its text, by the call)
+    return d, ctypes.byref(d), r, rref, need.value if st == 0 else 0
+
+
+def _weights_key(w) -> tuple:
+    return _w4_key(w) if isinstance(w, tuple) else (w.shape, w.dtype, w.is_contiguous())
+
+
+def moe(x, route, gate_up, down, y, *, top_k: Optional[int] = None, activation: str = "silu",
+        renormalize: bool = True, scale: float = 1.0, intermediate: Optional[int] = None,
+        stream=None):
+    """A layer of gated experts for few tokens (tc_moe_async):
+
+        y[t] = sum_j p[t, j] * down[e] (act(gate[e] x[t]) * (up[e] x[t])),  e = ids[t, j]
+
+    x and y [T, H], y of x's type or f32.  route: the router's logits [T, E]
+    (then top_k, renormalize and scale choose as moe_route does) or a tuple
+    (ids int32, weights float32), both [T, top_k]; an id outside [0, E) adds
+    nothing.  gate_up [E, 2, I, H] (gate, then up; [E, 2 I, H] is the same
+    memory) and down [E, H, I]: tensors of x's type, or both in 4 bits
+    (W4Weight of leading shapes (E, 2) and (E,)); then I is `intermediate`,
+    by default gate_up's rows rounded up to 16.  activation: "silu" or
+    "gelu_tanh".  Scratch memory comes from torch's allocator, for this call
+    alone.  Returns y."""
+    import torch
+    if isinstance(gate_up, (tuple, list)):
+        gate_up = _as_w4(gate_up)
+    if isinstance(down, (tuple, list)):
+        down = _as_w4(down)
+    held = gate_up if isinstance(gate_up, tuple) else (gate_up,)
+    held = held + (down if isinstance(down, tuple) else (down,))
+    given = tuple(route) if isinstance(route, (tuple, list)) else (route,)
+    if isinstance(route, (tuple, list)):
+        if len(given) != 2:
+            raise TcGemmError(1, "route must be logits or (ids, weights)")
+        route = given
+    device = _same_device(y, x, *given, *held)
+    key = ("moe", x.shape, x.stride(), x.dtype, y.shape, y.stride(), y.dtype,
+           tuple((g.shape, g.stride(), g.dtype) for g in given), _weights_key(gate_up),
+           _weights_key(down), top_k, activation, renormalize, scale, intermediate)
+    _, d, _, r, need = _cached(key, lambda: _make_moe(x, route, gate_up, down, y, top_k, activation,
+                                                      renormalize, scale, intermediate))
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    if stream is None:
+        space = torch.empty(need, dtype=torch.uint8, device=y.device)
+    else:
+        with _on_stream(device, stream):
+            space = torch.empty(need, dtype=torch.uint8, device=y.device)
+    up = _w4_ptrs(gate_up) if isinstance(gate_up, tuple) else QWeightT(gate_up.data_ptr(), None, None)
+    dn = _w4_ptrs(down) if isinstance(down, tuple) else QWeightT(down.data_ptr(), None, None)
+    if len(given) == 2:
+        logits, ids, weights = None, given[0].data_ptr(), given[1].data_ptr()
+    else:
+        logits, ids, weights = given[0].data_ptr(), None, None
+    st = lib.tc_moe_async(ctx, d, x.data_ptr(), r, logits, ids, weights, ctypes.byref(up),
+                          ctypes.byref(dn), y.data_ptr(), space.data_ptr(), need, s)
+    if st != 0:
+        _check(st, ctx)
+    return y
 
 
 def gemm_sync(a, b, c, *, alpha: float = 1.0, beta: float = 0.0, transpose_a: bool = False,

@@ -27,7 +27,12 @@ ARCH = "gfx950"
 # dispatch object, and one GEMM object per input type and layout.
 _DT = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3}
 SOURCES = [("tcgemm", "tcgemm.cpp", []), ("epilogue_kernels", "epilogue_kernels.hip", []),
-           ("thin_kernel", "thin_kernel.hip", [])]
+           ("thin_kernel", "thin_kernel.hip", []), ("qweight", "qweight.cpp", []),
+           ("w4_format", "w4_format.hip", []), ("moe", "moe.cpp", []),
+           ("moe_route", "moe_route.hip", [])]
+for _name, _code in (("f16", 1), ("bf16", 2)):
+    SOURCES += [("w4_gemm_" + _name, "w4_gemm.hip", ["-DW4_DT=%d" % _code]),
+                ("moe_layer_" + _name, "moe_layer.hip", ["-DMOE_DT=%d" % _code])]
 for _name, _code in _DT.items():
     for _ta in (0, 1):
         for _tb in (0, 1):

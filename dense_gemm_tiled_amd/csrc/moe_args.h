@@ -1,0 +1,58 @@
+// moe_args.h -- what the host hands to the mixture-of-experts kernels.  Not
+// part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace tcg {
+
+constexpr int kMaxExperts = 512, kMaxTopK = 16;
+constexpr int kMoeChunk = 128;            // tokens handled together
+
+struct RouteArgs {
+    const void *logits;
+    int64_t ld;                // elements
+    int32_t T, E, top_k;
+    int32_t dtype;             // of the logits
+    int32_t renormalize;
+    float scale;
+    int32_t *ids;              // [T, top_k]
+    float *weights;            // [T, top_k]
+};
+
+// Per chunk of tokens, what the layer's kernels need of the routing: the
+// experts that have tokens, and the (token, weight) pairs sorted by expert.
+struct MoeChunkMeta {
+    int32_t active;                       // experts with at least one token
+    int32_t expert[kMaxExperts];          // in ascending order
+    int32_t start[kMaxExperts + 1];       // first pair of each; then their number
+    int32_t pad[2];
+};
+
+struct MoeArgs {
+    RouteArgs route;           // logits null: ids and weights are the caller's
+    const void *x;
+    void *y;
+    int64_t ldx, ldy;          // elements
+    int64_t x_bytes;
+    int32_t T, H, I, E, top_k;
+    int32_t dtype, y_dtype;
+    int32_t gate;              // 0 silu, 1 gelu_tanh
+    int32_t group;             // 0: 16-bit weights
+    const void *gate_up[3];    // codes (or weights), scales, zeros
+    const void *down[3];
+    // workspace
+    MoeChunkMeta *meta;        // [chunks]
+    int32_t *tok;              // [T * top_k] tokens (inside their chunk), by expert
+    float *wgt;                // [T * top_k] their weights
+    void *h;                   // [T * top_k][I16 / 8][16] 16-bit: 8 high parts, 8 low parts
+};
+
+}  // namespace tcg
+
+hipError_t tcg_launch_moe_route(const tcg::RouteArgs &a, hipStream_t s);
+hipError_t tcg_launch_moe_sort(const tcg::MoeArgs &a, hipStream_t s);
+// the layer's two products; *launches counts kernels
+hipError_t tcg_launch_moe_f16(const tcg::MoeArgs &a, int *launches, hipStream_t s);
+hipError_t tcg_launch_moe_bf16(const tcg::MoeArgs &a, int *launches, hipStream_t s);

@@ -1,0 +1,335 @@
+// w4_core.hpp -- the inner product that the 4-bit weight kernels and the
+// mixture-of-experts kernels share: one wave multiplies 16 * MT rows of
+// activations with NB blocks of 16 weight rows over a set of 128-wide blocks
+// of K, weights held in 4 bits (with group scales) or in 16.
+//
+// The 4-bit format.  W[n, k] = s[n, g] (q[n, k] - z[n, g]), q and z whole
+// numbers in 0..15 (z = 8 where none is held), g = k / G, G = 32, 64 or 128.
+// A block holds 16 rows x 128 k in 1024 bytes, 16 per lane: lane 16 kq + r
+// has row r, dword i its k = 32 i + 8 kq + j, j = 0..7 -- the right operand
+// of the i-th of four 16x16x32 matrix instructions.  j sits at bits
+// 4 (j / 2) + 16 (j % 2), so that a shift and a mask give two neighbouring k
+// in the two halves of a dword.
+//
+// Codes into 16-bit floats.  The four code bits go into the top mantissa
+// bits of a number with exponent 4: 16 + q exactly, in bf16 (7 mantissa
+// bits) and f16 (10) alike: one shift and one v_and_or per two weights.
+// Then per group, with every product exact and the sum in fp32,
+//     sum_k x (q - z)  =  sum_k x (16 + q)  +  sum_k x (-(16 + z)),
+// where the second sum is a matrix instruction too, whose right operand is
+// the constant -(16 + z) of lane n's row (whole numbers below 32 are exact
+// in both types).  The two nearly cancel: their terms are at most 4 times
+// the size of x * 8, so the fp32 sum loses about two of its 24 bits.  The
+// group's sum is multiplied by s in fp32 and added to the running result.
+// An infinity or NaN in x gives NaN in its row.
+//
+// Operand order: x is the left operand (row m = lane % 16 of the fragment),
+// the weights the right one, so a lane ends with column n = lane % 16 and
+// rows m = 4 (lane / 16) + 0..3, and needs one scale per group.  Row m of
+// the result depends on row m of x alone: lanes past the last row read some
+// valid row and their results are not stored.
+#pragma once
+
+#include "gemm_kernel.hpp"
+
+namespace tcg {
+namespace {
+
+typedef unsigned short u16;
+
+constexpr int kBlkN = 16, kBlkK = 128, kBlkBytes = 1024;
+
+template <int DT>
+__device__ inline f32x4 mfma_x_w(u32x4 x, u32x4 w, f32x4 c) {
+    if constexpr (DT == DT_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x),
+                                                      __builtin_bit_cast(f16x8, w), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
+                                                       __builtin_bit_cast(bf16x8, w), c, 0, 0, 0);
+}
+
+// A 16-bit float as fp32 (exact), and fp32 rounded to one (to nearest even).
+template <int DT>
+__device__ inline float from16(u32 v) {
+    if constexpr (DT == DT_F16) return (float)__builtin_bit_cast(_Float16, (u16)v);
+    else return as_f32(v << 16);
+}
+template <int DT>
+__device__ inline u16 to16(float v) {
+    if constexpr (DT == DT_F16) return __builtin_bit_cast(u16, (_Float16)v);
+    else return __builtin_bit_cast(u16, (__bf16)v);
+}
+
+// Eight codes of a dword as eight 16-bit floats 16 + q.
+template <int DT>
+__device__ inline u32x4 w4_expand(u32 d) {
+    constexpr u32 mask = DT == DT_F16 ? 0x03C003C0u : 0x00780078u;
+    constexpr u32 base = DT == DT_F16 ? 0x4C004C00u : 0x41804180u;
+    u32x4 r;
+    if constexpr (DT == DT_F16) {
+        r[0] = ((d << 6) & mask) | base;
+        r[1] = ((d << 2) & mask) | base;
+        r[2] = ((d >> 2) & mask) | base;
+        r[3] = ((d >> 6) & mask) | base;
+    } else {
+        r[0] = ((d << 3) & mask) | base;
+        r[1] = ((d >> 1) & mask) | base;
+        r[2] = ((d >> 5) & mask) | base;
+        r[3] = ((d >> 9) & mask) | base;
+    }
+    return r;
+}
+
+// -(16 + z) in both halves of a dword.
+template <int DT>
+__device__ inline u32 w4_neg_offset(u32 z) {
+    const u32 h = DT == DT_F16 ? 0xCC00u | (z << 6) : 0xC180u | (z << 3);
+    return h | (h << 16);
+}
+
+// What a kernel instance knows of its weights at compile time.  GP: groups
+// per block (1, 2, 4), 0 for 16-bit weights; ZP: zero points held.
+template <int DT_, int GP_, bool ZP_>
+struct WeightKind {
+    static constexpr int DT = DT_, GP = GP_;
+    static constexpr bool W4 = GP_ > 0, ZP = ZP_;
+};
+
+// One matrix [N, K] as the kernels see it.  16-bit weights: `codes` is the
+// first element, rows K apart.
+struct MatrixRef {
+    const char *codes;
+    const char *scales;
+    const char *zeros;
+};
+
+__host__ __device__ inline int64_t w4_blocks(int64_t N, int64_t K) {
+    return ((N + kBlkN - 1) / kBlkN) * ((K + kBlkK - 1) / kBlkK);
+}
+
+template <class WK>
+__device__ inline MatrixRef matrix_of(const MatrixRef &m, int64_t index, int N, int K) {
+    if constexpr (WK::W4) {
+        const int64_t b = index * w4_blocks(N, K);
+        return {m.codes + b * kBlkBytes, m.scales + b * (16 * WK::GP * 2),
+                WK::ZP ? m.zeros + b * (16 * WK::GP) : nullptr};
+    } else {
+        return {m.codes + index * N * K * 2, nullptr, nullptr};
+    }
+}
+
+// This lane's share of one block of weights, as loaded.
+template <class WK>
+struct WFrag {
+    u32x4 q[WK::W4 ? 1 : 4];
+    u32 s[WK::GP == 4 ? 2 : 1];    // GP 16-bit scales
+    u32 z;                         // GP zero points, a byte each
+};
+
+// The 16 weight rows from 16 nb on, as a stream of blocks along K.
+template <class WK>
+struct WStream {
+    const char *codes;     // W4: this lane's 16 bytes of block 0
+    const char *scales;    // W4: this lane's scales of block 0
+    const char *zeros;
+    __amdgpu_buffer_rsrc_t rows;   // 16-bit: the rows from 16 nb to N
+    int row_off;                   // 16-bit: byte offset of this lane's row, plus 16 kq
+    int K;
+
+    __device__ inline WStream() {}
+    __device__ inline WStream(const MatrixRef &m, int nb, int N, int K_, int lane) : K(K_) {
+        const int r = lane & 15, kq = lane >> 4;
+        if constexpr (WK::W4) {
+            const int64_t b = (int64_t)nb * ((K + kBlkK - 1) / kBlkK);
+            codes = m.codes + b * kBlkBytes + lane * 16;
+            scales = m.scales + (b * 16 + r) * (WK::GP * 2);
+            zeros = WK::ZP ? m.zeros + (b * 16 + r) * WK::GP : nullptr;
+        } else {
+            // rows past N lie past the range and read as zero
+            const int64_t first = (int64_t)nb * kBlkN;
+            rows = make_rsrc(m.codes + first * K * 2, (N - first) * K * 2);
+            row_off = r * K * 2 + kq * 16;
+        }
+    }
+
+    // kv: values of K from this block's first on (>= 128: a whole block).
+    __device__ inline void load(WFrag<WK> &f, int kb, int kv, int lane) const {
+        if constexpr (WK::W4) {
+            f.q[0] = *reinterpret_cast<const u32x4 *>(codes + (int64_t)kb * kBlkBytes);
+            const char *sp = scales + (int64_t)kb * (16 * WK::GP * 2);
+            if constexpr (WK::GP == 4) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
+                f.s[0] = v[0];
+                f.s[1] = v[1];
+            } else if constexpr (WK::GP == 2) {
+                f.s[0] = *reinterpret_cast<const u32 *>(sp);
+            } else {
+                f.s[0] = *reinterpret_cast<const u16 *>(sp);
+            }
+            if constexpr (WK::ZP) {
+                const char *zp = zeros + (int64_t)kb * (16 * WK::GP);
+                if constexpr (WK::GP == 4) f.z = *reinterpret_cast<const u32 *>(zp);
+                else if constexpr (WK::GP == 2) f.z = *reinterpret_cast<const u16 *>(zp);
+                else f.z = *reinterpret_cast<const unsigned char *>(zp);
+            }
+            // groups past the last value of K hold nothing: their codes meet
+            // zeros of x, and their scales, whatever is stored, become zero
+            if (WK::GP > 1 && kv < kBlkK) {
+                constexpr int G = kBlkK / (WK::GP ? WK::GP : 1);
+#pragma unroll
+                for (int g = 1; g < WK::GP; ++g)
+                    if (g * G >= kv) f.s[g >> 1] &= (g & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+            }
+        } else {
+            const int off = row_off + kb * (kBlkK * 2);
+            if (kv >= kBlkK) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f.q[i] = ld128(rows, off + i * 64);
+            } else {
+                const int k0 = (lane >> 4) * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = kv - (k0 + i * 32);
+                    f.q[i] = u32x4{0u, 0u, 0u, 0u};
+                    if (v >= 8) f.q[i] = ld128(rows, off + i * 64);
+                    else if (v > 0) f.q[i] = ld_partial<2>(rows, off + i * 64, v);
+                }
+            }
+        }
+    }
+};
+
+// One 16-row tile of 16-bit activations along K: row offsets are this lane's
+// (bytes from the resource's base, 16 kq included).
+struct XFrag {
+    u32x4 v[4];
+};
+
+__device__ inline void load_x(XFrag &f, __amdgpu_buffer_rsrc_t rx, int row_off, int kb, int kv,
+                              int lane) {
+    const int off = row_off + kb * (kBlkK * 2);
+    if (kv >= kBlkK) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.v[i] = ld128(rx, off + i * 64);
+    } else {
+        const int k0 = (lane >> 4) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = kv - (k0 + i * 32);
+            f.v[i] = u32x4{0u, 0u, 0u, 0u};
+            if (v >= 8) f.v[i] = ld128(rx, off + i * 64);
+            else if (v > 0) f.v[i] = ld_partial<2>(rx, off + i * 64, v);
+        }
+    }
+}
+
+// acc += x @ (one block of weights)^T.  XP: parts of x (1, or 2 where x is
+// held as the sum of two 16-bit numbers).  zsum (symmetric codes only): the
+// groups' -24 sum_k x, the same for every block of weight rows.
+template <class WK, int XP>
+__device__ inline void block_offset_sums(const XFrag (&x)[XP], f32x4 (&zsum)[WK::GP ? WK::GP : 1]) {
+    constexpr int GP = WK::GP ? WK::GP : 1, S = 4 / GP;
+    const u32 c = w4_neg_offset<WK::DT>(8);
+    const u32x4 cz = {c, c, c, c};
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+        zsum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = g * S; i < (g + 1) * S; ++i)
+#pragma unroll
+            for (int p = 0; p < XP; ++p) zsum[g] = mfma_x_w<WK::DT>(x[p].v[i], cz, zsum[g]);
+    }
+}
+
+template <class WK, int XP>
+__device__ inline void block_mma(const XFrag (&x)[XP], const u32x4 (&w)[4], const WFrag<WK> &f,
+                                 const f32x4 (&zsum)[WK::GP ? WK::GP : 1], f32x4 &acc) {
+    if constexpr (!WK::W4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < XP; ++p) acc = mfma_x_w<WK::DT>(x[p].v[i], w[i], acc);
+    } else {
+        constexpr int S = 4 / WK::GP;
+#pragma unroll
+        for (int g = 0; g < WK::GP; ++g) {
+            f32x4 c = zsum[g];
+            if constexpr (WK::ZP) {
+                const u32 o = w4_neg_offset<WK::DT>((f.z >> (8 * g)) & 15);
+                const u32x4 cz = {o, o, o, o};
+                c = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = g * S; i < (g + 1) * S; ++i)
+#pragma unroll
+                    for (int p = 0; p < XP; ++p) c = mfma_x_w<WK::DT>(x[p].v[i], cz, c);
+            }
+#pragma unroll
+            for (int i = g * S; i < (g + 1) * S; ++i)
+#pragma unroll
+                for (int p = 0; p < XP; ++p) c = mfma_x_w<WK::DT>(x[p].v[i], w[i], c);
+            const float s = from16<WK::DT>((f.s[g >> 1] >> (16 * (g & 1))) & 0xFFFFu);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(s, c[e], acc[e]);
+        }
+    }
+}
+
+// One wave: acc[nb][mt] += x rows @ weights^T over the K blocks kb0, kb0 +
+// step, .. below kb1.  Weights and activations of the next block are in
+// flight while one is multiplied (the same depth for both: loads return in
+// order, so a shallower queue of x would wait for every weight load issued
+// before it).  mts: 16-row tiles in use (uniform).
+template <class WK, int NB, int MT, int XP, class LoadX>
+__device__ inline void wave_products(const WStream<WK> (&w)[NB], const LoadX &loadx, int K, int kb0,
+                                     int step, int kb1, int mts, int lane, f32x4 (&acc)[NB][MT]) {
+    struct Stage {
+        WFrag<WK> w[NB];
+        XFrag x[MT][XP];
+    };
+    Stage st[2];
+    auto fetch = [&](Stage &s, int kb) {
+        const int kv = K - kb * kBlkK;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) w[b].load(s.w[b], kb, kv, lane);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            if (t == 0 || t < mts) loadx(s.x[t], t, kb, kv);
+    };
+    auto compute = [&](const Stage &s) {
+        f32x4 zsum[MT][WK::GP ? WK::GP : 1];
+        if constexpr (WK::W4 && !WK::ZP) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                if (t == 0 || t < mts) block_offset_sums<WK, XP>(s.x[t], zsum[t]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            u32x4 wv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if constexpr (WK::W4) wv[i] = w4_expand<WK::DT>(s.w[b].q[0][i]);
+                else wv[i] = s.w[b].q[i];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                if (t == 0 || t < mts) block_mma<WK, XP>(s.x[t], wv, s.w[b], zsum[t], acc[b][t]);
+        }
+    };
+    int kb = kb0;
+    if (kb >= kb1) return;
+    fetch(st[0], kb);
+#pragma unroll 1
+    while (true) {
+        if (kb + step < kb1) fetch(st[1], kb + step);
+        compute(st[0]);
+        kb += step;
+        if (kb >= kb1) break;
+        if (kb + step < kb1) fetch(st[0], kb + step);
+        compute(st[1]);
+        kb += step;
+        if (kb >= kb1) break;
+    }
+}
+
+}  // namespace
+}  // namespace tcg

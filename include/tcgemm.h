@@ -227,6 +227,142 @@ tc_status_t tc_gemm_epilogue_async(tc_context *ctx, const tc_gemm_batched_desc *
                                    const tc_epilogue *ep, const void *A,
                                    const void *B, void *C, tc_stream *s);
 
+/* ---------------------------------------------------------------------------
+ * Weights held in 4 bits, with a scale per group of K
+ *
+ *     W[n, k] = s[n, g] * (q[n, k] - z[n, g]),   g = k / group,
+ *
+ * q and z whole numbers in 0..15 (z = 8 where no zero points are held), s of
+ * the activations' type (f16 or bf16).  The arrays, for each of `batch`
+ * matrices one after the other, NB = ceil(N / 16), KB = ceil(K / 128):
+ *     codes   [NB][KB][1024] bytes: a block is 16 rows x 128 k.  Bytes
+ *             256 kq + 16 r + 4 i .. + 3 (kq, i = 0..3, r = 0..15) hold row r's
+ *             k = 32 i + 8 kq + j of the block, j = 0..7, a nibble each: byte
+ *             0 holds j = 0 (low) and 2 (high), byte 1 j = 4 and 6, byte 2
+ *             j = 1 and 3, byte 3 j = 5 and 7.
+ *     scales  [NB][KB][16][128 / group] of scale_dtype
+ *     zeros   the same shape, one byte each (its low 4 bits count), or NULL
+ * What the arrays hold past N and K is never part of a result.  All three
+ * start at 16-byte aligned addresses.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t batch;                /* matrices */
+    int32_t N, K;                 /* rows and columns of each */
+    int32_t group;                /* 32, 64 or 128 */
+    tc_dtype_t scale_dtype;       /* TC_F16 or TC_BF16 */
+    bool has_zeros;
+} tc_qweight_desc;
+
+typedef struct {
+    const void *codes;            /* device pointers, caller-owned */
+    const void *scales;
+    const void *zeros;            /* NULL exactly where !has_zeros */
+} tc_qweight;
+
+/* Bytes of the three arrays (host only; out pointers may be NULL). */
+tc_status_t tc_qweight_sizes(const tc_qweight_desc *d, int64_t *codes, int64_t *scales,
+                             int64_t *zeros);
+
+/* W (f32, f16 or bf16; row n of matrix b at W + b*stride_w + n*ldw elements,
+ * ldw 0 = K, stride_w 0 = N*ldw) into the arrays of *out.  Over each group
+ * (the last one may be short), with hi its largest and lo its smallest value:
+ *     without zeros  m = -lo > hi ? lo : hi,  s = m / -8,
+ *                    q = 8 + clamp(rint(w / s), -8, 7);
+ *     with zeros     hi = max(hi, 0), lo = min(lo, 0), s = (hi - lo) * (1/15),
+ *                    z = clamp(rint(-lo / s), 0, 15),
+ *                    q = clamp(rint(w / s) + z, 0, 15).
+ * s is computed in fp32 (1/15 its nearest number) and rounded to scale_dtype (its largest finite number
+ * where it overflows); the quotients go by that s and are rounded as exact
+ * ones are, ties to even.  A group whose s is 0 stands for zeros, one that
+ * holds a NaN or infinity gets a NaN scale. */
+tc_status_t tc_quantize_async(tc_context *ctx, const tc_qweight_desc *d, const void *W,
+                              tc_dtype_t w_dtype, int64_t ldw, int64_t stride_w,
+                              const tc_qweight *out, tc_stream *s);
+
+/* The values, rounded once to out_dtype (f32, f16 or bf16); ldo and stride_o
+ * as above.  Only the N x K values of each matrix are written. */
+tc_status_t tc_dequantize_async(tc_context *ctx, const tc_qweight_desc *d, const tc_qweight *w,
+                                void *out, tc_dtype_t out_dtype, int64_t ldo, int64_t stride_o,
+                                tc_stream *s);
+
+/* Lay out what another quantizer made: codes [batch][N][ceil(K/2)] (two per
+ * byte, the even k in the low nibble), scales and zeros (a byte each)
+ * [batch][N][ceil(K/group)], contiguous, into the arrays of *out. */
+tc_status_t tc_qweight_pack_async(tc_context *ctx, const tc_qweight_desc *d,
+                                  const tc_qweight *row_major, const tc_qweight *out, tc_stream *s);
+
+/* y[M,N] = activation(alpha * x[M,K] @ W^T + beta * y + bias): a linear
+ * layer whose weight (d, w; batch 1) is held in 4 bits, for one row of x or
+ * for many.  x has the type of the scales, y that type or f32; ep may be NULL
+ * and holds no col_scale.  fp32 sums, y written once.  A row of x that holds
+ * a NaN or infinity gives NaN.  No workspace. */
+typedef struct {
+    int32_t M;
+    tc_dtype_t x_dtype, y_dtype;
+    float alpha, beta;
+    int32_t ldx, ldy;             /* elements; 0 = contiguous */
+} tc_qgemm_desc;
+
+tc_status_t tc_qgemm_async(tc_context *ctx, const tc_qgemm_desc *g, const tc_qweight_desc *d,
+                           const void *x, const tc_qweight *w, void *y, const tc_epilogue *ep,
+                           tc_stream *s);
+
+/* ---------------------------------------------------------------------------
+ * Mixture of experts
+ * ------------------------------------------------------------------------- */
+
+/* ids[t, j], weights[t, j], j < top_k: the experts with the largest logits[t]
+ * (f32, f16 or bf16, rows ld apart, 0 = E), the largest first, ties to the
+ * lowest index, and
+ *     weights = scale * exp(l - l_max) / sum,
+ * the sum over the chosen ones (renormalize) or over all E.  A logit of -inf
+ * or NaN is never chosen and counts for nothing; a token with fewer than
+ * top_k others has id -1 and weight 0 in the places left.  +inf counts as the
+ * largest finite number.  E <= 512, top_k <= min(E, 16). */
+typedef struct {
+    int32_t T, E, top_k;
+    tc_dtype_t dtype;             /* of the logits */
+    int32_t ld;
+    bool renormalize;
+    float scale;
+} tc_route_desc;
+
+tc_status_t tc_moe_route_async(tc_context *ctx, const tc_route_desc *r, const void *logits,
+                               int32_t *ids, float *weights, tc_stream *s);
+
+/* A whole layer of gated experts:
+ *     y[t] = sum_j weights[t,j] * Wd[e] (act(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t,j].
+ * gate_up holds E x 2 matrices [I, H] (gate, up, gate, up, ..), down E
+ * matrices [H, I]: in x's type, contiguous (codes is the pointer, scales and
+ * zeros NULL, group 0), or in 4 bits (group, has_zeros; both alike).
+ * The routing is given by logits (then as tc_moe_route_async chooses, *r
+ * naming their type and layout; r->T, E and top_k equal the layer's) or by
+ * ids and weights [T, top_k], contiguous, with logits NULL and r NULL; an id
+ * outside [0, E) adds nothing, a token none of whose ids is inside has y = 0.
+ * act(gate) * up is held as the sum of two numbers of x's type (so f16
+ * overflows past 65504), every sum in fp32; results do not depend on the
+ * order in which the GPU runs the workgroups.  For few tokens: time grows
+ * with the experts touched, and from 128 tokens on with T.
+ * workspace: tc_moe_workspace bytes of device memory, 16-byte aligned, the
+ * caller's until the work on s has ended; nothing is kept in it. */
+typedef enum { TC_GATE_SILU = 0, TC_GATE_GELU_TANH = 1 } tc_gate_t;
+
+typedef struct {
+    int32_t T, H, I, E, top_k;
+    tc_dtype_t x_dtype, y_dtype;  /* f16 or bf16; x_dtype or f32 */
+    int32_t ldx, ldy;             /* elements; 0 = contiguous */
+    tc_gate_t gate;
+    int32_t group;                /* 0: weights of x_dtype */
+    bool has_zeros;
+} tc_moe_desc;
+
+tc_status_t tc_moe_workspace(const tc_moe_desc *d, int64_t *bytes);
+
+tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
+                         const tc_route_desc *r, const void *logits, const int32_t *ids,
+                         const float *weights, const tc_qweight *gate_up, const tc_qweight *down,
+                         void *y, void *workspace, int64_t workspace_bytes, tc_stream *s);
+
 /* First-call autotuning (the tile-class choice the pages leave to a
  * measured cache; tessl "Architecture", "GEMM Pipeline & Kernel Selection").
  * With it on, the first call of each problem (types, layout, M, N, K, batch,

@@ -61,11 +61,15 @@ __device__ inline u16 to16(float v) {
     else return __builtin_bit_cast(u16, (__bf16)v);
 }
 
-// Eight codes of a dword as eight 16-bit floats 16 + q.
+// Eight codes of a dword as eight 16-bit floats 16 + q.  The two constants
+// are kept in registers (a v_and_or takes one scalar and no literal; with
+// literals the compiler makes an and and an or of it).
 template <int DT>
 __device__ inline u32x4 w4_expand(u32 d) {
-    constexpr u32 mask = DT == DT_F16 ? 0x03C003C0u : 0x00780078u;
-    constexpr u32 base = DT == DT_F16 ? 0x4C004C00u : 0x41804180u;
+    u32 mask = DT == DT_F16 ? 0x03C003C0u : 0x00780078u;
+    u32 base = DT == DT_F16 ? 0x4C004C00u : 0x41804180u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(base));
     u32x4 r;
     if constexpr (DT == DT_F16) {
         r[0] = ((d << 6) & mask) | base;
@@ -130,22 +134,21 @@ struct WFrag {
 // The 16 weight rows from 16 nb on, as a stream of blocks along K.
 template <class WK>
 struct WStream {
-    const char *codes;     // W4: this lane's 16 bytes of block 0
-    const char *scales;    // W4: this lane's scales of block 0
-    const char *zeros;
+    __amdgpu_buffer_rsrc_t codes, scales, zeros;   // W4: these rows' blocks
     __amdgpu_buffer_rsrc_t rows;   // 16-bit: the rows from 16 nb to N
     int row_off;                   // 16-bit: byte offset of this lane's row, plus 16 kq
     int K;
 
     __device__ inline WStream() {}
     __device__ inline WStream(const MatrixRef &m, int nb, int N, int K_, int lane) : K(K_) {
-        const int r = lane & 15, kq = lane >> 4;
         if constexpr (WK::W4) {
-            const int64_t b = (int64_t)nb * ((K + kBlkK - 1) / kBlkK);
-            codes = m.codes + b * kBlkBytes + lane * 16;
-            scales = m.scales + (b * 16 + r) * (WK::GP * 2);
-            zeros = WK::ZP ? m.zeros + (b * 16 + r) * WK::GP : nullptr;
+            const int kbs = (K + kBlkK - 1) / kBlkK;
+            const int64_t b = (int64_t)nb * kbs;
+            codes = make_rsrc(m.codes + b * kBlkBytes, (int64_t)kbs * kBlkBytes);
+            scales = make_rsrc(m.scales + b * (16 * WK::GP * 2), (int64_t)kbs * (16 * WK::GP * 2));
+            if (WK::ZP) zeros = make_rsrc(m.zeros + b * (16 * WK::GP), (int64_t)kbs * (16 * WK::GP));
         } else {
+            const int r = lane & 15, kq = lane >> 4;
             // rows past N lie past the range and read as zero
             const int64_t first = (int64_t)nb * kBlkN;
             rows = make_rsrc(m.codes + first * K * 2, (N - first) * K * 2);
@@ -156,22 +159,24 @@ struct WStream {
     // kv: values of K from this block's first on (>= 128: a whole block).
     __device__ inline void load(WFrag<WK> &f, int kb, int kv, int lane) const {
         if constexpr (WK::W4) {
-            f.q[0] = *reinterpret_cast<const u32x4 *>(codes + (int64_t)kb * kBlkBytes);
-            const char *sp = scales + (int64_t)kb * (16 * WK::GP * 2);
+            // (lane part in a register, block part in a scalar one)
+            const int r = lane & 15;
+            f.q[0] = __builtin_amdgcn_raw_buffer_load_b128(codes, lane * 16, kb * kBlkBytes, 0);
+            const int so = r * (WK::GP * 2), sb = kb * (16 * WK::GP * 2);
             if constexpr (WK::GP == 4) {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales, so, sb, 0);
                 f.s[0] = v[0];
                 f.s[1] = v[1];
             } else if constexpr (WK::GP == 2) {
-                f.s[0] = *reinterpret_cast<const u32 *>(sp);
+                f.s[0] = __builtin_amdgcn_raw_buffer_load_b32(scales, so, sb, 0);
             } else {
-                f.s[0] = *reinterpret_cast<const u16 *>(sp);
+                f.s[0] = __builtin_amdgcn_raw_buffer_load_b16(scales, so, sb, 0);
             }
             if constexpr (WK::ZP) {
-                const char *zp = zeros + (int64_t)kb * (16 * WK::GP);
-                if constexpr (WK::GP == 4) f.z = *reinterpret_cast<const u32 *>(zp);
-                else if constexpr (WK::GP == 2) f.z = *reinterpret_cast<const u16 *>(zp);
-                else f.z = *reinterpret_cast<const unsigned char *>(zp);
+                const int zo = r * WK::GP, zb = kb * (16 * WK::GP);
+                if constexpr (WK::GP == 4) f.z = __builtin_amdgcn_raw_buffer_load_b32(zeros, zo, zb, 0);
+                else if constexpr (WK::GP == 2) f.z = __builtin_amdgcn_raw_buffer_load_b16(zeros, zo, zb, 0);
+                else f.z = __builtin_amdgcn_raw_buffer_load_b8(zeros, zo, zb, 0);
             }
             // groups past the last value of K hold nothing: their codes meet
             // zeros of x, and their scales, whatever is stored, become zero

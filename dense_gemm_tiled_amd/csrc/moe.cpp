@@ -41,7 +41,7 @@ tc_status_t check_route(const tc_route_desc *r, RouteArgs *a, int64_t *bytes, st
 
 // The layer's workspace: offsets of its parts.
 struct MoeSpace {
-    int64_t meta, tok, wgt, ids, weights, h, bytes;
+    int64_t meta, tok, wgt, place, ids, weights, h, part, bytes;
 };
 
 tc_status_t check_moe(const tc_moe_desc *d, MoeSpace *sp, std::string *err) {
@@ -68,16 +68,21 @@ tc_status_t check_moe(const tc_moe_desc *d, MoeSpace *sp, std::string *err) {
         return fail(err, TC_ERR_OVERFLOW, "H=%d or I=%d > %d", d->H, d->I, kMaxRowElems);
     if ((int64_t)d->E * ((d->I + 15) / 16) > 0x7FFFFFFF)
         return fail(err, TC_ERR_OVERFLOW, "E * I / 16 > 2^31-1");
+    if ((int64_t)d->T * ((d->H + 255) / 256) > 0x7FFFFFFF ||
+        (int64_t)d->E * ((d->H + 15) / 16) > 0x7FFFFFFF)
+        return fail(err, TC_ERR_OVERFLOW, "T * H / 256 or E * H / 16 > 2^31-1");
     // T <= 2^23, top_k <= 2^4, I <= 2^22: no product below wraps
     const int64_t chunks = (d->T + kMoeChunk - 1) / kMoeChunk, pairs = (int64_t)d->T * d->top_k;
     const int64_t I16 = up_to(d->I, 16);
     sp->meta = 0;
     sp->tok = up_to(chunks * (int64_t)sizeof(MoeChunkMeta), 256);
     sp->wgt = up_to(sp->tok + pairs * 4, 256);
-    sp->ids = up_to(sp->wgt + pairs * 4, 256);
+    sp->place = up_to(sp->wgt + pairs * 4, 256);
+    sp->ids = up_to(sp->place + pairs * 4, 256);
     sp->weights = up_to(sp->ids + pairs * 4, 256);
     sp->h = up_to(sp->weights + pairs * 4, 256);
-    sp->bytes = sp->h + pairs * I16 * 4;
+    sp->part = up_to(sp->h + pairs * I16 * 4, 256);
+    sp->bytes = sp->part + pairs * d->H * 4;
     return TC_OK;
 }
 
@@ -250,22 +255,30 @@ tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
     a.meta = reinterpret_cast<MoeChunkMeta *>(ws + sp.meta);
     a.tok = reinterpret_cast<int32_t *>(ws + sp.tok);
     a.wgt = reinterpret_cast<float *>(ws + sp.wgt);
+    a.place = reinterpret_cast<int32_t *>(ws + sp.place);
     a.h = ws + sp.h;
+    a.part = reinterpret_cast<float *>(ws + sp.part);
+    a.route.logits = logits;
+    a.route.ids = const_cast<int32_t *>(ids);
+    a.route.weights = const_cast<float *>(weights);
+    // The lists: none for one token; made together with the routing up to 16
+    // tokens (a wave each); after a routing launch of its own from there on.
     std::string name;
     hipError_t e = hipSuccess;
-    if (logits) {
-        a.route.logits = logits;
-        a.route.ids = reinterpret_cast<int32_t *>(ws + sp.ids);
-        a.route.weights = reinterpret_cast<float *>(ws + sp.weights);
-        e = tcg_launch_moe_route(a.route, s->stream);
+    const bool one = tcg_moe_one_fits(a);
+    if (!one) {
+        const bool fused = d->T <= 16;
+        if (logits && !fused) {
+            a.route.ids = reinterpret_cast<int32_t *>(ws + sp.ids);
+            a.route.weights = reinterpret_cast<float *>(ws + sp.weights);
+            e = tcg_launch_moe_route(a.route, s->stream);
+            if (e == hipSuccess) ctx->dispatches += 1;
+            name = "moe_route+";
+        }
+        if (e == hipSuccess) e = tcg_launch_moe_sort(a, fused, s->stream);
         if (e == hipSuccess) ctx->dispatches += 1;
-        name = "moe_route+";
-    } else {
-        a.route.ids = const_cast<int32_t *>(ids);
-        a.route.weights = const_cast<float *>(weights);
+        name += "moe_sort+";
     }
-    if (e == hipSuccess) e = tcg_launch_moe_sort(a, s->stream);
-    if (e == hipSuccess) ctx->dispatches += 1;
     int launches = 0;
     if (e == hipSuccess)
         e = d->x_dtype == TC_F16 ? tcg_launch_moe_f16(a, &launches, s->stream)
@@ -275,7 +288,7 @@ tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
         (void)hipGetLastError();
         return fail(err, TC_ERR_DEVICE, "kernel launch failed: %s", hipGetErrorString(e));
     }
-    ctx->last_kernel = name + "moe_sort+moe_up+moe_down";
+    ctx->last_kernel = name + (one ? "moe_one_up+moe_one_down" : "moe_up+moe_down+moe_combine");
     return TC_OK;
 }
 

@@ -9,6 +9,7 @@ namespace tcg {
 
 constexpr int kMaxExperts = 512, kMaxTopK = 16;
 constexpr int kMoeChunk = 128;            // tokens handled together
+constexpr int kMoeOneLds = 128 << 10;     // most bytes of h the one-token layer keeps in LDS
 
 struct RouteArgs {
     const void *logits;
@@ -46,13 +47,18 @@ struct MoeArgs {
     MoeChunkMeta *meta;        // [chunks]
     int32_t *tok;              // [T * top_k] tokens (inside their chunk), by expert
     float *wgt;                // [T * top_k] their weights
+    int32_t *place;            // [T * top_k] where a (token, choice) pair is in the lists, or -1
     void *h;                   // [T * top_k][I16 / 8][16] 16-bit: 8 high parts, 8 low parts
+    float *part;               // [T * top_k][H] each pair's second product
 };
 
 }  // namespace tcg
 
 hipError_t tcg_launch_moe_route(const tcg::RouteArgs &a, hipStream_t s);
-hipError_t tcg_launch_moe_sort(const tcg::MoeArgs &a, hipStream_t s);
-// the layer's two products; *launches counts kernels
+// route: choose from the logits (or the caller's ids) too, for T <= 16
+hipError_t tcg_launch_moe_sort(const tcg::MoeArgs &a, bool route, hipStream_t s);
+// one token: the whole layer in two kernels (tcg_moe_one_fits says whether)
+bool tcg_moe_one_fits(const tcg::MoeArgs &a);
+// the layer's products after the lists; *launches counts kernels
 hipError_t tcg_launch_moe_f16(const tcg::MoeArgs &a, int *launches, hipStream_t s);
 hipError_t tcg_launch_moe_bf16(const tcg::MoeArgs &a, int *launches, hipStream_t s);

@@ -1,214 +1,416 @@
-// moe_layer.hip -- the two products of a mixture-of-experts layer for few
-// tokens, experts in 16 or 4 bits.  One object per type of x (MOE_DT).
+// moe_layer.hip -- the products of a mixture-of-experts layer for few tokens,
+// experts in 16 or 4 bits.  One object per type of x (MOE_DT).
 //
-// Both are bound by reading the weights of the experts that have tokens:
-// each is read once per chunk of 128 tokens.  The first kernel makes
-// h = act(Wg x) * (Wu x) for every (token, expert) pair; the second
-// multiplies by Wd, weights and sums over a token's experts.  Between them h
-// is held as the sum of two 16-bit numbers, high and low part (16 mantissa
-// bits in bf16, 22 in f16): one number would add a second rounding of the
-// result's own size, and the second matrix instruction costs nothing where
-// memory is the bound.
+// They are bound by reading the weights of the experts that have tokens, each
+// once per chunk of 128 tokens.  The first product makes h = act(Wg x) * (Wu
+// x) for every (token, expert) pair, the second multiplies by Wd; the pairs
+// of a token are weighted and summed last.  h is held as the sum of two
+// 16-bit numbers, high and low part (16 mantissa bits in bf16, 22 in f16):
+// one number would add a second rounding of the result's own size, and the
+// second matrix instruction costs nothing where memory is the bound.
 #include "w4_core.hpp"
 
 #include "moe_args.h"
+#include "moe_route.hpp"
 
 namespace tcg {
 namespace {
 
 __device__ inline float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
-// First product.  A workgroup owns 16 rows of one expert's gate matrix and
-// the same 16 of its up matrix; its waves split K (= H) and add their sums in
-// LDS in wave order.  Tokens of the expert go 16 MT at a time.
-template <class WK, int MT>
-__global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs a) {
-    constexpr int W = 8;
-    __shared__ __attribute__((aligned(16))) float red[W * 2 * 256];
-    const MoeChunkMeta *meta = a.meta + blockIdx.y;
-    const int tiles = (a.I + 15) >> 4;
-    const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
-    if (slot >= meta->active) return;
-    const int e = meta->expert[slot], p0 = meta->start[slot], count = meta->start[slot + 1] - p0;
+// h = act(g) * u into its place: hi parts of 8 neighbours, then their lo parts.
+template <int DT>
+__device__ inline void store_h(u16 *row, int i, float g, float u, int gate) {
+    const float v = (gate == 0 ? silu(g) : gelu_tanh(g)) * u;
+    const u16 hi = to16<DT>(v);
+    // (an infinite high part stands alone)
+    const u16 lo = fabsf(from16<DT>(hi)) < INFINITY ? to16<DT>(v - from16<DT>(hi)) : (u16)0;
+    u16 *o = row + (i >> 3) * 16 + (i & 7);
+    o[0] = hi;
+    o[8] = lo;
+}
+
+// Rows m0 .. m0 + rows of an expert's list (at most 16 MT) through this
+// workgroup's 16 UT rows of its gate and up matrices; red: the waves' x
+// tiles, then their sums.
+constexpr int kUpWaves = 8;
+
+template <class WK, int MT, int UT, bool ONE, bool DIRECT>
+__device__ inline void up_rows(const MoeArgs &a, const WStream<WK> (&w)[2 * UT], __amdgpu_buffer_rsrc_t rx, u16 *h,
+                               const int32_t *tok, int m0, int rows, int tile0, int wave, int lane, float *red) {
+    constexpr int W = kUpWaves, NB = 2 * UT;
+    const int tid = wave * 64 + lane, I16 = (a.I + 15) / 16 * 16;
+    f32x4 acc[NB][MT];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    char *const buf = reinterpret_cast<char *>(red) + wave * RowTile<1>::LDS_BYTES;
+    if constexpr (DIRECT) {
+        static_assert(MT == 1, "one tile");
+        const int t = ONE ? 0 : tok[m0 + min(lane & 15, rows - 1)];
+        const int x_off[1][1] = {{t * (int)a.ldx * 2 + (lane >> 4) * 16}};
+        wave_products<WK, NB, 1, 1, true>(w, rx, x_off, buf, a.H, wave, W, lane, acc);
+    } else {
+        int x_off[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = min(16 * t + 4 * q + (lane >> 4), rows - 1);
+                x_off[t][q] = tok[m0 + r] * (int)a.ldx * 2 + (lane & 15) * 16;
+            }
+        wave_products<WK, NB, MT, 1, false>(w, rx, x_off, buf, a.H, wave, W, lane, acc);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        if (t) __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                red[(wave * NB + b) * 256 + ((lane >> 4) * 4 + q) * 16 + (lane & 15)] = acc[b][t][q];
+        __syncthreads();
+        const int live = min(rows - 16 * t, 16) * 16 * UT;
+        if (tid < live) {
+            const int m = tid / (16 * UT), ut = tid / 16 % UT, c = tid & 15;
+            float g = 0.f, u = 0.f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) {
+                g += red[(q * NB + 2 * ut) * 256 + m * 16 + c];
+                u += red[(q * NB + 2 * ut + 1) * 256 + m * 16 + c];
+            }
+            const int i = (tile0 + ut) * 16 + c;
+            // (zeros from I to the next multiple of 16)
+            if (i >= a.I) g = u = 0.f;
+            if (i < I16) store_h<WK::DT>(h + (int64_t)(m0 + 16 * t + m) * I16 * 2, i, g, u, a.gate);
+        }
+    }
+}
+
+// First product.  A workgroup owns 16 UT rows of one expert's gate matrix and
+// the same rows of its up matrix; its waves split K (= H) and add their sums
+// in LDS in wave order.  Tokens of the expert go 16 MT at a time.  ONE: the
+// only token of the layer, whose routing every workgroup makes for itself
+// (workgroups are numbered by the choice, not by the list of experts) and
+// hands on to the second product.  MT 1 is for at most 16 tokens: an expert
+// has few of them then, and x goes straight into operand layout.
+template <class WK, int MT, int UT, bool ONE>
+__global__ __launch_bounds__(512, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
+    constexpr int W = kUpWaves, NB = 2 * UT;
+    // the waves' x tiles, then their sums
+    constexpr int RED = W * NB * 256, TILES = W * RowTile<1>::LDS_BYTES / 4;
+    __shared__ __attribute__((aligned(16))) float red[RED > TILES ? RED : TILES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tiles = (a.I + 15) >> 4, groups = (tiles + UT - 1) / UT;
+    const int slot = blockIdx.x / groups, tile0 = (blockIdx.x - slot * groups) * UT;
     const int t0 = blockIdx.y * kMoeChunk;
+    int e, p0, count;
+    if constexpr (ONE) {
+        __shared__ int one;
+        if (wave == 0) {
+            int id;
+            float w;
+            token_choices(a.route, 0, lane, id, w);
+            if (lane == slot) {
+                one = id;
+                if (tile0 == 0) {
+                    a.place[slot] = id;
+                    a.wgt[slot] = w;
+                }
+            }
+        }
+        __syncthreads();
+        e = __builtin_amdgcn_readfirstlane(one);
+        if (e < 0) return;
+        p0 = slot;
+        count = 1;
+    } else {
+        const MoeChunkMeta *meta = a.meta + blockIdx.y;
+        if (slot >= meta->active) return;
+        e = meta->expert[slot];
+        p0 = meta->start[slot];
+        count = meta->start[slot + 1] - p0;
+    }
     const int64_t list = (int64_t)t0 * a.top_k + p0;
-    const int K = a.H, kbs = (K + kBlkK - 1) / kBlkK, I16 = tiles * 16;
+    const int K = a.H, I16 = tiles * 16;
 
     const MatrixRef all = {static_cast<const char *>(a.gate_up[0]), static_cast<const char *>(a.gate_up[1]),
                            static_cast<const char *>(a.gate_up[2])};
-    WStream<WK> w[2];
+    WStream<WK> w[NB];
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-        w[g] = WStream<WK>(matrix_of<WK>(all, (int64_t)e * 2 + g, a.I, K), tile, a.I, K, lane);
+    for (int b = 0; b < NB; ++b)
+        w[b] = WStream<WK>(matrix_of<WK>(all, (int64_t)e * 2 + (b & 1), a.I, K),
+                           min(tile0 + (b >> 1), tiles - 1), a.I, K, lane);
     const int64_t x_org = (int64_t)t0 * a.ldx * 2;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + x_org, a.x_bytes - x_org);
     u16 *h = static_cast<u16 *>(a.h) + list * I16 * 2;
 
+    float *const r = red;
     for (int m0 = 0; m0 < count; m0 += 16 * MT) {
-        const int rows = min(count - m0, 16 * MT), mts = (rows + 15) >> 4;
-        int x_off[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            x_off[t] = a.tok[list + m0 + min(16 * t + (lane & 15), rows - 1)] * (int)a.ldx * 2 +
-                       (lane >> 4) * 16;
-        auto loadx = [&](XFrag (&f)[1], int t, int kb, int kv) { load_x(f[0], rx, x_off[t], kb, kv, lane); };
-        f32x4 acc[2][MT];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        wave_products<WK, 2, MT, 1>(w, loadx, K, wave, W, kbs, mts, lane, acc);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if (t > 0 && t >= mts) break;
-            __syncthreads();
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    red[(wave * 2 + b) * 256 + ((lane >> 4) * 4 + q) * 16 + (lane & 15)] = acc[b][t][q];
-            __syncthreads();
-            const int m = tid >> 4, c = tid & 15;
-            if (m < min(rows - 16 * t, 16)) {
-                float g = 0.f, u = 0.f;
-#pragma unroll
-                for (int q = 0; q < W; ++q) {
-                    g += red[(q * 2) * 256 + m * 16 + c];
-                    u += red[(q * 2 + 1) * 256 + m * 16 + c];
-                }
-                const int i = tile * 16 + c;
-                const float v = i < a.I ? (a.gate == 0 ? silu(g) : gelu_tanh(g)) * u : 0.f;
-                const u16 hi = to16<WK::DT>(v);
-                const float rest = v - from16<WK::DT>(hi);
-                // (an infinite high part stands alone)
-                const u16 lo = fabsf(from16<WK::DT>(hi)) < INFINITY ? to16<WK::DT>(rest) : (u16)0;
-                u16 *o = h + (int64_t)(m0 + 16 * t + m) * I16 * 2 + (i >> 3) * 16 + (i & 7);
-                o[0] = hi;
-                o[8] = lo;
-            }
-        }
+        const int rows = min(count - m0, 16 * MT);
+        if (MT == 1 || rows <= 16)
+            up_rows<WK, 1, UT, ONE, MT == 1>(a, w, rx, h, ONE ? nullptr : a.tok + list, m0, rows, tile0, wave, lane, r);
+        else
+            up_rows<WK, MT, UT, ONE, false>(a, w, rx, h, a.tok + list, m0, rows, tile0, wave, lane, r);
+        __syncthreads();   // (the sums' LDS is the next rows' tiles)
     }
 }
 
-// Second product.  A workgroup owns 16 columns of y for every token of the
-// chunk, and goes through all experts that have tokens: its waves share out
-// the (expert, block of K) units in order, each adds what its units give,
-// weighted, to sums of its own in LDS, and at the end the waves' sums are
-// added in wave order.  No sum crosses workgroups, so no atomics and no
-// second pass, and the result does not depend on timing.
-template <class WK, int MT>
-__global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs a) {
-    constexpr int W = 8;
+// Second product of the one-token layer.  A workgroup owns 16 columns of y
+// and all of the token's experts: h of all of them lies in LDS, the waves
+// share out the (expert, block of K) units in order, DEPTH of them in flight
+// each, weight what an expert gives, and their sums are added in wave order.
+// Straight into y: no third kernel, which would be a fifth of the time here.
+template <class WK>
+__global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
+    constexpr int W = 16, DEPTH = WK::W4 ? 6 : 4;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int t0 = blockIdx.y * kMoeChunk, tokens = min(a.T - t0, kMoeChunk);
-    const MoeChunkMeta *meta = a.meta + blockIdx.y;
-    const int active = meta->active, pairs = meta->start[active];
-    float *sums = reinterpret_cast<float *>(lds);                      // [W][tokens][16]
-    int *tok = reinterpret_cast<int *>(sums + W * tokens * 16);        // [pairs]
-    float *wgt = reinterpret_cast<float *>(tok + tokens * a.top_k);    // [pairs]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t list = (int64_t)t0 * a.top_k;
-    for (int i = tid; i < W * tokens * 16; i += W * 64) sums[i] = 0.f;
-    for (int i = tid; i < pairs; i += W * 64) {
-        tok[i] = a.tok[list + i];
-        wgt[i] = a.wgt[list + i];
+    const int K = a.I, kbs = (K + kBlkK - 1) / kBlkK, I16 = (a.I + 15) / 16 * 16;
+    const int row = kbs * kBlkK * 4;                 // bytes of h per expert in LDS
+    float *red = reinterpret_cast<float *>(lds + a.top_k * row);
+    __shared__ int expert[kMaxTopK], choice[kMaxTopK];
+    __shared__ float weight[kMaxTopK];
+    // the choices that hold an expert (the same in every wave), closed up
+    const int id = lane < a.top_k ? a.place[lane] : -1;
+    const uint64_t have = __ballot(id >= 0);
+    const int n = __builtin_popcountll(have);
+    if (wave == 0 && id >= 0) {
+        const int at = __builtin_popcountll(have & ((1ull << lane) - 1));
+        choice[at] = lane;
+        expert[at] = id;
+        weight[at] = a.wgt[lane];
     }
     __syncthreads();
-
-    const int K = a.I, kbs = (K + kBlkK - 1) / kBlkK, I16 = (a.I + 15) / 16 * 16;
     const MatrixRef all = {static_cast<const char *>(a.down[0]), static_cast<const char *>(a.down[1]),
                            static_cast<const char *>(a.down[2])};
-    const int units = active * kbs;
-    const int u1 = (int)((int64_t)units * (wave + 1) / W);
-    float *mine = sums + wave * tokens * 16;
-    for (int u = (int)((int64_t)units * wave / W); u < u1;) {
-        const int slot = u / kbs, kb0 = u - slot * kbs, kb1 = min(kbs, kb0 + u1 - u);
-        u += kb1 - kb0;
-        const int p0 = meta->start[slot], count = meta->start[slot + 1] - p0;
-        const WStream<WK> w[1] = {
-            WStream<WK>(matrix_of<WK>(all, meta->expert[slot], a.H, K), blockIdx.x, a.H, K, lane)};
-        const char *h = static_cast<const char *>(a.h) + (list + p0) * I16 * 4;
-        const __amdgpu_buffer_rsrc_t rh = make_rsrc(h, (int64_t)count * I16 * 4);
-        for (int m0 = 0; m0 < count; m0 += 16 * MT) {
-            const int rows = min(count - m0, 16 * MT), mts = (rows + 15) >> 4;
-            int h_off[MT];
+    const int units = n * kbs;
+    const int u0 = units * wave / W, u1 = units * (wave + 1) / W;
+    WFrag<WK> f[DEPTH];
+    auto fetch = [&](WFrag<WK> &s, int u) {
+        const int j = u / kbs, kb = u - j * kbs;
+        const int e = __builtin_amdgcn_readfirstlane(expert[j]);
+        const WStream<WK> w(matrix_of<WK>(all, e, a.H, K), blockIdx.x, a.H, K, lane);
+        if (K - kb * kBlkK < kBlkK) w.template load<true>(s, kb, K - kb * kBlkK, lane);
+        else w.template load<false>(s, kb, kBlkK, lane);
+    };
+    // h (few, and read by everyone) into LDS first: loads return in order
+    for (int i = tid; i < n * (row / 16); i += W * 64) {
+        const int j = i / (row / 16), at = (i - j * (row / 16)) * 16;
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (at < I16 * 4)
+            v = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.h) + (int64_t)choice[j] * I16 * 4 + at);
+        *reinterpret_cast<u32x4 *>(lds + j * row + at) = v;
+    }
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                h_off[t] = (m0 + min(16 * t + (lane & 15), rows - 1)) * I16 * 4 + (lane >> 4) * 32;
-            auto loadx = [&](XFrag (&f)[2], int t, int kb, int kv) {
-                const int k0 = (lane >> 4) * 8;
+    for (int d = 0; d < DEPTH; ++d)
+        if (u0 + d < u1) fetch(f[d], u0 + d);
+    // (not __syncthreads: the weights stay in flight)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    float total = 0.f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](const WFrag<WK> &s, int u) {
+        const int j = u / kbs, kb = u - j * kbs;
+        XFrag x[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // h is zero from I to the next multiple of 16
-                    const int off = h_off[t] + (kb * kBlkK + i * 32) * 4;
-                    f[0].v[i] = f[1].v[i] = u32x4{0u, 0u, 0u, 0u};
-                    if (k0 + i * 32 < kv) {
-                        f[0].v[i] = ld128(rh, off);
-                        f[1].v[i] = ld128(rh, off + 16);
-                    }
-                }
-            };
-            f32x4 acc[1][MT];
+        for (int i = 0; i < 4; ++i) {
+            const char *at = lds + j * row + (kb * kBlkK + i * 32 + (lane >> 4) * 8) * 4;
+            x[0].v[i] = *reinterpret_cast<const u32x4 *>(at);
+            x[1].v[i] = *reinterpret_cast<const u32x4 *>(at + 16);
+        }
+        f32x4 zsum[WK::GP ? WK::GP : 1];
+        if constexpr (WK::W4 && !WK::ZP) block_offset_sums<WK, 2>(x, zsum);
+        u32x4 wv[4];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            wave_products<WK, 1, MT, 2>(w, loadx, K, kb0, 1, kb1, mts, lane, acc);
+        for (int i = 0; i < 4; ++i)
+            if constexpr (WK::W4) wv[i] = w4_expand<WK::DT>(s.q[0][i]);
+            else wv[i] = s.q[i];
+        block_mma<WK, 2>(x, wv, s, zsum, acc);
+        if (kb + 1 == kbs || u + 1 == u1) {
+            // (all rows of the fragment are the token's)
+            total = __builtin_fmaf(weight[j], acc[0], total);
+            acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    };
+#pragma unroll 1
+    for (int u = u0; u < u1; u += DEPTH) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = 16 * t + (lane >> 4) * 4 + q;
-                    if (m < rows) {
-                        const int p = p0 + m0 + m;
-                        float *s = mine + tok[p] * 16 + (lane & 15);
-                        *s = __builtin_fmaf(wgt[p], acc[0][t][q], *s);
-                    }
-                }
-            }
+        for (int d = 0; d < DEPTH; ++d) {
+            if (u + d >= u1) break;
+            compute(f[d], u + d);
+            if (u + d + DEPTH < u1) fetch(f[d], u + d + DEPTH);
         }
     }
+    if (lane < 16) red[wave * 16 + lane] = total;
     __syncthreads();
-    for (int i = tid; i < tokens * 16; i += W * 64) {
-        const int n = blockIdx.x * 16 + (i & 15);
-        if (n >= a.H) continue;
+    const int c = blockIdx.x * 16 + tid;
+    if (tid < 16 && c < a.H) {
         float v = 0.f;
 #pragma unroll
-        for (int q = 0; q < W; ++q) v += sums[q * tokens * 16 + i];
-        const int64_t at = (int64_t)(t0 + (i >> 4)) * a.ldy + n;
-        if (a.y_dtype == DT_F32) static_cast<float *>(a.y)[at] = v;
-        else static_cast<u16 *>(a.y)[at] = to16<WK::DT>(v);
+        for (int q = 0; q < W; ++q) v += red[q * 16 + tid];
+        if (a.y_dtype == DT_F32) static_cast<float *>(a.y)[c] = v;
+        else static_cast<u16 *>(a.y)[c] = to16<WK::DT>(v);
     }
 }
 
-template <class WK, int MT>
-hipError_t launch_mt(const MoeArgs &a, int *launches, hipStream_t s) {
-    const int chunk = a.T < kMoeChunk ? a.T : kMoeChunk;
-    const unsigned chunks = (unsigned)((a.T + kMoeChunk - 1) / kMoeChunk);
-    const int slots = a.E < chunk * a.top_k ? a.E : chunk * a.top_k;
-    const int64_t up = (int64_t)slots * ((a.I + 15) / 16);
-    if (up > 0x7FFFFFFF || chunks > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((moe_up_kernel<WK, MT>), dim3((unsigned)up, chunks), dim3(512), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    ++*launches;
-    const size_t lds = (size_t)chunk * (8 * 16 * 4 + a.top_k * 8);
-    hipLaunchKernelGGL((moe_down_kernel<WK, MT>), dim3((unsigned)((a.H + 15) / 16), chunks), dim3(512),
-                       lds, s, a);
-    e = hipGetLastError();
+// Second product.  A workgroup owns 16 NB columns and one expert's pairs; its
+// waves split K (= I).  Each pair's product goes to scratch memory in fp32
+// (T top_k H values, a few percent of the weights that were read for them),
+// and moe_combine_kernel adds a token's: no atomics, and a result that does
+// not depend on timing.
+template <class WK, int NB, bool DIRECT>
+__global__ __launch_bounds__(256, 2) void moe_down_kernel(MoeArgs a) {
+    constexpr int W = 4;
+    // the waves' h tiles, then their sums
+    constexpr int RED = W * NB * 256, TILES = W * RowTile<2>::LDS_BYTES / 4;
+    __shared__ __attribute__((aligned(16))) float red[RED > TILES ? RED : TILES];
+    const MoeChunkMeta *meta = a.meta + blockIdx.y;
+    const int tiles = (a.H + 15) >> 4, groups = (tiles + NB - 1) / NB;
+    const int slot = blockIdx.x / groups, tile0 = (blockIdx.x - slot * groups) * NB;
+    if (slot >= meta->active) return;
+    const int e = meta->expert[slot], p0 = meta->start[slot], count = meta->start[slot + 1] - p0;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t list = (int64_t)blockIdx.y * kMoeChunk * a.top_k + p0;
+    const int K = a.I, I16 = (a.I + 15) / 16 * 16;
+    const MatrixRef all = {static_cast<const char *>(a.down[0]), static_cast<const char *>(a.down[1]),
+                           static_cast<const char *>(a.down[2])};
+    WStream<WK> w[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        w[b] = WStream<WK>(matrix_of<WK>(all, e, a.H, K), min(tile0 + b, tiles - 1), a.H, K, lane);
+    const __amdgpu_buffer_rsrc_t rh =
+        make_rsrc(static_cast<const char *>(a.h) + list * I16 * 4, (int64_t)count * I16 * 4);
+    for (int m0 = 0; m0 < count; m0 += 16) {
+        const int rows = min(count - m0, 16);
+        f32x4 acc[NB][1];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            acc[b][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+        char *const buf = reinterpret_cast<char *>(red) + wave * RowTile<2>::LDS_BYTES;
+        if constexpr (DIRECT) {
+            const int h_off[1][1] = {{(m0 + min(lane & 15, rows - 1)) * I16 * 4 + (lane >> 4) * 32}};
+            wave_products<WK, NB, 1, 2, true>(w, rh, h_off, buf, K, wave, W, lane, acc);
+        } else {
+            int h_off[1][8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                h_off[0][q] = (m0 + min(2 * q + (lane >> 5), rows - 1)) * I16 * 4 + (lane & 31) * 16;
+            wave_products<WK, NB, 1, 2, false>(w, rh, h_off, buf, K, wave, W, lane, acc);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                red[(wave * NB + b) * 256 + ((lane >> 4) * 4 + q) * 16 + (lane & 15)] = acc[b][0][q];
+        __syncthreads();
+        for (int o = tid; o < rows * 16 * NB; o += W * 64) {
+            const int m = o / (16 * NB), b = o / 16 % NB, c = o & 15;
+            const int n = (tile0 + b) * 16 + c;
+            if (n >= a.H) continue;
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) v += red[(q * NB + b) * 256 + m * 16 + c];
+            a.part[(list + m0 + m) * a.H + n] = v;
+        }
+        __syncthreads();   // (the sums' LDS is the next rows' tiles)
+    }
+}
+
+// y[t] = sum of the token's pairs, weighted, in the order of its choices.
+template <int DT>
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
+    const int cols = (a.H + 255) / 256;
+    const int64_t t = blockIdx.x / cols;
+    const int n = (int)(blockIdx.x - t * cols) * 256 + threadIdx.x;
+    if (n >= a.H) return;
+    const int64_t list = t / kMoeChunk * kMoeChunk * a.top_k;
+    // all the places, then all the products: two latencies, not two a choice
+    int at[kMaxTopK];
+    float p[kMaxTopK], w[kMaxTopK];
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) at[j] = j < a.top_k ? a.place[t * a.top_k + j] : -1;
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) {
+        p[j] = w[j] = 0.f;
+        if (at[j] >= 0) {
+            p[j] = a.part[(list + at[j]) * a.H + n];
+            w[j] = a.wgt[list + at[j]];
+        }
+    }
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) v = __builtin_fmaf(w[j], p[j], v);
+    const int64_t o = t * a.ldy + n;
+    if (a.y_dtype == DT_F32) static_cast<float *>(a.y)[o] = v;
+    else static_cast<u16 *>(a.y)[o] = to16<DT>(v);
+}
+
+template <class WK, int MT, int UT, bool ONE>
+hipError_t launch_up(const MoeArgs &a, int slots, unsigned chunks, int *launches, hipStream_t s) {
+    const int64_t grid = (int64_t)slots * (((a.I + 15) / 16 + UT - 1) / UT);
+    if (grid > 0x7FFFFFFF || chunks > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((moe_up_kernel<WK, MT, UT, ONE>), dim3((unsigned)grid, chunks), dim3(512), 0, s, a);
+    const hipError_t e = hipGetLastError();
     if (e == hipSuccess) ++*launches;
     return e;
 }
 
+template <class WK, int NB, bool DIRECT>
+hipError_t launch_down(const MoeArgs &a, int slots, unsigned chunks, int *launches, hipStream_t s) {
+    const int64_t grid = (int64_t)slots * (((a.H + 15) / 16 + NB - 1) / NB);
+    if (grid > 0x7FFFFFFF || chunks > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((moe_down_kernel<WK, NB, DIRECT>), dim3((unsigned)grid, chunks), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e == hipSuccess) ++*launches;
+    return e;
+}
+
+int one_lds_bytes(const MoeArgs &a) { return a.top_k * ((a.I + kBlkK - 1) / kBlkK * kBlkK * 4) + 16 * 16 * 4; }
+
 template <class WK>
 hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
-    if (a.T <= 16) return launch_mt<WK, 1>(a, launches, s);
-    return launch_mt<WK, 2>(a, launches, s);
+    hipError_t e;
+    if (tcg_moe_one_fits(a)) {
+        if ((e = launch_up<WK, 1, 1, true>(a, a.top_k, 1, launches, s)) != hipSuccess) return e;
+        hipLaunchKernelGGL(moe_one_down_kernel<WK>, dim3((unsigned)((a.H + 15) / 16)), dim3(1024),
+                           one_lds_bytes(a), s, a);
+        e = hipGetLastError();
+        if (e == hipSuccess) ++*launches;
+        return e;
+    }
+    const int chunk = a.T < kMoeChunk ? a.T : kMoeChunk;
+    const unsigned chunks = (unsigned)((a.T + kMoeChunk - 1) / kMoeChunk);
+    const int slots = a.E < chunk * a.top_k ? a.E : chunk * a.top_k;
+    // (as many blocks of the second product as two stages of them and of h
+    // leave registers for)
+    constexpr int NB = WK::GP == 1 || WK::GP == 2 ? 4 : 2;
+    if (a.T <= 16) {
+        if ((e = launch_up<WK, 1, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
+        e = launch_down<WK, NB, true>(a, slots, chunks, launches, s);
+    } else {
+        if ((e = launch_up<WK, 2, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
+        e = launch_down<WK, NB, false>(a, slots, chunks, launches, s);
+    }
+    if (e != hipSuccess) return e;
+    const int64_t grid = (int64_t)a.T * ((a.H + 255) / 256);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(moe_combine_kernel<WK::DT>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    e = hipGetLastError();
+    if (e == hipSuccess) ++*launches;
+    return e;
 }
 
 }  // namespace
 }  // namespace tcg
 
 using namespace tcg;
+
+#if MOE_DT == 1
+bool tcg_moe_one_fits(const MoeArgs &a) { return a.T == 1 && one_lds_bytes(a) <= kMoeOneLds; }
+#endif
 
 #if MOE_DT == 1
 #define MOE_LAUNCHER tcg_launch_moe_f16

@@ -1,99 +1,9 @@
 // moe_route.hip -- which experts each token goes to, and the lists that the
 // layer's kernels (moe_layer.hip) work from.
-#include "gemm_kernel.hpp"
-
-#include "moe_args.h"
+#include "moe_route.hpp"
 
 namespace tcg {
 namespace {
-
-typedef unsigned short u16;
-
-// Wave-wide maximum and sum over DPP (row shifts, then row broadcasts): the
-// result is in lane 63.  No LDS: a cross-lane read there costs an order of
-// magnitude more, and the top-k loop below takes one maximum per choice.
-template <int CTRL, int ROW_MASK>
-__device__ inline u32 dpp_u32(u32 v) {
-    return (u32)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false);
-}
-__device__ inline u32 wave_max(u32 v) {
-    v = max(v, dpp_u32<0x111, 0xF>(v));   // row_shr 1, 2, 4, 8
-    v = max(v, dpp_u32<0x112, 0xF>(v));
-    v = max(v, dpp_u32<0x114, 0xF>(v));
-    v = max(v, dpp_u32<0x118, 0xF>(v));
-    v = max(v, dpp_u32<0x142, 0xA>(v));   // row_bcast 15, 31
-    v = max(v, dpp_u32<0x143, 0xC>(v));
-    return (u32)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ inline float wave_sum(float x) {
-    u32 v = as_u32(x);
-    v = as_u32(as_f32(v) + as_f32(dpp_u32<0x111, 0xF>(v)));
-    v = as_u32(as_f32(v) + as_f32(dpp_u32<0x112, 0xF>(v)));
-    v = as_u32(as_f32(v) + as_f32(dpp_u32<0x114, 0xF>(v)));
-    v = as_u32(as_f32(v) + as_f32(dpp_u32<0x118, 0xF>(v)));
-    v = as_u32(as_f32(v) + as_f32(dpp_u32<0x142, 0xA>(v)));
-    v = as_u32(as_f32(v) + as_f32(dpp_u32<0x143, 0xC>(v)));
-    return as_f32((u32)__builtin_amdgcn_readlane((int)v, 63));
-}
-
-__device__ inline float load_logit(const void *p, int64_t i, int dtype) {
-    if (dtype == DT_F32) return static_cast<const float *>(p)[i];
-    const u16 v = static_cast<const u16 *>(p)[i];
-    return dtype == DT_F16 ? (float)__builtin_bit_cast(_Float16, v) : as_f32((u32)v << 16);
-}
-
-// One token by one wave: on return lane j < top_k holds the j-th choice (id
-// -1, weight 0 where there is none).  A logit becomes a whole number in the
-// same order (0: never chosen), S of them per lane, neighbours in one lane:
-// then the first lane that holds the maximum holds the lowest index.
-template <int S>
-__device__ inline void route_token(const RouteArgs &a, int64_t t, int lane, int &id, float &weight) {
-    u32 key[S];
-    float val[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int e = lane * S + s;
-        val[s] = e < a.E ? load_logit(a.logits, t * a.ld + e, a.dtype) : -INFINITY;
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const bool none = !(val[s] > -INFINITY);       // -inf or NaN
-        val[s] = fminf(val[s], 3.4028235e38f) + 0.f;   // +inf; -0 becomes 0
-        const u32 b = as_u32(val[s]);
-        key[s] = none ? 0u : ((b >> 31) ? ~b : b | 0x80000000u);
-    }
-    float top = 0.f, mine = 0.f, sum = 0.f;
-    id = -1;
-    for (int j = 0; j < a.top_k; ++j) {
-        u32 best = 0;
-        int at = 0;
-#pragma unroll
-        for (int s = S - 1; s >= 0; --s)
-            if (key[s] >= best) best = key[s], at = s;
-        const u32 m = wave_max(best);
-        if (m == 0) break;
-        const int src = __builtin_ctzll(__ballot(best == m));
-        const int e = __builtin_amdgcn_readlane(lane * S + at, src);
-        const float v = as_f32((m >> 31) ? m & 0x7FFFFFFFu : ~m);
-        if (j == 0) top = v;
-        if (lane == j) {
-            id = e;
-            mine = v;
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (lane * S + s == e) key[s] = 0;
-        if (j == 0 && !a.renormalize) {
-            // every expert counts: the ones left, and this one
-#pragma unroll
-            for (int s = 0; s < S; ++s) sum += key[s] ? expf(val[s] - v) : 0.f;
-            sum = wave_sum(sum) + 1.f;
-        }
-    }
-    const float p = id >= 0 ? expf(mine - top) : 0.f;
-    if (a.renormalize) sum = wave_sum(p);
-    weight = id >= 0 ? a.scale * (p / sum) : 0.f;
-}
 
 template <int S>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
@@ -112,10 +22,13 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
 // The lists of one chunk of tokens: pairs (token, choice) sorted by expert,
 // tokens ascending.  A set of 128 bits per expert says which tokens chose
 // it; a pair's place is its expert's first place plus the number of bits
-// below its own, so the order does not depend on timing.  An expert that a
-// caller's ids name twice for one token counts once, with the sum of both
-// weights; ids outside [0, E) are left out.
+// below its own, so the order does not depend on timing.  With ROUTE (chunks
+// of at most 16 tokens) each wave first makes one token's choices itself;
+// otherwise logits were routed by a launch of their own.
+template <bool ROUTE>
 __global__ __launch_bounds__(1024) void moe_sort_kernel(MoeArgs a) {
+    __shared__ int own_id[16 * kMaxTopK];
+    __shared__ float own_w[16 * kMaxTopK];
     __shared__ u32 mask[kMaxExperts][kMoeChunk / 32];
     __shared__ int first[kMaxExperts];
     __shared__ int wave_pairs[8], wave_active[8];
@@ -127,6 +40,17 @@ __global__ __launch_bounds__(1024) void moe_sort_kernel(MoeArgs a) {
     MoeChunkMeta *meta = a.meta + blockIdx.x;
 
     for (int i = tid; i < kMaxExperts * (kMoeChunk / 32); i += 1024) (&mask[0][0])[i] = 0;
+    if constexpr (ROUTE) {
+        if (wave < tokens) {
+            int id;
+            float w;
+            token_choices(a.route, t0 + wave, lane, id, w);
+            if (lane < k) {
+                own_id[wave * k + lane] = id;
+                own_w[wave * k + lane] = w;
+            }
+        }
+    }
     __syncthreads();
     int my_id[2];
     float my_w[2];
@@ -135,7 +59,14 @@ __global__ __launch_bounds__(1024) void moe_sort_kernel(MoeArgs a) {
         const int p = tid + q * 1024;
         my_id[q] = -1;
         my_w[q] = 0.f;
-        if (p < pairs) {
+        if (ROUTE) {
+            if (p < pairs) {
+                const int t = p / k;
+                my_id[q] = own_id[p];
+                my_w[q] = own_w[p];
+                if (my_id[q] >= 0) atomicOr(&mask[my_id[q]][t >> 5], 1u << (t & 31));
+            }
+        } else if (p < pairs) {
             const int t = p / k, j = p - t * k, id = ids[p];
             bool take = id >= 0 && id < a.E;
             for (int i = 0; i < j; ++i) take = take && ids[t * k + i] != id;
@@ -192,14 +123,18 @@ __global__ __launch_bounds__(1024) void moe_sort_kernel(MoeArgs a) {
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const int id = my_id[q];
-        if (id < 0) continue;
-        const int t = (tid + q * 1024) / k;
+        const int id = my_id[q], p = tid + q * 1024;
+        if (id < 0) {
+            if (p < pairs) a.place[(int64_t)t0 * k + p] = -1;
+            continue;
+        }
+        const int t = p / k;
         int at = first[id];
         for (int w = 0; w < (t >> 5); ++w) at += __builtin_popcount(mask[id][w]);
         at += __builtin_popcount(mask[id][t >> 5] & ((1u << (t & 31)) - 1u));
         a.tok[(int64_t)t0 * k + at] = t;
         a.wgt[(int64_t)t0 * k + at] = my_w[q];
+        a.place[(int64_t)t0 * k + p] = at;
     }
 }
 
@@ -223,9 +158,10 @@ hipError_t tcg_launch_moe_route(const RouteArgs &a, hipStream_t s) {
     return launch_route<8>(a, s);
 }
 
-hipError_t tcg_launch_moe_sort(const MoeArgs &a, hipStream_t s) {
-    if (a.E > kMaxExperts || a.top_k > kMaxTopK) return hipErrorInvalidValue;
+hipError_t tcg_launch_moe_sort(const MoeArgs &a, bool route, hipStream_t s) {
+    if (a.E > kMaxExperts || a.top_k > kMaxTopK || (route && a.T > 16)) return hipErrorInvalidValue;
     const unsigned chunks = (unsigned)((a.T + kMoeChunk - 1) / kMoeChunk);
-    hipLaunchKernelGGL(moe_sort_kernel, dim3(chunks), dim3(1024), 0, s, a);
+    if (route) hipLaunchKernelGGL(moe_sort_kernel<true>, dim3(chunks), dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL(moe_sort_kernel<false>, dim3(chunks), dim3(1024), 0, s, a);
     return hipGetLastError();
 }

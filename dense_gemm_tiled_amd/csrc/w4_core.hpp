@@ -156,7 +156,8 @@ struct WStream {
         }
     }
 
-    // kv: values of K from this block's first on (>= 128: a whole block).
+    // TAIL: the block may hold fewer than 128 values, kv of them.
+    template <bool TAIL>
     __device__ inline void load(WFrag<WK> &f, int kb, int kv, int lane) const {
         if constexpr (WK::W4) {
             // (lane part in a register, block part in a scalar one)
@@ -180,7 +181,7 @@ struct WStream {
             }
             // groups past the last value of K hold nothing: their codes meet
             // zeros of x, and their scales, whatever is stored, become zero
-            if (WK::GP > 1 && kv < kBlkK) {
+            if (TAIL && WK::GP > 1) {
                 constexpr int G = kBlkK / (WK::GP ? WK::GP : 1);
 #pragma unroll
                 for (int g = 1; g < WK::GP; ++g)
@@ -188,7 +189,7 @@ struct WStream {
             }
         } else {
             const int off = row_off + kb * (kBlkK * 2);
-            if (kv >= kBlkK) {
+            if constexpr (!TAIL) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f.q[i] = ld128(rows, off + i * 64);
             } else {
@@ -205,28 +206,76 @@ struct WStream {
     }
 };
 
-// One 16-row tile of 16-bit activations along K: row offsets are this lane's
-// (bytes from the resource's base, 16 kq included).
+// The left operand of one block of K: four 16x16x32 fragments.
 struct XFrag {
     u32x4 v[4];
 };
 
-__device__ inline void load_x(XFrag &f, __amdgpu_buffer_rsrc_t rx, int row_off, int kb, int kv,
-                              int lane) {
-    const int off = row_off + kb * (kBlkK * 2);
-    if (kv >= kBlkK) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.v[i] = ld128(rx, off + i * 64);
+// 16-row tiles of activations on their way to a wave.  A block of K is XP *
+// 256 bytes of a row (XP: 1 for 16-bit values, 2 where 8 high parts and 8 low
+// parts alternate), and a load instruction takes 4 / XP whole rows of it:
+// neighbouring lanes read neighbouring bytes.  From registers the rows go
+// through LDS that is the wave's own, 16-byte piece c of row r at c ^ (r %
+// 16), without a barrier.  (Straight into operand layout, 16 rows x 64 bytes
+// an instruction, every lane is a cache line of its own: 16 rows by 8192x4096
+// took 7.7 us so against 6.9, 32 rows 11.9 against 9.4.  With up to 4 rows the
+// lanes past the last one repeat it and the direct loads are ahead, 4.3
+// against 4.7 for one row by 4096x4096: they are kept for that.)
+template <int XP>
+struct RowTile {
+    static constexpr int LOADS = 4 * XP, ROWS = 4 / XP, LPR = 16 * XP;
+    static constexpr int LDS_BYTES = 16 * 256 * XP;
+};
+
+// off: this lane's byte offset in row ROWS * q + lane / LPR, piece lane %
+// LPR included.
+template <int XP, bool TAIL>
+__device__ inline u32x4 load_piece(__amdgpu_buffer_rsrc_t rx, int off, int kb, int kv, int lane) {
+    if constexpr (!TAIL) return __builtin_amdgcn_raw_buffer_load_b128(rx, off, kb * (256 * XP), 0);
+    const int v = kv - (lane % RowTile<XP>::LPR) / XP * 8;
+    if constexpr (XP == 2) {
+        // (held in whole groups of 8, zeros past the last value)
+        return v > 0 ? ld128(rx, off + kb * 512) : u32x4{0u, 0u, 0u, 0u};
     } else {
-        const int k0 = (lane >> 4) * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = kv - (k0 + i * 32);
-            f.v[i] = u32x4{0u, 0u, 0u, 0u};
-            if (v >= 8) f.v[i] = ld128(rx, off + i * 64);
-            else if (v > 0) f.v[i] = ld_partial<2>(rx, off + i * 64, v);
-        }
+        if (v >= 8) return ld128(rx, off + kb * 256);
+        return v > 0 ? ld_partial<2>(rx, off + kb * 256, v) : u32x4{0u, 0u, 0u, 0u};
     }
+}
+
+// The same block of the tile straight into operand layout; off: this lane's
+// byte offset in row lane % 16, 16 XP (lane / 16) included.
+template <int XP, bool TAIL>
+__device__ inline void load_frags(XFrag (&x)[XP], __amdgpu_buffer_rsrc_t rx, int off, int kb, int kv, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < XP; ++p) {
+            const int at = off + i * (64 * XP) + p * 16, v = kv - (i * 32 + (lane >> 4) * 8);
+            if constexpr (!TAIL) {
+                x[p].v[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, kb * (256 * XP), 0);
+            } else {
+                x[p].v[i] = u32x4{0u, 0u, 0u, 0u};
+                if (v >= 8 || (XP == 2 && v > 0)) x[p].v[i] = ld128(rx, at + kb * (256 * XP));
+                else if (v > 0) x[p].v[i] = ld_partial<2>(rx, at + kb * (256 * XP), v);
+            }
+        }
+}
+
+template <int XP>
+__device__ inline void write_piece(char *buf, int q, int lane, u32x4 v) {
+    const int r = RowTile<XP>::ROWS * q + lane / RowTile<XP>::LPR, c = lane % RowTile<XP>::LPR;
+    *reinterpret_cast<u32x4 *>(buf + r * (256 * XP) + ((c ^ (r & 15)) << 4)) = v;
+}
+
+template <int XP>
+__device__ inline void read_frags(const char *buf, int lane, XFrag (&x)[XP]) {
+    const int r = lane & 15, kq = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < XP; ++p)
+            x[p].v[i] = *reinterpret_cast<const u32x4 *>(buf + r * (256 * XP) +
+                                                         ((((i * 4 + kq) * XP + p) ^ r) << 4));
 }
 
 // acc += x @ (one block of weights)^T.  XP: parts of x (1, or 2 where x is
@@ -281,32 +330,61 @@ __device__ inline void block_mma(const XFrag (&x)[XP], const u32x4 (&w)[4], cons
 }
 
 // One wave: acc[nb][mt] += x rows @ weights^T over the K blocks kb0, kb0 +
-// step, .. below kb1.  Weights and activations of the next block are in
-// flight while one is multiplied (the same depth for both: loads return in
+// step, .. of ceil(K / 128).  Weights and activations of the next block are
+// in flight while one is multiplied (the same depth for both: loads return in
 // order, so a shallower queue of x would wait for every weight load issued
-// before it).  mts: 16-row tiles in use (uniform).
-template <class WK, int NB, int MT, int XP, class LoadX>
-__device__ inline void wave_products(const WStream<WK> (&w)[NB], const LoadX &loadx, int K, int kb0,
-                                     int step, int kb1, int mts, int lane, f32x4 (&acc)[NB][MT]) {
+// before it); a short last block comes first, so that its element loads are
+// not waited for alone at the end.  DIRECT: x straight into operand layout
+// (see RowTile); x_off[t][q]: see load_piece, or load_frags (q = 0 alone);
+// buf: RowTile<XP>::LDS_BYTES of this wave's own.
+//
+// No branch may stand between a matrix instruction and what reads its
+// result: where a tile was skipped by a branch, the compiler left out the
+// wait states before the reader on the other side, and the results were
+// wrong.  So MT is the number of tiles in use, and callers choose by it.
+template <class WK, int NB, int MT, int XP, bool DIRECT>
+__device__ inline void wave_products(const WStream<WK> (&w)[NB], __amdgpu_buffer_rsrc_t rx,
+                                     const int (&x_off)[MT][DIRECT ? 1 : RowTile<XP>::LOADS], char *buf, int K,
+                                     int kb0, int step, int lane, f32x4 (&acc)[NB][MT]) {
     struct Stage {
         WFrag<WK> w[NB];
-        XFrag x[MT][XP];
+        u32x4 x[MT][DIRECT ? 1 : RowTile<XP>::LOADS];
+        XFrag f[DIRECT ? MT : 1][XP];
     };
     Stage st[2];
-    auto fetch = [&](Stage &s, int kb) {
+    auto fetch = [&](Stage &s, int block, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        // (the same in every lane, which the compiler loses sight of)
+        const int kb = __builtin_amdgcn_readfirstlane(block);
         const int kv = K - kb * kBlkK;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) w[b].load(s.w[b], kb, kv, lane);
+        for (int b = 0; b < NB; ++b) w[b].template load<TAIL>(s.w[b], kb, kv, lane);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-            if (t == 0 || t < mts) loadx(s.x[t], t, kb, kv);
+        for (int t = 0; t < MT; ++t) {
+            if constexpr (DIRECT) {
+                load_frags<XP, TAIL>(s.f[t], rx, x_off[t][0], kb, kv, lane);
+            } else {
+#pragma unroll
+                for (int q = 0; q < RowTile<XP>::LOADS; ++q)
+                    s.x[t][q] = load_piece<XP, TAIL>(rx, x_off[t][q], kb, kv, lane);
+            }
+        }
     };
     auto compute = [&](const Stage &s) {
+        XFrag x[MT][XP];
         f32x4 zsum[MT][WK::GP ? WK::GP : 1];
-        if constexpr (WK::W4 && !WK::ZP) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                if (t == 0 || t < mts) block_offset_sums<WK, XP>(s.x[t], zsum[t]);
+        for (int t = 0; t < MT; ++t) {
+            if constexpr (DIRECT) {
+#pragma unroll
+                for (int p = 0; p < XP; ++p) x[t][p] = s.f[t][p];
+            } else {
+                // (one wave's LDS operations are done in order)
+#pragma unroll
+                for (int q = 0; q < RowTile<XP>::LOADS; ++q) write_piece<XP>(buf, q, lane, s.x[t][q]);
+                read_frags<XP>(buf, lane, x[t]);
+            }
+            if constexpr (WK::W4 && !WK::ZP) block_offset_sums<WK, XP>(x[t], zsum[t]);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -316,23 +394,28 @@ __device__ inline void wave_products(const WStream<WK> (&w)[NB], const LoadX &lo
                 if constexpr (WK::W4) wv[i] = w4_expand<WK::DT>(s.w[b].q[0][i]);
                 else wv[i] = s.w[b].q[i];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                if (t == 0 || t < mts) block_mma<WK, XP>(s.x[t], wv, s.w[b], zsum[t], acc[b][t]);
+            for (int t = 0; t < MT; ++t) block_mma<WK, XP>(x[t], wv, s.w[b], zsum[t], acc[b][t]);
         }
     };
+    constexpr std::integral_constant<bool, true> short_block{};
+    constexpr std::integral_constant<bool, false> whole{};
+    const int full = K / kBlkK;
+    const bool tail = full * kBlkK < K && full % step == kb0;
     int kb = kb0;
-    if (kb >= kb1) return;
-    fetch(st[0], kb);
+    if (tail) fetch(st[1], full, short_block);
+    if (kb < full) fetch(st[0], kb, whole);
+    if (tail) compute(st[1]);
+    if (kb >= full) return;
 #pragma unroll 1
     while (true) {
-        if (kb + step < kb1) fetch(st[1], kb + step);
+        if (kb + step < full) fetch(st[1], kb + step, whole);
         compute(st[0]);
         kb += step;
-        if (kb >= kb1) break;
-        if (kb + step < kb1) fetch(st[0], kb + step);
+        if (kb >= full) break;
+        if (kb + step < full) fetch(st[0], kb + step, whole);
         compute(st[1]);
         kb += step;
-        if (kb >= kb1) break;
+        if (kb >= full) break;
     }
 }
 

@@ -29,20 +29,18 @@ __device__ inline void finish(const W4GemmArgs &a, int m, int n, float v) {
 // Few rows (a decoding step): the time is reading W once.  A workgroup owns
 // NB blocks of 16 weight rows and 16 MT rows of x; its waves split K among
 // themselves, block by block, so that even a matrix of few rows has many
-// loads in flight, and add their sums in LDS in wave order.  No LDS before
-// that: a wave reads 1024 contiguous bytes of codes per block, and the x it
-// needs (nobody else in the workgroup needs it) straight into the operand
-// layout.
+// loads in flight, and add their sums in LDS in wave order.  A wave reads
+// 1024 contiguous bytes of codes per block straight into operand layout, and
+// the x of its own blocks, which no other wave needs.
 template <class WK, int NB, int MT, int MAXT>
 __global__ __launch_bounds__(MAXT) void w4_rows_kernel(W4GemmArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float red[];   // [waves][NB][16][16]
+    // [waves][NB][16][16] sums at the end, before them the waves' x tiles
+    extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int waves = blockDim.x >> 6;
     const int N = a.w.N, K = a.w.K;
-    // (alpha 0 reads neither operand)
-    const int kbs = a.alpha == 0.f ? 0 : (K + kBlkK - 1) / kBlkK;
     const int nb0 = blockIdx.x * NB, nblocks = (N + kBlkN - 1) / kBlkN;
-    const int m0 = blockIdx.y * (16 * MT), rows = min(a.M - m0, 16 * MT), mts = (rows + 15) >> 4;
+    const int m0 = blockIdx.y * (16 * MT), rows = min(a.M - m0, 16 * MT);
 
     const MatrixRef mat = {static_cast<const char *>(a.w.codes), static_cast<const char *>(a.w.scales),
                            static_cast<const char *>(a.w.zeros)};
@@ -51,22 +49,33 @@ __global__ __launch_bounds__(MAXT) void w4_rows_kernel(W4GemmArgs a) {
     for (int b = 0; b < NB; ++b) w[b] = WStream<WK>(mat, min(nb0 + b, nblocks - 1), N, K, lane);
     const int64_t x_org = (int64_t)m0 * a.ldx * 2;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + x_org, a.x_bytes - x_org);
-    int x_off[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        x_off[t] = min(16 * t + (lane & 15), rows - 1) * (int)a.ldx * 2 + (lane >> 4) * 16;
-    auto loadx = [&](XFrag (&f)[1], int t, int kb, int kv) { load_x(f[0], rx, x_off[t], kb, kv, lane); };
-
     f32x4 acc[NB][MT];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    wave_products<WK, NB, MT, 1>(w, loadx, K, wave, waves, kbs, mts, lane, acc);
+    char *const tile = reinterpret_cast<char *>(red) + wave * RowTile<1>::LDS_BYTES;
+    // (alpha 0 reads neither operand)
+    if (a.alpha != 0.f) {
+        if (MT == 1 && rows <= 4) {
+            const int x_off[1][1] = {{min(lane & 15, rows - 1) * (int)a.ldx * 2 + (lane >> 4) * 16}};
+            if constexpr (MT == 1) wave_products<WK, NB, 1, 1, true>(w, rx, x_off, tile, K, wave, waves, lane, acc);
+        } else {
+            int x_off[MT][4];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    x_off[t][q] =
+                        min(16 * t + 4 * q + (lane >> 4), rows - 1) * (int)a.ldx * 2 + (lane & 15) * 16;
+            wave_products<WK, NB, MT, 1, false>(w, rx, x_off, tile, K, wave, waves, lane, acc);
+        }
+    }
+    __syncthreads();
 
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        if (t > 0 && t >= mts) break;
+        if (t > 0 && 16 * t >= rows) break;
         if (t) __syncthreads();
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -92,7 +101,7 @@ hipError_t launch_rows(const W4GemmArgs &a, int waves, hipStream_t s) {
     const dim3 grid((unsigned)((nblocks + NB - 1) / NB), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
     if (grid.y > 65535) return hipErrorInvalidValue;
     hipLaunchKernelGGL((w4_rows_kernel<WK, NB, MT, MAXT>), grid, dim3(waves * 64),
-                       waves * NB * 1024, s, a);
+                       waves * (NB * 1024 > RowTile<1>::LDS_BYTES ? NB * 1024 : RowTile<1>::LDS_BYTES), s, a);
     return hipGetLastError();
 }
 
@@ -166,7 +175,10 @@ __global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, in
     auto load_codes = [&](WFrag<WK> (&f)[NBW], int s) {
         const int kb = min(s * KG + kg, kbs - 1);
 #pragma unroll
-        for (int b = 0; b < NBW; ++b) w[b].load(f[b], kb, K - kb * kBlkK, lane);
+        for (int b = 0; b < NBW; ++b) {
+            if (GP > 1 && K - kb * kBlkK < kBlkK) w[b].template load<true>(f[b], kb, K - kb * kBlkK, lane);
+            else w[b].template load<false>(f[b], kb, kBlkK, lane);
+        }
     };
     auto write_rows = [&](const u32x4 (&v)[P], int slot) {
 #pragma unroll
@@ -368,7 +380,9 @@ hipError_t launch_kind(const W4GemmArgs &a, const char **name, hipStream_t s) {
         *name = WK::DT == DT_F16 ? "w4_rows_f16" : "w4_rows_bf16";
         if (a.M > 16) return launch_rows<WK, 2, 2, 512>(a, kbs >= 8 ? 8 : 4, s);
         const int waves = kbs >= 32 ? 16 : kbs >= 8 ? 8 : 4;
-        if (nblocks >= 512) return launch_rows<WK, 2, 1, 1024>(a, waves, s);
+        // (groups of 32: 16 waves of two blocks would not fit the registers)
+        constexpr int MOST = WK::GP == 4 ? 512 : 1024;
+        if (nblocks >= 512) return launch_rows<WK, 2, 1, MOST>(a, waves * 64 > MOST ? MOST / 64 : waves, s);
         return launch_rows<WK, 1, 1, 1024>(a, waves, s);
     }
     *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";

@@ -92,6 +92,25 @@ __device__ inline u32 w4_neg_offset(u32 z) {
     return h | (h << 16);
 }
 
+// The 16-byte chunk at off of which the first v values (of 8) lie below K;
+// the rest is zero.  No branch per lane: what is not to be read has an offset
+// past any range, where a buffer load gives zero, so all loads are in flight
+// together (branches around each element's load were waited for one by one:
+// 13 rows by 4099x4093 took 10.6 us so).  odd: K is no multiple of 8.
+__device__ inline u32x4 ld_chunk_tail(__amdgpu_buffer_rsrc_t r, int off, int v, bool odd) {
+    constexpr int kPast = (int)0xFFFFFFF0u;
+    u32x4 c = ld128(r, v >= 8 ? off : kPast);
+    if (odd) {
+        u32 e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            e[j] = __builtin_amdgcn_raw_buffer_load_b16(r, v < 8 && j < v ? off + 2 * j : kPast, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] |= e[2 * j] | (e[2 * j + 1] << 16);
+    }
+    return c;
+}
+
 // What a kernel instance knows of its weights at compile time.  GP: groups
 // per block (1, 2, 4), 0 for 16-bit weights; ZP: zero points held.
 template <int DT_, int GP_, bool ZP_>
@@ -195,12 +214,8 @@ struct WStream {
             } else {
                 const int k0 = (lane >> 4) * 8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int v = kv - (k0 + i * 32);
-                    f.q[i] = u32x4{0u, 0u, 0u, 0u};
-                    if (v >= 8) f.q[i] = ld128(rows, off + i * 64);
-                    else if (v > 0) f.q[i] = ld_partial<2>(rows, off + i * 64, v);
-                }
+                for (int i = 0; i < 4; ++i)
+                    f.q[i] = ld_chunk_tail(rows, off + i * 64, kv - (k0 + i * 32), (K & 7) != 0);
             }
         }
     }
@@ -235,10 +250,9 @@ __device__ inline u32x4 load_piece(__amdgpu_buffer_rsrc_t rx, int off, int kb, i
     const int v = kv - (lane % RowTile<XP>::LPR) / XP * 8;
     if constexpr (XP == 2) {
         // (held in whole groups of 8, zeros past the last value)
-        return v > 0 ? ld128(rx, off + kb * 512) : u32x4{0u, 0u, 0u, 0u};
+        return ld_chunk_tail(rx, off + kb * 512, v > 0 ? 8 : 0, false);
     } else {
-        if (v >= 8) return ld128(rx, off + kb * 256);
-        return v > 0 ? ld_partial<2>(rx, off + kb * 256, v) : u32x4{0u, 0u, 0u, 0u};
+        return ld_chunk_tail(rx, off + kb * 256, v, (kv & 7) != 0);
     }
 }
 
@@ -254,9 +268,9 @@ __device__ inline void load_frags(XFrag (&x)[XP], __amdgpu_buffer_rsrc_t rx, int
             if constexpr (!TAIL) {
                 x[p].v[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, kb * (256 * XP), 0);
             } else {
-                x[p].v[i] = u32x4{0u, 0u, 0u, 0u};
-                if (v >= 8 || (XP == 2 && v > 0)) x[p].v[i] = ld128(rx, at + kb * (256 * XP));
-                else if (v > 0) x[p].v[i] = ld_partial<2>(rx, at + kb * (256 * XP), v);
+                // (two parts: held in whole groups of 8, zeros past the last value)
+                x[p].v[i] = ld_chunk_tail(rx, at + kb * (256 * XP), XP == 2 && v > 0 ? 8 : v,
+                                          XP == 1 && (kv & 7) != 0);
             }
         }
 }

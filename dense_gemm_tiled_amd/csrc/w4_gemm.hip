@@ -32,8 +32,8 @@ __device__ inline void finish(const W4GemmArgs &a, int m, int n, float v) {
 // loads in flight, and add their sums in LDS in wave order.  A wave reads
 // 1024 contiguous bytes of codes per block straight into operand layout, and
 // the x of its own blocks, which no other wave needs.
-template <class WK, int NB, int MT, int MAXT>
-__global__ __launch_bounds__(MAXT) void w4_rows_kernel(W4GemmArgs a) {
+template <class WK, int NB, int MT>
+__global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a) {
     // [waves][NB][16][16] sums at the end, before them the waves' x tiles
     extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -95,12 +95,12 @@ __global__ __launch_bounds__(MAXT) void w4_rows_kernel(W4GemmArgs a) {
     }
 }
 
-template <class WK, int NB, int MT, int MAXT>
+template <class WK, int NB, int MT>
 hipError_t launch_rows(const W4GemmArgs &a, int waves, hipStream_t s) {
     const int nblocks = (a.w.N + kBlkN - 1) / kBlkN;
     const dim3 grid((unsigned)((nblocks + NB - 1) / NB), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
     if (grid.y > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((w4_rows_kernel<WK, NB, MT, MAXT>), grid, dim3(waves * 64),
+    hipLaunchKernelGGL((w4_rows_kernel<WK, NB, MT>), grid, dim3(waves * 64),
                        waves * (NB * 1024 > RowTile<1>::LDS_BYTES ? NB * 1024 : RowTile<1>::LDS_BYTES), s, a);
     return hipGetLastError();
 }
@@ -164,11 +164,8 @@ __global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, in
                 v[j] = __builtin_amdgcn_raw_buffer_load_b128(rx, x_off[j], kb * 256, 0);
         } else {
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-                v[j] = u32x4{0u, 0u, 0u, 0u};
-                if (kb < kbs && have >= 8) v[j] = ld128(rx, x_off[j] + kb * 256);
-                else if (kb < kbs && have > 0) v[j] = ld_partial<2>(rx, x_off[j] + kb * 256, have);
-            }
+            for (int j = 0; j < P; ++j)
+                v[j] = ld_chunk_tail(rx, x_off[j] + kb * 256, kb < kbs ? have : 0, (K & 7) != 0);
         }
     };
     // (past the last block: that block again, which is then not used)
@@ -365,31 +362,34 @@ hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
 
 // Which kernel.  Measured on one box, us per call, bf16, group 128 (rows, then
 // 32x64 tiles with 4 sets, 64x64 with 2, 64x128 with 1):
-//     N 8192 K 4096, M 16:     7.7 /    - /    - /    -
-//     N 8192 K 4096, M 32:    11.9 / 17.2 / 26.8 / 42.0
+//     N 8192 K 4096, M 16:     6.9 /    - /    - /    -
+//     N 8192 K 4096, M 32:     9.3 / 17.2 / 26.8 / 42.0
 //     N 8192 K 4096, M 64:    22.9 / 17.8 / 27.7 / 43.9
 //     N 4096 K 4096, M 128:      - / 17.9 / 27.9 / 44.1
 //     N 4096 K 4096, M 256:      - / 32.6 / 29.3 / 44.4
 //     N 4096 K 4096, M 512:      - / 60.4 / 55.0 / 45.4
 //     N 4096 K 4096, M 2048: 330.5 / 232 / 212 / 96.9
 // so: rows up to 32; then the tiles by how many of them there are per CU.
+// Rows: one block of 16 weight rows per workgroup up to two workgroups a CU,
+// two blocks beyond (N 4096 K 4096 M 1: 4.45 / 5.3; N 8192 K 8192 M 1: 11.4 /
+// 9.5; N 16384 K 8192 M 4: 22.7 / 16.7), 8 waves (16: no faster anywhere, and
+// 18.3 on the last shape; 4: 5.3 on the first).
 template <class WK>
 hipError_t launch_kind(const W4GemmArgs &a, const char **name, hipStream_t s) {
     const int kbs = (a.w.K + kBlkK - 1) / kBlkK, nblocks = (a.w.N + kBlkN - 1) / kBlkN;
     if (a.M <= 32) {
         *name = WK::DT == DT_F16 ? "w4_rows_f16" : "w4_rows_bf16";
-        if (a.M > 16) return launch_rows<WK, 2, 2, 512>(a, kbs >= 8 ? 8 : 4, s);
-        const int waves = kbs >= 32 ? 16 : kbs >= 8 ? 8 : 4;
-        // (groups of 32: 16 waves of two blocks would not fit the registers)
-        constexpr int MOST = WK::GP == 4 ? 512 : 1024;
-        if (nblocks >= 512) return launch_rows<WK, 2, 1, MOST>(a, waves * 64 > MOST ? MOST / 64 : waves, s);
-        return launch_rows<WK, 1, 1, 1024>(a, waves, s);
+        const int waves = kbs >= 8 ? 8 : 4;
+        if (a.M > 16) return launch_rows<WK, 2, 2>(a, waves, s);
+        if (nblocks >= 512) return launch_rows<WK, 2, 1>(a, waves, s);
+        return launch_rows<WK, 1, 1>(a, waves, s);
     }
     *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";
     const int64_t tiles_64 = (int64_t)((a.M + 63) / 64) * ((a.w.N + 63) / 64);
     if (tiles_64 > 256) return launch_tile<WK, 4, 2, 1, 1, 1>(a, s);
     if (tiles_64 > 128 && a.M > 128) return launch_tile<WK, 4, 1, 1, 2, 2>(a, s);
-    return launch_tile<WK, 2, 1, 1, 4, 2>(a, s);
+    // (groups of 32: a second set of registers would not fit)
+    return launch_tile<WK, 2, 1, 1, 4, WK::GP == 4 ? 1 : 2>(a, s);
 }
 
 }  // namespace

@@ -627,16 +627,25 @@ def w4_gemm(x, w, y, *, alpha: float = 1.0, beta: float = 0.0, bias=None,
     of x's type or f32, bias [N] of y's type; activation None, "none", "relu"
     or "gelu_tanh".  Runs on torch's current stream (or `stream`), needs no
     workspace.  Returns y."""
-    w = _as_w4(w)
-    device = _same_device(y, x, bias, *w)
-    key = ("w4_gemm", x.shape, x.stride(), x.dtype, y.shape, y.stride(), y.dtype, alpha, beta,
-           _w4_key(w))
-    _, _, g, wd = _cached(key, lambda: _make_qgemm(x, w, y, alpha, beta))
+    codes, scales, zeros = w = _as_w4(w)
+    device = y.get_device()
+    if (device < 0 or x.get_device() != device or codes.get_device() != device
+            or scales.get_device() != device
+            or (zeros is not None and zeros.get_device() != device)
+            or (bias is not None and bias.get_device() != device)):
+        raise TcGemmError(1, "the operands must be on one GPU")
+    key = (x.shape, x.stride(), x.dtype, y.shape, y.stride(), y.dtype, alpha, beta, codes.shape,
+           codes.dtype, codes.is_contiguous(), scales.shape, scales.dtype, scales.is_contiguous(),
+           None if zeros is None else (zeros.shape, zeros.dtype, zeros.is_contiguous()))
+    d = _op_cache.get(key)
+    if d is None:
+        d = _cached(key, lambda: _make_qgemm(x, w, y, alpha, beta))
+    g, wd = d[2], d[3]
     lib = _lib if _lib is not None else load_library()
     ctx, s = _torch_stream(device, stream)
     q = _w4_ptrs(w)
     ep = None
-    if bias is not None or activation is not None:
+    if bias is not None or activation not in (None, "none"):
         ep = ctypes.byref(make_epilogue(y, bias, activation))
     st = lib.tc_qgemm_async(ctx, g, wd, x.data_ptr(), ctypes.byref(q), y.data_ptr(), ep, s)
     if st != 0:
@@ -667,9 +676,14 @@ def moe_route(logits, top_k: int, *, renormalize: bool = True, scale: float = 1.
     d, r = _cached(key, lambda: _make_route(logits, top_k, renormalize, scale))
     lib = _lib if _lib is not None else load_library()
     ctx, s = _torch_stream(device, stream)
-    with _on_stream(device, stream):
-        ids = torch.empty((d.T, d.top_k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((d.T, d.top_k), dtype=torch.float32, device=logits.device)
+    shape, where = (d.T, d.top_k), logits.device
+    if stream is None:
+        ids = torch.empty(shape, dtype=torch.int32, device=where)
+        weights = torch.empty(shape, dtype=torch.float32, device=where)
+    else:
+        with _on_stream(device, stream):
+            ids = torch.empty(shape, dtype=torch.int32, device=where)
+            weights = torch.empty(shape, dtype=torch.float32, device=where)
     st = lib.tc_moe_route_async(ctx, r, logits.data_ptr(), ids.data_ptr(), weights.data_ptr(), s)
     if st != 0:
         _check(st, ctx)

@@ -127,6 +127,11 @@ struct DeviceScope {
             (void)hipGetLastError();
             before = -1;
         }
+        status = TC_OK;
+        if (before >= 0 && before == ctx->device) {
+            before = -1;   // current already
+            return;
+        }
         status = bind_device(ctx);
         if (before == ctx->device) before = -1;
     }

@@ -20,10 +20,12 @@ tc_status_t check_qweight(const tc_qweight_desc *d, QWeightSizes *out, std::stri
                     dt_name(d->scale_dtype));
     if (d->K > kMaxRowElems)
         return fail(err, TC_ERR_OVERFLOW, "K=%d > %d", d->K, kMaxRowElems);
-    // at most 2^27 x 2^15 blocks a matrix, so none of the products below wraps
-    const int64_t blocks = (((int64_t)d->N + 15) / 16) * (((int64_t)d->K + 127) / 128) * d->batch;
-    if ((blocks + 3) / 4 > 0x7FFFFFFF)
-        return fail(err, TC_ERR_OVERFLOW, "the matrices hold more than 2^33 blocks of 16 x 128");
+    // (N, batch < 2^31, K < 2^22: no product wraps before it is refused)
+    const int64_t rows = (((int64_t)d->N + 15) / 16) * d->batch, kbs = ((int64_t)d->K + 127) / 128;
+    const int64_t blocks = rows * kbs;
+    // (the conversions give four blocks of a row to a workgroup)
+    if (rows > 0x7FFFFFFF || rows * ((kbs + 3) / 4) > 0x7FFFFFFF)
+        return fail(err, TC_ERR_OVERFLOW, "the matrices hold more than 2^31-1 groups of 16 x 512");
     out->codes = blocks * 1024;
     out->scales = blocks * 16 * (128 / d->group) * 2;
     out->zeros = d->has_zeros ? blocks * 16 * (128 / d->group) : 0;

@@ -16,56 +16,57 @@ __device__ constexpr int code_bit(int j) { return 4 * (j >> 1) + 16 * (j & 1); }
 
 struct BlockPos {
     int64_t block;      // over all matrices
-    int64_t z;          // matrix
+    int z;              // matrix
     int n, k0, kb;      // this lane's row and first k; block along K
 };
 
-__device__ inline bool block_pos(int batch, int N, int K, BlockPos &p) {
-    const int kbs = (K + kBlkK - 1) / kBlkK;
-    const int64_t per = w4_blocks(N, K);
-    p.block = (int64_t)blockIdx.x * (kFmtThreads / 64) + (threadIdx.x >> 6);
-    if (p.block >= per * batch) return false;
-    p.z = p.block / per;
-    const int64_t b = p.block - p.z * per;
-    p.kb = (int)(b % kbs);
-    const int lane = threadIdx.x & 63;
-    p.n = (int)(b / kbs) * kBlkN + (lane & 15);
+// Four neighbouring blocks of K to a workgroup, one to a wave.  (One 32-bit
+// division per step: with 64-bit ones over all blocks a wave spent more on
+// finding its block than on it.)
+__device__ inline bool block_pos(int N, int K, BlockPos &p) {
+    const int kbs = (K + kBlkK - 1) / kBlkK, nbs = (N + kBlkN - 1) / kBlkN;
+    const int kgroups = (kbs + kFmtThreads / 64 - 1) / (kFmtThreads / 64);
+    const int row = blockIdx.x / (unsigned)kgroups;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    p.kb = (blockIdx.x - row * kgroups) * (kFmtThreads / 64) + wave;
+    if (p.kb >= kbs) return false;
+    p.z = (unsigned)row / (unsigned)nbs;
+    p.block = (int64_t)row * kbs + p.kb;
+    p.n = (row - p.z * nbs) * kBlkN + (lane & 15);
     p.k0 = p.kb * kBlkK + (lane >> 4) * 8;
     return true;
 }
 
-template <int SRC>
-__device__ inline float load_value(const void *p, int64_t i) {
-    if constexpr (SRC == DT_F32) return static_cast<const float *>(p)[i];
-    else return from16<SRC>(static_cast<const u16 *>(p)[i]);
-}
-
-// Eight neighbouring values of a row, zeros from nvalid on.
-template <int SRC>
+// Eight neighbouring values of a row.  TAIL: nvalid of them, then zeros.
+template <int SRC, bool TAIL>
 __device__ inline void load8(const void *src, int64_t at, int nvalid, float (&v)[8]) {
-    if (nvalid >= 8) {
-        if constexpr (SRC == DT_F32) {
-            struct __attribute__((packed)) V { u32 w[4]; };
-            const float *q = static_cast<const float *>(src) + at;
-            const V a = *reinterpret_cast<const V *>(q), b = *reinterpret_cast<const V *>(q + 4);
+    if constexpr (TAIL) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = as_f32(a.w[j]);
-                v[4 + j] = as_f32(b.w[j]);
-            }
-        } else {
-            // rows of 16-bit values start at any even address
-            struct __attribute__((packed, aligned(2))) V { u32 w[4]; };
-            const V a = *reinterpret_cast<const V *>(static_cast<const u16 *>(src) + at);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = from16<SRC>(a.w[j] & 0xFFFFu);
-                v[2 * j + 1] = from16<SRC>(a.w[j] >> 16);
+        for (int j = 0; j < 8; ++j) {
+            v[j] = 0.f;
+            if (j < nvalid) {
+                if constexpr (SRC == DT_F32) v[j] = static_cast<const float *>(src)[at + j];
+                else v[j] = from16<SRC>(static_cast<const u16 *>(src)[at + j]);
             }
         }
-    } else {
+    } else if constexpr (SRC == DT_F32) {
+        struct __attribute__((packed, aligned(4))) V { u32 w[4]; };
+        const float *q = static_cast<const float *>(src) + at;
+        const V a = *reinterpret_cast<const V *>(q), b = *reinterpret_cast<const V *>(q + 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < nvalid ? load_value<SRC>(src, at + j) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+            v[j] = as_f32(a.w[j]);
+            v[4 + j] = as_f32(b.w[j]);
+        }
+    } else {
+        // rows of 16-bit values start at any even address
+        struct __attribute__((packed, aligned(2))) V { u32 w[4]; };
+        const V a = *reinterpret_cast<const V *>(static_cast<const u16 *>(src) + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = from16<SRC>(a.w[j] & 0xFFFFu);
+            v[2 * j + 1] = from16<SRC>(a.w[j] >> 16);
+        }
     }
 }
 
@@ -74,18 +75,26 @@ __device__ inline float max_over_group(float v) {
     return fmaxf(v, __shfl_xor(v, 32));
 }
 
-// rint(w / s) clamped to [lo, hi], as if the quotient were exact: the fp32
-// product with 1/s is off by less than half, so the whole number nearest to
-// it is the answer or a neighbour, and the remainder w - q s (exact in one
-// fma: w has 24 bits, q s 15, and their difference cancels to within |s|)
-// says which; a remainder of exactly s/2 rounds to the even q.
+// rint(w / s) clamped to [lo, hi], as if the quotient were exact (inv: 1/s
+// to a step).  One correction by the remainder makes q the fp32 number
+// nearest to the quotient, and a quotient that is a whole number and a half
+// comes out as that, so ties go to even.  Rounding to fp32 can only mislead
+// rint by moving the quotient onto such a tie: not where w has 11 bits or
+// fewer, like s, since their quotient then stays 2^-13 of a step away from a
+// tie that it does not meet.  Where w is fp32, the remainder at the chosen
+// whole number (exact in one fma: w has 24 bits, q s 15, and the difference
+// cancels to within |s|) says whether the other neighbour is nearer.
+template <int SRC>
 __device__ inline float quotient(float w, float s, float inv, float lo, float hi) {
-    const float q = fminf(fmaxf(rintf(w * inv), lo), hi);
-    const float r = __builtin_fmaf(-q, s, w), a = fabsf(s), half = 0.5f * a;
-    const float dir = ((r < 0.f) != (s < 0.f)) ? -1.f : 1.f;
-    const bool odd = ((int)q & 1) != 0;
-    const bool move = fabsf(r) > half || (fabsf(r) == half && odd);
-    return move ? fminf(fmaxf(q + dir, lo), hi) : q;
+    float q = w * inv;
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, w), inv, q);
+    q = rintf(q);
+    if constexpr (SRC == DT_F32) {
+        const float r = __builtin_fmaf(-q, s, w);
+        const float dir = as_f32(((as_u32(r) ^ as_u32(s)) & 0x80000000u) | 0x3F800000u);
+        q = fabsf(r) > 0.5f * fabsf(s) ? q + dir : q;
+    }
+    return fminf(fmaxf(q, lo), hi);
 }
 
 // Quantize: per group the scale (and zero point) from its largest and
@@ -95,35 +104,39 @@ __device__ inline float quotient(float w, float s, float inv, float lo, float hi
 template <int SRC, int DT, int GP, bool ZP>
 __global__ __launch_bounds__(kFmtThreads) void w4_quantize_kernel(W4Args w, W4DenseArgs src) {
     BlockPos p;
-    if (!block_pos(w.batch, w.N, w.K, p)) return;
+    if (!block_pos(w.N, w.K, p)) return;
     const int lane = threadIdx.x & 63, r = lane & 15;
     float v[4][8];
-    const bool row = p.n < w.N;
-    const int64_t at = p.z * src.stride + (int64_t)(row ? p.n : 0) * src.ld + p.k0;
+    // (rows past N: the last one once more)
+    const int64_t at = p.z * src.stride + (int64_t)min(p.n, w.N - 1) * src.ld + p.k0;
+    if ((p.kb + 1) * kBlkK <= w.K) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load8<SRC>(src.ptr, at + i * 32, row ? w.K - p.k0 - i * 32 : 0, v[i]);
+        for (int i = 0; i < 4; ++i) load8<SRC, false>(src.ptr, at + i * 32, 8, v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load8<SRC, true>(src.ptr, at + i * 32, w.K - p.k0 - i * 32, v[i]);
+    }
 
     constexpr int S = 4 / GP;
     u32 code[4], sbits[GP], zbits[GP];
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
         float hi = -INFINITY, nlo = -INFINITY;   // nlo: the largest of -v
-        u32 bad = 0;                             // an exponent of all ones
+        bool bad = false;                        // a NaN or infinity
 #pragma unroll
         for (int i = g * S; i < (g + 1) * S; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 hi = fmaxf(hi, v[i][j]);
                 nlo = fmaxf(nlo, -v[i][j]);
-                bad |= (as_u32(v[i][j]) & 0x7F800000u) == 0x7F800000u;
+                bad |= !(fabsf(v[i][j]) < INFINITY);
             }
         }
         // zeros past K change neither: the scale comes from the larger
         // magnitude (or from values clamped to zero)
-        hi = max_over_group(hi);
+        hi = max_over_group(bad ? INFINITY : hi);
         nlo = max_over_group(nlo);
-        bad |= __shfl_xor(bad, 16);
-        bad |= __shfl_xor(bad, 32);
+        bad = hi == INFINITY;
         float s, z = 8.f;
         if constexpr (ZP) {
             hi = fmaxf(hi, 0.f);
@@ -140,9 +153,9 @@ __global__ __launch_bounds__(kFmtThreads) void w4_quantize_kernel(W4Args w, W4De
         // 1/s would overflow
         const float lift = fabsf(s) < 0x1p-64f ? 0x1p64f : 1.f;
         s *= lift;
-        const bool none = !(fabsf(s) > 0.f);     // zero, or NaN
-        const float inv = none ? 0.f : 1.f / s;
-        if constexpr (ZP) z = none ? 0.f : quotient(nlo * lift, s, inv, 0.f, 15.f);
+        const bool none = !(fabsf(s) > 0.f);     // zero, or NaN: all codes z
+        const float inv = none ? 0.f : __builtin_amdgcn_rcpf(s);
+        if constexpr (ZP) z = none ? 0.f : quotient<DT_F32>(nlo * lift, s, inv, 0.f, 15.f);
         sbits[g] = sb;
         zbits[g] = (u32)z;
 #pragma unroll
@@ -150,7 +163,7 @@ __global__ __launch_bounds__(kFmtThreads) void w4_quantize_kernel(W4Args w, W4De
             u32 d = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float q = none ? 0.f : quotient(v[i][j] * lift, s, inv, -z, 15.f - z);
+                const float q = quotient<SRC>(none ? 0.f : v[i][j] * lift, none ? 1.f : s, inv, -z, 15.f - z);
                 d |= (u32)(int)(q + z) << code_bit(j);
             }
             code[i] = d;
@@ -176,7 +189,7 @@ __global__ __launch_bounds__(kFmtThreads) void w4_quantize_kernel(W4Args w, W4De
 template <int DT, int OUT>
 __global__ __launch_bounds__(kFmtThreads) void w4_dequantize_kernel(W4Args w, W4DenseArgs dst) {
     BlockPos p;
-    if (!block_pos(w.batch, w.N, w.K, p)) return;
+    if (!block_pos(w.N, w.K, p)) return;
     const int lane = threadIdx.x & 63, r = lane & 15, gp = kBlkK / w.group;
     const u32x4 q = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(w.codes) +
                                                      p.block * kBlkBytes + lane * 16);
@@ -223,11 +236,11 @@ __global__ __launch_bounds__(kFmtThreads) void w4_dequantize_kernel(W4Args w, W4
 // K becomes code 8 with scale 0.
 __global__ __launch_bounds__(kFmtThreads) void w4_pack_kernel(W4Args w, W4RowMajorArgs src) {
     BlockPos p;
-    if (!block_pos(w.batch, w.N, w.K, p)) return;
+    if (!block_pos(w.N, w.K, p)) return;
     const int lane = threadIdx.x & 63, r = lane & 15, gp = kBlkK / w.group;
     const int64_t row_bytes = ((int64_t)w.K + 1) / 2, groups = ((int64_t)w.K + w.group - 1) / w.group;
     const bool row = p.n < w.N;
-    const int64_t at_row = p.z * w.N + (row ? p.n : 0);
+    const int64_t at_row = (int64_t)p.z * w.N + (row ? p.n : 0);
     const unsigned char *cp = static_cast<const unsigned char *>(src.codes) + at_row * row_bytes;
     u32 code[4];
 #pragma unroll
@@ -258,8 +271,8 @@ __global__ __launch_bounds__(kFmtThreads) void w4_pack_kernel(W4Args w, W4RowMaj
 }
 
 int64_t format_grid(const W4Args &w) {
-    const int64_t blocks = w4_blocks(w.N, w.K) * w.batch;
-    return (blocks + kFmtThreads / 64 - 1) / (kFmtThreads / 64);
+    const int64_t kbs = (w.K + kBlkK - 1) / kBlkK, nbs = ((int64_t)w.N + kBlkN - 1) / kBlkN;
+    return (kbs + kFmtThreads / 64 - 1) / (kFmtThreads / 64) * nbs * w.batch;
 }
 
 template <int SRC, int DT, int GP>

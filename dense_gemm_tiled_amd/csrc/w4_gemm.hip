@@ -360,36 +360,35 @@ hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Which kernel.  Measured on one box, us per call, bf16, group 128 (rows, then
-// 32x64 tiles with 4 sets, 64x64 with 2, 64x128 with 1):
-//     N 8192 K 4096, M 16:     6.9 /    - /    - /    -
-//     N 8192 K 4096, M 32:     9.3 / 17.2 / 26.8 / 42.0
-//     N 8192 K 4096, M 64:    22.9 / 17.8 / 27.7 / 43.9
-//     N 4096 K 4096, M 128:      - / 17.9 / 27.9 / 44.1
-//     N 4096 K 4096, M 256:      - / 32.6 / 29.3 / 44.4
-//     N 4096 K 4096, M 512:      - / 60.4 / 55.0 / 45.4
-//     N 4096 K 4096, M 2048: 330.5 / 232 / 212 / 96.9
-// so: rows up to 32; then the tiles by how many of them there are per CU.
-// Rows: one block of 16 weight rows per workgroup up to two workgroups a CU,
-// two blocks beyond (N 4096 K 4096 M 1: 4.45 / 5.3; N 8192 K 8192 M 1: 11.4 /
-// 9.5; N 16384 K 8192 M 4: 22.7 / 16.7), 8 waves (16: no faster anywhere, and
-// 18.3 on the last shape; 4: 5.3 on the first).
+// Which kernel.  Measured on one box, us per call, bf16, group 128 where not
+// said.  Up to 16 rows: one block of 16 weight rows per workgroup up to two
+// workgroups a CU, two blocks beyond (N 4096 K 4096 M 1: 4.45 / 5.3; N 8192 K
+// 8192 M 1: 11.4 / 9.5; N 16384 K 8192 M 4: 22.7 / 16.7), 8 waves (16: no
+// faster anywhere, and 18.3 on the last shape; 4: 5.3 on the first).  More
+// rows, 32 to a workgroup: two blocks while that is at most a workgroup a CU,
+// four beyond, tiles once four make more than four workgroups a CU (two
+// blocks / four / tiles):
+//     N 4096 K 4096 M 64       8.7 / 10.9 /     -
+//     N 8192 K 4096 M 64      16.2 / 12.0 /  43.9
+//     N 4096 K 4096 M 256     28.9 / 22.1 /  44.4
+//     N 4096 K 4096 M 512     53.7 / 40.4 /  42.4
+//     N 4096 K 4096 M 2048       - /  160 /   101
+//     N 8192 K 4096 M 64, group 32 with zero points: 19.2 / 20.7 (four blocks
+//     do not fit the registers then)
 template <class WK>
 hipError_t launch_kind(const W4GemmArgs &a, const char **name, hipStream_t s) {
     const int kbs = (a.w.K + kBlkK - 1) / kBlkK, nblocks = (a.w.N + kBlkN - 1) / kBlkN;
-    if (a.M <= 32) {
-        *name = WK::DT == DT_F16 ? "w4_rows_f16" : "w4_rows_bf16";
-        const int waves = kbs >= 8 ? 8 : 4;
-        if (a.M > 16) return launch_rows<WK, 2, 2>(a, waves, s);
-        if (nblocks >= 512) return launch_rows<WK, 2, 1>(a, waves, s);
-        return launch_rows<WK, 1, 1>(a, waves, s);
+    const int64_t mtiles = (a.M + 31) / 32;
+    if (mtiles * ((nblocks + 3) / 4) > 1024) {
+        *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";
+        return launch_tile<WK, 4, 2, 1, 1, 1>(a, s);
     }
-    *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";
-    const int64_t tiles_64 = (int64_t)((a.M + 63) / 64) * ((a.w.N + 63) / 64);
-    if (tiles_64 > 256) return launch_tile<WK, 4, 2, 1, 1, 1>(a, s);
-    if (tiles_64 > 128 && a.M > 128) return launch_tile<WK, 4, 1, 1, 2, 2>(a, s);
-    // (groups of 32: a second set of registers would not fit)
-    return launch_tile<WK, 2, 1, 1, 4, WK::GP == 4 ? 1 : 2>(a, s);
+    *name = WK::DT == DT_F16 ? "w4_rows_f16" : "w4_rows_bf16";
+    const int waves = kbs >= 8 ? 8 : 4;
+    if (a.M <= 16 && nblocks < 512) return launch_rows<WK, 1, 1>(a, waves, s);
+    if (a.M <= 16) return launch_rows<WK, 2, 1>(a, waves, s);
+    if (WK::GP < 4 && mtiles * ((nblocks + 1) / 2) > 256) return launch_rows<WK, WK::GP < 4 ? 4 : 2, 2>(a, waves, s);
+    return launch_rows<WK, 2, 2>(a, waves, s);
 }
 
 }  // namespace

@@ -157,6 +157,16 @@ def test_product_strides_and_odd_addresses(tg, M, ldx, ldy, shift):
     run_product(tg, M, 75, 300, "f16", 32, False, ldx=ldx, ldy=ldy, shift=shift)
 
 
+@pytest.mark.parametrize("M,N,K", [(2090, 1010, 264), (33000, 33, 130), (1100, 2000, 1001), (2048, 1024, 128),
+                                   (4200, 520, 77)])
+@pytest.mark.parametrize("dtype,group,zeros,out", [("bf16", 128, False, "bf16"), ("f16", 32, True, "f32"),
+                                                   ("bf16", 64, True, "f32"), ("f16", 64, False, "f16"),
+                                                   ("bf16", 32, False, "f32"), ("f16", 128, True, "f32")])
+def test_product_many_rows(tg, M, N, K, dtype, group, zeros, out):
+    """The tiles of long prompts, ragged in every direction."""
+    run_product(tg, M, N, K, dtype, group, zeros, out=out, seed=K, bias=True)
+
+
 def test_product_long_k(tg):
     run_product(tg, 2, 40, 65536, "bf16", 128, False, out="f32")
     run_product(tg, 80, 40, 16400, "f16", 64, True, out="f32")

@@ -1,6 +1,7 @@
 // w4_gemm.hip -- y = act(alpha * x @ W^T + beta * y + bias) for a weight
 // matrix in the 4-bit format (w4_core.hpp).  One object per type of x
 // (W4_DT).
+#include "gemm_dma_kernel.hpp"
 #include "w4_core.hpp"
 
 #include "w4_args.h"
@@ -105,40 +106,39 @@ hipError_t launch_rows(const W4GemmArgs &a, int waves, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Many rows (a prompt, a batch of sequences).  A workgroup owns R = 16 MT WM
-// rows of x and 64 NBW of W: 4 WM waves, each 16 MT x 16 NBW of the result,
-// and KG such sets of waves that share out the blocks of K (128 wide) and add
-// their results in LDS at the end, for outputs with too few tiles to keep
-// the chip busy.
+// Many rows (a prompt).  A workgroup of 8 waves owns a tile of 128 rows of x
+// and 256 of W (128 with groups under 128: their scales, offsets and sums take
+// the registers), a wave 64 x 64 (64 x 32) of it, and walks K in blocks of 128.
 //
-// x comes through LDS, three blocks at a time: rows of 256 bytes with 16-byte
-// piece c of row r at c ^ (r % 16), so that the reads of 16 rows fall into
-// different banks; all waves read it.  The weights do not: a wave loads the
-// blocks of its own 16 NBW rows straight into registers and expands each
-// once.  In step s the waves multiply block s, write block s + 2 to LDS from
-// registers loaded DIST steps ago, and issue the loads of later steps.
+// x comes through LDS, by direct-to-LDS loads, three blocks at a time: rows of
+// 256 bytes with 16-byte piece c of row r at c ^ (r % 16), so that the reads
+// of 16 rows fall into different banks; all waves read it.  The weights do
+// not: a wave loads the blocks of its own 64 rows into registers and expands
+// each once.  In step s block s is multiplied while block s + 2 of x and block
+// s + 1 of the weights arrive.
 //
 // The sums of x that the offset 16 + z needs are matrix instructions with a
-// constant right operand, made in step s for block s + 1, every wave a share
-// of the rows, and handed over in LDS (as -24 sum x where every z is 8).
-// They are the first addend of the group's products, so with symmetric codes
-// the offset costs no instruction per result.
-template <class WK, int MT, int NBW, int WM, int KG, int DIST>
-__global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, int tiles_m, int tiles_n) {
-    constexpr int R = 16 * MT * WM, GP = WK::GP, S = 4 / GP;
-    constexpr int P = MT;                          // pieces of x a thread stages per block
-    constexpr int SLOT = R * 256;
-    __shared__ __attribute__((aligned(16))) char xbuf[KG][3][SLOT];
-    __shared__ __attribute__((aligned(16))) float xsum[KG][2][GP][R];
+// constant right operand, made in step s for block s + 1, a tile of 16 rows to
+// a wave, and handed over in LDS (as -24 sum x where every z is 8).  They are
+// the first addend of the group's products, so with symmetric codes the
+// offset costs no instruction per result.
+constexpr int kTileM = 128, kTileThreads = 512;
+template <class WK>
+constexpr int kTileBlocks = WK::GP == 1 ? 4 : 2;   // blocks of 16 weight rows a wave
+
+template <class WK>
+__global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int tiles_m, int tiles_n) {
+    constexpr int MT = 4, NBW = kTileBlocks<WK>, GP = WK::GP, S = 4 / GP, SLOT = kTileM * 256;
+    __shared__ __attribute__((aligned(16))) char xbuf[3][SLOT];
+    __shared__ __attribute__((aligned(16))) float xsum[2][GP][kTileM];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = wave & 3, wm = (wave >> 2) % WM, kg = wave / (4 * WM);
+    const int wn = wave & 3, wm = wave >> 2;
     int tm, tn, group;
     tile_of_workgroup(tiles_m, tiles_n, 8, blockIdx.x, (int64_t)tiles_m * tiles_n, &tm, &tn, &group);
     const int N = a.w.N, K = a.w.K;
     // (alpha 0 reads neither operand)
     const int kbs = a.alpha == 0.f ? 0 : (K + kBlkK - 1) / kBlkK;
-    const int steps = (kbs + KG - 1) / KG;
-    const int m0 = tm * R, rows = min(a.M - m0, R);
+    const int m0 = tm * kTileM, rows = min(a.M - m0, kTileM);
     const int nb0 = (tn * 4 + wn) * NBW, nblocks = (N + kBlkN - 1) / kBlkN;
 
     const MatrixRef mat = {static_cast<const char *>(a.w.codes), static_cast<const char *>(a.w.scales),
@@ -146,51 +146,41 @@ __global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, in
     WStream<WK> w[NBW];
 #pragma unroll
     for (int b = 0; b < NBW; ++b) w[b] = WStream<WK>(mat, min(nb0 + b, nblocks - 1), N, K, lane);
-    const int64_t x_org = (int64_t)m0 * a.ldx * 2;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + x_org, a.x_bytes - x_org);
-    // this thread's pieces of a block of x: piece c of rows r0 + 16 WM j
-    const int gt = tid % (256 * WM), c = gt & 15, r0 = gt >> 4;
-    int x_off[P];
+    const char *const x0 = static_cast<const char *>(a.x) + (int64_t)m0 * a.ldx * 2;
+    const int64_t x_bytes = a.x_bytes - (int64_t)m0 * a.ldx * 2;
+    // this lane's pieces of a block of x: LDS piece lane % 16 of rows 16 wave
+    // + 4 u + lane / 16 (rows past the last are past x: they load as zeros)
+    const int x_row = (16 * wave + (lane >> 4)) * (int)a.ldx * 2, x_step = 8 * (int)a.ldx;
+    const int x_piece = ((lane & 15) ^ (lane >> 4)) << 4;
+    auto x_off = [&](int u) { return x_row + u * x_step + (x_piece ^ (64 * u)); };
+    const u32 lds0 = (u32)(uintptr_t)&xbuf[0][0] + wave * 4096;
+    auto stage = [&](int kb, int slot) {
+        if (kb >= kbs) return;
+        if ((kb + 1) * kBlkK <= K) {
+            const i32x4 rx = rsrc4(x0 + (int64_t)kb * 256, x_bytes - (int64_t)kb * 256);
 #pragma unroll
-    for (int j = 0; j < P; ++j) x_off[j] = min(r0 + 16 * WM * j, rows - 1) * (int)a.ldx * 2 + c * 16;
-    const int lds_off0 = r0 * 256 + ((c ^ (r0 & 15)) << 4);   // (16 WM rows further: the same c ^ r)
-
-    // block s of this set of waves; zeros from K on
-    auto load_rows = [&](u32x4 (&v)[P], int s) {
-        const int kb = s * KG + kg, kv = K - kb * kBlkK, have = kv - c * 8;
-        if (kv >= kBlkK && kb < kbs) {
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                v[j] = __builtin_amdgcn_raw_buffer_load_b128(rx, x_off[j], kb * 256, 0);
-        } else {
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                v[j] = ld_chunk_tail(rx, x_off[j] + kb * 256, kb < kbs ? have : 0, (K & 7) != 0);
+            for (int u = 0; u < 4; ++u) dma16(rx, lds0 + slot * SLOT + u * 1024, x_off(u));
+            return;
         }
-    };
-    // (past the last block: that block again, which is then not used)
-    auto load_codes = [&](WFrag<WK> (&f)[NBW], int s) {
-        const int kb = min(s * KG + kg, kbs - 1);
+        // the short last block: through registers, with zeros from K on
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(x0 + (int64_t)kb * 256, x_bytes - (int64_t)kb * 256);
+        u32x4 v[4];
 #pragma unroll
-        for (int b = 0; b < NBW; ++b) {
-            if (GP > 1 && K - kb * kBlkK < kBlkK) w[b].template load<true>(f[b], kb, K - kb * kBlkK, lane);
-            else w[b].template load<false>(f[b], kb, kBlkK, lane);
+        for (int u = 0; u < 4; ++u) {
+            v[u] = ld_chunk_tail(rx, x_off(u), K - kb * kBlkK - (x_piece ^ (64 * u)) / 2, (K & 7) != 0);
         }
-    };
-    auto write_rows = [&](const u32x4 (&v)[P], int slot) {
 #pragma unroll
-        for (int j = 0; j < P; ++j)
-            *reinterpret_cast<u32x4 *>(&xbuf[kg][slot][lds_off0 + 16 * WM * 256 * j]) = v[j];
+        for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<u32x4 *>(&xbuf[slot][wave * 4096 + u * 1024 + lane * 16]) = v[u];
     };
-    const int rl = wm * 16 * MT + (lane & 15), kq = lane >> 4;
+    const int rl = wm * 64 + (lane & 15), kq = lane >> 4;
     auto read_x = [&](u32x4 (&x)[4], int slot, int t) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             x[i] = *reinterpret_cast<const u32x4 *>(
-                &xbuf[kg][slot][(rl + 16 * t) * 256 + (((i * 4 + kq) ^ (rl & 15)) << 4)]);
+                &xbuf[slot][(rl + 16 * t) * 256 + (((i * 4 + kq) ^ (rl & 15)) << 4)]);
     };
-    // sums of block s for the rows of tile wn (the first MT waves)
-    static_assert(MT <= 4, "one wave per tile makes the sums");
+    // sums of block s for the rows of tile wn of this half
     auto make_sums = [&](const u32x4 (&x)[4], int s) {
         const u32 one = WK::ZP ? (WK::DT == DT_F16 ? 0x3C003C00u : 0x3F803F80u) : w4_neg_offset<WK::DT>(8);
         const u32x4 ones = {one, one, one, one};
@@ -199,73 +189,83 @@ __global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, in
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = g * S; i < (g + 1) * S; ++i) p = mfma_x_w<WK::DT>(x[i], ones, p);
-            if ((lane & 15) == 0 && wn < MT)
-                *reinterpret_cast<f32x4 *>(&xsum[kg][s & 1][g][wm * 16 * MT + 16 * (wn % MT) + kq * 4]) = p;
+            if ((lane & 15) == 0) *reinterpret_cast<f32x4 *>(&xsum[s & 1][g][wm * 64 + 16 * wn + kq * 4]) = p;
         }
     };
+    // (all of this wave's loads and LDS writes, then everybody's)
+    auto barrier = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     f32x4 acc[MT][NBW];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int b = 0; b < NBW; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 xv[DIST][P];
-    WFrag<WK> wf[DIST][NBW];
-    auto step = [&](int s, WFrag<WK> (&f)[NBW], u32x4 (&xr)[P]) {
-        __syncthreads();
-        const int slot = s % 3, next = slot == 2 ? 0 : slot + 1, after = 3 - slot - next;
+    WFrag<WK> f[NBW];
+    auto load_codes = [&](int block) {
+        const int kb = min(block, kbs - 1);
+#pragma unroll
+        for (int b = 0; b < NBW; ++b) {
+            if (GP > 1 && K - kb * kBlkK < kBlkK) w[b].template load<true>(f[b], kb, K - kb * kBlkK, lane);
+            else w[b].template load<false>(f[b], kb, kBlkK, lane);
+        }
+    };
+    if (kbs > 0) {
+        stage(0, 0);
+        stage(1, 1);
+        load_codes(0);
+        barrier();
+        u32x4 x[4];
+        read_x(x, 0, wn);
+        make_sums(x, 0);
+    }
+    int slot = 0;
+#pragma unroll 1
+    for (int s = 0; s < kbs; ++s) {
+        const int next = slot == 2 ? 0 : slot + 1, after = 3 - slot - next;
+        barrier();
+        stage(s + 2, after);
         u32x4 x[2][4];
         f32x4 xs[2][GP];
         auto read_tile = [&](int t) {
             read_x(x[t & 1], slot, t);
 #pragma unroll
             for (int g = 0; g < GP; ++g)
-                xs[t & 1][g] = *reinterpret_cast<const f32x4 *>(
-                    &xsum[kg][s & 1][g][wm * 16 * MT + 16 * t + kq * 4]);
+                xs[t & 1][g] = *reinterpret_cast<const f32x4 *>(&xsum[s & 1][g][wm * 64 + 16 * t + kq * 4]);
         };
         read_tile(0);
         u32x4 wv[NBW][4];
-        float ws[NBW][GP], wz[NBW][GP];
+        u32 sc[NBW][GP == 4 ? 2 : 1], zc[NBW];
 #pragma unroll
         for (int b = 0; b < NBW; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
-#pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                ws[b][g] = from16<WK::DT>((f[b].s[g >> 1] >> (16 * (g & 1))) & 0xFFFFu);
-                if (WK::ZP) wz[b][g] = -16.f - (float)((f[b].z >> (8 * g)) & 15);
-            }
+            sc[b][0] = f[b].s[0];
+            if (GP == 4) sc[b][GP == 4 ? 1 : 0] = f[b].s[GP == 4 ? 1 : 0];
+            zc[b] = f[b].z;
         }
-        write_rows(xr, after);
-        load_rows(xr, s + 2 + DIST);
-        load_codes(f, s + DIST);
-        // a set of waves with no block left in the last step has zeros in x
-        // and an earlier block's weights: its products are left out
-        const bool live = KG == 1 || s * KG + kg < kbs;
+        load_codes(s + 1);
         f32x4 p[2][NBW];
         // (group u of the step's MT * GP) its products, scaled and added
         auto add = [&](int u) {
+            const int g = u % GP;
 #pragma unroll
-            for (int b = 0; b < NBW; ++b)
+            for (int b = 0; b < NBW; ++b) {
+                const float ws = from16<WK::DT>((sc[b][g >> 1] >> (16 * (g & 1))) & 0xFFFFu);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[u / GP][b][e] = __builtin_fmaf(ws[b][u % GP], p[u & 1][b][e], acc[u / GP][b][e]);
-        };
-        auto pin = [&](int u) {
-            // (keeps the compiler from moving them to the end of the step,
-            // where every p would be alive at once)
-#pragma unroll
-            for (int b = 0; b < NBW; ++b) asm volatile("" : "+v"(acc[u / GP][b]));
+                for (int e = 0; e < 4; ++e) acc[u / GP][b][e] = __builtin_fmaf(ws, p[u & 1][b][e], acc[u / GP][b][e]);
+                // (keeps the compiler from moving these to the end of the
+                // step, where every p would be alive at once)
+                asm volatile("" : "+v"(acc[u / GP][b]));
+            }
         };
 #pragma unroll
         for (int t = 0; t <= MT; ++t) {
             // the next tile's reads go out ahead of this one's products; the
             // last of them is the tile whose sums this wave makes
             if (t + 1 < MT) read_tile(t + 1);
-            if (t + 1 == MT) read_x(x[MT & 1], next, wn % MT);
+            if (t + 1 == MT) read_x(x[MT & 1], next, wn);
             __builtin_amdgcn_sched_barrier(0);
             if (t == MT) break;
-            if (!live) continue;
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const int u = t * GP + g;
@@ -275,67 +275,18 @@ __global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, in
 #pragma unroll
                 for (int b = 0; b < NBW; ++b) {
                     p[u & 1][b] = xs[t & 1][g];
-                    if constexpr (WK::ZP) p[u & 1][b] *= wz[b][g];
+                    if constexpr (WK::ZP) p[u & 1][b] *= -16.f - (float)((zc[b] >> (8 * g)) & 15);
                 }
 #pragma unroll
                 for (int i = g * S; i < (g + 1) * S; ++i)
 #pragma unroll
                     for (int b = 0; b < NBW; ++b) p[u & 1][b] = mfma_x_w<WK::DT>(x[t & 1][i], wv[b][i], p[u & 1][b]);
-                if (u > 0) {
-                    add(u - 1);
-                    pin(u - 1);
-                }
+                if (u > 0) add(u - 1);
             }
         }
         make_sums(x[MT & 1], s + 1);
-        if (live) {
-            add(MT * GP - 1);
-            pin(MT * GP - 1);
-        }
-    };
-    if (steps > 0) {
-        load_rows(xv[0], 0);
-        write_rows(xv[0], 0);
-        load_rows(xv[0], 1);
-        write_rows(xv[0], 1);
-#pragma unroll
-        for (int d = 0; d < DIST; ++d) {
-            load_rows(xv[d], 2 + d);
-            load_codes(wf[d], d);
-        }
-        __syncthreads();
-        u32x4 x[4];
-        read_x(x, 0, wn % MT);
-        make_sums(x, 0);
-    }
-#pragma unroll 1
-    for (int s = 0; s < steps; s += DIST) {
-#pragma unroll
-        for (int d = 0; d < DIST; ++d)
-            if (s + d < steps) step(s + d, wf[d], xv[d]);
-    }
-    // the other sets' results, added in order
-    if constexpr (KG > 1) {
-        float *part = reinterpret_cast<float *>(&xbuf[0][0][0]);
-        constexpr int PER = MT * NBW * 256 * 4 * WM;   // floats of one set
-        static_assert((KG - 1) * PER * 4 <= (int)sizeof xbuf, "the partial results fit the buffers of x");
-        __syncthreads();
-        if (kg > 0) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int b = 0; b < NBW; ++b)
-                    *reinterpret_cast<f32x4 *>(&part[(kg - 1) * PER + ((t * NBW + b) * 256 * WM + gt) * 4]) = acc[t][b];
-        }
-        __syncthreads();
-        if (kg > 0) return;
-#pragma unroll
-        for (int q = 0; q < KG - 1; ++q)
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int b = 0; b < NBW; ++b)
-                    acc[t][b] += *reinterpret_cast<const f32x4 *>(&part[q * PER + ((t * NBW + b) * 256 * WM + gt) * 4]);
+        add(MT * GP - 1);
+        slot = next;
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -344,19 +295,17 @@ __global__ __launch_bounds__(256 * WM * KG) void w4_tile_kernel(W4GemmArgs a, in
             const int n = (nb0 + b) * 16 + (lane & 15);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int m = wm * 16 * MT + 16 * t + kq * 4 + e;
+                const int m = wm * 64 + 16 * t + kq * 4 + e;
                 if (m < rows && n < N) finish<WK::DT>(a, m0 + m, n, acc[t][b][e]);
             }
         }
 }
 
-template <class WK, int MT, int NBW, int WM, int KG, int DIST>
+template <class WK>
 hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
-    constexpr int R = 16 * MT * WM;
-    const int64_t tm = (a.M + R - 1) / R, tn = ((int64_t)a.w.N + 64 * NBW - 1) / (64 * NBW);
+    const int64_t tm = (a.M + kTileM - 1) / kTileM, tn = ((int64_t)a.w.N + 64 * kTileBlocks<WK> - 1) / (64 * kTileBlocks<WK>);
     if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((w4_tile_kernel<WK, MT, NBW, WM, KG, DIST>), dim3((unsigned)(tm * tn)), dim3(256 * WM * KG),
-                       0, s, a, (int)tm, (int)tn);
+    hipLaunchKernelGGL(w4_tile_kernel<WK>, dim3((unsigned)(tm * tn)), dim3(kTileThreads), 0, s, a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
@@ -381,7 +330,7 @@ hipError_t launch_kind(const W4GemmArgs &a, const char **name, hipStream_t s) {
     const int64_t mtiles = (a.M + 31) / 32;
     if (mtiles * ((nblocks + 3) / 4) > 1024) {
         *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";
-        return launch_tile<WK, 4, 2, 1, 1, 1>(a, s);
+        return launch_tile<WK>(a, s);
     }
     *name = WK::DT == DT_F16 ? "w4_rows_f16" : "w4_rows_bf16";
     const int waves = kbs >= 8 ? 8 : 4;

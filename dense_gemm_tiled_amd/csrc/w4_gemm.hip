@@ -107,28 +107,45 @@ hipError_t launch_rows(const W4GemmArgs &a, int waves, hipStream_t s) {
 }
 
 // Many rows (a prompt).  A workgroup of 8 waves owns a tile of 128 rows of x
-// and 256 of W (128 with groups under 128: their scales, offsets and sums take
-// the registers), a wave 64 x 64 (64 x 32) of it, and walks K in blocks of 128.
+// and 64 NBW of W, a wave 64 x 16 NBW of it, and walks K in blocks of 128.
 //
 // x comes through LDS, by direct-to-LDS loads, three blocks at a time: rows of
 // 256 bytes with 16-byte piece c of row r at c ^ (r % 16), so that the reads
 // of 16 rows fall into different banks; all waves read it.  The weights do
-// not: a wave loads the blocks of its own 64 rows into registers and expands
-// each once.  In step s block s is multiplied while block s + 2 of x and block
-// s + 1 of the weights arrive.
+// not: a wave loads the blocks of its own rows into registers and expands each
+// once.  In step s block s is multiplied while block s + 2 of x and block s + 1
+// of the weights arrive.
 //
 // The sums of x that the offset 16 + z needs are matrix instructions with a
 // constant right operand, made in step s for block s + 1, a tile of 16 rows to
 // a wave, and handed over in LDS (as -24 sum x where every z is 8).  They are
 // the first addend of the group's products, so with symmetric codes the
 // offset costs no instruction per result.
+//
+// NBW: with a group of 128, 4 blocks of weight rows a wave are as many as the
+// 256 registers of two waves a SIMD hold, and 2048 rows by 4096x4096 take 80.9
+// us (850 TFLOP/s; 33 us at the rate of a large matrix product in 16 bits,
+// 101.8 with 128x64 tiles of 4 waves and x through registers).  A round of
+// 128x256 tiles over the CUs is worth 1.5 of 128x128, so the smaller ones are
+// taken where they need less than 1.5 times the rounds (1024 rows by
+// 4096x4096: 72 / 55 us; 256 rows by 16384x4096: 74 / 56).  Smaller groups
+// hold more scales and sums and have 2 blocks only: 2048 rows by 4096x4096
+// take 116 us with groups of 64, 160 with groups of 32 and zero points (a
+// multiplication per result and group comes on top).
+//
+// What bounds it: every wave's 64 matrix instructions a step take a quarter to
+// a half of the step, expanding and scaling on the VALU about as much again,
+// and with two waves a SIMD in step with each other the two overlap in part
+// only.  Expanding between the first products instead of before them is faster
+// with 2 blocks (groups of 64: 127 -> 116 us) and slower with 4 (80.9 -> 86.8:
+// the next codes are then loaded later).
 constexpr int kTileM = 128, kTileThreads = 512;
-template <class WK>
-constexpr int kTileBlocks = WK::GP == 1 ? 4 : 2;   // blocks of 16 weight rows a wave
 
-template <class WK>
+template <class WK, int NBW>
 __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int tiles_m, int tiles_n) {
-    constexpr int MT = 4, NBW = kTileBlocks<WK>, GP = WK::GP, S = 4 / GP, SLOT = kTileM * 256;
+    // (LATE: the codes are expanded between the first products)
+    constexpr bool LATE = NBW == 2 && WK::GP < 4;
+    constexpr int MT = 4, GP = WK::GP, S = 4 / GP, SLOT = kTileM * 256;
     __shared__ __attribute__((aligned(16))) char xbuf[3][SLOT];
     __shared__ __attribute__((aligned(16))) float xsum[2][GP][kTileM];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -238,12 +255,12 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
 #pragma unroll
         for (int b = 0; b < NBW; ++b) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
+            for (int i = 0; i < 4 && !LATE; ++i) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
             sc[b][0] = f[b].s[0];
             if (GP == 4) sc[b][GP == 4 ? 1 : 0] = f[b].s[GP == 4 ? 1 : 0];
             zc[b] = f[b].z;
         }
-        load_codes(s + 1);
+        if (!LATE) load_codes(s + 1);
         f32x4 p[2][NBW];
         // (group u of the step's MT * GP) its products, scaled and added
         auto add = [&](int u) {
@@ -266,6 +283,7 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
             if (t + 1 == MT) read_x(x[MT & 1], next, wn);
             __builtin_amdgcn_sched_barrier(0);
             if (t == MT) break;
+            if (LATE && t == 1) load_codes(s + 1);
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const int u = t * GP + g;
@@ -280,7 +298,10 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
 #pragma unroll
                 for (int i = g * S; i < (g + 1) * S; ++i)
 #pragma unroll
-                    for (int b = 0; b < NBW; ++b) p[u & 1][b] = mfma_x_w<WK::DT>(x[t & 1][i], wv[b][i], p[u & 1][b]);
+                    for (int b = 0; b < NBW; ++b) {
+                        if (LATE && t == 0) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
+                        p[u & 1][b] = mfma_x_w<WK::DT>(x[t & 1][i], wv[b][i], p[u & 1][b]);
+                    }
                 if (u > 0) add(u - 1);
             }
         }
@@ -301,11 +322,11 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
         }
 }
 
-template <class WK>
+template <class WK, int NBW>
 hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
-    const int64_t tm = (a.M + kTileM - 1) / kTileM, tn = ((int64_t)a.w.N + 64 * kTileBlocks<WK> - 1) / (64 * kTileBlocks<WK>);
+    const int64_t tm = (a.M + kTileM - 1) / kTileM, tn = ((int64_t)a.w.N + 64 * NBW - 1) / (64 * NBW);
     if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(w4_tile_kernel<WK>, dim3((unsigned)(tm * tn)), dim3(kTileThreads), 0, s, a, (int)tm, (int)tn);
+    hipLaunchKernelGGL((w4_tile_kernel<WK, NBW>), dim3((unsigned)(tm * tn)), dim3(kTileThreads), 0, s, a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
@@ -318,10 +339,10 @@ hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
 // four beyond, tiles once four make more than four workgroups a CU (two
 // blocks / four / tiles):
 //     N 4096 K 4096 M 64       8.7 / 10.9 /     -
-//     N 8192 K 4096 M 64      16.2 / 12.0 /  43.9
-//     N 4096 K 4096 M 256     28.9 / 22.1 /  44.4
-//     N 4096 K 4096 M 512     53.7 / 40.4 /  42.4
-//     N 4096 K 4096 M 2048       - /  160 /   101
+//     N 8192 K 4096 M 64      16.2 / 12.0 /     -
+//     N 4096 K 4096 M 256     28.9 / 22.1 /     -
+//     N 4096 K 4096 M 512     53.7 / 40.4 /     -
+//     N 4096 K 4096 M 2048       - /  160 /  80.9
 //     N 8192 K 4096 M 64, group 32 with zero points: 19.2 / 20.7 (four blocks
 //     do not fit the registers then)
 template <class WK>
@@ -330,7 +351,13 @@ hipError_t launch_kind(const W4GemmArgs &a, const char **name, hipStream_t s) {
     const int64_t mtiles = (a.M + 31) / 32;
     if (mtiles * ((nblocks + 3) / 4) > 1024) {
         *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";
-        return launch_tile<WK>(a, s);
+        if constexpr (WK::GP == 1) {
+            // (rounds over the CUs)
+            const int64_t tm = (a.M + kTileM - 1) / kTileM;
+            const int64_t t4 = tm * ((nblocks + 15) / 16), t2 = tm * ((nblocks + 7) / 8);
+            if ((t4 + 255) / 256 * 3 <= (t2 + 255) / 256 * 2) return launch_tile<WK, 4>(a, s);
+        }
+        return launch_tile<WK, 2>(a, s);
     }
     *name = WK::DT == DT_F16 ? "w4_rows_f16" : "w4_rows_bf16";
     const int waves = kbs >= 8 ? 8 : 4;

@@ -158,7 +158,7 @@ def test_product_strides_and_odd_addresses(tg, M, ldx, ldy, shift):
 
 
 @pytest.mark.parametrize("M,N,K", [(2090, 1010, 264), (33000, 33, 130), (1100, 2000, 1001), (2048, 1024, 128),
-                                   (4200, 520, 77)])
+                                   (4200, 520, 77), (4200, 1010, 264), (16700, 500, 129), (2048, 4096, 520)])
 @pytest.mark.parametrize("dtype,group,zeros,out", [("bf16", 128, False, "bf16"), ("f16", 32, True, "f32"),
                                                    ("bf16", 64, True, "f32"), ("f16", 64, False, "f16"),
                                                    ("bf16", 32, False, "f32"), ("f16", 128, True, "f32")])

@@ -261,10 +261,10 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
 // and moe_combine_kernel adds a token's: no atomics, and a result that does
 // not depend on timing.
 template <class WK, int NB, bool DIRECT>
-__global__ __launch_bounds__(256, 2) void moe_down_kernel(MoeArgs a) {
-    constexpr int W = 4;
+__global__ __launch_bounds__(256, DIRECT ? 4 : 2) void moe_down_kernel(MoeArgs a) {
+    constexpr int W = 4, ROWS = DIRECT ? 8 : 16;
     // the waves' h tiles, then their sums
-    constexpr int RED = W * NB * 256, TILES = W * RowTile<2>::LDS_BYTES / 4;
+    constexpr int RED = W * NB * 256, TILES = DIRECT ? 0 : W * RowTile<2>::LDS_BYTES / 4;
     __shared__ __attribute__((aligned(16))) float red[RED > TILES ? RED : TILES];
     const MoeChunkMeta *meta = a.meta + blockIdx.y;
     const int tiles = (a.H + 15) >> 4, groups = (tiles + NB - 1) / NB;
@@ -282,17 +282,18 @@ __global__ __launch_bounds__(256, 2) void moe_down_kernel(MoeArgs a) {
         w[b] = WStream<WK>(matrix_of<WK>(all, e, a.H, K), min(tile0 + b, tiles - 1), a.H, K, lane);
     const __amdgpu_buffer_rsrc_t rh =
         make_rsrc(static_cast<const char *>(a.h) + list * I16 * 4, (int64_t)count * I16 * 4);
-    for (int m0 = 0; m0 < count; m0 += 16) {
-        const int rows = min(count - m0, 16);
+    for (int m0 = 0; m0 < count; m0 += ROWS) {
+        const int rows = min(count - m0, ROWS);
         f32x4 acc[NB][1];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
             acc[b][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-        char *const buf = reinterpret_cast<char *>(red) + wave * RowTile<2>::LDS_BYTES;
         if constexpr (DIRECT) {
-            const int h_off[1][1] = {{(m0 + min(lane & 15, rows - 1)) * I16 * 4 + (lane >> 4) * 32}};
-            wave_products<WK, NB, 1, 2, true>(w, rh, h_off, buf, K, wave, W, lane, acc);
+            // operand row r is the high part of pair r % 8, from 8 on the low
+            const int h_off[1][1] = {{(m0 + min(lane & 7, rows - 1)) * I16 * 4 + (lane >> 4) * 32 + (lane & 8) * 2}};
+            wave_products<WK, NB, 1, 1, true, 2>(w, rh, h_off, nullptr, K, wave, W, lane, acc);
         } else {
+            char *const buf = reinterpret_cast<char *>(red) + wave * RowTile<2>::LDS_BYTES;
             int h_off[1][8];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -312,7 +313,10 @@ __global__ __launch_bounds__(256, 2) void moe_down_kernel(MoeArgs a) {
             if (n >= a.H) continue;
             float v = 0.f;
 #pragma unroll
-            for (int q = 0; q < W; ++q) v += red[(q * NB + b) * 256 + m * 16 + c];
+            for (int q = 0; q < W; ++q) {
+                v += red[(q * NB + b) * 256 + m * 16 + c];
+                if (DIRECT) v += red[(q * NB + b) * 256 + (m + 8) * 16 + c];
+            }
             a.part[(list + m0 + m) * a.H + n] = v;
         }
         __syncthreads();   // (the sums' LDS is the next rows' tiles)

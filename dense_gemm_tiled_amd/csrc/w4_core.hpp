@@ -257,20 +257,21 @@ __device__ inline u32x4 load_piece(__amdgpu_buffer_rsrc_t rx, int off, int kb, i
 }
 
 // The same block of the tile straight into operand layout; off: this lane's
-// byte offset in row lane % 16, 16 XP (lane / 16) included.
-template <int XP, bool TAIL>
+// byte offset in row lane % 16, 16 XB (lane / 16) included; XB: parts that x
+// is held in, XP: parts that are loaded.
+template <int XP, int XB, bool TAIL>
 __device__ inline void load_frags(XFrag (&x)[XP], __amdgpu_buffer_rsrc_t rx, int off, int kb, int kv, int lane) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int p = 0; p < XP; ++p) {
-            const int at = off + i * (64 * XP) + p * 16, v = kv - (i * 32 + (lane >> 4) * 8);
+            const int at = off + i * (64 * XB) + p * 16, v = kv - (i * 32 + (lane >> 4) * 8);
             if constexpr (!TAIL) {
-                x[p].v[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, kb * (256 * XP), 0);
+                x[p].v[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, kb * (256 * XB), 0);
             } else {
                 // (two parts: held in whole groups of 8, zeros past the last value)
-                x[p].v[i] = ld_chunk_tail(rx, at + kb * (256 * XP), XP == 2 && v > 0 ? 8 : v,
-                                          XP == 1 && (kv & 7) != 0);
+                x[p].v[i] = ld_chunk_tail(rx, at + kb * (256 * XB), XB == 2 && v > 0 ? 8 : v,
+                                          XB == 1 && (kv & 7) != 0);
             }
         }
 }
@@ -356,7 +357,7 @@ __device__ inline void block_mma(const XFrag (&x)[XP], const u32x4 (&w)[4], cons
 // result: where a tile was skipped by a branch, the compiler left out the
 // wait states before the reader on the other side, and the results were
 // wrong.  So MT is the number of tiles in use, and callers choose by it.
-template <class WK, int NB, int MT, int XP, bool DIRECT>
+template <class WK, int NB, int MT, int XP, bool DIRECT, int XB = XP>
 __device__ inline void wave_products(const WStream<WK> (&w)[NB], __amdgpu_buffer_rsrc_t rx,
                                      const int (&x_off)[MT][DIRECT ? 1 : RowTile<XP>::LOADS], char *buf, int K,
                                      int kb0, int step, int lane, f32x4 (&acc)[NB][MT]) {
@@ -376,7 +377,7 @@ __device__ inline void wave_products(const WStream<WK> (&w)[NB], __amdgpu_buffer
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if constexpr (DIRECT) {
-                load_frags<XP, TAIL>(s.f[t], rx, x_off[t][0], kb, kv, lane);
+                load_frags<XP, XB, TAIL>(s.f[t], rx, x_off[t][0], kb, kv, lane);
             } else {
 #pragma unroll
                 for (int q = 0; q < RowTile<XP>::LOADS; ++q)

@@ -31,14 +31,12 @@ __device__ inline void store_h(u16 *row, int i, float g, float u, int gate) {
 }
 
 // Rows m0 .. m0 + rows of an expert's list (at most 16 MT) through this
-// workgroup's 16 UT rows of its gate and up matrices; red: the waves' x
+// workgroup's 16 rows of its gate and up matrices; red: the waves' x
 // tiles, then their sums.
-constexpr int kUpWaves = 8;
-
-template <class WK, int MT, int UT, bool ONE, bool DIRECT>
-__device__ inline void up_rows(const MoeArgs &a, const WStream<WK> (&w)[2 * UT], __amdgpu_buffer_rsrc_t rx, u16 *h,
-                               const int32_t *tok, int m0, int rows, int tile0, int wave, int lane, float *red) {
-    constexpr int W = kUpWaves, NB = 2 * UT;
+template <class WK, int W, int MT, bool ONE, bool DIRECT>
+__device__ inline void up_rows(const MoeArgs &a, const WStream<WK> (&w)[2], __amdgpu_buffer_rsrc_t rx, u16 *h,
+                               const int32_t *tok, int m0, int rows, int tile, int wave, int lane, float *red) {
+    constexpr int NB = 2;
     const int tid = wave * 64 + lane, I16 = (a.I + 15) / 16 * 16;
     f32x4 acc[NB][MT];
 #pragma unroll
@@ -72,16 +70,16 @@ __device__ inline void up_rows(const MoeArgs &a, const WStream<WK> (&w)[2 * UT],
             for (int q = 0; q < 4; ++q)
                 red[(wave * NB + b) * 256 + ((lane >> 4) * 4 + q) * 16 + (lane & 15)] = acc[b][t][q];
         __syncthreads();
-        const int live = min(rows - 16 * t, 16) * 16 * UT;
-        if (tid < live) {
-            const int m = tid / (16 * UT), ut = tid / 16 % UT, c = tid & 15;
+        const int live = min(rows - 16 * t, 16) * 16;
+        for (int o = tid; o < live; o += W * 64) {
+            const int m = o >> 4, c = o & 15;
             float g = 0.f, u = 0.f;
 #pragma unroll
             for (int q = 0; q < W; ++q) {
-                g += red[(q * NB + 2 * ut) * 256 + m * 16 + c];
-                u += red[(q * NB + 2 * ut + 1) * 256 + m * 16 + c];
+                g += red[q * NB * 256 + m * 16 + c];
+                u += red[(q * NB + 1) * 256 + m * 16 + c];
             }
-            const int i = (tile0 + ut) * 16 + c;
+            const int i = tile * 16 + c;
             // (zeros from I to the next multiple of 16)
             if (i >= a.I) g = u = 0.f;
             if (i < I16) store_h<WK::DT>(h + (int64_t)(m0 + 16 * t + m) * I16 * 2, i, g, u, a.gate);
@@ -89,22 +87,25 @@ __device__ inline void up_rows(const MoeArgs &a, const WStream<WK> (&w)[2 * UT],
     }
 }
 
-// First product.  A workgroup owns 16 UT rows of one expert's gate matrix and
+// First product.  A workgroup owns 16 rows of one expert's gate matrix and
 // the same rows of its up matrix; its waves split K (= H) and add their sums
 // in LDS in wave order.  Tokens of the expert go 16 MT at a time.  ONE: the
 // only token of the layer, whose routing every workgroup makes for itself
 // (workgroups are numbered by the choice, not by the list of experts) and
-// hands on to the second product.  MT 1 is for at most 16 tokens: an expert
-// has few of them then, and x goes straight into operand layout.
-template <class WK, int MT, int UT, bool ONE>
-__global__ __launch_bounds__(512, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
-    constexpr int W = kUpWaves, NB = 2 * UT;
+// hands on to the second product.  MT 1 is for few tokens an expert: x goes
+// straight into operand layout.  4 waves: 16 tokens over 64 4-bit experts of
+// 4096 x 1408, the layer 110 us, 121 with 8 and 113 with 2; 61 tokens over 32
+// 16-bit experts of 4096 x 1400, 229, 240 and 239.  Its share there is 65 us,
+// 5.2 TB/s of weights, and 129 us, 5.7 TB/s.
+template <class WK, int W, int MT, bool ONE>
+__global__ __launch_bounds__(W * 64, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
+    constexpr int NB = 2;
     // the waves' x tiles, then their sums
     constexpr int RED = W * NB * 256, TILES = W * RowTile<1>::LDS_BYTES / 4;
     __shared__ __attribute__((aligned(16))) float red[RED > TILES ? RED : TILES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tiles = (a.I + 15) >> 4, groups = (tiles + UT - 1) / UT;
-    const int slot = blockIdx.x / groups, tile0 = (blockIdx.x - slot * groups) * UT;
+    const int tiles = (a.I + 15) >> 4;
+    const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
     const int t0 = blockIdx.y * kMoeChunk;
     int e, p0, count;
     if constexpr (ONE) {
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(512, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(
             token_choices(a.route, 0, lane, id, w);
             if (lane == slot) {
                 one = id;
-                if (tile0 == 0) {
+                if (tile == 0) {
                     a.place[slot] = id;
                     a.wgt[slot] = w;
                 }
@@ -141,8 +142,7 @@ __global__ __launch_bounds__(512, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(
     WStream<WK> w[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-        w[b] = WStream<WK>(matrix_of<WK>(all, (int64_t)e * 2 + (b & 1), a.I, K),
-                           min(tile0 + (b >> 1), tiles - 1), a.I, K, lane);
+        w[b] = WStream<WK>(matrix_of<WK>(all, (int64_t)e * 2 + b, a.I, K), tile, a.I, K, lane);
     const int64_t x_org = (int64_t)t0 * a.ldx * 2;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + x_org, a.x_bytes - x_org);
     u16 *h = static_cast<u16 *>(a.h) + list * I16 * 2;
@@ -151,9 +151,9 @@ __global__ __launch_bounds__(512, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(
     for (int m0 = 0; m0 < count; m0 += 16 * MT) {
         const int rows = min(count - m0, 16 * MT);
         if (MT == 1 || rows <= 16)
-            up_rows<WK, 1, UT, ONE, MT == 1>(a, w, rx, h, ONE ? nullptr : a.tok + list, m0, rows, tile0, wave, lane, r);
+            up_rows<WK, W, 1, ONE, MT == 1>(a, w, rx, h, ONE ? nullptr : a.tok + list, m0, rows, tile, wave, lane, r);
         else
-            up_rows<WK, MT, UT, ONE, false>(a, w, rx, h, a.tok + list, m0, rows, tile0, wave, lane, r);
+            up_rows<WK, W, MT, ONE, false>(a, w, rx, h, a.tok + list, m0, rows, tile, wave, lane, r);
         __syncthreads();   // (the sums' LDS is the next rows' tiles)
     }
 }
@@ -163,6 +163,9 @@ __global__ __launch_bounds__(512, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kernel(
 // share out the (expert, block of K) units in order, DEPTH of them in flight
 // each, weight what an expert gives, and their sums are added in wave order.
 // Straight into y: no third kernel, which would be a fifth of the time here.
+// 8 16-bit experts of 2048 x 1024: 11.4 us, 2.9 TB/s (first product 14.9 us,
+// 4.5 TB/s): with 128 workgroups half the CUs have none, and starting up and
+// the first loads' latency are most of it.
 template <class WK>
 __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
     constexpr int W = 16, DEPTH = WK::W4 ? 6 : 4;
@@ -256,7 +259,12 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
 }
 
 // Second product.  A workgroup owns 16 NB columns and one expert's pairs; its
-// waves split K (= I).  Each pair's product goes to scratch memory in fp32
+// waves split K (= I).  DIRECT, for few pairs an expert: 8 of them a pass,
+// their high parts in rows 0 - 7 of the operand and their low parts in rows 8
+// - 15, which halves the loads of h and the matrix instructions and leaves
+// registers for twice the waves (16 tokens over 64 4-bit experts of 4096 x
+// 1408: 33 us, 5.1 TB/s of weights, for 45).  Else 16 pairs a pass through LDS
+// (61 tokens over 32 16-bit experts of 4096 x 1400: 82 us, 4.5 TB/s).  Each pair's product goes to scratch memory in fp32
 // (T top_k H values, a few percent of the weights that were read for them),
 // and moe_combine_kernel adds a token's: no atomics, and a result that does
 // not depend on timing.
@@ -352,11 +360,11 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
     else static_cast<u16 *>(a.y)[o] = to16<DT>(v);
 }
 
-template <class WK, int MT, int UT, bool ONE>
+template <class WK, int W, int MT, bool ONE>
 hipError_t launch_up(const MoeArgs &a, int slots, unsigned chunks, int *launches, hipStream_t s) {
-    const int64_t grid = (int64_t)slots * (((a.I + 15) / 16 + UT - 1) / UT);
+    const int64_t grid = (int64_t)slots * ((a.I + 15) / 16);
     if (grid > 0x7FFFFFFF || chunks > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((moe_up_kernel<WK, MT, UT, ONE>), dim3((unsigned)grid, chunks), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((moe_up_kernel<WK, W, MT, ONE>), dim3((unsigned)grid, chunks), dim3(W * 64), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e == hipSuccess) ++*launches;
     return e;
@@ -378,7 +386,8 @@ template <class WK>
 hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     hipError_t e;
     if (tcg_moe_one_fits(a)) {
-        if ((e = launch_up<WK, 1, 1, true>(a, a.top_k, 1, launches, s)) != hipSuccess) return e;
+        // (8 waves: 16-bit experts of 2048 x 1024, 8 a token, 28.0 us for 28.5)
+        if ((e = launch_up<WK, WK::W4 ? 4 : 8, 1, true>(a, a.top_k, 1, launches, s)) != hipSuccess) return e;
         hipLaunchKernelGGL(moe_one_down_kernel<WK>, dim3((unsigned)((a.H + 15) / 16)), dim3(1024),
                            one_lds_bytes(a), s, a);
         e = hipGetLastError();
@@ -391,11 +400,19 @@ hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     // (as many blocks of the second product as two stages of them and of h
     // leave registers for)
     constexpr int NB = WK::GP == 1 || WK::GP == 2 ? 4 : 2;
-    if (a.T <= 16) {
-        if ((e = launch_up<WK, 1, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
+    // By the mean number of pairs an expert has.  Us per layer, direct kernels
+    // against those through LDS: 4-bit experts (64 of 4096 x 1408, 8 a token)
+    // of 24 tokens, 3 pairs an expert, 120 / 157; of 48 tokens, 6 pairs, 142 /
+    // 170; 16-bit experts (64 of 2048 x 1024, 8 a token) of 32 tokens, 4
+    // pairs, 157 / 171.  Above, with one of the two products direct (first,
+    // second) and with none: 16-bit experts (32 of 4096 x 1400, 4 a token) of
+    // 61 tokens, 7.6 pairs, 232, 239 / 229; the 4-bit ones of 128 tokens, 16
+    // pairs, 224, 216 / 212.
+    if ((int64_t)chunk * a.top_k <= 6 * (int64_t)a.E) {
+        if ((e = launch_up<WK, 4, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
         e = launch_down<WK, NB, true>(a, slots, chunks, launches, s);
     } else {
-        if ((e = launch_up<WK, 2, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
+        if ((e = launch_up<WK, 4, 2, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
         e = launch_down<WK, NB, false>(a, slots, chunks, launches, s);
     }
     if (e != hipSuccess) return e;

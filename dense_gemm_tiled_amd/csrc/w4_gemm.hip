@@ -144,7 +144,7 @@ constexpr int kTileM = 128, kTileThreads = 512;
 template <class WK, int NBW>
 __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int tiles_m, int tiles_n) {
     // (LATE: the codes are expanded between the first products)
-    constexpr bool LATE = NBW == 2 && WK::GP < 4;
+    constexpr bool LATE = false;
     constexpr int MT = 4, GP = WK::GP, S = 4 / GP, SLOT = kTileM * 256;
     __shared__ __attribute__((aligned(16))) char xbuf[3][SLOT];
     __shared__ __attribute__((aligned(16))) float xsum[2][GP][kTileM];
@@ -235,6 +235,13 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
         read_x(x, 0, wn);
         make_sums(x, 0);
     }
+    // (see above: the second half of the waves runs half a step behind)
+    auto turn = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (wm == 1) turn();
     int slot = 0;
 #pragma unroll 1
     for (int s = 0; s < kbs; ++s) {
@@ -261,6 +268,7 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
             zc[b] = f[b].z;
         }
         if (!LATE) load_codes(s + 1);
+        turn();
         f32x4 p[2][NBW];
         // (group u of the step's MT * GP) its products, scaled and added
         auto add = [&](int u) {
@@ -309,6 +317,7 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
         add(MT * GP - 1);
         slot = next;
     }
+    if (wm == 0) turn();
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll

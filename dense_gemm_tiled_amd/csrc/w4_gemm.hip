@@ -143,8 +143,6 @@ constexpr int kTileM = 128, kTileThreads = 512;
 
 template <class WK, int NBW>
 __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int tiles_m, int tiles_n) {
-    // (LATE: the codes are expanded between the first products)
-    constexpr bool LATE = false;
     constexpr int MT = 4, GP = WK::GP, S = 4 / GP, SLOT = kTileM * 256;
     __shared__ __attribute__((aligned(16))) char xbuf[3][SLOT];
     __shared__ __attribute__((aligned(16))) float xsum[2][GP][kTileM];
@@ -191,11 +189,13 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
             *reinterpret_cast<u32x4 *>(&xbuf[slot][wave * 4096 + u * 1024 + lane * 16]) = v[u];
     };
     const int rl = wm * 64 + (lane & 15), kq = lane >> 4;
+    // piece 4 i + kq of row r is at (4 i + kq) ^ (r % 16) = (4 i) ^ (kq ^ r % 16)
+    const u32 x_at = rl * 256 + ((kq ^ (rl & 15)) << 4);
     auto read_x = [&](u32x4 (&x)[4], int slot, int t) {
+        const u32 at = x_at + slot * SLOT;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const u32x4 *>(
-                &xbuf[slot][(rl + 16 * t) * 256 + (((i * 4 + kq) ^ (rl & 15)) << 4)]);
+            x[i] = *reinterpret_cast<const u32x4 *>(&xbuf[0][0] + (at ^ (i * 64)) + t * 4096);
     };
     // sums of block s for the rows of tile wn of this half
     auto make_sums = [&](const u32x4 (&x)[4], int s) {
@@ -247,7 +247,6 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
     for (int s = 0; s < kbs; ++s) {
         const int next = slot == 2 ? 0 : slot + 1, after = 3 - slot - next;
         barrier();
-        stage(s + 2, after);
         u32x4 x[2][4];
         f32x4 xs[2][GP];
         auto read_tile = [&](int t) {
@@ -262,12 +261,21 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
 #pragma unroll
         for (int b = 0; b < NBW; ++b) {
 #pragma unroll
-            for (int i = 0; i < 4 && !LATE; ++i) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
+            for (int i = 0; i < 4; ++i) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
             sc[b][0] = f[b].s[0];
             if (GP == 4) sc[b][GP == 4 ? 1 : 0] = f[b].s[GP == 4 ? 1 : 0];
-            zc[b] = f[b].z;
+            asm volatile("" : "+v"(sc[b][0]));
+            if (GP == 4) asm volatile("" : "+v"(sc[b][GP == 4 ? 1 : 0]));
+            if (WK::ZP) {
+                zc[b] = GP == 1 ? as_u32(-16.f - (float)(f[b].z & 15)) : f[b].z;
+                asm volatile("" : "+v"(zc[b]));
+            }
         }
-        if (!LATE) load_codes(s + 1);
+        // (behind the expansion: the compiler's waits for the codes count only
+        // its own loads and would wait for these as well)
+        __builtin_amdgcn_sched_barrier(0);
+        stage(s + 2, after);
+        load_codes(s + 1);
         turn();
         f32x4 p[2][NBW];
         // (group u of the step's MT * GP) its products, scaled and added
@@ -291,7 +299,6 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
             if (t + 1 == MT) read_x(x[MT & 1], next, wn);
             __builtin_amdgcn_sched_barrier(0);
             if (t == MT) break;
-            if (LATE && t == 1) load_codes(s + 1);
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const int u = t * GP + g;
@@ -301,15 +308,13 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
 #pragma unroll
                 for (int b = 0; b < NBW; ++b) {
                     p[u & 1][b] = xs[t & 1][g];
-                    if constexpr (WK::ZP) p[u & 1][b] *= -16.f - (float)((zc[b] >> (8 * g)) & 15);
+                    if constexpr (WK::ZP)
+                        p[u & 1][b] *= GP == 1 ? as_f32(zc[b]) : -16.f - (float)((zc[b] >> (8 * g)) & 15);
                 }
 #pragma unroll
                 for (int i = g * S; i < (g + 1) * S; ++i)
 #pragma unroll
-                    for (int b = 0; b < NBW; ++b) {
-                        if (LATE && t == 0) wv[b][i] = w4_expand<WK::DT>(f[b].q[0][i]);
-                        p[u & 1][b] = mfma_x_w<WK::DT>(x[t & 1][i], wv[b][i], p[u & 1][b]);
-                    }
+                    for (int b = 0; b < NBW; ++b) p[u & 1][b] = mfma_x_w<WK::DT>(x[t & 1][i], wv[b][i], p[u & 1][b]);
                 if (u > 0) add(u - 1);
             }
         }

@@ -32,7 +32,11 @@ __device__ inline void finish(const W4GemmArgs &a, int m, int n, float v) {
 // themselves, block by block, so that even a matrix of few rows has many
 // loads in flight, and add their sums in LDS in wave order.  A wave reads
 // 1024 contiguous bytes of codes per block straight into operand layout, and
-// the x of its own blocks, which no other wave needs.
+// the x of its own blocks, which no other wave needs.  One row by 4096x4096,
+// bf16, group 128, takes 4.4 us (1.9 TB/s of codes: starting up and the first
+// loads' latency are most of it), 4 rows by 16384x8192 in fp16 13.3 us (5.0 TB/s
+// of codes), 64 rows by 8192x4096 with groups of 64 and zero points 14.3:
+// there the CUs together read x and W several times from L2.
 template <class WK, int NB, int MT>
 __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a) {
     // [waves][NB][16][16] sums at the end, before them the waves' x tiles
@@ -122,23 +126,29 @@ hipError_t launch_rows(const W4GemmArgs &a, int waves, hipStream_t s) {
 // the first addend of the group's products, so with symmetric codes the
 // offset costs no instruction per result.
 //
+// Each SIMD has one wave of either half of the rows.  The second half runs
+// half a step behind: one expands its codes while the other multiplies, with
+// a barrier at each change (2048 rows by 4096x4096, fp16, group 128 with zero
+// points: 97.3 -> 82.2 us), and the wave that multiplies issues first (1024
+// rows by 4096x4096, bf16, group 128: 49.6 -> 47.6).
+//
 // NBW: with a group of 128, 4 blocks of weight rows a wave are as many as the
-// 256 registers of two waves a SIMD hold, and 2048 rows by 4096x4096 take 80.9
-// us (850 TFLOP/s; 33 us at the rate of a large matrix product in 16 bits,
+// 256 registers of two waves a SIMD hold, and 2048 rows by 4096x4096 take 75.4
+// us (912 TFLOP/s; 49 us at the rate of a large matrix product in 16 bits,
 // 101.8 with 128x64 tiles of 4 waves and x through registers).  A round of
 // 128x256 tiles over the CUs is worth 1.5 of 128x128, so the smaller ones are
 // taken where they need less than 1.5 times the rounds (1024 rows by
-// 4096x4096: 72 / 55 us; 256 rows by 16384x4096: 74 / 56).  Smaller groups
-// hold more scales and sums and have 2 blocks only: 2048 rows by 4096x4096
-// take 116 us with groups of 64, 160 with groups of 32 and zero points (a
-// multiplication per result and group comes on top).
+// 4096x4096: 72 / 55 us, 256 rows by 16384x4096: 74 / 56, before the halves
+// were set apart; 47.6 and 48.6 since).  Smaller groups hold more scales and
+// sums and have 2 blocks only: 2048 rows by 4096x4096 take 102 us with groups
+// of 64, 149 with groups of 32 and zero points (a multiplication per result
+// and group comes on top).
 //
-// What bounds it: every wave's 64 matrix instructions a step take a quarter to
-// a half of the step, expanding and scaling on the VALU about as much again,
-// and with two waves a SIMD in step with each other the two overlap in part
-// only.  Expanding between the first products instead of before them is faster
-// with 2 blocks (groups of 64: 127 -> 116 us) and slower with 4 (80.9 -> 86.8:
-// the next codes are then loaded later).
+// What bounds it: the matrix units are busy two fifths of the time (counters:
+// 2180 of 5600 cycles a step, no bank conflict in LDS).  The rest is the
+// scaling on the VALU between them, one fused multiply-add per result and
+// group, and the reads of x from LDS, which run one tile of 16 rows ahead
+// because registers for two are not there.
 constexpr int kTileM = 128, kTileThreads = 512;
 
 template <class WK, int NBW>
@@ -277,6 +287,7 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
         stage(s + 2, after);
         load_codes(s + 1);
         turn();
+        __builtin_amdgcn_s_setprio(1);
         f32x4 p[2][NBW];
         // (group u of the step's MT * GP) its products, scaled and added
         auto add = [&](int u) {
@@ -320,6 +331,7 @@ __global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(W4GemmArgs a, int
         }
         make_sums(x[MT & 1], s + 1);
         add(MT * GP - 1);
+        __builtin_amdgcn_s_setprio(0);
         slot = next;
     }
     if (wm == 0) turn();
@@ -356,7 +368,7 @@ hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
 //     N 8192 K 4096 M 64      16.2 / 12.0 /     -
 //     N 4096 K 4096 M 256     28.9 / 22.1 /     -
 //     N 4096 K 4096 M 512     53.7 / 40.4 /     -
-//     N 4096 K 4096 M 2048       - /  160 /  80.9
+//     N 4096 K 4096 M 2048       - /  160 /  75.4
 //     N 8192 K 4096 M 64, group 32 with zero points: 19.2 / 20.7 (four blocks
 //     do not fit the registers then)
 template <class WK>

@@ -271,10 +271,10 @@ tc_status_t tc_qweight_sizes(const tc_qweight_desc *d, int64_t *codes, int64_t *
  *     with zeros     hi = max(hi, 0), lo = min(lo, 0), s = (hi - lo) * (1/15),
  *                    z = clamp(rint(-lo / s), 0, 15),
  *                    q = clamp(rint(w / s) + z, 0, 15).
- * s is computed in fp32 (1/15 its nearest number) and rounded to scale_dtype (its largest finite number
- * where it overflows); the quotients go by that s and are rounded as exact
- * ones are, ties to even.  A group whose s is 0 stands for zeros, one that
- * holds a NaN or infinity gets a NaN scale. */
+ * s is computed in fp32 (1/15 its nearest number) and rounded to scale_dtype
+ * (its largest finite number where it overflows); the quotients go by that s
+ * and are rounded as exact ones are, ties to even.  A group whose s is 0
+ * stands for zeros, one that holds a NaN or infinity gets a NaN scale. */
 tc_status_t tc_quantize_async(tc_context *ctx, const tc_qweight_desc *d, const void *W,
                               tc_dtype_t w_dtype, int64_t ldw, int64_t stride_w,
                               const tc_qweight *out, tc_stream *s);
@@ -295,7 +295,7 @@ tc_status_t tc_qweight_pack_async(tc_context *ctx, const tc_qweight_desc *d,
  * layer whose weight (d, w; batch 1) is held in 4 bits, for one row of x or
  * for many.  x has the type of the scales, y that type or f32; ep may be NULL
  * and holds no col_scale.  fp32 sums, y written once.  A row of x that holds
- * a NaN or infinity gives NaN.  No workspace. */
+ * a NaN or infinity gives NaN (before the activation).  No workspace. */
 typedef struct {
     int32_t M;
     tc_dtype_t x_dtype, y_dtype;

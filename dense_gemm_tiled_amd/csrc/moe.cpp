@@ -25,6 +25,8 @@ tc_status_t check_route(const tc_route_desc *r, RouteArgs *a, int64_t *bytes, st
         return fail(err, TC_ERR_UNSUPPORTED, "logits must be f32, f16 or bf16 (got %s)", dt_name(r->dtype));
     if (!std::isfinite(r->scale))
         return fail(err, TC_ERR_INVALID_ARGUMENT, "scale must be finite");
+    if ((r->T + 3LL) / 4 > kMaxGroups)
+        return fail(err, TC_ERR_OVERFLOW, "T=%d > %lld", r->T, (long long)kMaxGroups * 4);
     memset(a, 0, sizeof *a);
     a->ld = r->ld == 0 ? r->E : r->ld;
     if (a->ld < r->E)
@@ -66,11 +68,9 @@ tc_status_t check_moe(const tc_moe_desc *d, MoeSpace *sp, std::string *err) {
         return fail(err, TC_ERR_OVERFLOW, "T=%d > %d", d->T, 65535 * kMoeChunk);
     if (d->H > kMaxRowElems || d->I > kMaxRowElems)
         return fail(err, TC_ERR_OVERFLOW, "H=%d or I=%d > %d", d->H, d->I, kMaxRowElems);
-    if ((int64_t)d->E * ((d->I + 15) / 16) > 0x7FFFFFFF)
-        return fail(err, TC_ERR_OVERFLOW, "E * I / 16 > 2^31-1");
-    if ((int64_t)d->T * ((d->H + 255) / 256) > 0x7FFFFFFF ||
-        (int64_t)d->E * ((d->H + 15) / 16) > 0x7FFFFFFF)
-        return fail(err, TC_ERR_OVERFLOW, "T * H / 256 or E * H / 16 > 2^31-1");
+    if ((int64_t)d->E * ((d->I + 15) / 16) > kMaxGroups || (int64_t)d->E * ((d->H + 15) / 16) > kMaxGroups ||
+        (int64_t)d->T * ((d->H + 255) / 256) > kMaxGroups)
+        return fail(err, TC_ERR_OVERFLOW, "E * I / 16, E * H / 16 or T * H / 256 > %lld", (long long)kMaxGroups);
     // T <= 2^23, top_k <= 2^4, I <= 2^22: no product below wraps
     const int64_t chunks = (d->T + kMoeChunk - 1) / kMoeChunk, pairs = (int64_t)d->T * d->top_k;
     const int64_t I16 = up_to(d->I, 16);

@@ -24,8 +24,9 @@ tc_status_t check_qweight(const tc_qweight_desc *d, QWeightSizes *out, std::stri
     const int64_t rows = (((int64_t)d->N + 15) / 16) * d->batch, kbs = ((int64_t)d->K + 127) / 128;
     const int64_t blocks = rows * kbs;
     // (the conversions give four blocks of a row to a workgroup)
-    if (rows > 0x7FFFFFFF || rows * ((kbs + 3) / 4) > 0x7FFFFFFF)
-        return fail(err, TC_ERR_OVERFLOW, "the matrices hold more than 2^31-1 groups of 16 x 512");
+    if (rows * ((kbs + 3) / 4) > kMaxGroups)
+        return fail(err, TC_ERR_OVERFLOW, "the matrices hold more than %lld groups of 16 x 512",
+                    (long long)kMaxGroups);
     out->codes = blocks * 1024;
     out->scales = blocks * 16 * (128 / d->group) * 2;
     out->zeros = d->has_zeros ? blocks * 16 * (128 / d->group) : 0;
@@ -239,6 +240,10 @@ tc_status_t tc_qgemm_async(tc_context *ctx, const tc_qgemm_desc *g, const tc_qwe
         return fail(err, TC_ERR_OVERFLOW, "ldx=%lld > %d", (long long)a.ldx, kMaxRowElems);
     if (g->M > 65535 * 16)
         return fail(err, TC_ERR_OVERFLOW, "M=%d > %d", g->M, 65535 * 16);
+    // (tiles of 128 x 128, 512 threads each)
+    if ((int64_t)((g->M + 127) / 128) * ((d->N + 127LL) / 128) > kMaxGroups / 2)
+        return fail(err, TC_ERR_OVERFLOW, "M=%d by N=%d has more than %lld tiles of 128 x 128", g->M, d->N,
+                    (long long)kMaxGroups / 2);
     // (M, ld < 2^31: the spans fit 64 bits)
     a.x_bytes = span(g->M, d->K, a.ldx) * 2;
     const int es = dt_size(g->y_dtype);

@@ -10,6 +10,9 @@ namespace tcg {
 // The longest row and the most rows the kernels' 32-bit offsets inside a
 // block of rows allow (8 MiB of 16-bit values, as for the dense operands).
 constexpr int32_t kMaxRowElems = (1 << 22) - 64;
+// Workgroups of 256 threads a launch may have (its threads fit 32 bits), less
+// a few so that half as many of 512 stay below as well.
+constexpr int64_t kMaxGroups = (1 << 24) - 16;
 
 struct QWeightSizes {
     int64_t codes, scales, zeros;

@@ -155,6 +155,11 @@ BAD_MOE = [("T", dict(T=0), 1), ("H", dict(H=0), 1), ("I", dict(I=-4), 1), ("E",
            ("H long", dict(H=1 << 22), 3), ("I long", dict(I=1 << 22), 3)]
 
 
+# launches whose threads would not fit 32 bits
+BAD_MOE += [("T by H", dict(T=1 << 20, H=4352), 3), ("E by I", dict(E=512, I=1 << 20), 3),
+            ("E by H", dict(E=512, H=1 << 20), 3)]
+
+
 @pytest.mark.parametrize("name,kw,status", BAD_MOE, ids=[b[0] for b in BAD_MOE])
 def test_bad_layer(lib, ctx, name, kw, status):
     d, n, w = mdesc(**kw), ctypes.c_int64(), tg.QWeightT(P[0], None, None)
@@ -205,3 +210,20 @@ def test_python_refusals_without_a_gpu():
               lambda: tg.w4_gemm(x, (x, x), y), lambda: tg.w4_pack(x, x), lambda: tg.moe(x, y, x, x, y)):
         with pytest.raises(tg.TcGemmError):
             f()
+
+
+def test_grids_past_32_bits(lib, ctx):
+    """Refused before anything is launched; at the limit (2^24 - 16 workgroups
+    of 256 threads: 16 (2^20 - 1) for T and H here) the host's
+    checks pass (sizes only, no launch)."""
+    n = ctypes.c_int64()
+    assert lib.tc_moe_workspace(ctypes.byref(mdesc(T=(1 << 20) - 1, H=4080)), ctypes.byref(n)) == 0
+    r = rdesc(T=1 << 27)
+    assert lib.tc_moe_route_async(ctx, ctypes.byref(r), P[0], P[1], P[2], P[9]) == 3
+    d = wdesc(N=1 << 28, K=16)
+    assert lib.tc_qweight_sizes(ctypes.byref(d), None, None, None) == 3
+    d = wdesc(N=(1 << 28) - 256, K=16)
+    assert lib.tc_qweight_sizes(ctypes.byref(d), None, None, None) == 0
+    d, w = wdesc(N=1 << 18, K=16), weight()
+    g = tg.QGemmDescT(65535 * 16, d.scale_dtype, d.scale_dtype, 1.0, 0.0, 0, 0)
+    assert lib.tc_qgemm_async(ctx, ctypes.byref(g), ctypes.byref(d), P[3], ctypes.byref(w), P[4], None, P[9]) == 3

@@ -135,6 +135,18 @@ def test_every_token_to_one_expert(tg, held, T):
     run_layer(tg, T, 136, 64, 8, 2, "bf16", held, logits=l)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("held", [None, (128, False), (64, True), (32, True)])
+@pytest.mark.parametrize("T", [9, 17, 128, 150])
+def test_few_of_many_experts(tg, dtype, held, T):
+    """Many experts, nearly all tokens to the same two: the kernels that are
+    chosen for few pairs an expert go through their list in many passes."""
+    l = rand(torch.Generator().manual_seed(T), T, 150)
+    l[:, 7] += 30
+    l[: T - 3, 149] += 20
+    run_layer(tg, T, 140, 33, 150, 2, dtype, held, logits=l, seed=T)
+
+
 def test_tokens_without_experts(tg):
     """A padded batch: tokens whose mask leaves no expert get zeros, even
     where x is NaN; a batch of nothing but those too."""

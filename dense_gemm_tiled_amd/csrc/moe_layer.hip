@@ -163,16 +163,20 @@ __global__ __launch_bounds__(W * 64, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kern
 // share out the (expert, block of K) units in order, DEPTH of them in flight
 // each, weight what an expert gives, and their sums are added in wave order.
 // Straight into y: no third kernel, which would be a fifth of the time here.
-// 8 16-bit experts of 2048 x 1024: 11.4 us, 2.9 TB/s (first product 14.9 us,
-// 4.5 TB/s): with 128 workgroups half the CUs have none, and starting up and
-// the first loads' latency are most of it.
-template <class WK>
+// HALF, where that would leave half the CUs without a workgroup: 8 columns,
+// and two blocks of K at a time.  Columns 0 - 7 of the right operand are the
+// weights of the first block, 8 - 15 of the second; even rows of the left one
+// are h of the first, odd rows of the second, so row 0 and row 1 of the result
+// hold the two products.  8 16-bit experts of 2048 x 1024: the layer
+// 25.5 us for 28.2, of which the first product is 14.9, 4.5 TB/s.
+template <class WK, bool HALF>
 __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
-    constexpr int W = 16, DEPTH = WK::W4 ? 6 : 4;
+    constexpr int W = 16, DEPTH = WK::W4 ? 6 : 4, KB = HALF ? 2 : 1, COLS = HALF ? 8 : 16;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int K = a.I, kbs = (K + kBlkK - 1) / kBlkK, I16 = (a.I + 15) / 16 * 16;
-    const int row = kbs * kBlkK * 4;                 // bytes of h per expert in LDS
+    const int K = a.I, I16 = (a.I + 15) / 16 * 16;
+    const int kbs = (K + KB * kBlkK - 1) / (KB * kBlkK);   // steps of KB blocks
+    const int row = kbs * KB * kBlkK * 4;            // bytes of h per expert in LDS
     float *red = reinterpret_cast<float *>(lds + a.top_k * row);
     __shared__ int expert[kMaxTopK], choice[kMaxTopK];
     __shared__ float weight[kMaxTopK];
@@ -192,12 +196,14 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
     const int units = n * kbs;
     const int u0 = units * wave / W, u1 = units * (wave + 1) / W;
     WFrag<WK> f[DEPTH];
+    // (whose share of the 16 rows this lane loads)
+    const int wl = HALF ? (lane & 48) + (blockIdx.x & 1) * 8 + (lane & 7) + (lane & 8) * 8 : lane;
     auto fetch = [&](WFrag<WK> &s, int u) {
-        const int j = u / kbs, kb = u - j * kbs;
+        const int j = u / kbs, kb = (u - j * kbs) * KB;
         const int e = __builtin_amdgcn_readfirstlane(expert[j]);
-        const WStream<WK> w(matrix_of<WK>(all, e, a.H, K), blockIdx.x, a.H, K, lane);
-        if (K - kb * kBlkK < kBlkK) w.template load<true>(s, kb, K - kb * kBlkK, lane);
-        else w.template load<false>(s, kb, kBlkK, lane);
+        const WStream<WK> w(matrix_of<WK>(all, e, a.H, K), blockIdx.x / KB, a.H, K, wl);
+        if (K - kb * kBlkK < KB * kBlkK) w.template load<true>(s, kb, K - kb * kBlkK, wl);
+        else w.template load<false>(s, kb, KB * kBlkK, wl);
     };
     // h (few, and read by everyone) into LDS first: loads return in order
     for (int i = tid; i < n * (row / 16); i += W * 64) {
@@ -215,7 +221,7 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
     float total = 0.f;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     auto compute = [&](const WFrag<WK> &s, int u) {
-        const int j = u / kbs, kb = u - j * kbs;
+        const int j = u / kbs, kb = (u - j * kbs) * KB + (HALF ? lane & 1 : 0);
         XFrag x[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -231,9 +237,9 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
             if constexpr (WK::W4) wv[i] = w4_expand<WK::DT>(s.q[0][i]);
             else wv[i] = s.q[i];
         block_mma<WK, 2>(x, wv, s, zsum, acc);
-        if (kb + 1 == kbs || u + 1 == u1) {
+        if ((u + 1) % kbs == 0 || u + 1 == u1) {
             // (all rows of the fragment are the token's)
-            total = __builtin_fmaf(weight[j], acc[0], total);
+            total = __builtin_fmaf(weight[j], HALF && (lane & 8) ? acc[1] : acc[0], total);
             acc = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     };
@@ -248,11 +254,14 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
     }
     if (lane < 16) red[wave * 16 + lane] = total;
     __syncthreads();
-    const int c = blockIdx.x * 16 + tid;
-    if (tid < 16 && c < a.H) {
+    const int c = blockIdx.x * COLS + tid;
+    if (tid < COLS && c < a.H) {
         float v = 0.f;
 #pragma unroll
-        for (int q = 0; q < W; ++q) v += red[q * 16 + tid];
+        for (int q = 0; q < W; ++q) {
+            v += red[q * 16 + tid];
+            if (HALF) v += red[q * 16 + tid + 8];
+        }
         if (a.y_dtype == DT_F32) static_cast<float *>(a.y)[c] = v;
         else static_cast<u16 *>(a.y)[c] = to16<WK::DT>(v);
     }
@@ -380,16 +389,27 @@ hipError_t launch_down(const MoeArgs &a, int slots, unsigned chunks, int *launch
     return e;
 }
 
-int one_lds_bytes(const MoeArgs &a) { return a.top_k * ((a.I + kBlkK - 1) / kBlkK * kBlkK * 4) + 16 * 16 * 4; }
+// (128 workgroups of 16 columns are half the CUs)
+bool one_half(const MoeArgs &a) { return (a.H + 15) / 16 <= 128; }
+
+int one_lds_bytes(const MoeArgs &a) {
+    const int step = one_half(a) ? 2 * kBlkK : kBlkK;
+    return a.top_k * ((a.I + step - 1) / step * step * 4) + 16 * 16 * 4;
+}
 
 template <class WK>
 hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     hipError_t e;
     if (tcg_moe_one_fits(a)) {
-        // (8 waves: 16-bit experts of 2048 x 1024, 8 a token, 28.0 us for 28.5)
+        // (8 waves: 16-bit experts of 2048 x 1024, 8 a token, the layer 28.0 us
+        // for 28.5 with 4, before the second product's columns were halved)
         if ((e = launch_up<WK, WK::W4 ? 4 : 8, 1, true>(a, a.top_k, 1, launches, s)) != hipSuccess) return e;
-        hipLaunchKernelGGL(moe_one_down_kernel<WK>, dim3((unsigned)((a.H + 15) / 16)), dim3(1024),
-                           one_lds_bytes(a), s, a);
+        if (one_half(a))
+            hipLaunchKernelGGL((moe_one_down_kernel<WK, true>), dim3((unsigned)((a.H + 7) / 8)), dim3(1024),
+                               one_lds_bytes(a), s, a);
+        else
+            hipLaunchKernelGGL((moe_one_down_kernel<WK, false>), dim3((unsigned)((a.H + 15) / 16)), dim3(1024),
+                               one_lds_bytes(a), s, a);
         e = hipGetLastError();
         if (e == hipSuccess) ++*launches;
         return e;

@@ -150,7 +150,9 @@ struct WFrag {
     u32 z;                         // GP zero points, a byte each
 };
 
-// The 16 weight rows from 16 nb on, as a stream of blocks along K.
+// The 16 weight rows from 16 nb on, as a stream of blocks along K.  lane says
+// whose share is loaded, not necessarily the caller's: lane + 64 is the same
+// share of the next block (whole blocks past K load as zeros, with TAIL).
 template <class WK>
 struct WStream {
     __amdgpu_buffer_rsrc_t codes, scales, zeros;   // W4: these rows' blocks
@@ -167,11 +169,11 @@ struct WStream {
             scales = make_rsrc(m.scales + b * (16 * WK::GP * 2), (int64_t)kbs * (16 * WK::GP * 2));
             if (WK::ZP) zeros = make_rsrc(m.zeros + b * (16 * WK::GP), (int64_t)kbs * (16 * WK::GP));
         } else {
-            const int r = lane & 15, kq = lane >> 4;
+            const int r = lane & 15, kq = (lane >> 4) & 3;
             // rows past N lie past the range and read as zero
             const int64_t first = (int64_t)nb * kBlkN;
             rows = make_rsrc(m.codes + first * K * 2, (N - first) * K * 2);
-            row_off = r * K * 2 + kq * 16;
+            row_off = r * K * 2 + kq * 16 + (lane >> 6) * (kBlkK * 2);
         }
     }
 
@@ -180,7 +182,7 @@ struct WStream {
     __device__ inline void load(WFrag<WK> &f, int kb, int kv, int lane) const {
         if constexpr (WK::W4) {
             // (lane part in a register, block part in a scalar one)
-            const int r = lane & 15;
+            const int r = (lane & 15) + (lane >> 6) * 16;
             f.q[0] = __builtin_amdgcn_raw_buffer_load_b128(codes, lane * 16, kb * kBlkBytes, 0);
             const int so = r * (WK::GP * 2), sb = kb * (16 * WK::GP * 2);
             if constexpr (WK::GP == 4) {
@@ -204,7 +206,7 @@ struct WStream {
                 constexpr int G = kBlkK / (WK::GP ? WK::GP : 1);
 #pragma unroll
                 for (int g = 1; g < WK::GP; ++g)
-                    if (g * G >= kv) f.s[g >> 1] &= (g & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                    if (g * G >= kv - (lane >> 6) * kBlkK) f.s[g >> 1] &= (g & 1) ? 0x0000FFFFu : 0xFFFF0000u;
             }
         } else {
             const int off = row_off + kb * (kBlkK * 2);
@@ -212,7 +214,7 @@ struct WStream {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f.q[i] = ld128(rows, off + i * 64);
             } else {
-                const int k0 = (lane >> 4) * 8;
+                const int k0 = ((lane >> 4) & 3) * 8 + (lane >> 6) * kBlkK;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     f.q[i] = ld_chunk_tail(rows, off + i * 64, kv - (k0 + i * 32), (K & 7) != 0);

@@ -147,6 +147,14 @@ def test_few_of_many_experts(tg, dtype, held, T):
     run_layer(tg, T, 140, 33, 150, 2, dtype, held, logits=l, seed=T)
 
 
+@pytest.mark.parametrize("held,dtype", [(h, ("f16", "bf16")[i % 2]) for i, h in enumerate(HELD)])
+@pytest.mark.parametrize("H,I,E,k", [(9, 130, 5, 3), (24, 385, 4, 2), (100, 128, 3, 3), (2048, 257, 4, 2),
+                                     (2049, 200, 4, 2), (2500, 640, 9, 8)])
+def test_one_token(tg, H, I, E, k, held, dtype):
+    """Both widths of the second product, whole and odd numbers of blocks."""
+    run_layer(tg, 1, H, I, E, k, dtype, held, out="f32", seed=H + I)
+
+
 def test_tokens_without_experts(tg):
     """A padded batch: tokens whose mask leaves no expert get zeros, even
     where x is NaN; a batch of nothing but those too."""

@@ -518,19 +518,30 @@ def _w4_empty(lead, N: int, K: int, group: int, zeros: bool, scale_dtype, device
                     torch.empty(shape, dtype=torch.uint8, device=device) if zeros else None)
 
 
+def _pitch(t, name: str) -> int:
+    """_ld of a tensor whose rows are apart: 0, which a broadcast tensor has,
+    means contiguous to the library."""
+    ld = _ld(t)
+    if ld == 0 and t.size(-2) > 1:
+        raise TcGemmError(1, "the rows of %s must not be broadcast" % name)
+    return ld
+
+
 def _dense_batch(t, name: str):
     """(leading shape, N, K, row pitch, matrix stride) of a [.., N, K] tensor
     whose matrices are evenly spaced."""
     if t.dim() < 2:
         raise TcGemmError(1, "%s must have at least 2 dimensions" % name)
     lead, N, K = tuple(t.shape[:-2]), int(t.size(-2)), int(t.size(-1))
-    ld = _ld(t)
+    ld = _pitch(t, name)
     stride, expect = 0, None
     for d in range(len(lead) - 1, -1, -1):
         if lead[d] == 1:
             continue
         if expect is None:
             stride = int(t.stride(d))
+            if stride == 0:
+                raise TcGemmError(1, "the matrices of %s must not be broadcast" % name)
         elif int(t.stride(d)) != expect:
             raise TcGemmError(1, "the matrices of %s must be evenly spaced" % name)
         expect = int(t.stride(d)) * lead[d]
@@ -616,7 +627,7 @@ def _make_qgemm(x, w, y, alpha, beta):
                           % (tuple(x.shape), tuple(y.shape)))
     wd = _w4_desc(w, int(y.size(1)), int(x.size(1)))
     g = QGemmDescT(int(x.size(0)), _dtype_code(x), _dtype_code(y), float(alpha), float(beta),
-                   _ld(x), _ld(y))
+                   _pitch(x, "x"), _pitch(y, "y"))
     return g, wd, ctypes.byref(g), ctypes.byref(wd)
 
 
@@ -628,6 +639,8 @@ def w4_gemm(x, w, y, *, alpha: float = 1.0, beta: float = 0.0, bias=None,
     or "gelu_tanh".  Runs on torch's current stream (or `stream`), needs no
     workspace.  Returns y."""
     codes, scales, zeros = w = _as_w4(w)
+    # (numbers: a tensor as a key would keep the value of its first call)
+    alpha, beta = float(alpha), float(beta)
     device = y.get_device()
     if (device < 0 or x.get_device() != device or codes.get_device() != device
             or scales.get_device() != device
@@ -658,7 +671,7 @@ def _make_route(logits, top_k, renormalize, scale):
     if logits.dim() != 2:
         raise TcGemmError(1, "logits must be [T, E] (got %s)" % (tuple(logits.shape),))
     r = RouteDescT(int(logits.size(0)), int(logits.size(1)), int(top_k), _dtype_code(logits),
-                   _ld(logits), bool(renormalize), float(scale))
+                   _pitch(logits, "the logits"), bool(renormalize), float(scale))
     return r, ctypes.byref(r)
 
 
@@ -672,6 +685,7 @@ def moe_route(logits, top_k: int, *, renormalize: bool = True, scale: float = 1.
     device = _same_device(logits)
     if not (isinstance(top_k, int) and top_k >= 1):
         raise TcGemmError(1, "top_k must be a whole number >= 1 (got %r)" % (top_k,))
+    renormalize, scale = bool(renormalize), float(scale)
     key = ("route", logits.shape, logits.stride(), logits.dtype, top_k, renormalize, scale)
     d, r = _cached(key, lambda: _make_route(logits, top_k, renormalize, scale))
     lib = _lib if _lib is not None else load_library()
@@ -742,7 +756,7 @@ def _make_moe(x, route, gate_up, down, y, top_k, activation, renormalize, scale,
         if tuple(route.shape) != (T, E):
             raise TcGemmError(1, "logits must be [T, E] = %s (got %s)" % ((T, E), tuple(route.shape)))
         r, rref = _make_route(route, k, renormalize, scale)
-    d = MoeDescT(T, H, I, E, k, _dtype_code(x), _dtype_code(y), _ld(x), _ld(y), GATES[activation],
+    d = MoeDescT(T, H, I, E, k, _dtype_code(x), _dtype_code(y), _pitch(x, "x"), _pitch(y, "y"), GATES[activation],
                  group, zeros)
     need = ctypes.c_int64()
     st = load_library().tc_moe_workspace(ctypes.byref(d), ctypes.byref(need))
@@ -783,6 +797,9 @@ def moe(x, route, gate_up, down, y, *, top_k: Optional[int] = None, activation: 
             raise TcGemmError(1, "route must be logits or (ids, weights)")
         route = given
     device = _same_device(y, x, *given, *held)
+    renormalize, scale = bool(renormalize), float(scale)
+    top_k = None if top_k is None else int(top_k)
+    intermediate = None if intermediate is None else int(intermediate)
     key = ("moe", x.shape, x.stride(), x.dtype, y.shape, y.stride(), y.dtype,
            tuple((g.shape, g.stride(), g.dtype) for g in given), _weights_key(gate_up),
            _weights_key(down), top_k, activation, renormalize, scale, intermediate)

@@ -3,6 +3,7 @@ sizes, and every refusal with its status, before anything is enqueued."""
 import ctypes
 
 import pytest
+import torch
 
 import dense_gemm_tiled_amd as tg
 
@@ -227,3 +228,22 @@ def test_grids_past_32_bits(lib, ctx):
     d, w = wdesc(N=1 << 18, K=16), weight()
     g = tg.QGemmDescT(65535 * 16, d.scale_dtype, d.scale_dtype, 1.0, 0.0, 0, 0)
     assert lib.tc_qgemm_async(ctx, ctypes.byref(g), ctypes.byref(d), P[3], ctypes.byref(w), P[4], None, P[9]) == 3
+
+
+def test_broadcast_operands_refused():
+    """A stride of 0 means contiguous to the library: rows or matrices that
+    are broadcast would be read past the end of the tensor."""
+    row, w = torch.zeros(1, 128), tg.W4Weight(torch.zeros(1, 1, 1024, dtype=torch.uint8),
+                                              torch.zeros(1, 1, 16, 1, dtype=torch.bfloat16))
+    x, y = row.bfloat16().expand(4, 128), torch.zeros(4, 16, dtype=torch.bfloat16)
+    for f in (lambda: tg._make_qgemm(x, tuple(w), y, 1.0, 0.0),
+              lambda: tg._make_qgemm(x.contiguous(), tuple(w), y[:1].expand(4, 16), 1.0, 0.0),
+              lambda: tg._make_route(row.expand(4, 128), 2, True, 1.0),
+              lambda: tg._dense_batch(row.expand(4, 128), "w"),
+              lambda: tg._dense_batch(torch.zeros(1, 3, 128).expand(2, 3, 128), "w"),
+              lambda: tg._dense_batch(torch.zeros(3, 128).expand(2, 2, 3, 128), "w")):
+        with pytest.raises(tg.TcGemmError, match="broadcast"):
+            f()
+    # one row, or one matrix, has no pitch to get wrong
+    tg._make_qgemm(row.bfloat16().expand(1, 128), tuple(w), y[:1], 1.0, 0.0)
+    assert tg._dense_batch(torch.zeros(3, 128).expand(1, 3, 128), "w")[3:] == (128, 0)

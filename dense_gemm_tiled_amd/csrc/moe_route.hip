@@ -5,6 +5,9 @@
 namespace tcg {
 namespace {
 
+// One token to a wave.  Bound by the chain of cross-lane steps, a maximum per
+// choice: 8 of 128 for one token take 2.5 us, hardly more than any launch, 8
+// of 256 for 4096 tokens 6.2 (four waves a SIMD, all in one round).
 template <int S>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
@@ -24,7 +27,9 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
 // it; a pair's place is its expert's first place plus the number of bits
 // below its own, so the order does not depend on timing.  With ROUTE (chunks
 // of at most 16 tokens) each wave first makes one token's choices itself;
-// otherwise logits were routed by a launch of their own.
+// otherwise logits were routed by a launch of their own.  One workgroup, a
+// few dependent steps in LDS: 5.3 us with 16 tokens' routing, 4.8 for the
+// lists of 61 tokens alone.
 template <bool ROUTE>
 __global__ __launch_bounds__(1024) void moe_sort_kernel(MoeArgs a) {
     __shared__ int own_id[16 * kMaxTopK];

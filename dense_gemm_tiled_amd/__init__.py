@@ -507,15 +507,29 @@ def _on_stream(device: int, stream):
     return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
 
 
-def _w4_empty(lead, N: int, K: int, group: int, zeros: bool, scale_dtype, device) -> W4Weight:
+def _w4_new(lead, N: int, K: int, group: int, zeros: bool, scale_dtype):
+    """Descriptor of a new W4Weight, a reference to it and the shapes of its
+    arrays."""
     import torch
     if group not in (32, 64, 128):
         raise TcGemmError(1, "group must be 32, 64 or 128 (got %r)" % (group,))
+    batch = 1
+    for n in lead:
+        batch *= n
     nb, kb = (N + 15) // 16, (K + 127) // 128
-    shape = (*lead, nb, kb, 16, 128 // group)
-    return W4Weight(torch.empty(*lead, nb, kb, 1024, dtype=torch.uint8, device=device),
-                    torch.empty(shape, dtype=scale_dtype, device=device),
-                    torch.empty(shape, dtype=torch.uint8, device=device) if zeros else None)
+    code = F16 if scale_dtype is torch.float16 else BF16
+    d = QWeightDescT(batch, N, K, group, code, zeros)
+    return d, ctypes.byref(d), (*lead, nb, kb, 1024), (*lead, nb, kb, 16, 128 // group)
+
+
+def _w4_empty(new, zeros: bool, scale_dtype, where, device: int, stream) -> W4Weight:
+    import torch
+    if stream is not None:
+        with _on_stream(device, stream):
+            return _w4_empty(new, zeros, scale_dtype, where, device, None)
+    return W4Weight(torch.empty(new[2], dtype=torch.uint8, device=where),
+                    torch.empty(new[3], dtype=scale_dtype, device=where),
+                    torch.empty(new[3], dtype=torch.uint8, device=where) if zeros else None)
 
 
 def _pitch(t, name: str) -> int:
@@ -548,14 +562,8 @@ def _dense_batch(t, name: str):
     return lead, N, K, ld, stride
 
 
-def w4_quantize(w, *, group: int = 128, zeros: bool = False, scale_dtype=None, stream=None) -> W4Weight:
-    """w [.., N, K] (f32, f16 or bf16) in 4 bits, with a scale per `group`
-    values of K (32, 64 or 128) and, with zeros, a zero point
-    (tc_quantize_async has the formulas).  scale_dtype: torch.float16 or
-    torch.bfloat16, the type of the activations it will meet; by default w's,
-    bfloat16 for f32."""
+def _make_quantize(w, group, zeros, scale_dtype):
     import torch
-    device = _same_device(w)
     code = _float_code(w, "w")
     if scale_dtype is None:
         scale_dtype = torch.bfloat16 if code == F32 else w.dtype
@@ -564,14 +572,34 @@ def w4_quantize(w, *, group: int = 128, zeros: bool = False, scale_dtype=None, s
     lead, N, K, ld, stride = _dense_batch(w, "w")
     if w.numel() == 0:
         raise TcGemmError(1, "dims must be >= 1 (shape %s)" % (tuple(w.shape),))
-    lib = load_library()
+    return _w4_new(lead, N, K, group, zeros, scale_dtype), code, ld, stride, scale_dtype
+
+
+def w4_quantize(w, *, group: int = 128, zeros: bool = False, scale_dtype=None, stream=None) -> W4Weight:
+    """w [.., N, K] (f32, f16 or bf16) in 4 bits, with a scale per `group`
+    values of K (32, 64 or 128) and, with zeros, a zero point
+    (tc_quantize_async has the formulas).  scale_dtype: torch.float16 or
+    torch.bfloat16, the type of the activations it will meet; by default w's,
+    bfloat16 for f32."""
+    device = _same_device(w)
+    zeros = bool(zeros)
+    key = ("quantize", w.shape, w.stride(), w.dtype, group, zeros, scale_dtype)
+    new, code, ld, stride, scale_dtype = _cached(key, lambda: _make_quantize(w, group, zeros, scale_dtype))
+    lib = _lib if _lib is not None else load_library()
     ctx, s = _torch_stream(device, stream)
-    with _on_stream(device, stream):
-        out = _w4_empty(lead, N, K, group, zeros, scale_dtype, w.device)
-    d, q = _w4_desc(out, N, K, lead), _w4_ptrs(out)
-    _check(lib.tc_quantize_async(ctx, ctypes.byref(d), w.data_ptr(), code, ld, stride,
-                                 ctypes.byref(q), s), ctx)
+    out = _w4_empty(new, zeros, scale_dtype, w.device, device, stream)
+    q = _w4_ptrs(out)
+    st = lib.tc_quantize_async(ctx, new[1], w.data_ptr(), code, ld, stride, ctypes.byref(q), s)
+    if st != 0:
+        _check(st, ctx)
     return out
+
+
+def _make_dequantize(w, out):
+    code = _float_code(out, "out")
+    lead, N, K, ld, stride = _dense_batch(out, "out")
+    d = _w4_desc(w, N, K, lead)
+    return d, ctypes.byref(d), code, ld, stride
 
 
 def w4_dequantize(w, out, *, stream=None):
@@ -579,12 +607,14 @@ def w4_dequantize(w, out, *, stream=None):
     bf16), rounded once.  Returns out."""
     w = _as_w4(w)
     device = _same_device(out, *w)
-    code = _float_code(out, "out")
-    lead, N, K, ld, stride = _dense_batch(out, "out")
-    d, q = _w4_desc(w, N, K, lead), _w4_ptrs(w)
+    key = ("dequantize", out.shape, out.stride(), out.dtype, _w4_key(w))
+    _, d, code, ld, stride = _cached(key, lambda: _make_dequantize(w, out))
+    lib = _lib if _lib is not None else load_library()
     ctx, s = _torch_stream(device, stream)
-    _check(load_library().tc_dequantize_async(ctx, ctypes.byref(d), ctypes.byref(q), out.data_ptr(),
-                                              code, ld, stride, s), ctx)
+    q = _w4_ptrs(w)
+    st = lib.tc_dequantize_async(ctx, d, ctypes.byref(q), out.data_ptr(), code, ld, stride, s)
+    if st != 0:
+        _check(st, ctx)
     return out
 
 
@@ -613,11 +643,10 @@ def w4_pack(codes, scales, zeros=None, *, K: Optional[int] = None, group: int = 
     if not all(t is None or t.is_contiguous() for t in (codes, scales, zeros)):
         raise TcGemmError(1, "codes, scales and zeros must be contiguous")
     ctx, s = _torch_stream(device, stream)
-    with _on_stream(device, stream):
-        out = _w4_empty(lead, N, K, group, zeros is not None, scales.dtype, codes.device)
-    d, q, src = _w4_desc(out, N, K, lead), _w4_ptrs(out), _w4_ptrs((codes, scales, zeros))
-    _check(load_library().tc_qweight_pack_async(ctx, ctypes.byref(d), ctypes.byref(src),
-                                                ctypes.byref(q), s), ctx)
+    new = _w4_new(lead, N, K, group, zeros is not None, scales.dtype)
+    out = _w4_empty(new, zeros is not None, scales.dtype, codes.device, device, stream)
+    q, src = _w4_ptrs(out), _w4_ptrs((codes, scales, zeros))
+    _check(load_library().tc_qweight_pack_async(ctx, new[1], ctypes.byref(src), ctypes.byref(q), s), ctx)
     return out
 
 

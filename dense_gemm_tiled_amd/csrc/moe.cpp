@@ -81,7 +81,7 @@ tc_status_t check_moe(const tc_moe_desc *d, MoeSpace *sp, std::string *err) {
     sp->ids = up_to(sp->place + pairs * 4, 256);
     sp->weights = up_to(sp->ids + pairs * 4, 256);
     sp->h = up_to(sp->weights + pairs * 4, 256);
-    sp->part = up_to(sp->h + pairs * I16 * 4, 256);
+    sp->part = up_to(sp->h + pairs * I16 * 2 * moe_parts(d->x_dtype, d->y_dtype), 256);
     sp->bytes = sp->part + pairs * d->H * 4;
     return TC_OK;
 }
@@ -244,6 +244,7 @@ tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
     a.dtype = d->x_dtype;
     a.y_dtype = d->y_dtype;
     a.gate = d->gate;
+    a.parts = moe_parts(d->x_dtype, d->y_dtype);
     a.group = d->group;
     const tc_qweight *w[2] = {gate_up, down};
     const void **to[2] = {a.gate_up, a.down};

@@ -4,10 +4,10 @@
 // They are bound by reading the weights of the experts that have tokens, each
 // once per chunk of 128 tokens.  The first product makes h = act(Wg x) * (Wu
 // x) for every (token, expert) pair, the second multiplies by Wd; the pairs
-// of a token are weighted and summed last.  h is held as the sum of two
-// 16-bit numbers, high and low part (16 mantissa bits in bf16, 22 in f16):
-// one number would add a second rounding of the result's own size, and the
-// second matrix instruction costs nothing where memory is the bound.
+// of a token are weighted and summed last.  h is held as the sum of two or
+// three 16-bit numbers (moe_parts): one number would add a second rounding of
+// the result's own size, and the further matrix instructions cost little where
+// memory is the bound.
 #include "w4_core.hpp"
 
 #include "moe_args.h"
@@ -18,16 +18,19 @@ namespace {
 
 __device__ inline float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
-// h = act(g) * u into its place: hi parts of 8 neighbours, then their lo parts.
+// h = act(g) * u into its place: first parts of 8 neighbours, then their second
+// (and third) ones.
 template <int DT>
-__device__ inline void store_h(u16 *row, int i, float g, float u, int gate) {
+__device__ inline void store_h(u16 *row, int i, float g, float u, int gate, int parts) {
     const float v = (gate == 0 ? silu(g) : gelu_tanh(g)) * u;
-    const u16 hi = to16<DT>(v);
-    // (an infinite high part stands alone)
-    const u16 lo = fabsf(from16<DT>(hi)) < INFINITY ? to16<DT>(v - from16<DT>(hi)) : (u16)0;
-    u16 *o = row + (i >> 3) * 16 + (i & 7);
-    o[0] = hi;
-    o[8] = lo;
+    u16 *o = row + (i >> 3) * (8 * parts) + (i & 7);
+    const u16 first = to16<DT>(v);
+    // (an infinite first part stands alone; the differences are exact)
+    const float rest = fabsf(from16<DT>(first)) < INFINITY ? v - from16<DT>(first) : 0.f;
+    const u16 second = to16<DT>(rest);
+    o[0] = first;
+    o[8] = second;
+    if (parts == 3) o[16] = to16<DT>(rest - from16<DT>(second));
 }
 
 // Rows m0 .. m0 + rows of an expert's list (at most 16 MT) through this
@@ -82,7 +85,8 @@ __device__ inline void up_rows(const MoeArgs &a, const WStream<WK> (&w)[2], __am
             const int i = tile * 16 + c;
             // (zeros from I to the next multiple of 16)
             if (i >= a.I) g = u = 0.f;
-            if (i < I16) store_h<WK::DT>(h + (int64_t)(m0 + 16 * t + m) * I16 * 2, i, g, u, a.gate);
+            if (i < I16)
+                store_h<WK::DT>(h + (int64_t)(m0 + 16 * t + m) * I16 * a.parts, i, g, u, a.gate, a.parts);
         }
     }
 }
@@ -145,7 +149,7 @@ __global__ __launch_bounds__(W * 64, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kern
         w[b] = WStream<WK>(matrix_of<WK>(all, (int64_t)e * 2 + b, a.I, K), tile, a.I, K, lane);
     const int64_t x_org = (int64_t)t0 * a.ldx * 2;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + x_org, a.x_bytes - x_org);
-    u16 *h = static_cast<u16 *>(a.h) + list * I16 * 2;
+    u16 *h = static_cast<u16 *>(a.h) + list * I16 * a.parts;
 
     float *const r = red;
     for (int m0 = 0; m0 < count; m0 += 16 * MT) {
@@ -169,14 +173,14 @@ __global__ __launch_bounds__(W * 64, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kern
 // are h of the first, odd rows of the second, so row 0 and row 1 of the result
 // hold the two products.  8 16-bit experts of 2048 x 1024: the layer
 // 25.5 us for 28.2, of which the first product is 14.9, 4.5 TB/s.
-template <class WK, bool HALF>
+template <class WK, bool HALF, int P>
 __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
-    constexpr int W = 16, DEPTH = WK::W4 ? 6 : 4, KB = HALF ? 2 : 1, COLS = HALF ? 8 : 16;
+    constexpr int W = 16, DEPTH = WK::W4 && P == 2 ? 6 : 4, KB = HALF ? 2 : 1, COLS = HALF ? 8 : 16;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.I, I16 = (a.I + 15) / 16 * 16;
     const int kbs = (K + KB * kBlkK - 1) / (KB * kBlkK);   // steps of KB blocks
-    const int row = kbs * KB * kBlkK * 4;            // bytes of h per expert in LDS
+    const int row = kbs * KB * kBlkK * (2 * P);      // bytes of h per expert in LDS
     float *red = reinterpret_cast<float *>(lds + a.top_k * row);
     __shared__ int expert[kMaxTopK], choice[kMaxTopK];
     __shared__ float weight[kMaxTopK];
@@ -209,8 +213,9 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
     for (int i = tid; i < n * (row / 16); i += W * 64) {
         const int j = i / (row / 16), at = (i - j * (row / 16)) * 16;
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (at < I16 * 4)
-            v = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.h) + (int64_t)choice[j] * I16 * 4 + at);
+        if (at < I16 * (2 * P))
+            v = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.h) +
+                                                 (int64_t)choice[j] * I16 * (2 * P) + at);
         *reinterpret_cast<u32x4 *>(lds + j * row + at) = v;
     }
 #pragma unroll
@@ -222,21 +227,21 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     auto compute = [&](const WFrag<WK> &s, int u) {
         const int j = u / kbs, kb = (u - j * kbs) * KB + (HALF ? lane & 1 : 0);
-        XFrag x[2];
+        XFrag x[P];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const char *at = lds + j * row + (kb * kBlkK + i * 32 + (lane >> 4) * 8) * 4;
-            x[0].v[i] = *reinterpret_cast<const u32x4 *>(at);
-            x[1].v[i] = *reinterpret_cast<const u32x4 *>(at + 16);
+            const char *at = lds + j * row + (kb * kBlkK + i * 32 + (lane >> 4) * 8) * (2 * P);
+#pragma unroll
+            for (int p = 0; p < P; ++p) x[p].v[i] = *reinterpret_cast<const u32x4 *>(at + 16 * p);
         }
         f32x4 zsum[WK::GP ? WK::GP : 1];
-        if constexpr (WK::W4 && !WK::ZP) block_offset_sums<WK, 2>(x, zsum);
+        if constexpr (WK::W4 && !WK::ZP) block_offset_sums<WK, P>(x, zsum);
         u32x4 wv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if constexpr (WK::W4) wv[i] = w4_expand<WK::DT>(s.q[0][i]);
             else wv[i] = s.q[i];
-        block_mma<WK, 2>(x, wv, s, zsum, acc);
+        block_mma<WK, P>(x, wv, s, zsum, acc);
         if ((u + 1) % kbs == 0 || u + 1 == u1) {
             // (all rows of the fragment are the token's)
             total = __builtin_fmaf(weight[j], HALF && (lane & 8) ? acc[1] : acc[0], total);
@@ -269,19 +274,22 @@ __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
 
 // Second product.  A workgroup owns 16 NB columns and one expert's pairs; its
 // waves split K (= I).  DIRECT, for few pairs an expert: 8 of them a pass,
-// their high parts in rows 0 - 7 of the operand and their low parts in rows 8
-// - 15, which halves the loads of h and the matrix instructions and leaves
-// registers for twice the waves (16 tokens over 64 4-bit experts of 4096 x
+// their first parts in rows 0 - 7 of the operand and their second ones in rows
+// 8 - 15 (5 with three parts, in rows 0 - 4, 5 - 9 and 10 - 14), which divides
+// the loads of h and the matrix instructions by the parts and leaves registers
+// for twice the waves (16 tokens over 64 4-bit experts of 4096 x
 // 1408: 33 us, 5.1 TB/s of weights, for 45).  Else 16 pairs a pass through LDS
-// (61 tokens over 32 16-bit experts of 4096 x 1400: 82 us, 4.5 TB/s).  Each pair's product goes to scratch memory in fp32
-// (T top_k H values, a few percent of the weights that were read for them),
-// and moe_combine_kernel adds a token's: no atomics, and a result that does
-// not depend on timing.
-template <class WK, int NB, bool DIRECT>
+// (61 tokens over 32 16-bit experts of 4096 x 1400: 82 us, 4.5 TB/s), or, with
+// three parts, straight into operand layout: through LDS they would be 48
+// registers a stage more, which are not there.  Each pair's product goes to
+// scratch memory in fp32 (T top_k H values, a few percent of the weights that
+// were read for them), and moe_combine_kernel adds a token's: no atomics, and a
+// result that does not depend on timing.
+template <class WK, int NB, bool DIRECT, int P>
 __global__ __launch_bounds__(256, DIRECT ? 4 : 2) void moe_down_kernel(MoeArgs a) {
-    constexpr int W = 4, ROWS = DIRECT ? 8 : 16;
+    constexpr int W = 4, ROWS = DIRECT ? 16 / P : 16;
     // the waves' h tiles, then their sums
-    constexpr int RED = W * NB * 256, TILES = DIRECT ? 0 : W * RowTile<2>::LDS_BYTES / 4;
+    constexpr int RED = W * NB * 256, TILES = DIRECT || P == 3 ? 0 : W * RowTile<2>::LDS_BYTES / 4;
     __shared__ __attribute__((aligned(16))) float red[RED > TILES ? RED : TILES];
     const MoeChunkMeta *meta = a.meta + blockIdx.y;
     const int tiles = (a.H + 15) >> 4, groups = (tiles + NB - 1) / NB;
@@ -297,24 +305,31 @@ __global__ __launch_bounds__(256, DIRECT ? 4 : 2) void moe_down_kernel(MoeArgs a
 #pragma unroll
     for (int b = 0; b < NB; ++b)
         w[b] = WStream<WK>(matrix_of<WK>(all, e, a.H, K), min(tile0 + b, tiles - 1), a.H, K, lane);
-    const __amdgpu_buffer_rsrc_t rh =
-        make_rsrc(static_cast<const char *>(a.h) + list * I16 * 4, (int64_t)count * I16 * 4);
     for (int m0 = 0; m0 < count; m0 += ROWS) {
         const int rows = min(count - m0, ROWS);
+        // (from these rows on: a chunk's may span more than 2^31 bytes)
+        const __amdgpu_buffer_rsrc_t rh = make_rsrc(
+            static_cast<const char *>(a.h) + (list + m0) * I16 * (2 * P), (int64_t)rows * I16 * (2 * P));
         f32x4 acc[NB][1];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
             acc[b][0] = f32x4{0.f, 0.f, 0.f, 0.f};
         if constexpr (DIRECT) {
-            // operand row r is the high part of pair r % 8, from 8 on the low
-            const int h_off[1][1] = {{(m0 + min(lane & 7, rows - 1)) * I16 * 4 + (lane >> 4) * 32 + (lane & 8) * 2}};
-            wave_products<WK, NB, 1, 1, true, 2>(w, rh, h_off, nullptr, K, wave, W, lane, acc);
+            // operand row r is part r / ROWS of pair r % ROWS (row 15 of three
+            // parts repeats row 10 and is not added)
+            const int r = lane & 15;
+            const int h_off[1][1] = {{min(r % ROWS, rows - 1) * I16 * (2 * P) + (lane >> 4) * (16 * P) +
+                                      min(r / ROWS, P - 1) * 16}};
+            wave_products<WK, NB, 1, 1, true, P>(w, rh, h_off, nullptr, K, wave, W, lane, acc);
+        } else if constexpr (P == 3) {
+            const int h_off[1][1] = {{min(lane & 15, rows - 1) * I16 * (2 * P) + (lane >> 4) * (16 * P)}};
+            wave_products<WK, NB, 1, 3, true>(w, rh, h_off, nullptr, K, wave, W, lane, acc);
         } else {
             char *const buf = reinterpret_cast<char *>(red) + wave * RowTile<2>::LDS_BYTES;
             int h_off[1][8];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                h_off[0][q] = (m0 + min(2 * q + (lane >> 5), rows - 1)) * I16 * 4 + (lane & 31) * 16;
+                h_off[0][q] = min(2 * q + (lane >> 5), rows - 1) * I16 * 4 + (lane & 31) * 16;
             wave_products<WK, NB, 1, 2, false>(w, rh, h_off, buf, K, wave, W, lane, acc);
         }
         __syncthreads();
@@ -331,8 +346,8 @@ __global__ __launch_bounds__(256, DIRECT ? 4 : 2) void moe_down_kernel(MoeArgs a
             float v = 0.f;
 #pragma unroll
             for (int q = 0; q < W; ++q) {
-                v += red[(q * NB + b) * 256 + m * 16 + c];
-                if (DIRECT) v += red[(q * NB + b) * 256 + (m + 8) * 16 + c];
+#pragma unroll
+                for (int p = 0; p < (DIRECT ? P : 1); ++p) v += red[(q * NB + b) * 256 + (m + p * ROWS) * 16 + c];
             }
             a.part[(list + m0 + m) * a.H + n] = v;
         }
@@ -380,11 +395,11 @@ hipError_t launch_up(const MoeArgs &a, int slots, unsigned chunks, int *launches
     return e;
 }
 
-template <class WK, int NB, bool DIRECT>
+template <class WK, int NB, bool DIRECT, int P>
 hipError_t launch_down(const MoeArgs &a, int slots, unsigned chunks, int *launches, hipStream_t s) {
     const int64_t grid = (int64_t)slots * (((a.H + 15) / 16 + NB - 1) / NB);
     if (grid > 0x7FFFFFFF || chunks > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((moe_down_kernel<WK, NB, DIRECT>), dim3((unsigned)grid, chunks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<WK, NB, DIRECT, P>), dim3((unsigned)grid, chunks), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e == hipSuccess) ++*launches;
     return e;
@@ -395,10 +410,10 @@ bool one_half(const MoeArgs &a) { return (a.H + 15) / 16 <= 128; }
 
 int one_lds_bytes(const MoeArgs &a) {
     const int step = one_half(a) ? 2 * kBlkK : kBlkK;
-    return a.top_k * ((a.I + step - 1) / step * step * 4) + 16 * 16 * 4;
+    return a.top_k * ((a.I + step - 1) / step * step * 2 * a.parts) + 16 * 16 * 4;
 }
 
-template <class WK>
+template <class WK, int P>
 hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     hipError_t e;
     if (tcg_moe_one_fits(a)) {
@@ -406,10 +421,10 @@ hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
         // for 28.5 with 4, before the second product's columns were halved)
         if ((e = launch_up<WK, WK::W4 ? 4 : 8, 1, true>(a, a.top_k, 1, launches, s)) != hipSuccess) return e;
         if (one_half(a))
-            hipLaunchKernelGGL((moe_one_down_kernel<WK, true>), dim3((unsigned)((a.H + 7) / 8)), dim3(1024),
+            hipLaunchKernelGGL((moe_one_down_kernel<WK, true, P>), dim3((unsigned)((a.H + 7) / 8)), dim3(1024),
                                one_lds_bytes(a), s, a);
         else
-            hipLaunchKernelGGL((moe_one_down_kernel<WK, false>), dim3((unsigned)((a.H + 15) / 16)), dim3(1024),
+            hipLaunchKernelGGL((moe_one_down_kernel<WK, false, P>), dim3((unsigned)((a.H + 15) / 16)), dim3(1024),
                                one_lds_bytes(a), s, a);
         e = hipGetLastError();
         if (e == hipSuccess) ++*launches;
@@ -431,10 +446,10 @@ hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     // pairs, 224, 216 / 212.
     if ((int64_t)chunk * a.top_k <= 6 * (int64_t)a.E) {
         if ((e = launch_up<WK, 4, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
-        e = launch_down<WK, NB, true>(a, slots, chunks, launches, s);
+        e = launch_down<WK, NB, true, P>(a, slots, chunks, launches, s);
     } else {
         if ((e = launch_up<WK, 4, 2, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
-        e = launch_down<WK, NB, false>(a, slots, chunks, launches, s);
+        e = launch_down<WK, NB, false, P>(a, slots, chunks, launches, s);
     }
     if (e != hipSuccess) return e;
     const int64_t grid = (int64_t)a.T * ((a.H + 255) / 256);
@@ -443,6 +458,13 @@ hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     e = hipGetLastError();
     if (e == hipSuccess) ++*launches;
     return e;
+}
+
+template <class WK>
+hipError_t launch_parts(const MoeArgs &a, int *launches, hipStream_t s) {
+    if constexpr (WK::DT == DT_BF16)
+        if (a.parts == 3) return launch_kind<WK, 3>(a, launches, s);
+    return launch_kind<WK, 2>(a, launches, s);
 }
 
 }  // namespace
@@ -463,16 +485,16 @@ bool tcg_moe_one_fits(const MoeArgs &a) { return a.T == 1 && one_lds_bytes(a) <=
 hipError_t MOE_LAUNCHER(const MoeArgs &a, int *launches, hipStream_t s) {
     const bool zp = a.gate_up[2] != nullptr;
     switch (a.group) {
-    case 0: return launch_kind<WeightKind<MOE_DT, 0, false>>(a, launches, s);
+    case 0: return launch_parts<WeightKind<MOE_DT, 0, false>>(a, launches, s);
     case 32:
-        return zp ? launch_kind<WeightKind<MOE_DT, 4, true>>(a, launches, s)
-                  : launch_kind<WeightKind<MOE_DT, 4, false>>(a, launches, s);
+        return zp ? launch_parts<WeightKind<MOE_DT, 4, true>>(a, launches, s)
+                  : launch_parts<WeightKind<MOE_DT, 4, false>>(a, launches, s);
     case 64:
-        return zp ? launch_kind<WeightKind<MOE_DT, 2, true>>(a, launches, s)
-                  : launch_kind<WeightKind<MOE_DT, 2, false>>(a, launches, s);
+        return zp ? launch_parts<WeightKind<MOE_DT, 2, true>>(a, launches, s)
+                  : launch_parts<WeightKind<MOE_DT, 2, false>>(a, launches, s);
     case 128:
-        return zp ? launch_kind<WeightKind<MOE_DT, 1, true>>(a, launches, s)
-                  : launch_kind<WeightKind<MOE_DT, 1, false>>(a, launches, s);
+        return zp ? launch_parts<WeightKind<MOE_DT, 1, true>>(a, launches, s)
+                  : launch_parts<WeightKind<MOE_DT, 1, false>>(a, launches, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -271,8 +271,8 @@ __device__ inline void load_frags(XFrag (&x)[XP], __amdgpu_buffer_rsrc_t rx, int
             if constexpr (!TAIL) {
                 x[p].v[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, kb * (256 * XB), 0);
             } else {
-                // (two parts: held in whole groups of 8, zeros past the last value)
-                x[p].v[i] = ld_chunk_tail(rx, at + kb * (256 * XB), XB == 2 && v > 0 ? 8 : v,
+                // (parts: held in whole groups of 8, zeros past the last value)
+                x[p].v[i] = ld_chunk_tail(rx, at + kb * (256 * XB), XB > 1 && v > 0 ? 8 : v,
                                           XB == 1 && (kv & 7) != 0);
             }
         }
@@ -295,8 +295,8 @@ __device__ inline void read_frags(const char *buf, int lane, XFrag (&x)[XP]) {
                                                          ((((i * 4 + kq) * XP + p) ^ r) << 4));
 }
 
-// acc += x @ (one block of weights)^T.  XP: parts of x (1, or 2 where x is
-// held as the sum of two 16-bit numbers).  zsum (symmetric codes only): the
+// acc += x @ (one block of weights)^T.  XP: parts of x (more than 1 where x is
+// held as a sum of 16-bit numbers).  zsum (symmetric codes only): the
 // groups' -24 sum_k x, the same for every block of weight rows.
 template <class WK, int XP>
 __device__ inline void block_offset_sums(const XFrag (&x)[XP], f32x4 (&zsum)[WK::GP ? WK::GP : 1]) {

@@ -339,9 +339,10 @@ tc_status_t tc_moe_route_async(tc_context *ctx, const tc_route_desc *r, const vo
  * naming their type and layout; r->T, E and top_k equal the layer's) or by
  * ids and weights [T, top_k], contiguous, with logits NULL and r NULL; an id
  * outside [0, E) adds nothing, a token none of whose ids is inside has y = 0.
- * act(gate) * up is held as the sum of two numbers of x's type (so f16
- * overflows past 65504), every sum in fp32; results do not depend on the
- * order in which the GPU runs the workgroups.  For few tokens: time grows
+ * act(gate) * up is held as the sum of two numbers of x's type, three where x
+ * is bf16 and y f32 (22, 16 and 24 bits; f16 overflows past 65504), every sum
+ * in fp32; results do not depend on the order in which the GPU runs the
+ * workgroups.  For few tokens: time grows
  * with the experts touched, and from 128 tokens on with T.
  * workspace: tc_moe_workspace bytes of device memory, 16-byte aligned, the
  * caller's until the work on s has ended; nothing is kept in it. */

@@ -371,11 +371,18 @@ hipError_t launch_tile(const W4GemmArgs &a, hipStream_t s) {
 //     N 4096 K 4096 M 2048       - /  160 /  75.4
 //     N 8192 K 4096 M 64, group 32 with zero points: 19.2 / 20.7 (four blocks
 //     do not fit the registers then)
+// Up to 32 rows never take the tiles, whose 128 rows would be mostly empty,
+// however wide the output is (few rows / tiles; from 33 rows on the former
+// would read W twice):
+//     N 131072 K 4096 M 1     57.3 / 114    group 32 with zero points 87.6 / 283
+//     N 131072 K 4096 M 16    65.6 / 117                             103.0 / 284
+//     N 131072 K 4096 M 32    96.3 / 120                             154.4 / 287
+//     N 151936 K 5120 M 1     76.9 / 204                             124.5 / 435
 template <class WK>
 hipError_t launch_kind(const W4GemmArgs &a, const char **name, hipStream_t s) {
     const int kbs = (a.w.K + kBlkK - 1) / kBlkK, nblocks = (a.w.N + kBlkN - 1) / kBlkN;
     const int64_t mtiles = (a.M + 31) / 32;
-    if (mtiles * ((nblocks + 3) / 4) > 1024) {
+    if (a.M > 32 && mtiles * ((nblocks + 3) / 4) > 1024) {
         *name = WK::DT == DT_F16 ? "w4_tile_f16" : "w4_tile_bf16";
         if constexpr (WK::GP == 1) {
             // (rounds over the CUs)

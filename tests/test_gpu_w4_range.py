@@ -1,0 +1,52 @@
+"""4-bit products and expert layers at the ends of their ranges, on the GPU:
+which kernels run there, and their results."""
+import numpy as np
+import pytest
+import torch
+
+import op_util as ou
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+DT = ou.DT
+
+
+@pytest.fixture(scope="module")
+def tg():
+    import dense_gemm_tiled_amd as t
+    t.load_library()
+    return t
+
+
+def rand(gen, *shape, dtype="f32", scale=1.0):
+    return (torch.randn(*shape, generator=gen) * scale).to(DT[dtype])
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 32])
+@pytest.mark.parametrize("N", [65536, 65540, 151936])
+@pytest.mark.parametrize("dtype,group,zeros", [("bf16", 128, False), ("f16", 32, True)])
+def test_few_rows_by_a_wide_output(tg, M, N, dtype, group, zeros):
+    """A vocabulary's projection while decoding: up to 32 rows never take the
+    tiles of 128, however many rows the weight has."""
+    gen = torch.Generator().manual_seed(M)
+    K = 136
+    w = ou.w4_random(gen, (), N, K, dtype, group, zeros, "cuda")
+    x = rand(gen, M, K, dtype=dtype)
+    y = torch.full((M, N), 7.0, dtype=torch.float32, device="cuda")
+    say("GPU case: w4_gemm few rows", M, N, K, dtype, group)
+    tg.w4_gemm(x.cuda(), w, y)
+    assert tg.last_kernel() == "w4_rows_" + dtype
+    v, e = ou.gemm_ref(x, w, N)
+    ou.check(y, v, e)
+
+
+def test_many_rows_take_the_tiles(tg):
+    gen = torch.Generator().manual_seed(2)
+    w = ou.w4_random(gen, (), 65540, 136, "bf16", 128, False, "cuda")
+    x = rand(gen, 33, 136, dtype="bf16")
+    y = torch.empty(33, 65540, dtype=torch.bfloat16, device="cuda")
+    tg.w4_gemm(x.cuda(), w, y)
+    assert tg.last_kernel() == "w4_tile_bf16"
+    v, e = ou.gemm_ref(x, w, 65540, out="bf16")
+    ou.check(y, v, e)

@@ -104,7 +104,8 @@ __device__ inline float quotient(float w, float s, float inv, float lo, float hi
 // Quantize: per group the scale (and zero point) from its largest and
 // smallest value, then the codes.  A group that holds a NaN or infinity gets
 // a NaN scale, so that what it meets shows it; a scale that the 16-bit type
-// cannot hold becomes the type's largest finite number.
+// cannot hold becomes the type's largest finite number.  What lies past N and K
+// stands for 0 (scale 0, code z).
 template <int SRC, int DT, int GP, bool ZP>
 __global__ __launch_bounds__(kFmtThreads) void w4_quantize_kernel(W4Args w, W4DenseArgs src) {
     BlockPos p;
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(kFmtThreads) void w4_quantize_kernel(W4Args w, W4De
         const bool none = !(fabsf(s) > 0.f);     // zero, or NaN: all codes z
         const float inv = none ? 0.f : __builtin_amdgcn_rcpf(s);
         if constexpr (ZP) z = none ? 0.f : quotient<DT_F32>(nlo * lift, s, inv, 0.f, 15.f);
-        sbits[g] = sb;
+        sbits[g] = p.n < w.N ? sb : 0u;
         zbits[g] = (u32)z;
 #pragma unroll
         for (int i = g * S; i < (g + 1) * S; ++i) {
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(kFmtThreads) void w4_dequantize_kernel(W4Args w, W4
 }
 
 // Row-major codes, scales and zero points into blocks.  What lies past N and
-// K becomes code 8 with scale 0.
+// K stands for 0: scale 0, and in a group that K ends in its zero point.
 __global__ __launch_bounds__(kFmtThreads) void w4_pack_kernel(W4Args w, W4RowMajorArgs src) {
     BlockPos p;
     if (!block_pos(w.N, w.K, p)) return;
@@ -249,11 +250,14 @@ __global__ __launch_bounds__(kFmtThreads) void w4_pack_kernel(W4Args w, W4RowMaj
     u32 code[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        u32 d = 0;
+        u32 d = 0, none = 8u;
+        const int64_t gi = (int64_t)p.kb * gp + i * gp / 4;
+        if (w.zeros && row && gi < groups && p.k0 + i * 32 + 8 > w.K)
+            none = static_cast<const unsigned char *>(src.zeros)[at_row * groups + gi] & 15u;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int k = p.k0 + i * 32 + j;
-            const u32 c = row && k < w.K ? (u32)(cp[k >> 1] >> (4 * (k & 1))) & 15u : 8u;
+            const u32 c = row && k < w.K ? (u32)(cp[k >> 1] >> (4 * (k & 1))) & 15u : none;
             d |= c << code_bit(j);
         }
         code[i] = d;

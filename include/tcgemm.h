@@ -242,8 +242,9 @@ tc_status_t tc_gemm_epilogue_async(tc_context *ctx, const tc_gemm_batched_desc *
  *             j = 1 and 3, byte 3 j = 5 and 7.
  *     scales  [NB][KB][16][128 / group] of scale_dtype
  *     zeros   the same shape, one byte each (its low 4 bits count), or NULL
- * What the arrays hold past N and K is never part of a result.  All three
- * start at 16-byte aligned addresses.
+ * What the arrays hold past N and K is never part of a result (what
+ * tc_quantize_async and tc_qweight_pack_async write there stands for 0).  All
+ * three start at 16-byte aligned addresses.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t batch;                /* matrices */

@@ -50,3 +50,33 @@ def test_many_rows_take_the_tiles(tg):
     assert tg.last_kernel() == "w4_tile_bf16"
     v, e = ou.gemm_ref(x, w, 65540, out="bf16")
     ou.check(y, v, e)
+
+
+# ------------------------------------------------------------------ past N and K
+def packed(tg, gen, lead, N, K, dtype, group, zeros):
+    """Random row-major codes (none of them 8), scales and zero points through w4_pack."""
+    q = torch.randint(0, 8, (*lead, N, K + K % 2), generator=gen, dtype=torch.uint8)
+    s = rand(gen, *lead, N, -(-K // group), dtype=dtype, scale=K ** -0.5 / 4)
+    z = torch.randint(0, 8, s.shape, generator=gen, dtype=torch.uint8) if zeros else None
+    return tg.w4_pack((q[..., ::2] | (q[..., 1::2] << 4)).cuda(), s.cuda(), None if z is None else z.cuda(), K=K,
+                      group=group)
+
+
+@pytest.mark.parametrize("N,K", [(1, 1), (33, 40), (40, 203), (16, 256), (19, 129)])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True), (128, False)])
+@pytest.mark.parametrize("how", ["quantize", "pack"])
+def test_past_the_matrix_stands_for_zero(tg, N, K, group, zeros, how):
+    """The whole blocks read as a matrix of their own: zeros past N and K."""
+    gen = torch.Generator().manual_seed(N + K)
+    say("GPU case: past N and K", N, K, group, zeros, how)
+    if how == "pack":
+        w = packed(tg, gen, (2,), N, K, "f16", group, zeros)
+    else:
+        w = tg.w4_quantize(rand(gen, 2, N, K, dtype="f16").cuda() + 1, group=group, zeros=zeros)
+    whole = torch.empty(2, -(-N // 16) * 16, -(-K // 128) * 128, device="cuda")
+    tg.w4_dequantize(w, whole)
+    inside = torch.empty(2, N, K, device="cuda")
+    tg.w4_dequantize(w, inside)
+    assert torch.equal(whole[:, :N, :K], inside) and (inside != 0).any()
+    whole[:, :N, :K] = 0
+    assert (whole == 0).all()

@@ -410,16 +410,31 @@ def gemm(a, b, c, *, alpha: float = 1.0, beta: float = 0.0, transpose_a: bool = 
 
 
 # ------------------------------------------------------------------ weights in 4 bits
-class W4Weight(NamedTuple):
+class _W4Arrays(NamedTuple):
+    codes: "torch.Tensor"
+    scales: "torch.Tensor"
+    zeros: "Optional[torch.Tensor]" = None
+
+
+class W4Weight(_W4Arrays):
     """Matrices held in 4 bits with a scale (and zero point) per group of K
     (the layout is in include/tcgemm.h): codes uint8 [.., ceil(N/16),
     ceil(K/128), 1024], scales f16 or bf16 [.., ceil(N/16), ceil(K/128), 16,
     128/group], zeros uint8 of the scales' shape or None.  Contiguous; the
     leading dims, if any, count matrices.  Functions that take one accept a
-    plain tuple too."""
-    codes: "torch.Tensor"
-    scales: "torch.Tensor"
-    zeros: "Optional[torch.Tensor]" = None
+    plain tuple of the three (or two) too.  N and K, the matrices' own sizes,
+    are known where w4_quantize or w4_pack made the weight or the constructor
+    was told them, else None."""
+    N: Optional[int] = None
+    K: Optional[int] = None
+
+    def __new__(cls, codes, scales, zeros=None, *, N: Optional[int] = None, K: Optional[int] = None):
+        self = super().__new__(cls, codes, scales, zeros)
+        if N is not None:
+            self.N = int(N)
+        if K is not None:
+            self.K = int(K)
+        return self
 
 
 def _float_code(t, name: str, types=(F32, F16, BF16)) -> int:
@@ -508,8 +523,8 @@ def _on_stream(device: int, stream):
 
 
 def _w4_new(lead, N: int, K: int, group: int, zeros: bool, scale_dtype):
-    """Descriptor of a new W4Weight, a reference to it and the shapes of its
-    arrays."""
+    """Descriptor of a new W4Weight, a reference to it, the shapes of its
+    arrays, N and K."""
     import torch
     if group not in (32, 64, 128):
         raise TcGemmError(1, "group must be 32, 64 or 128 (got %r)" % (group,))
@@ -519,7 +534,7 @@ def _w4_new(lead, N: int, K: int, group: int, zeros: bool, scale_dtype):
     nb, kb = (N + 15) // 16, (K + 127) // 128
     code = F16 if scale_dtype is torch.float16 else BF16
     d = QWeightDescT(batch, N, K, group, code, zeros)
-    return d, ctypes.byref(d), (*lead, nb, kb, 1024), (*lead, nb, kb, 16, 128 // group)
+    return d, ctypes.byref(d), (*lead, nb, kb, 1024), (*lead, nb, kb, 16, 128 // group), N, K
 
 
 def _w4_empty(new, zeros: bool, scale_dtype, where, device: int, stream) -> W4Weight:
@@ -529,7 +544,8 @@ def _w4_empty(new, zeros: bool, scale_dtype, where, device: int, stream) -> W4We
             return _w4_empty(new, zeros, scale_dtype, where, device, None)
     return W4Weight(torch.empty(new[2], dtype=torch.uint8, device=where),
                     torch.empty(new[3], dtype=scale_dtype, device=where),
-                    torch.empty(new[3], dtype=torch.uint8, device=where) if zeros else None)
+                    torch.empty(new[3], dtype=torch.uint8, device=where) if zeros else None,
+                    N=new[4], K=new[5])
 
 
 def _pitch(t, name: str) -> int:
@@ -793,6 +809,15 @@ def _make_moe(x, route, gate_up, down, y, top_k, activation, renormalize, scale,
     return d, ctypes.byref(d), r, rref, need.value if st == 0 else 0
 
 
+def _intermediate(gate_up, down) -> Optional[int]:
+    """The intermediate size that 4-bit experts know of themselves: gate_up's
+    rows, down's columns; None where neither knows."""
+    rows, cols = getattr(gate_up, "N", None), getattr(down, "K", None)
+    if rows is not None and cols is not None and rows != cols:
+        raise TcGemmError(1, "gate_up has %d rows and down %d columns" % (rows, cols))
+    return cols if rows is None else rows
+
+
 def _weights_key(w) -> tuple:
     return _w4_key(w) if isinstance(w, tuple) else (w.shape, w.dtype, w.is_contiguous())
 
@@ -810,11 +835,15 @@ def moe(x, route, gate_up, down, y, *, top_k: Optional[int] = None, activation: 
     nothing.  gate_up [E, 2, I, H] (gate, then up; [E, 2 I, H] is the same
     memory) and down [E, H, I]: tensors of x's type, or both in 4 bits
     (W4Weight of leading shapes (E, 2) and (E,)); then I is `intermediate`,
-    by default gate_up's rows rounded up to 16.  activation: "silu" or
+    by default the size that one of the weights knows (W4Weight.N, .K).  Plain
+    tuples know none: without `intermediate` they are taken to hold whole
+    blocks of 16 rows, all of them used.  activation: "silu" or
     "gelu_tanh".  Scratch memory comes from torch's allocator, for this call
     alone.  Returns y."""
     import torch
     if isinstance(gate_up, (tuple, list)):
+        if intermediate is None:
+            intermediate = _intermediate(gate_up, down)
         gate_up = _as_w4(gate_up)
     if isinstance(down, (tuple, list)):
         down = _as_w4(down)

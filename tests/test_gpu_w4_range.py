@@ -80,3 +80,35 @@ def test_past_the_matrix_stands_for_zero(tg, N, K, group, zeros, how):
     assert torch.equal(whole[:, :N, :K], inside) and (inside != 0).any()
     whole[:, :N, :K] = 0
     assert (whole == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+@pytest.mark.parametrize("H,I", [(64, 33), (72, 40), (130, 121)])
+@pytest.mark.parametrize("form", ["library", "tuples", "sized"])
+def test_experts_know_their_intermediate_size(tg, T, H, I, form):
+    """Experts whose I is no multiple of 16, without `intermediate`: gate_up
+    from the quantizer, down from w4_pack (its zero points are not 8); the
+    same as plain tuples; and arrays laid out by someone else, whose
+    padding holds code 15 and scale NaN, with their sizes."""
+    gen = torch.Generator().manual_seed(I)
+    E, k, dtype = 5, 2, "f16"
+    if form == "sized":
+        up = tg.W4Weight(*ou.w4_random(gen, (E, 2), I, H, dtype, 32, True, "cuda"), N=I, K=H)
+        dn = tg.W4Weight(*ou.w4_random(gen, (E,), H, I, dtype, 32, True, "cuda"), N=H, K=I)
+    else:
+        up = tg.w4_quantize(rand(gen, E, 2, I, H, dtype=dtype).cuda() * H ** -0.5 + 0.1, group=32, zeros=True)
+        dn = packed(tg, gen, (E,), H, I, dtype, 32, True)
+        assert (up.N, up.K, dn.N, dn.K) == (I, H, H, I)
+        if form == "tuples":
+            up, dn = tuple(up), tuple(dn)
+    x, l = rand(gen, T, H, dtype=dtype), rand(gen, T, E)
+    y = torch.empty(T, H, device="cuda")
+    say("GPU case: moe without intermediate", T, H, I, form)
+    tg.moe(x.cuda(), l.cuda(), up, dn, y, top_k=k)
+    ids, w = ou.route_ref(l, k)
+    one = lambda t, *i: [v if v is None else v[i] for v in t]  # noqa: E731
+    v, e = ou.moe_ref(x, ids, w, lambda a, b: one(up, a, b), lambda a: one(dn, a), I, "silu", "f32")
+    ou.check(y, v, e)
+    # (the elementwise bound is the worst case of every rounding; padding that counted would be 24 % of the
+    # whole or more, 7 rows of 121, fp32 sums over groups of 32 are at most gamma_64 * 38 * 0.8 * 32 / 18.7, 2e-4)
+    assert np.linalg.norm(ou.f64(y) - v) <= 1e-3 * np.linalg.norm(v)

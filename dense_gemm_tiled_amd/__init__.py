@@ -294,6 +294,15 @@ def _ld(t) -> int:
     return int(t.stride(-2))
 
 
+def _i32(**sizes):
+    """The values of sizes that a descriptor holds in 32 bits (ctypes would
+    keep the lower half of a longer one)."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise TcGemmError(3, "%s=%d does not fit 32 bits" % (name, v))
+    return tuple(sizes.values())
+
+
 def make_desc(a, b, c, alpha: float = 1.0, beta: float = 0.0,
               transpose_a: bool = False, transpose_b: bool = False) -> BatchedDescT:
     """Build the batched descriptor for tensors a, b, c (2-D or 3-D)."""
@@ -314,12 +323,12 @@ def make_desc(a, b, c, alpha: float = 1.0, beta: float = 0.0,
     accum = I32 if ad == I8 else F32
     desc = BatchedDescT()
     base = desc.base
-    base.M, base.N, base.K = M, N, K
+    base.M, base.N, base.K = _i32(M=M, N=N, K=K)
     base.a_dtype, base.b_dtype, base.c_dtype, base.accum_dtype = ad, bd, cd, accum
     base.transpose_a, base.transpose_b = bool(transpose_a), bool(transpose_b)
     base.alpha, base.beta = float(alpha), float(beta)
-    base.lda, base.ldb, base.ldc = _ld(a), _ld(b), _ld(c)
-    desc.batch = batch
+    base.lda, base.ldb, base.ldc = _i32(lda=_ld(a), ldb=_ld(b), ldc=_ld(c))
+    desc.batch, = _i32(batch=batch)
     desc.stride_a = int(a.stride(0)) if a.dim() == 3 else 0
     desc.stride_b = int(b.stride(0)) if b.dim() == 3 else 0
     desc.stride_c = int(c.stride(0)) if c.dim() == 3 else 0
@@ -493,7 +502,7 @@ def _w4_desc(w, N: int, K: int, lead=()):
     batch = 1
     for n in lead:
         batch *= n
-    return QWeightDescT(batch, N, K, 128 // per, _float_code(scales, "scales", (F16, BF16)),
+    return QWeightDescT(*_i32(batch=batch, N=N, K=K), 128 // per, _float_code(scales, "scales", (F16, BF16)),
                         zeros is not None)
 
 
@@ -533,7 +542,7 @@ def _w4_new(lead, N: int, K: int, group: int, zeros: bool, scale_dtype):
         batch *= n
     nb, kb = (N + 15) // 16, (K + 127) // 128
     code = F16 if scale_dtype is torch.float16 else BF16
-    d = QWeightDescT(batch, N, K, group, code, zeros)
+    d = QWeightDescT(*_i32(batch=batch, N=N, K=K), group, code, zeros)
     return d, ctypes.byref(d), (*lead, nb, kb, 1024), (*lead, nb, kb, 16, 128 // group), N, K
 
 
@@ -671,8 +680,8 @@ def _make_qgemm(x, w, y, alpha, beta):
         raise TcGemmError(1, "x must be [M, K] and y [M, N] (got %s and %s)"
                           % (tuple(x.shape), tuple(y.shape)))
     wd = _w4_desc(w, int(y.size(1)), int(x.size(1)))
-    g = QGemmDescT(int(x.size(0)), _dtype_code(x), _dtype_code(y), float(alpha), float(beta),
-                   _pitch(x, "x"), _pitch(y, "y"))
+    M, ldx, ldy = _i32(M=int(x.size(0)), ldx=_pitch(x, "x"), ldy=_pitch(y, "y"))
+    g = QGemmDescT(M, _dtype_code(x), _dtype_code(y), float(alpha), float(beta), ldx, ldy)
     return g, wd, ctypes.byref(g), ctypes.byref(wd)
 
 
@@ -715,8 +724,9 @@ def w4_gemm(x, w, y, *, alpha: float = 1.0, beta: float = 0.0, bias=None,
 def _make_route(logits, top_k, renormalize, scale):
     if logits.dim() != 2:
         raise TcGemmError(1, "logits must be [T, E] (got %s)" % (tuple(logits.shape),))
-    r = RouteDescT(int(logits.size(0)), int(logits.size(1)), int(top_k), _dtype_code(logits),
-                   _pitch(logits, "the logits"), bool(renormalize), float(scale))
+    T, E, k, ld = _i32(T=int(logits.size(0)), E=int(logits.size(1)), top_k=int(top_k),
+                       ld=_pitch(logits, "the logits"))
+    r = RouteDescT(T, E, k, _dtype_code(logits), ld, bool(renormalize), float(scale))
     return r, ctypes.byref(r)
 
 
@@ -801,8 +811,8 @@ def _make_moe(x, route, gate_up, down, y, top_k, activation, renormalize, scale,
         if tuple(route.shape) != (T, E):
             raise TcGemmError(1, "logits must be [T, E] = %s (got %s)" % ((T, E), tuple(route.shape)))
         r, rref = _make_route(route, k, renormalize, scale)
-    d = MoeDescT(T, H, I, E, k, _dtype_code(x), _dtype_code(y), _pitch(x, "x"), _pitch(y, "y"), GATES[activation],
-                 group, zeros)
+    d = MoeDescT(*_i32(T=T, H=H, I=I, E=E, top_k=k), _dtype_code(x), _dtype_code(y),
+                 *_i32(ldx=_pitch(x, "x"), ldy=_pitch(y, "y")), GATES[activation], group, zeros)
     need = ctypes.c_int64()
     st = load_library().tc_moe_workspace(ctypes.byref(d), ctypes.byref(need))
     # (a descriptor the library refuses is refused again, with its text, by the call)

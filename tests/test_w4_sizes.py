@@ -79,9 +79,9 @@ CALLS = [
     ("matrices", lambda: tg._make_quantize(meta((2 ** 32 + 1, 16, 128), (2048, 128, 1)), 128, False, None)),
     ("rows", lambda: tg._make_quantize(meta((2 ** 32 + 16, 128), (128, 1)), 128, False, None)),
     ("columns", lambda: tg._make_quantize(meta((16, 2 ** 32 + 128), (2 ** 32 + 128, 1)), 128, False, None)),
-    ("dequantized rows", lambda: tg._w4_desc(tuple(meta((2 ** 28 + 1, 1, *s), (1, 1, *([1] * len(s))), t)
-                                                   for s, t in (((1024,), torch.uint8), ((16, 1), torch.bfloat16))) + (None,),
-                                             2 ** 32 + 16, 128)),
+    ("dequantized rows", lambda: tg._w4_desc((torch.empty(2 ** 28 + 1, 1, 1024, dtype=torch.uint8, device="meta"),
+                                              torch.empty(2 ** 28 + 1, 1, 16, 1, dtype=torch.float16, device="meta"),
+                                              None), 2 ** 32 + 16, 128)),
     ("dense lda", lambda: tg.make_desc(meta((2, 64), (BIG, 1)), meta((64, 8), (8, 1)), meta((2, 8), (8, 1)))),
     ("dense ldc", lambda: tg.make_desc(meta((2, 64), (64, 1)), meta((64, 8), (8, 1)), meta((2, 8), (BIG, 1)))),
     ("dense M", lambda: tg.make_desc(meta((BIG, 64), (64, 1)), meta((64, 8), (8, 1)), meta((BIG, 8), (8, 1)))),

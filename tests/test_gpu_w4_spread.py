@@ -124,3 +124,18 @@ def test_one_token(tg, H, I, E, k, held, dtype):
                                         ("bf16", (64, False)), ("f16", None)])
 def test_layer(tg, T, H, I, E, k, dtype, held):
     run_layer(tg, T, H, I, E, k, dtype, held, act="gelu_tanh" if T % 2 else "silu", seed=T + H)
+
+
+@pytest.mark.parametrize("H,I,E,k,dtype,out,kernel", [
+    # h of two parts in LDS, in steps of 256 columns (H up to 2048) or 128: 65 and 113 KiB, exactly the 128 KiB it may
+    # take with the sums, and past it
+    (24, 2048, 9, 8, "f16", "f16", ONE), (24, 14336, 2, 2, "bf16", "bf16", ONE), (24, 32512, 1, 1, "f16", "f16", ONE),
+    (24, 32513, 1, 1, "f16", "f16", GENERAL), (24, 4096, 8, 8, "bf16", "bf16", GENERAL),
+    (2064, 14336, 2, 2, "f16", "f16", ONE), (2064, 16256, 2, 2, "bf16", "bf16", ONE),
+    (2064, 16257, 2, 2, "bf16", "bf16", GENERAL),
+    # three parts
+    (24, 10752, 2, 2, "bf16", "f32", ONE), (24, 10753, 2, 2, "bf16", "f32", GENERAL), (2064, 2688, 9, 8, "bf16", "f32", ONE),
+    (2064, 2689, 9, 8, "bf16", "f32", GENERAL)])
+@pytest.mark.parametrize("held", [None, (128, False), (32, True)])
+def test_one_token_fills_lds(tg, H, I, E, k, dtype, out, kernel, held):
+    run_layer(tg, 1, H, I, E, k, dtype, held, seed=I, kernel=kernel, outs=(out,))

@@ -48,8 +48,11 @@ tc_status_t check_ranges(const Range *r, int n, int n_out, bool allocations, std
     for (int i = 0; i < n_out; ++i)
         for (int j = i + 1; j < n; ++j)
             if (r[i].ptr && r[j].ptr && r[i].bytes > 0 && r[j].bytes > 0 &&
-                ranges_overlap(r[i].ptr, r[i].bytes, r[j].ptr, r[j].bytes))
+                ranges_overlap(r[i].ptr, r[i].bytes, r[j].ptr, r[j].bytes)) {
+                for (const Range *o : {&r[i], &r[j]})
+                    if (overruns(o->ptr, o->bytes)) return check_allocation(o->name, o->ptr, o->bytes, err);
                 return fail(err, TC_ERR_ALIASING, "%s overlaps %s", r[i].name, r[j].name);
+            }
     if (!allocations) return TC_OK;
     for (int i = 0; i < n; ++i) {
         if (!r[i].ptr) continue;

@@ -104,6 +104,19 @@ inline tc_status_t check_allocation(const char *name, const void *ptr, int64_t b
     return TC_OK;
 }
 
+// Whether the range starts inside a device allocation and runs past its end.
+// What such a range overlaps depends on where the allocator put other things,
+// so a call is refused for its length first.
+inline bool overruns(const void *ptr, int64_t bytes) {
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)ptr) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    return (uintptr_t)ptr >= (uintptr_t)base && (uintptr_t)ptr + (uintptr_t)bytes > (uintptr_t)base + size;
+}
+
 inline tc_status_t bind_device(tc_context *ctx) {
     if (ctx->device >= 0) return hipSetDevice(ctx->device) == hipSuccess ? TC_OK : TC_ERR_DEVICE;
     int dev = -1;

@@ -1207,8 +1207,12 @@ tc_status_t run(tc_context *ctx, const tc_gemm_batched_desc *bd, const void *A, 
     if (st != TC_OK) return st;
     Epilogue epi;
     if (ep && (st = validate_epilogue(p, ep, C, &epi, err)) != TC_OK) return st;
-    if (ranges_overlap(C, p.c_total, A, p.a_total) || ranges_overlap(C, p.c_total, B, p.b_total))
+    if (ranges_overlap(C, p.c_total, A, p.a_total) || ranges_overlap(C, p.c_total, B, p.b_total)) {
+        if (overruns(A, p.a_total)) return check_allocation("A", A, p.a_total, err);
+        if (overruns(B, p.b_total)) return check_allocation("B", B, p.b_total, err);
+        if (overruns(C, p.c_total)) return check_allocation("C", C, p.c_total, err);
         return fail(err, TC_ERR_ALIASING, "C overlaps A or B");
+    }
 
     st = bind_device(ctx);
     if (st != TC_OK) return st;

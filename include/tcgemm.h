@@ -34,7 +34,9 @@
  * Boundary"): every argument is validated, with checked 64-bit arithmetic,
  * before anything is enqueued.  A call that returns an error has launched
  * nothing and tc_dispatch_count() is unchanged; tc_last_error() describes the
- * failure.  The library refuses rather than silently falling back.
+ * failure.  The library refuses rather than silently falling back.  A range
+ * that runs past the end of its allocation is refused for that
+ * (TC_ERR_INVALID_ARGUMENT), whatever else it overlaps.
  *
  * Streams (tensorcore "GEMM", section "Async, batched, and streams"): the
  * _async calls enqueue on a tc_stream and return; tc_stream_sync waits.  The

@@ -112,3 +112,34 @@ def test_experts_know_their_intermediate_size(tg, T, H, I, form):
     # (the elementwise bound is the worst case of every rounding; padding that counted would be 24 % of the
     # whole or more, 7 rows of 121, fp32 sums over groups of 32 are at most gamma_64 * 38 * 0.8 * 32 / 18.7, 2e-4)
     assert np.linalg.norm(ou.f64(y) - v) <= 1e-3 * np.linalg.norm(v)
+
+
+# ------------------------------------------------------------------ refusals
+def test_a_span_too_long_is_refused_for_its_length(tg):
+    """An operand that runs past its allocation and over the output that lies
+    before it in memory: refused as too long wherever the allocator puts
+    things, and without a launch."""
+    import ctypes
+    lib, (ctx, s) = tg.load_library(), tg._torch_stream(0)
+    M, K = 1 << 19, 64
+    store = torch.zeros(100 << 20, dtype=torch.uint8, device="cuda")
+    end, = (m["address"] + m["total_size"] for m in torch.cuda.memory_snapshot()
+            if m["address"] <= store.data_ptr() < m["address"] + m["total_size"])
+    out, a = end - (100 << 20), end - (50 << 20)         # [M, 64] 16-bit values are 64 MiB
+    b = torch.zeros(K, K, dtype=torch.bfloat16, device="cuda")
+    w = tg.w4_quantize(b)
+    torch.cuda.synchronize()
+    n0 = tg.dispatch_count()
+    d = tg.BatchedDescT()
+    d.base.M, d.base.N, d.base.K = M, K, K
+    d.base.a_dtype = d.base.b_dtype = d.base.c_dtype = tg.BF16
+    d.base.accum_dtype, d.base.alpha, d.batch = tg.F32, 1.0, 1
+    g = tg.QGemmDescT(M, tg.BF16, tg.BF16, 1.0, 0.0, 0, 0)
+    wd, q = tg._w4_desc(w, K, K), tg._w4_ptrs(w)
+    R = ctypes.byref
+    for x, y, status in ((a, out, 1), (out, a, 1), (out, out + 4096, 4)):
+        for call in (lambda: lib.tc_gemm_batched_async(ctx, R(d), x, b.data_ptr(), y, s),
+                     lambda: lib.tc_qgemm_async(ctx, R(g), R(wd), x, R(q), y, None, s)):
+            assert call() == status, (x, y)
+            assert (b"allocation" if status == 1 else b"overlaps") in lib.tc_last_error(ctx)
+    assert tg.dispatch_count() == n0

@@ -355,10 +355,14 @@ __device__ inline void block_mma(const XFrag (&x)[XP], const u32x4 (&w)[4], cons
 // (see RowTile); x_off[t][q]: see load_piece, or load_frags (q = 0 alone);
 // buf: RowTile<XP>::LDS_BYTES of this wave's own.
 //
-// No branch may stand between a matrix instruction and what reads its
-// result: where a tile was skipped by a branch, the compiler left out the
-// wait states before the reader on the other side, and the results were
-// wrong.  So MT is the number of tiles in use, and callers choose by it.
+// No branch may skip matrix instructions between another one and what reads
+// its result: where a tile past the last row was skipped so, the compiler
+// counted the wait states before the reader along the path through the skipped
+// instructions only (8 are needed; the other path had 1), and the results were
+// wrong.  So MT is the number of tiles in use, and callers choose by it.  (A
+// branch around the reader alone, as in the one-token layer's second product,
+// is on the straight path and counted.  tests/test_matrix_waits.py walks all
+// paths of the built kernels.)
 template <class WK, int NB, int MT, int XP, bool DIRECT, int XB = XP>
 __device__ inline void wave_products(const WStream<WK> (&w)[NB], __amdgpu_buffer_rsrc_t rx,
                                      const int (&x_off)[MT][DIRECT ? 1 : RowTile<XP>::LOADS], char *buf, int K,

@@ -1,8 +1,12 @@
 // moe_layer.hip -- the products of a mixture-of-experts layer for few tokens,
 // experts in 16 or 4 bits.  One object per type of x (MOE_DT).
 //
-// They are bound by reading the weights of the experts that have tokens, each
-// once per chunk of 128 tokens.  The first product makes h = act(Wg x) * (Wu
+// They are bound by reading the weights of the experts that have tokens.  Tokens
+// are taken 128 at a time (a chunk); in a chunk, an expert's pairs walk over its
+// weights 32 at a time in the first product and 16 in the second, 16 and 8 (5
+// with three parts) in the direct forms for few pairs an expert, so an expert
+// with more pairs than that is read again, from L2 where its share of it
+// holds a workgroup's slice.  The first product makes h = act(Wg x) * (Wu
 // x) for every (token, expert) pair, the second multiplies by Wd; the pairs
 // of a token are weighted and summed last.  h is held as the sum of two or
 // three 16-bit numbers (moe_parts): one number would add a second rounding of
@@ -434,7 +438,8 @@ hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     const unsigned chunks = (unsigned)((a.T + kMoeChunk - 1) / kMoeChunk);
     const int slots = a.E < chunk * a.top_k ? a.E : chunk * a.top_k;
     // (as many blocks of the second product as two stages of them and of h
-    // leave registers for)
+    // leave registers for, but for a few: the direct kernel of groups of 64, and
+    // of 128 with zero points, keeps 2 to 9 registers in scratch memory)
     constexpr int NB = WK::GP == 1 || WK::GP == 2 ? 4 : 2;
     // By the mean number of pairs an expert has.  Us per layer, direct kernels
     // against those through LDS: 4-bit experts (64 of 4096 x 1408, 8 a token)

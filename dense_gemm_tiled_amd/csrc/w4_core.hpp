@@ -347,11 +347,16 @@ __device__ inline void block_mma(const XFrag (&x)[XP], const u32x4 (&w)[4], cons
 }
 
 // One wave: acc[nb][mt] += x rows @ weights^T over the K blocks kb0, kb0 +
-// step, .. of ceil(K / 128).  Weights and activations of the next block are
-// in flight while one is multiplied (the same depth for both: loads return in
-// order, so a shallower queue of x would wait for every weight load issued
-// before it); a short last block comes first, so that its element loads are
-// not waited for alone at the end.  DIRECT: x straight into operand layout
+// step, .. of ceil(K / 128).  Two blocks' weights and activations are loaded
+// ahead (the same depth for both: loads return in order, so a shallower queue
+// of x would wait for every weight load issued before it).  As built, every
+// second block is multiplied with the next one's loads in flight, the others
+// after both have come: the loads that a branch may skip are not in the
+// compiler's count, so the wait behind the branch holds for them as well.  (With
+// the last blocks taken out of the loop instead, it moved the loads behind the
+// products, spilled up to 31 registers and put readers too close behind
+// matrix instructions at the new branch.)  A short last block comes first, so
+// that its element loads are not waited for alone at the end.  DIRECT: x straight into operand layout
 // (see RowTile); x_off[t][q]: see load_piece, or load_frags (q = 0 alone);
 // buf: RowTile<XP>::LDS_BYTES of this wave's own.
 //

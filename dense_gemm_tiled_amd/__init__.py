@@ -230,8 +230,7 @@ def _context(device: int) -> int:
     if h is None:
         out = _VP()
         _check(load_library().tc_context_create(ctypes.byref(out)), None)
-        h = out.value
-        _ctx[device] = h
+        h = _ctx.setdefault(device, out.value)     # (another thread may have been first)
     return h
 
 
@@ -254,8 +253,7 @@ def _torch_stream(device: int, stream=None) -> Tuple[int, int]:
         out = _VP()
         with torch.cuda.device(device):
             _check(load_library().tc_stream_wrap(ctx, _VP(handle), ctypes.byref(out)), ctx)
-        s = out.value
-        _streams[key] = s
+        s = _streams.setdefault(key, out.value)
     return ctx, s
 
 

@@ -125,6 +125,7 @@ extern "C" {
 tc_status_t tc_moe_route_async(tc_context *ctx, const tc_route_desc *r, const void *logits,
                                int32_t *ids, float *weights, tc_stream *s) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
     if (!logits || !ids || !weights || !s)
@@ -167,6 +168,7 @@ tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
                          const float *weights, const tc_qweight *gate_up, const tc_qweight *down,
                          void *y, void *workspace, int64_t workspace_bytes, tc_stream *s) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
     MoeSpace sp;

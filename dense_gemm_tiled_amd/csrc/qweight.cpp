@@ -134,6 +134,7 @@ tc_status_t tc_quantize_async(tc_context *ctx, const tc_qweight_desc *d, const v
                               tc_dtype_t w_dtype, int64_t ldw, int64_t stride_w,
                               const tc_qweight *out, tc_stream *s) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
     if (!s || !W) return fail(err, TC_ERR_INVALID_ARGUMENT, "W and the stream must be non-NULL");
@@ -158,6 +159,7 @@ tc_status_t tc_dequantize_async(tc_context *ctx, const tc_qweight_desc *d, const
                                 void *out, tc_dtype_t out_dtype, int64_t ldo, int64_t stride_o,
                                 tc_stream *s) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
     if (!s || !out) return fail(err, TC_ERR_INVALID_ARGUMENT, "out and the stream must be non-NULL");
@@ -181,6 +183,7 @@ tc_status_t tc_dequantize_async(tc_context *ctx, const tc_qweight_desc *d, const
 tc_status_t tc_qweight_pack_async(tc_context *ctx, const tc_qweight_desc *d,
                                   const tc_qweight *row_major, const tc_qweight *out, tc_stream *s) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
     if (!s) return fail(err, TC_ERR_INVALID_ARGUMENT, "stream is NULL");
@@ -215,6 +218,7 @@ tc_status_t tc_qgemm_async(tc_context *ctx, const tc_qgemm_desc *g, const tc_qwe
                            const void *x, const tc_qweight *w, void *y, const tc_epilogue *ep,
                            tc_stream *s) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
     if (!g || !s || !x || !y)

@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <map>
+#include <mutex>
 #include <string>
 
 #include "tc_internal.h"
@@ -30,6 +31,7 @@ struct Choice {
 };
 
 struct tc_context {
+    std::mutex mutex;            // held by every call: threads that share a context take turns
     int device = -1;             // bound at the first launch
     tc_stream *internal = nullptr;
     uint64_t dispatches = 0;
@@ -41,6 +43,14 @@ struct tc_context {
 };
 
 namespace tcg {
+
+// A context's turn for the length of a call (none for a null context).
+struct Turn {
+    std::unique_lock<std::mutex> lock;
+    explicit Turn(const tc_context *ctx) {
+        if (ctx) lock = std::unique_lock<std::mutex>(const_cast<tc_context *>(ctx)->mutex);
+    }
+};
 
 inline tc_status_t fail(std::string *err, tc_status_t st, const char *fmt, ...) {
     if (err) {

@@ -28,7 +28,7 @@ constexpr int64_t kMaxTileSpanBytes = 0x7FFFFFFF;  // byte offsets inside one ti
 constexpr int32_t kMaxInt8K = 131071;              // 16384 * 131072 = 2^31 would wrap
 constexpr int kMaxTileRows = 256;
 
-std::string g_plan_error;   // error text of tc_gemm_plan(NULL, ...)
+thread_local std::string g_plan_error;   // error text of tc_gemm_plan(NULL, ...)
 
 // The fused epilogue of a call (none: act == ACT_NONE and no bias).
 struct Epilogue {
@@ -1198,6 +1198,7 @@ tc_status_t run(tc_context *ctx, const tc_gemm_batched_desc *bd, const void *A, 
                 void *C, tc_stream *s, bool sync, const tc_epilogue *ep = nullptr,
                 bool noalloc = false) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     const KnobScope knobs;
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
@@ -1289,6 +1290,12 @@ tc_gemm_batched_desc single(const tc_gemm_desc *d) {
     return bd;
 }
 
+// An error found before a call has its context's turn.
+void note(tc_context *ctx, const char *text) {
+    const Turn turn(ctx);
+    if (ctx) ctx->last_error = text;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1310,6 +1317,7 @@ void tc_context_destroy(tc_context *ctx) {
 
 tc_status_t tc_stream_create(tc_context *ctx, tc_stream **out) {
     if (!ctx || !out) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     tc_status_t st = bind_device(ctx);
     if (st != TC_OK) return st;
     return create_stream(ctx, out, nullptr);
@@ -1317,6 +1325,7 @@ tc_status_t tc_stream_create(tc_context *ctx, tc_stream **out) {
 
 tc_status_t tc_stream_wrap(tc_context *ctx, void *hip_stream, tc_stream **out) {
     if (!ctx || !out) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     tc_status_t st = bind_device(ctx);
     if (st != TC_OK) return st;
     tc_stream *s = new (std::nothrow) tc_stream();
@@ -1333,7 +1342,7 @@ tc_status_t tc_stream_sync(tc_stream *s) {
     hipError_t e = hipStreamSynchronize(s->stream);
     if (e != hipSuccess) {
         (void)hipGetLastError();
-        if (s->ctx) s->ctx->last_error = std::string("hipStreamSynchronize: ") + hipGetErrorString(e);
+        note(s->ctx, (std::string("hipStreamSynchronize: ") + hipGetErrorString(e)).c_str());
         return TC_ERR_DEVICE;
     }
     return TC_OK;
@@ -1351,7 +1360,7 @@ void tc_stream_destroy(tc_stream *s) {
 
 tc_status_t tc_gemm(tc_context *ctx, const tc_gemm_desc *d, const void *A, const void *B, void *C) {
     if (!d) {
-        if (ctx) ctx->last_error = "descriptor is NULL";
+        note(ctx, "descriptor is NULL");
         return TC_ERR_INVALID_ARGUMENT;
     }
     tc_gemm_batched_desc bd = single(d);
@@ -1361,7 +1370,7 @@ tc_status_t tc_gemm(tc_context *ctx, const tc_gemm_desc *d, const void *A, const
 tc_status_t tc_gemm_async(tc_context *ctx, const tc_gemm_desc *d, const void *A, const void *B,
                           void *C, tc_stream *s) {
     if (!d || !s) {
-        if (ctx) ctx->last_error = !d ? "descriptor is NULL" : "stream is NULL";
+        note(ctx, !d ? "descriptor is NULL" : "stream is NULL");
         return TC_ERR_INVALID_ARGUMENT;
     }
     tc_gemm_batched_desc bd = single(d);
@@ -1376,7 +1385,7 @@ tc_status_t tc_gemm_batched(tc_context *ctx, const tc_gemm_batched_desc *bd, con
 tc_status_t tc_gemm_batched_async(tc_context *ctx, const tc_gemm_batched_desc *bd, const void *A,
                                   const void *B, void *C, tc_stream *s) {
     if (!s) {
-        if (ctx) ctx->last_error = "stream is NULL";
+        note(ctx, "stream is NULL");
         return TC_ERR_INVALID_ARGUMENT;
     }
     return run(ctx, bd, A, B, C, s, false);
@@ -1385,7 +1394,7 @@ tc_status_t tc_gemm_batched_async(tc_context *ctx, const tc_gemm_batched_desc *b
 tc_status_t tc_gemm_batched_async_noalloc(tc_context *ctx, const tc_gemm_batched_desc *bd,
                                           const void *A, const void *B, void *C, tc_stream *s) {
     if (!s) {
-        if (ctx) ctx->last_error = "stream is NULL";
+        note(ctx, "stream is NULL");
         return TC_ERR_INVALID_ARGUMENT;
     }
     return run(ctx, bd, A, B, C, s, false, nullptr, true);
@@ -1394,7 +1403,7 @@ tc_status_t tc_gemm_batched_async_noalloc(tc_context *ctx, const tc_gemm_batched
 tc_status_t tc_gemm_epilogue(tc_context *ctx, const tc_gemm_batched_desc *bd, const tc_epilogue *ep,
                              const void *A, const void *B, void *C) {
     if (!ep) {
-        if (ctx) ctx->last_error = "epilogue is NULL";
+        note(ctx, "epilogue is NULL");
         return TC_ERR_INVALID_ARGUMENT;
     }
     return run(ctx, bd, A, B, C, nullptr, true, ep);
@@ -1404,7 +1413,7 @@ tc_status_t tc_gemm_epilogue_async(tc_context *ctx, const tc_gemm_batched_desc *
                                    const tc_epilogue *ep, const void *A, const void *B, void *C,
                                    tc_stream *s) {
     if (!ep || !s) {
-        if (ctx) ctx->last_error = !ep ? "epilogue is NULL" : "stream is NULL";
+        note(ctx, !ep ? "epilogue is NULL" : "stream is NULL");
         return TC_ERR_INVALID_ARGUMENT;
     }
     return run(ctx, bd, A, B, C, s, false, ep);
@@ -1412,13 +1421,18 @@ tc_status_t tc_gemm_epilogue_async(tc_context *ctx, const tc_gemm_batched_desc *
 
 tc_status_t tc_set_autotune(tc_context *ctx, int enable) {
     if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->autotune = enable != 0;
     return TC_OK;
 }
 
-int64_t tc_autotune_entries(const tc_context *ctx) { return ctx ? (int64_t)ctx->tuned.size() : 0; }
+int64_t tc_autotune_entries(const tc_context *ctx) {
+    const Turn turn(ctx);
+    return ctx ? (int64_t)ctx->tuned.size() : 0;
+}
 
 tc_status_t tc_gemm_plan(tc_context *ctx, const tc_gemm_batched_desc *bd, tc_plan_info *info) {
+    const Turn turn(ctx);
     const KnobScope knobs;
     std::string *err = ctx ? &ctx->last_error : &g_plan_error;
     err->clear();
@@ -1431,12 +1445,21 @@ tc_status_t tc_gemm_plan(tc_context *ctx, const tc_gemm_batched_desc *bd, tc_pla
     return TC_OK;
 }
 
-const char *tc_last_kernel(const tc_context *ctx) { return ctx ? ctx->last_kernel.c_str() : ""; }
+const char *tc_last_kernel(const tc_context *ctx) {
+    if (!ctx) return "";
+    static thread_local std::string text;
+    const Turn turn(ctx);
+    return (text = ctx->last_kernel).c_str();
+}
 
-uint64_t tc_dispatch_count(const tc_context *ctx) { return ctx ? ctx->dispatches : 0; }
+uint64_t tc_dispatch_count(const tc_context *ctx) {
+    const Turn turn(ctx);
+    return ctx ? ctx->dispatches : 0;
+}
 
 tc_status_t tc_time_next_gemm(tc_context *ctx, void *start_event, void *end_event) {
     if (!ctx || (!start_event) != (!end_event)) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
     ctx->time_ev[0] = static_cast<hipEvent_t>(start_event);
     ctx->time_ev[1] = static_cast<hipEvent_t>(end_event);
     return TC_OK;
@@ -1456,7 +1479,9 @@ const char *tc_status_string(tc_status_t status) {
 }
 
 const char *tc_last_error(const tc_context *ctx) {
-    return ctx ? ctx->last_error.c_str() : g_plan_error.c_str();
+    static thread_local std::string text;
+    const Turn turn(ctx);
+    return (text = ctx ? ctx->last_error : g_plan_error).c_str();
 }
 
 tc_status_t tc_tile_of_workgroup(int32_t tiles_m, int32_t tiles_n, int32_t groups, int32_t band,

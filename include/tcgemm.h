@@ -41,7 +41,11 @@
  * Streams (tensorcore "GEMM", section "Async, batched, and streams"): the
  * _async calls enqueue on a tc_stream and return; tc_stream_sync waits.  The
  * synchronous calls run on the context's own stream and return after the
- * result is in C.  A tc_context is not thread-safe; use one per host thread.
+ * result is in C.  Threads may share a tc_context: calls on it take turns (a
+ * synchronous one holds it until its result is there).  tc_last_error and
+ * tc_last_kernel give the calling thread a copy, which its next call of the
+ * same function replaces; they name what the context's last call left,
+ * whichever thread made it.
  */
 #ifndef TCGEMM_H
 #define TCGEMM_H

@@ -21,7 +21,8 @@
 // in both types).  The two nearly cancel: their terms are at most 4 times
 // the size of x * 8, so the fp32 sum loses about two of its 24 bits.  The
 // group's sum is multiplied by s in fp32 and added to the running result.
-// An infinity or NaN in x gives NaN in its row.
+// An infinity or NaN in x gives NaN in its row, and so can numbers past 2^115,
+// of which 128 times 31 no longer fit fp32.
 //
 // Operand order: x is the left operand (row m = lane % 16 of the fragment),
 // the weights the right one, so a lane ends with column n = lane % 16 and

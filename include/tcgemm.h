@@ -302,7 +302,9 @@ tc_status_t tc_qweight_pack_async(tc_context *ctx, const tc_qweight_desc *d,
  * layer whose weight (d, w; batch 1) is held in 4 bits, for one row of x or
  * for many.  x has the type of the scales, y that type or f32; ep may be NULL
  * and holds no col_scale.  fp32 sums, y written once.  A row of x that holds
- * a NaN or infinity gives NaN (before the activation).  No workspace. */
+ * a NaN or infinity gives NaN (before the activation), and so may one that
+ * holds a bf16 number past 2^115: a group's sum of x times 16 .. 31 is formed
+ * before its scale and the offset are taken.  No workspace. */
 typedef struct {
     int32_t M;
     tc_dtype_t x_dtype, y_dtype;

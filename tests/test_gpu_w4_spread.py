@@ -139,3 +139,102 @@ def test_layer(tg, T, H, I, E, k, dtype, held):
 @pytest.mark.parametrize("held", [None, (128, False), (32, True)])
 def test_one_token_fills_lds(tg, H, I, E, k, dtype, out, kernel, held):
     run_layer(tg, 1, H, I, E, k, dtype, held, seed=I, kernel=kernel, outs=(out,))
+
+
+# ------------------------------------------------------------------ ends of the number types
+@pytest.mark.parametrize("dtype,group,zeros", [("bf16", 128, False), ("f16", 64, True), ("bf16", 32, True)])
+@pytest.mark.parametrize("M", [1, 20, 64])
+def test_products_of_tiny_and_huge_numbers(tg, dtype, group, zeros, M):
+    """Powers of two as factors of x change nothing but the results' exponents:
+    x down to its type's subnormal numbers, and up to 2^115 (a group's sums, 128
+    times 31 |x| at most, stay inside fp32 up to there)."""
+    gen = generator(M)
+    N, K = 48, 500
+    w = weight(gen, (), N, K, dtype, group, zeros)
+    x = torch.randint(-8, 9, (M, K), device="cuda", generator=gen).float()
+    ys = []
+    for e in (0, -24, 11) if dtype == "f16" else (0, -133, -60, 112):
+        y = torch.empty(M, N, device="cuda")
+        say("GPU case: w4_gemm scaled", M, dtype, e)
+        tg.w4_gemm((x * 2.0 ** e).to(DT[dtype]), w, y)
+        ys.append((y.double() * 2.0 ** -e, e))
+    for y, e in ys[1:]:
+        # (results below 2^-126 are rounded to fp32's subnormal numbers)
+        assert torch.allclose(y, ys[0][0], rtol=0, atol=2.0 ** (-150 - e + 10) if e < -100 else 0), e
+
+
+@pytest.mark.parametrize("group,zeros", [(128, False), (32, True)])
+@pytest.mark.parametrize("M", [1, 64])
+def test_subnormal_scales(tg, group, zeros, M):
+    gen = generator(9)
+    N, K = 48, 384
+    codes, s, z = weight(gen, (), N, K, "f16", group, zeros)
+    s = torch.randint(-1000, 1001, s.shape, device="cuda", generator=gen).float()
+    x, ys = randn(gen, M, K, dtype="f16"), []
+    for e in (-24, -10):
+        y = torch.empty(M, N, device="cuda")
+        tg.w4_gemm(x, (codes, (s * 2.0 ** e).half(), z), y)
+        ys.append(y * 2.0 ** -e)
+    assert torch.equal(*ys) and (ys[0] != 0).any()
+
+
+@pytest.mark.parametrize("dtype,e", [("f16", -24), ("bf16", -133)])
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_layer_reads_subnormal_weights(tg, dtype, e, T):
+    """down of subnormal numbers only.  To a matrix instruction they have the
+    exponent of the smallest normal number, 2^-14 or 2^-126, so its products
+    are added in steps of u of up to |h| times that, whatever the numbers'
+    own size: I + 32 sums, each within u |h| 2^-14, against the same numbers
+    times 2^24, which are exact to u of their own."""
+    gen = generator(T)
+    H, I, E, k = 40, 24, 4, 2
+    x, l = randn(gen, T, H, dtype=dtype), randn(gen, T, E)
+    up = randn(gen, E, 2, I, H, dtype=dtype)
+    dn = torch.randint(-8, 9, (E, H, I), device="cuda", generator=gen).float()
+    ys = []
+    for f in (e, 0):
+        y = torch.empty(T, H, device="cuda")
+        tg.moe(x, l, up, (dn * 2.0 ** f).to(DT[dtype]), y, top_k=k)
+        ys.append(y.double() * 2.0 ** -f)
+    ids, p = ou.route_ref(l, k)
+    normal = {"f16": 2.0 ** -14, "bf16": 2.0 ** -126}[dtype] * 2.0 ** -e
+    for t in range(T):
+        bound = 0.0
+        for j in range(k):
+            g, u = (x[t].double() @ up[ids[t, j], s].double().t() for s in (0, 1))
+            h = (sp.activation(g, "silu") * u).abs()
+            bound += p[t, j] * (I + 32) * ou.U * float(h.sum()) * (normal + 8)
+        assert float((ys[0][t] - ys[1][t]).abs().max()) <= bound
+        assert bound < 0.2 * float(ys[1][t].norm()) and float(ys[1][t].norm()) > 0
+
+
+# ------------------------------------------------------------------ rows past 4 GiB
+def test_product_rows_past_4_gib(tg):
+    M, N, K = 300000, 24, 8192
+    gen = generator(3)
+    w = weight(gen, (), N, K, "bf16", 128, False)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    assert x.numel() * 2 > 2 ** 32
+    y = torch.full((M, N), 7.0, device="cuda")
+    say("GPU case: w4_gemm rows past 4 GiB")
+    tg.w4_gemm(x, w, y)
+    for at in (slice(0, 130), slice(262140, 262150), slice(M - 70, M)):
+        v, var = sp.product(x[at].double(), w, N, K)
+        sp.check(y[at], v, var, "f32", str(at))
+
+
+def test_layer_rows_past_4_gib(tg):
+    T, H, I, E, k = 270000, 8192, 16, 2, 1
+    gen = generator(4)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    l = randn(gen, T, E)
+    up, dn = weight(gen, (E, 2), I, H, "bf16", 128, False), weight(gen, (E,), H, I, "bf16", 128, False)
+    y = torch.full((T, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    say("GPU case: moe rows past 4 GiB")
+    tg.moe(x, l, up, dn, y, top_k=k, intermediate=I)
+    for at in (slice(0, 20), slice(262140, 262150), slice(T - 40, T)):
+        ids, p = ou.route_ref(l[at], k)
+        v, var = sp.layer(x[at], ids.tolist(), torch.from_numpy(p).cuda(),
+                          lambda e, s: [t if t is None else t[e, s] for t in up],
+                          lambda e: [t if t is None else t[e] for t in dn], I, "silu", "bf16")
+        sp.check(y[at], v, var, "bf16", str(at))

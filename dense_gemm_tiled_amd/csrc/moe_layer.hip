@@ -448,7 +448,9 @@ hipError_t launch_kind(const MoeArgs &a, int *launches, hipStream_t s) {
     // pairs, 157 / 171.  Above, with one of the two products direct (first,
     // second) and with none: 16-bit experts (32 of 4096 x 1400, 4 a token) of
     // 61 tokens, 7.6 pairs, 232, 239 / 229; the 4-bit ones of 128 tokens, 16
-    // pairs, 224, 216 / 212.
+    // pairs, 224, 216 / 212.  With three parts of h (f32 results) the same rule:
+    // those 4-bit experts 124 / 153 and 153 / 170, the 16-bit ones 161 / 163, and
+    // of 48 tokens, 6 pairs, 188 / 178.
     if ((int64_t)chunk * a.top_k <= 6 * (int64_t)a.E) {
         if ((e = launch_up<WK, 4, 1, false>(a, slots, chunks, launches, s)) != hipSuccess) return e;
         e = launch_down<WK, NB, true, P>(a, slots, chunks, launches, s);

@@ -1,11 +1,14 @@
 // w4_format.hip -- into the 4-bit weight format and out of it.  Every kernel
 // gives one block (16 rows x 128 k) to a wave; lane 16 kq + r handles of row
 // r the k = 32 i + 8 kq + j, i = 0..3, j = 0..7, which are its 16 bytes of
-// codes.  All of them move each byte once and are bound by that: 8192x4096
-// bf16 with groups of 128 is quantized in 19.5 us (4.3 TB/s, graph replay)
-// and expanded to fp32 in 24.8 (6.1), 4099x4093 fp32 with groups of 32 and
-// zero points in 22.1 (3.5) and back in 20.5 (3.8): rows of odd length
-// start at odd addresses, and every 16-byte access crosses a boundary.
+// codes.  All of them move each byte once and, but for packing, are bound by
+// that: 8192x4096 bf16 with groups of 128 is quantized in 19.5 us (4.3 TB/s,
+// graph replay) and expanded to fp32 in 24.8 (6.1), 4099x4093 fp32 with groups
+// of 32 and zero points in 22.1 (3.5) and back in 20.5 (3.8): rows of odd length
+// start at odd addresses, and every 16-byte access crosses a boundary.  To bf16
+// instead of fp32: 20.5 us (4.1) and 18.5 (2.3).  Packing, done once a
+// checkpoint, loads its codes a byte at a time: 60.7 us for 8192x4096 (0.57 TB/s,
+// the bytes alone would take 7).
 #include "w4_core.hpp"
 
 #include "w4_args.h"

@@ -35,8 +35,11 @@ __device__ inline void finish(const W4GemmArgs &a, int m, int n, float v) {
 // the x of its own blocks, which no other wave needs.  One row by 4096x4096,
 // bf16, group 128, takes 4.4 us (1.9 TB/s of codes: starting up and the first
 // loads' latency are most of it), 4 rows by 16384x8192 in fp16 13.3 us (5.0 TB/s
-// of codes), 64 rows by 8192x4096 with groups of 64 and zero points 14.3:
-// there the CUs together read x and W several times from L2.
+// of codes), 64 rows by 8192x4096 with groups of 64 and zero points 14.3: two
+// waves a SIMD, which wait for loads 38 % of their cycles and for their turn to
+// issue 28 % (counters; the VALU is busy 43 % of the time, the matrix units 28
+// %, L2 gives 124 MB at 10 of the 20 TB/s and more that it can).  That instance
+// (4 blocks, bf16) keeps 12 registers in scratch memory.
 template <class WK, int NB, int MT>
 __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a) {
     // [waves][NB][16][16] sums at the end, before them the waves' x tiles
@@ -133,16 +136,18 @@ hipError_t launch_rows(const W4GemmArgs &a, int waves, hipStream_t s) {
 // rows by 4096x4096, bf16, group 128: 49.6 -> 47.6).
 //
 // NBW: with a group of 128, 4 blocks of weight rows a wave are as many as the
-// 256 registers of two waves a SIMD hold, and 2048 rows by 4096x4096 take 75.4
+// 256 registers of two waves a SIMD hold (with zero points 4 of them are in
+// scratch memory), and 2048 rows by 4096x4096 take 75.4
 // us (912 TFLOP/s; 49 us at the rate of a large matrix product in 16 bits,
 // 101.8 with 128x64 tiles of 4 waves and x through registers).  A round of
 // 128x256 tiles over the CUs is worth 1.5 of 128x128, so the smaller ones are
 // taken where they need less than 1.5 times the rounds (1024 rows by
 // 4096x4096: 72 / 55 us, 256 rows by 16384x4096: 74 / 56, before the halves
 // were set apart; 47.6 and 48.6 since).  Smaller groups hold more scales and
-// sums and have 2 blocks only: 2048 rows by 4096x4096 take 102 us with groups
+// sums and have 2 blocks only: 2048 rows by 4096x4096 take 100 us with groups
 // of 64, 149 with groups of 32 and zero points (a multiplication per result
-// and group comes on top).
+// and group comes on top).  w4_dequantize to 16 bits and the dense product take
+// 69 - 71 us there with any group, at one rounding of the weights.
 //
 // What bounds it: the matrix units are busy two fifths of the time (counters:
 // 69.8 of 181 thousand cycles, no bank conflict in LDS).  The rest is the

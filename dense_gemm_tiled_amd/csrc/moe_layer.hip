@@ -179,6 +179,7 @@ __global__ __launch_bounds__(W * 64, WK::W4 && MT == 1 ? 4 : 2) void moe_up_kern
 // 25.5 us for 28.2, of which the first product is 14.9, 4.5 TB/s.
 template <class WK, bool HALF, int P>
 __global__ __launch_bounds__(1024) void moe_one_down_kernel(MoeArgs a) {
+    // (with three parts of h, 6 units in flight keep 18 registers in scratch memory)
     constexpr int W = 16, DEPTH = WK::W4 && P == 2 ? 6 : 4, KB = HALF ? 2 : 1, COLS = HALF ? 8 : 16;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -21,6 +21,7 @@ from typing import Dict, NamedTuple, Optional, Tuple
 
 __all__ = [
     "gemm", "w4_quantize", "w4_dequantize", "w4_pack", "w4_gemm", "moe_route", "moe", "W4Weight",
+    "cross_entropy", "cross_entropy_backward", "moe_balance", "moe_route_backward",
     "plan", "TcGemmError", "last_kernel", "dispatch_count", "time_next_gemm", "library_path",
     "load_library", "F32", "F16", "BF16", "I8", "I32", "status_name", "DescT",
     "BatchedDescT", "PlanInfoT",
@@ -111,6 +112,21 @@ class MoeDescT(ctypes.Structure):
                 ("gate", ctypes.c_int), ("group", ctypes.c_int32), ("has_zeros", ctypes.c_bool)]
 
 
+class CeDescT(ctypes.Structure):
+    """tc_ce_desc"""
+    _fields_ = [("T", ctypes.c_int32), ("V", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("ldx", ctypes.c_int32), ("ldw", ctypes.c_int32),
+                ("targets64", ctypes.c_bool), ("scale", ctypes.c_float)]
+
+
+class CeGradsT(ctypes.Structure):
+    """tc_ce_grads"""
+    _fields_ = [("grad", ctypes.c_void_p), ("grad_stride", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("dx_dtype", ctypes.c_int), ("lddx", ctypes.c_int32),
+                ("dw", ctypes.c_void_p), ("dw_dtype", ctypes.c_int), ("lddw", ctypes.c_int32),
+                ("beta", ctypes.c_float)]
+
+
 # tc_gate_t
 GATES = {"silu": 0, "gelu_tanh": 1}
 
@@ -184,6 +200,22 @@ _SIGNATURES = {
     "tc_moe_async": (ctypes.c_int, [_VP, ctypes.POINTER(MoeDescT), _VP, ctypes.POINTER(RouteDescT),
                                     _VP, _VP, _VP, ctypes.POINTER(QWeightT),
                                     ctypes.POINTER(QWeightT), _VP, _VP, ctypes.c_int64, _VP]),
+    "tc_cross_entropy_workspace": (ctypes.c_int, [ctypes.POINTER(CeDescT), _VP, _VP,
+                                                  ctypes.POINTER(ctypes.c_int64)]),
+    "tc_cross_entropy_async": (ctypes.c_int, [_VP, ctypes.POINTER(CeDescT), _VP, _VP, _VP, _VP, _VP,
+                                              _VP, ctypes.c_int64, _VP]),
+    "tc_cross_entropy_backward_workspace": (ctypes.c_int, [ctypes.POINTER(CeDescT),
+                                                           ctypes.POINTER(CeGradsT), _VP, _VP,
+                                                           ctypes.POINTER(ctypes.c_int64)]),
+    "tc_cross_entropy_backward_async": (ctypes.c_int, [_VP, ctypes.POINTER(CeDescT),
+                                                       ctypes.POINTER(CeGradsT), _VP, _VP, _VP, _VP,
+                                                       _VP, ctypes.c_int64, _VP]),
+    "tc_moe_balance_workspace": (ctypes.c_int, [ctypes.POINTER(RouteDescT),
+                                                ctypes.POINTER(ctypes.c_int64)]),
+    "tc_moe_balance_async": (ctypes.c_int, [_VP, ctypes.POINTER(RouteDescT), _VP, _VP,
+                                            ctypes.c_float, _VP, _VP, _VP, _VP, ctypes.c_int64, _VP]),
+    "tc_moe_route_backward_async": (ctypes.c_int, [_VP, ctypes.POINTER(RouteDescT), _VP, _VP, _VP, _VP,
+                                                   _VP, _VP, ctypes.c_int, ctypes.c_int32, _VP]),
 }
 
 _lib = None
@@ -889,6 +921,225 @@ def moe(x, route, gate_up, down, y, *, top_k: Optional[int] = None, activation: 
     if st != 0:
         _check(st, ctx)
     return y
+
+
+# ------------------------------------------------------------------ losses
+def _scratch(need: int, like, device: int, stream):
+    """Scratch memory for one call on the stream it runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    with _on_stream(device, stream):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
+def _new(shapes, like, device: int, stream):
+    """New tensors of the given (shape, dtype)s, made for the stream a call
+    runs on."""
+    import torch
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=like.device) for shape, dtype in shapes]
+    with _on_stream(device, stream):
+        return [torch.empty(shape, dtype=dtype, device=like.device) for shape, dtype in shapes]
+
+
+def _make_ce(x, weight, targets, scale):
+    import torch
+    if x.dim() != 2 or weight.dim() != 2 or x.size(1) != weight.size(1):
+        raise TcGemmError(1, "x must be [T, H] and the weight [V, H] (got %s and %s)"
+                          % (tuple(x.shape), tuple(weight.shape)))
+    code = _float_code(x, "x")
+    if weight.dtype != x.dtype:
+        raise TcGemmError(2, "the weight must have x's dtype %s (got %s)" % (x.dtype, weight.dtype))
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TcGemmError(2, "targets must be int32 or int64 (got %s)" % targets.dtype)
+    T, V, H, ldx, ldw = _i32(T=int(x.size(0)), V=int(weight.size(0)), H=int(x.size(1)),
+                             ldx=_pitch(x, "x"), ldw=_pitch(weight, "the weight"))
+    if tuple(targets.shape) != (T,) or not targets.is_contiguous():
+        raise TcGemmError(1, "targets must be [T] = [%d], contiguous (got %s)" % (T, tuple(targets.shape)))
+    return CeDescT(T, V, H, code, ldx, ldw, targets.dtype == torch.int64, scale)
+
+
+def _make_ce_forward(x, weight, targets, scale):
+    d = _make_ce(x, weight, targets, scale)
+    need = ctypes.c_int64()
+    st = load_library().tc_cross_entropy_workspace(ctypes.byref(d), x.data_ptr(), weight.data_ptr(),
+                                                   ctypes.byref(need))
+    # (a descriptor the library refuses is refused again, with its text, by the call)
+    return d, ctypes.byref(d), need.value if st == 0 else 0
+
+
+def _ce_key(x, weight, targets) -> tuple:
+    return (x.shape, x.stride(), x.dtype, x.data_ptr() % 16, weight.shape, weight.stride(), weight.dtype,
+            weight.data_ptr() % 16, targets.shape, targets.stride(), targets.dtype)
+
+
+def cross_entropy(x, weight, targets, *, scale: float = 1.0, stream=None):
+    """(loss, lse), float32 [T]: the softmax cross entropy of the linear layer
+    scale * (x @ weight^T) against targets, and the log of each token's sum of
+    exponentials (tc_cross_entropy_async).  x [T, H] and weight [V, H], f32,
+    f16 or bf16; targets [T] int32 or int64.  A token whose target is outside
+    [0, V), -100 for instance, is ignored: its loss is 0.  The [T, V] products
+    are not kept.  Scratch memory comes from torch's allocator, for this call
+    alone."""
+    import torch
+    device = _same_device(x, weight, targets)
+    scale = float(scale)
+    d, dref, need = _cached(("ce", scale) + _ce_key(x, weight, targets),
+                            lambda: _make_ce_forward(x, weight, targets, scale))
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    (loss, lse), space = _new([((d.T,), torch.float32)] * 2, x, device, stream), _scratch(need, x, device, stream)
+    st = lib.tc_cross_entropy_async(ctx, dref, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+                                    loss.data_ptr(), lse.data_ptr(), space.data_ptr(), need, s)
+    if st != 0:
+        _check(st, ctx)
+    return loss, lse
+
+
+def _make_ce_backward(x, weight, targets, lse, grad, dx, dweight, scale, beta):
+    import torch
+    d = _make_ce(x, weight, targets, scale)
+    g = CeGradsT()
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (d.T,) or not lse.is_contiguous():
+        raise TcGemmError(1, "lse must be float32 [T] = [%d], contiguous" % d.T)
+    if grad.dtype != torch.float32 or tuple(grad.shape) not in ((), (1,), (d.T,)):
+        raise TcGemmError(1, "grad must be float32, one number or [T] = [%d] (got %s %s)"
+                          % (d.T, grad.dtype, tuple(grad.shape)))
+    g.grad_stride = int(grad.stride(0)) if grad.numel() > 1 else 0
+    for name, t, like in (("dx", dx, x), ("dweight", dweight, weight)):
+        if t is not None and t.shape != like.shape:
+            raise TcGemmError(1, "%s must be %s (got %s)" % (name, tuple(like.shape), tuple(t.shape)))
+    if dx is not None:
+        g.dx_dtype, (g.lddx,) = _float_code(dx, "dx"), _i32(lddx=_pitch(dx, "dx"))
+    if dweight is not None:
+        g.dw_dtype, (g.lddw,) = _float_code(dweight, "dweight"), _i32(lddw=_pitch(dweight, "dweight"))
+    g.beta = beta
+    # (any address of the right alignment: the size does not depend on more)
+    g.grad = 16
+    g.dx, g.dw = (None if dx is None else dx.data_ptr()), (None if dweight is None else dweight.data_ptr())
+    need = ctypes.c_int64()
+    st = load_library().tc_cross_entropy_backward_workspace(ctypes.byref(d), ctypes.byref(g), x.data_ptr(),
+                                                            weight.data_ptr(), ctypes.byref(need))
+    return d, ctypes.byref(d), g, need.value if st == 0 else 0
+
+
+def cross_entropy_backward(x, weight, targets, lse, grad, dx=None, dweight=None, *, scale: float = 1.0,
+                           beta: float = 0.0, stream=None):
+    """The gradients of cross_entropy's losses (tc_cross_entropy_backward_async):
+    dx [T, H] and dweight = beta * dweight + .. [V, H], either one None or of
+    x's type or f32.  lse: what cross_entropy returned for the same x, weight
+    and scale; grad float32: the losses' gradient, [T] of any stride or one
+    number for all of them.  Ignored tokens add nothing to dweight and have
+    dx = 0.  An f32 gradient from 16-bit inputs is as exact as fp32 sums and
+    takes two or three times the products; one in x's type is rounded like any
+    16-bit result.  Returns (dx, dweight)."""
+    outs = [t for t in (dx, dweight) if t is not None]
+    if not outs:
+        raise TcGemmError(1, "dx and dweight must not both be None")
+    device = _same_device(x, weight, targets, lse, grad, *outs)
+    scale, beta = float(scale), float(beta)
+    key = ("ceb", scale, beta, lse.shape, lse.stride(), lse.dtype, grad.shape, grad.stride(), grad.dtype,
+           None if dx is None else (dx.shape, dx.stride(), dx.dtype),
+           None if dweight is None else (dweight.shape, dweight.stride(), dweight.dtype))
+    _, dref, made, need = _cached(key + _ce_key(x, weight, targets),
+                                  lambda: _make_ce_backward(x, weight, targets, lse, grad, dx, dweight, scale,
+                                                            beta))
+    # (a copy: threads may share the cached one)
+    g = CeGradsT.from_buffer_copy(made)
+    g.grad = grad.data_ptr()
+    g.dx, g.dw = (None if dx is None else dx.data_ptr()), (None if dweight is None else dweight.data_ptr())
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    space = _scratch(need, x, device, stream)
+    st = lib.tc_cross_entropy_backward_async(ctx, dref, ctypes.byref(g), x.data_ptr(), weight.data_ptr(),
+                                             targets.data_ptr(), lse.data_ptr(), space.data_ptr(), need, s)
+    if st != 0:
+        _check(st, ctx)
+    return dx, dweight
+
+
+def _make_balance(logits, ids):
+    import torch
+    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise TcGemmError(1, "ids must be int32 [T, top_k], contiguous")
+    r, rref = _make_route(logits, int(ids.size(1)), True, 1.0)
+    if int(ids.size(0)) != r.T:
+        raise TcGemmError(1, "ids must have a row per token: %d (got %d)" % (r.T, ids.size(0)))
+    need = ctypes.c_int64()
+    st = load_library().tc_moe_balance_workspace(rref, ctypes.byref(need))
+    return r, rref, need.value if st == 0 else 0
+
+
+def moe_balance(logits, ids, *, coef: float = 1.0, stream=None):
+    """(loss float32 [], counts int32 [E], slope float32 [E]): the balance loss
+    of a router, coef * E * sum_e (share of the choices)[e] * (mean
+    probability)[e], the choices of each expert, and what moe_route_backward
+    needs for its gradient (tc_moe_balance_async has the formulas).  logits [T,
+    E] f32, f16 or bf16; ids int32 [T, top_k] as moe_route gives them; a token
+    with no id inside [0, E), padding for instance, does not count."""
+    import torch
+    device = _same_device(logits, ids)
+    r, rref, need = _cached(("balance", logits.shape, logits.stride(), logits.dtype, ids.shape, ids.stride(),
+                             ids.dtype), lambda: _make_balance(logits, ids))
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    loss, counts, slope, space = _new([((), torch.float32), ((r.E,), torch.int32), ((r.E,), torch.float32),
+                                       ((need,), torch.uint8)], logits, device, stream)
+    st = lib.tc_moe_balance_async(ctx, rref, logits.data_ptr(), ids.data_ptr(), float(coef), loss.data_ptr(),
+                                  counts.data_ptr(), slope.data_ptr(), space.data_ptr(), need, s)
+    if st != 0:
+        _check(st, ctx)
+    return loss, counts, slope
+
+
+def _make_route_backward(logits, ids, dweights, dlogits, renormalize, scale, slope, dloss):
+    import torch
+    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise TcGemmError(1, "ids must be int32 [T, top_k], contiguous")
+    r, rref = _make_route(logits, int(ids.size(1)), renormalize, scale)
+    if int(ids.size(0)) != r.T:
+        raise TcGemmError(1, "ids must have a row per token: %d (got %d)" % (r.T, ids.size(0)))
+    if dweights is not None and (dweights.dtype != torch.float32 or dweights.shape != ids.shape
+                                 or not dweights.is_contiguous()):
+        raise TcGemmError(1, "dweights must be float32 of ids' shape %s, contiguous" % (tuple(ids.shape),))
+    if (slope is None) != (dloss is None):
+        raise TcGemmError(1, "slope and dloss go together")
+    if slope is not None:
+        if slope.dtype != torch.float32 or tuple(slope.shape) != (r.E,) or not slope.is_contiguous():
+            raise TcGemmError(1, "slope must be float32 [E] = [%d], contiguous" % r.E)
+        if dloss.dtype != torch.float32 or dloss.numel() != 1:
+            raise TcGemmError(1, "dloss must be one float32 number")
+    if dlogits.shape != logits.shape:
+        raise TcGemmError(1, "dlogits must be %s (got %s)" % (tuple(logits.shape), tuple(dlogits.shape)))
+    code = _float_code(dlogits, "dlogits")
+    ldd, = _i32(ldd=_pitch(dlogits, "dlogits"))
+    return r, rref, code, ldd
+
+
+def moe_route_backward(logits, ids, dweights, dlogits, *, renormalize: bool = True, scale: float = 1.0,
+                       slope=None, dloss=None, stream=None):
+    """The gradient of a router's logits into dlogits [T, E] (of the logits'
+    type or f32), in one pass (tc_moe_route_backward_async): through the
+    weights that moe_route gave for ids with the same renormalize and scale,
+    whose gradient is dweights (float32 [T, top_k], or None), and through
+    moe_balance's loss, with its slope and the loss's gradient dloss (one
+    float32 number on the GPU), or neither.  Returns dlogits."""
+    device = _same_device(logits, ids, dweights, dlogits, slope, dloss)
+    renormalize, scale = bool(renormalize), float(scale)
+    sig = lambda t: None if t is None else (t.shape, t.stride(), t.dtype)  # noqa: E731
+    _, rref, code, ldd = _cached(
+        ("routeb", sig(logits), sig(ids), sig(dweights), sig(dlogits), renormalize, scale, sig(slope),
+         sig(dloss)),
+        lambda: _make_route_backward(logits, ids, dweights, dlogits, renormalize, scale, slope, dloss))
+    lib = _lib if _lib is not None else load_library()
+    ctx, s = _torch_stream(device, stream)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = lib.tc_moe_route_backward_async(ctx, rref, logits.data_ptr(), ids.data_ptr(), ptr(dweights),
+                                         ptr(slope), ptr(dloss), dlogits.data_ptr(), code, ldd, s)
+    if st != 0:
+        _check(st, ctx)
+    return dlogits
 
 
 def gemm_sync(a, b, c, *, alpha: float = 1.0, beta: float = 0.0, transpose_a: bool = False,

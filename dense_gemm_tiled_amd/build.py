@@ -29,7 +29,9 @@ _DT = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3}
 SOURCES = [("tcgemm", "tcgemm.cpp", []), ("epilogue_kernels", "epilogue_kernels.hip", []),
            ("thin_kernel", "thin_kernel.hip", []), ("qweight", "qweight.cpp", []),
            ("w4_format", "w4_format.hip", []), ("moe", "moe.cpp", []),
-           ("moe_route", "moe_route.hip", [])]
+           ("moe_route", "moe_route.hip", []), ("cross_entropy", "cross_entropy.cpp", []),
+           ("ce_kernels", "ce_kernels.hip", []), ("router", "router.cpp", []),
+           ("router_kernels", "router_kernels.hip", [])]
 for _name, _code in (("f16", 1), ("bf16", 2)):
     SOURCES += [("w4_gemm_" + _name, "w4_gemm.hip", ["-DW4_DT=%d" % _code]),
                 ("moe_layer_" + _name, "moe_layer.hip", ["-DMOE_DT=%d" % _code])]

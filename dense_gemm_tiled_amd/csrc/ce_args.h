@@ -1,0 +1,91 @@
+// ce_args.h -- what the host hands to the kernels of the cross entropy of a
+// linear layer that are no matrix products.  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tc_internal.h"
+
+namespace tcg {
+
+constexpr int kCeStatCols = 2048;   // columns a workgroup of ce_stat_kernel takes
+
+// Tokens' losses from the partial softmaxes of their products: parts
+// [num][T] of (maximum, sum) and the targets' products, in units of the
+// products (negated where scale < 0).
+struct CeJoinArgs {
+    const float2 *parts;
+    const float *logit;        // [T]; read where the target is inside [0, V)
+    const void *targets;
+    int32_t targets64;
+    int32_t T, V, num;
+    float scale;
+    float *loss, *lse;
+};
+
+// Partial softmaxes of stored products l [T, N] (fp32, rows ld apart), words
+// first .. first + N of V.
+struct CeStatArgs {
+    const float *l;
+    int64_t ld;
+    int32_t T, N, first, V;
+    float scale;
+    const void *targets;
+    int32_t targets64;
+    float2 *parts;             // [ceil(N / kCeStatCols)][T]
+    float *logit;
+};
+
+// The tokens of the backward pass: rows, and a copy of x whose rows are zeros
+// where the token adds nothing, at a pitch of whole 16-byte pieces.
+struct CePrepArgs {
+    const void *x;
+    int64_t ldx;               // elements
+    int32_t T, V, H;
+    int32_t dtype;
+    const void *targets;
+    int32_t targets64;
+    const float *lse, *grad;
+    int64_t grad_stride;       // elements
+    CeRow *rows;
+    void *xz;
+    int64_t xz_pitch;          // elements
+    // f16: the gradients are scaled by a power of two that brings the largest
+    // to 2^14 .. 2^15; its reciprocal, H times (null: no scaling)
+    float *unscale;
+};
+
+// The gradient of stored products: g = grad (exp(scale l - lse) - [target]),
+// fp32 over l itself, or the sum of `parts` 16-bit numbers, plane after plane.
+struct CeGradArgs {
+    float *l;
+    int64_t ld;                // elements, of l
+    int32_t T, N, first;
+    float scale;
+    const CeRow *rows;
+    void *g;
+    int64_t pitch, plane;      // elements of g; columns N .. pitch are written 0
+    int32_t dtype, parts;
+};
+
+// dx from its sums: times the reciprocal of the scale, 0 for tokens that add
+// nothing, rounded once.  src may be dst.
+struct CeFinishArgs {
+    const float *src;
+    int64_t ld_src;            // elements
+    void *dst;
+    int64_t ld_dst;
+    int32_t T, H;
+    int32_t dtype;             // of dst
+    const CeRow *rows;
+    const float *unscale;      // or null
+};
+
+}  // namespace tcg
+
+hipError_t tcg_launch_ce_join(const tcg::CeJoinArgs &a, hipStream_t s);
+hipError_t tcg_launch_ce_stat(const tcg::CeStatArgs &a, hipStream_t s);
+hipError_t tcg_launch_ce_prep(const tcg::CePrepArgs &a, int *launches, hipStream_t s);
+hipError_t tcg_launch_ce_grad(const tcg::CeGradArgs &a, hipStream_t s);
+hipError_t tcg_launch_ce_finish(const tcg::CeFinishArgs &a, hipStream_t s);

@@ -1,0 +1,622 @@
+// cross_entropy.cpp -- the C ABI's entry points for the cross entropy of a
+// linear layer.  They check everything before anything is enqueued and
+// allocate nothing: scratch memory is the caller's.
+
+#include "ce_args.h"
+#include "gemm_call.h"
+#include "qweight.h"
+
+#include <cmath>
+#include <cstring>
+
+namespace tcg {
+namespace {
+
+constexpr int64_t kMaxIndex = 0x7FFFFFFF;
+constexpr int64_t kMaxWords = 1 << 20;     // at a time: 256 rows of fp32 products stay below 2^31 bytes
+
+int64_t up_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool is_float(int dt) { return dt == TC_F32 || dt == TC_F16 || dt == TC_BF16; }
+
+struct CeProblem {
+    int64_t T, V, H, ldx, ldw;
+    int dt, es;
+    bool whole;        // x and W can be read by the direct-to-LDS loads as they are
+};
+
+tc_status_t check_ce(const tc_ce_desc *d, const void *x, const void *w, CeProblem *p, std::string *err) {
+    if (!d) return fail(err, TC_ERR_INVALID_ARGUMENT, "descriptor is NULL");
+    if (d->T < 1 || d->V < 1 || d->H < 1)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "dims must be >= 1 (T=%d V=%d H=%d)", d->T, d->V, d->H);
+    if (!is_float(d->dtype))
+        return fail(err, TC_ERR_UNSUPPORTED, "x and w must be f32, f16 or bf16 (got %s)", dt_name(d->dtype));
+    if (!std::isfinite(d->scale) || d->scale == 0.f)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "scale must be finite and not 0");
+    p->T = d->T;
+    p->V = d->V;
+    p->H = d->H;
+    p->dt = d->dtype;
+    p->es = dt_size(d->dtype);
+    p->ldx = d->ldx == 0 ? d->H : d->ldx;
+    p->ldw = d->ldw == 0 ? d->H : d->ldw;
+    if (p->ldx < d->H || p->ldw < d->H)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "ldx=%lld or ldw=%lld < H=%d", (long long)p->ldx,
+                    (long long)p->ldw, d->H);
+    const int64_t longest = (int64_t)kMaxRowElems * 2 / p->es;
+    if (p->ldx > longest || p->ldw > longest)
+        return fail(err, TC_ERR_OVERFLOW, "ldx=%lld or ldw=%lld > %lld", (long long)p->ldx, (long long)p->ldw,
+                    (long long)longest);
+    if ((uintptr_t)x % p->es != 0 || (uintptr_t)w % p->es != 0)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "x and w must be aligned to their elements");
+    // (tiles of 128 x 128, 256 threads each; rows, a workgroup each)
+    if (ceil_div(p->T, 128) * ceil_div(p->V, 128) > kMaxGroups || p->T > kMaxGroups)
+        return fail(err, TC_ERR_OVERFLOW, "T=%d by V=%d has more than %lld tiles of 128 x 128, or T is larger",
+                    d->T, d->V, (long long)kMaxGroups);
+    p->whole = p->es == 2 && p->H % 8 == 0 && p->ldw % 8 == 0 && (uintptr_t)w % 16 == 0;
+    return TC_OK;
+}
+
+// The tile class of the products with T rows and N words.  A round of 256 x
+// 256 tiles (one a CU) counts 1, of 128 x 128 tiles (two a CU) 0.625, as for
+// the plain product; 128 x 128 tiles that leave every CU at most one take the
+// variant with more loads in flight.
+int ce_class(int64_t T, int64_t N) {
+    const int64_t t256 = ceil_div(T, 256) * ceil_div(N, 256), t128 = ceil_div(T, 128) * ceil_div(N, 128);
+    if ((double)ceil_div(t256, 256) <= 0.625 * (double)ceil_div(t128, 512)) return TILE_256_DMA;
+    return t128 <= 256 ? TILE_128_DMA4 : TILE_128_DMA;
+}
+
+// Arguments of the products x W^T with an epilogue of their own.
+GemmArgs product_args(const CeProblem &p, const void *x, int64_t ldx, int64_t T, const void *w, int64_t N,
+                      float scale, int cls, int64_t *grid) {
+    GemmArgs a;
+    memset(&a, 0, sizeof a);
+    a.A = x;
+    a.B = w;
+    a.a_extent = ((T - 1) * ldx + p.H) * p.es;
+    a.b_extent = ((N - 1) * p.ldw + p.H) * p.es;
+    a.M = (int32_t)T;
+    a.N = (int32_t)N;
+    a.K = (int32_t)p.H;
+    a.lda = (int32_t)ldx;
+    a.ldb = (int32_t)p.ldw;
+    a.alpha = scale;
+    const TileShape ts = tile_shape(cls);
+    a.tiles_m = (int32_t)ceil_div(T, ts.bm);
+    a.tiles_n = (int32_t)ceil_div(N, ts.bn);
+    a.splits = 1;
+    a.k_per_split = (int32_t)up_to(p.H, kLdsRowBytes / p.es);
+    a.groups = 1;
+    a.band = 8;
+    *grid = (int64_t)a.tiles_m * a.tiles_n;
+    return a;
+}
+
+tc_gemm_desc gemm_desc(int64_t M, int64_t N, int64_t K, int dt, int cdt, bool ta, bool tb, float alpha,
+                       float beta, int64_t lda, int64_t ldb, int64_t ldc) {
+    tc_gemm_desc d;
+    d.M = (int32_t)M;
+    d.N = (int32_t)N;
+    d.K = (int32_t)K;
+    d.a_dtype = d.b_dtype = (tc_dtype_t)dt;
+    d.c_dtype = (tc_dtype_t)cdt;
+    d.accum_dtype = TC_F32;
+    d.transpose_a = ta;
+    d.transpose_b = tb;
+    d.alpha = alpha;
+    d.beta = beta;
+    d.lda = (int32_t)lda;
+    d.ldb = (int32_t)ldb;
+    d.ldc = (int32_t)ldc;
+    return d;
+}
+
+// ------------------------------------------------------------------ loss
+// Tokens are taken Tc at a time (bounds the partial softmaxes), and where the
+// products are stored, N words at a time.
+struct ForwardSpace {
+    bool fused;
+    int64_t Tc, N, pitch, num;         // num: shares of the words
+    int64_t parts, logit, l, gemm, gemm_bytes, bytes;
+};
+
+tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, ForwardSpace *f, std::string *err) {
+    f->fused = p.whole && p.ldx % 8 == 0 && (uintptr_t)x % 16 == 0;
+    f->Tc = p.T < 16384 ? p.T : 16384;
+    f->l = f->gemm = f->gemm_bytes = 0;
+    if (f->fused) {
+        f->N = p.V;
+        const int bn = tile_shape(ce_class(f->Tc, p.V)).bn, last = (int)(p.T % f->Tc);
+        f->num = 2 * ceil_div(p.V, bn);
+        if (last) {                    // (another class may take the last tokens)
+            const int64_t n = 2 * ceil_div(p.V, tile_shape(ce_class(last, p.V)).bn);
+            if (n > f->num) f->num = n;
+        }
+    } else {
+        // 2^26 products (256 MiB) at a time; W in spans of 2^31 elements
+        if (f->Tc > 4096) f->Tc = 4096;
+        while (f->Tc > 1 && f->Tc * p.ldx > kMaxIndex) f->Tc = (f->Tc + 1) / 2;
+        f->N = (1 << 26) / f->Tc;
+        if (f->N * p.ldw > kMaxIndex) f->N = kMaxIndex / p.ldw;
+        if (f->N > kMaxWords) f->N = kMaxWords;
+        if (f->N > kCeStatCols) f->N = f->N / kCeStatCols * kCeStatCols;
+        if (f->N > p.V) f->N = p.V;
+        f->pitch = up_to(f->N, 4);
+        f->num = ceil_div(p.V, f->N) * ceil_div(f->N, kCeStatCols);
+        for (const int64_t T : {f->Tc, p.T % f->Tc})
+            for (const int64_t N : {f->N, p.V % f->N}) {
+                if (T == 0 || N == 0) continue;
+                GemmCall c;
+                memset(&c, 0, sizeof c);
+                c.d = gemm_desc(T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, p.ldx, p.ldw, f->pitch);
+                c.A = x;
+                c.B = w;
+                int64_t bytes = 0;
+                const tc_status_t st = gemm_call_workspace(c, &bytes, err);
+                if (st != TC_OK) return st;
+                // (a later piece may start off 16-byte boundaries where the first does not)
+                if (bytes > f->gemm_bytes) f->gemm_bytes = bytes;
+                c.A = c.B = reinterpret_cast<const void *>((uintptr_t)p.es);
+                if (gemm_call_workspace(c, &bytes, err) == TC_OK && bytes > f->gemm_bytes) f->gemm_bytes = bytes;
+            }
+    }
+    f->parts = 0;
+    f->logit = up_to(f->num * f->Tc * 8, 256);
+    f->l = up_to(f->logit + f->Tc * 4, 256);
+    f->gemm = f->fused ? f->l : up_to(f->l + f->Tc * f->pitch * 4, 256);
+    f->bytes = f->gemm + f->gemm_bytes;
+    return TC_OK;
+}
+
+const void *at(const void *p, int64_t bytes) { return static_cast<const char *>(p) + bytes; }
+
+tc_status_t launch_failed(std::string *err, hipError_t e) {
+    (void)hipGetLastError();
+    return fail(err, TC_ERR_DEVICE, "kernel launch failed: %s", hipGetErrorString(e));
+}
+
+tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, const CeProblem &p,
+                        const ForwardSpace &f, const void *x, const void *w, const void *targets, float *loss,
+                        float *lse, char *ws, std::string *name, std::string *err) {
+    const int tbytes = d.targets64 ? 8 : 4;
+    for (int64_t t0 = 0; t0 < p.T; t0 += f.Tc) {
+        const int64_t T = p.T - t0 < f.Tc ? p.T - t0 : f.Tc;
+        const void *xt = at(x, t0 * p.ldx * p.es), *tt = at(targets, t0 * tbytes);
+        std::string here;
+        hipError_t e;
+        int64_t num = 0;
+        if (f.fused) {
+            const int cls = ce_class(T, p.V);
+            int64_t grid;
+            GemmArgs a = product_args(p, xt, p.ldx, T, w, p.V, d.scale, cls, &grid);
+            a.ws = ws + f.parts;
+            a.ce_targets = tt;
+            a.ce_targets64 = d.targets64;
+            a.ce_logit = reinterpret_cast<float *>(ws + f.logit);
+            num = 2 * a.tiles_n;
+            e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_STAT, a, grid, s->stream);
+            if (e != hipSuccess) return launch_failed(err, e);
+            ctx->dispatches += 1;
+            here = std::string(tcg_kernel_name(p.dt, false, true, cls)) + "_softmax";
+        } else {
+            for (int64_t v0 = 0; v0 < p.V; v0 += f.N) {
+                const int64_t N = p.V - v0 < f.N ? p.V - v0 : f.N;
+                GemmCall c;
+                memset(&c, 0, sizeof c);
+                c.d = gemm_desc(T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, p.ldx, p.ldw, f.pitch);
+                c.A = xt;
+                c.B = at(w, v0 * p.ldw * p.es);
+                c.C = ws + f.l;
+                std::string part;
+                const tc_status_t st =
+                    gemm_call_enqueue(ctx, s, c, ws + f.gemm, f.gemm_bytes, &part, err);
+                if (st != TC_OK) return st;
+                CeStatArgs a;
+                a.l = reinterpret_cast<const float *>(ws + f.l);
+                a.ld = f.pitch;
+                a.T = (int32_t)T;
+                a.N = (int32_t)N;
+                a.first = (int32_t)v0;
+                a.V = (int32_t)p.V;
+                a.scale = d.scale;
+                a.targets = tt;
+                a.targets64 = d.targets64;
+                a.parts = reinterpret_cast<float2 *>(ws + f.parts) + num * T;
+                a.logit = reinterpret_cast<float *>(ws + f.logit);
+                e = tcg_launch_ce_stat(a, s->stream);
+                if (e != hipSuccess) return launch_failed(err, e);
+                ctx->dispatches += 1;
+                num += ceil_div(N, kCeStatCols);
+                if (v0 == 0) here = part + "+ce_stat";
+            }
+        }
+        CeJoinArgs j;
+        j.parts = reinterpret_cast<const float2 *>(ws + f.parts);
+        j.logit = reinterpret_cast<const float *>(ws + f.logit);
+        j.targets = tt;
+        j.targets64 = d.targets64;
+        j.T = (int32_t)T;
+        j.V = (int32_t)p.V;
+        j.num = (int32_t)num;
+        j.scale = d.scale;
+        j.loss = loss + t0;
+        j.lse = lse + t0;
+        e = tcg_launch_ce_join(j, s->stream);
+        if (e != hipSuccess) return launch_failed(err, e);
+        ctx->dispatches += 1;
+        if (t0 == 0) *name = here + "+ce_join";
+    }
+    return TC_OK;
+}
+
+// ------------------------------------------------------------------ gradients
+// The gradient of N words' products at a time, all tokens: T x N numbers of
+// the inputs' type (parts times), then its two products.
+struct BackwardSpace {
+    bool fused;
+    bool own_dx;                       // dx is summed in the workspace
+    int parts, dx_parts, dw_parts;
+    int64_t N, pitch, xz_pitch;
+    int64_t rows, unscale, xz, acc, g, l, gemm, gemm_bytes, bytes;
+};
+
+GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
+                 float beta, const void *w) {
+    GemmCall c;
+    memset(&c, 0, sizeof c);
+    const int64_t ld = b.own_dx ? p.H : g.lddx == 0 ? p.H : g.lddx;
+    c.d = gemm_desc(p.T, p.H, N, p.dt, TC_F32, false, false, scale, beta, b.pitch, p.ldw, ld);
+    c.B = w;
+    c.whole[0] = true;
+    return c;
+}
+
+GemmCall dw_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
+                 float beta) {
+    GemmCall c;
+    memset(&c, 0, sizeof c);
+    const int64_t ld = g.lddw == 0 ? p.H : g.lddw;
+    c.d = gemm_desc(N, p.H, p.T, p.dt, g.dw_dtype, true, false, scale, beta, b.pitch, b.xz_pitch, ld);
+    c.whole[0] = c.whole[1] = true;
+    // (present or not is all that counts for the workspace)
+    c.col_scale = b.unscale >= 0 ? reinterpret_cast<const float *>(16) : nullptr;
+    return c;
+}
+
+GemmCall logits_call(const CeProblem &p, const BackwardSpace &b, int64_t N, const void *w) {
+    GemmCall c;
+    memset(&c, 0, sizeof c);
+    c.d = gemm_desc(p.T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, b.xz_pitch, p.ldw, b.pitch);
+    c.B = w;
+    c.whole[0] = true;
+    return c;
+}
+
+tc_status_t check_grads(const tc_ce_grads *g, const CeProblem &p, std::string *err) {
+    if (!g) return fail(err, TC_ERR_INVALID_ARGUMENT, "the gradients' descriptor is NULL");
+    if (!g->dx && !g->dw) return fail(err, TC_ERR_INVALID_ARGUMENT, "dx and dw must not both be NULL");
+    if (!g->grad || (uintptr_t)g->grad % 4 != 0)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "grad must be non-NULL and aligned to its elements");
+    if (g->grad_stride < 0 || g->grad_stride > kMaxIndex)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "grad_stride=%lld must be >= 0 and fit 32 bits",
+                    (long long)g->grad_stride);
+    const void *out[2] = {g->dx, g->dw};
+    const int dt[2] = {g->dx_dtype, g->dw_dtype};
+    const int32_t ld[2] = {g->lddx, g->lddw};
+    const char *name[2] = {"dx", "dw"};
+    for (int i = 0; i < 2; ++i) {
+        if (!out[i]) continue;
+        if (dt[i] != p.dt && dt[i] != TC_F32)
+            return fail(err, TC_ERR_UNSUPPORTED, "%s must be %s or f32 (got %s)", name[i], dt_name(p.dt),
+                        dt_name(dt[i]));
+        if (ld[i] != 0 && ld[i] < p.H)
+            return fail(err, TC_ERR_INVALID_ARGUMENT, "ld%s=%d < H=%lld", name[i], ld[i], (long long)p.H);
+        if ((int64_t)ld[i] * dt_size(dt[i]) > (int64_t)kMaxRowElems * 2)
+            return fail(err, TC_ERR_OVERFLOW, "rows of %s are %d apart: at most 8 MiB", name[i], ld[i]);
+        if ((uintptr_t)out[i] % dt_size(dt[i]) != 0)
+            return fail(err, TC_ERR_INVALID_ARGUMENT, "%s must be aligned to its elements", name[i]);
+    }
+    if (!std::isfinite(g->beta)) return fail(err, TC_ERR_INVALID_ARGUMENT, "beta must be finite");
+    return TC_OK;
+}
+
+tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale, const void *w,
+                          BackwardSpace *b, std::string *err) {
+    // A gradient in fp32 from 16-bit inputs: the products' gradient as the sum
+    // of as many numbers as fp32 shows (24 bits: three of bf16; two of f16
+    // have 22).  One in the inputs' type takes one: that rounding is as large
+    // as the result's own.
+    const int wide = p.dt == TC_BF16 ? 3 : p.dt == TC_F16 ? 2 : 1;
+    b->dx_parts = !g.dx ? 0 : g.dx_dtype == TC_F32 ? wide : 1;
+    b->dw_parts = !g.dw ? 0 : g.dw_dtype == TC_F32 ? wide : 1;
+    b->parts = b->dx_parts > b->dw_parts ? b->dx_parts : b->dw_parts;
+    b->fused = p.whole && b->parts == 1;
+    b->own_dx = g.dx && g.dx_dtype != TC_F32;
+    b->xz_pitch = up_to(p.H, 16 / p.es);
+    // Words at a time: 512 MiB of gradients, at least 8192 words (each piece
+    // reads and writes the sums of dx once).
+    int64_t N = (int64_t)(512 << 20) / (p.T * p.es * b->parts);
+    if (N < 8192) N = 8192;
+    const int64_t rows_w = g.dw && g.lddw > p.ldw ? g.lddw : p.ldw;
+    if (N > kMaxWords) N = kMaxWords;
+    if (N > kMaxIndex / p.T) N = kMaxIndex / p.T;
+    if (N > kMaxIndex / rows_w) N = kMaxIndex / rows_w;
+    if (N < 256)
+        return fail(err, TC_ERR_OVERFLOW, "T=%lld tokens or rows %lld apart leave less than 256 words at a time",
+                    (long long)p.T, (long long)rows_w);
+    const int64_t pieces = ceil_div(p.V, N);
+    const int64_t even = up_to(ceil_div(p.V, pieces), 256);   // pieces of about the same size
+    N = even < N ? even : N / 256 * 256;
+    b->N = N < p.V ? N : p.V;
+    b->pitch = up_to(b->N, 8);
+    if (p.T * b->pitch > kMaxIndex) return fail(err, TC_ERR_OVERFLOW, "T=%lld is too large", (long long)p.T);
+    const bool f16 = p.dt == TC_F16;
+    b->rows = 0;
+    b->unscale = f16 ? up_to(p.T * (int64_t)sizeof(CeRow), 256) : -1;
+    b->xz = up_to(p.T * (int64_t)sizeof(CeRow), 256) + (f16 ? up_to(p.H * 4, 256) : 0);
+    b->acc = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
+    b->g = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
+    b->l = up_to(b->g + p.T * b->pitch * p.es * b->parts, 256);
+    // (fp32: the gradient takes the place of its products)
+    b->gemm = b->fused || p.es == 4 ? b->l : up_to(b->l + p.T * b->pitch * 4, 256);
+    if (p.es == 4) b->l = b->g;
+    b->gemm_bytes = 0;
+    const void *odd = reinterpret_cast<const void *>((uintptr_t)p.es);
+    for (const int64_t n : {b->N, p.V % b->N}) {
+        if (n == 0) continue;
+        GemmCall c[6];
+        int k = 0;
+        // (a later piece of W may start off 16-byte boundaries)
+        for (const void *at : {w, odd}) {
+            if (at == odd && p.whole) continue;
+            if (!b->fused) c[k++] = logits_call(p, *b, n, at);
+            if (g.dx) {
+                c[k++] = dx_call(p, *b, g, scale, n, 0.f, at);
+                c[k++] = dx_call(p, *b, g, scale, n, 1.f, at);
+            }
+        }
+        tc_status_t st;
+        int64_t bytes = 0;
+        for (int i = 0; i < k; ++i) {
+            if ((st = gemm_call_workspace(c[i], &bytes, err)) != TC_OK) return st;
+            if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
+        }
+        for (const float beta : {g.beta, 1.f}) {
+            if (!g.dw) continue;
+            if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, n, beta), &bytes, err)) != TC_OK) return st;
+            if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
+        }
+    }
+    b->bytes = b->gemm + b->gemm_bytes;
+    return TC_OK;
+}
+
+tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, const CeProblem &p,
+                         const tc_ce_grads &g, const BackwardSpace &b, const void *x, const void *w,
+                         const void *targets, const float *lse, char *ws, std::string *name,
+                         std::string *err) {
+    const CeRow *rows = reinterpret_cast<const CeRow *>(ws + b.rows);
+    float *unscale = b.unscale >= 0 ? reinterpret_cast<float *>(ws + b.unscale) : nullptr;
+    CePrepArgs pa;
+    pa.x = x;
+    pa.ldx = p.ldx;
+    pa.T = (int32_t)p.T;
+    pa.V = (int32_t)p.V;
+    pa.H = (int32_t)p.H;
+    pa.dtype = p.dt;
+    pa.targets = targets;
+    pa.targets64 = d.targets64;
+    pa.lse = lse;
+    pa.grad = g.grad;
+    pa.grad_stride = g.grad_stride;
+    pa.rows = reinterpret_cast<CeRow *>(ws + b.rows);
+    pa.xz = ws + b.xz;
+    pa.xz_pitch = b.xz_pitch;
+    pa.unscale = unscale;
+    int launches = 0;
+    hipError_t e = tcg_launch_ce_prep(pa, &launches, s->stream);
+    ctx->dispatches += launches;
+    if (e != hipSuccess) return launch_failed(err, e);
+    *name = "ce_prep";
+    float *const sums = reinterpret_cast<float *>(b.own_dx ? ws + b.acc : static_cast<char *>(g.dx));
+    const int64_t plane = p.T * b.pitch;
+    tc_status_t st;
+    for (int64_t v0 = 0; v0 < p.V; v0 += b.N) {
+        const int64_t N = p.V - v0 < b.N ? p.V - v0 : b.N;
+        const void *wv = at(w, v0 * p.ldw * p.es);
+        std::string here;
+        if (b.fused) {
+            const int cls = ce_class(p.T, N);
+            int64_t grid;
+            GemmArgs a = product_args(p, ws + b.xz, b.xz_pitch, p.T, wv, N, d.scale, cls, &grid);
+            a.C = ws + b.g;
+            a.ldc = (int32_t)b.pitch;
+            a.c_extent = p.T * b.pitch * 2;
+            a.ce_first = (int32_t)v0;
+            a.ce_rows = rows;
+            e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_GRAD, a, grid, s->stream);
+            if (e != hipSuccess) return launch_failed(err, e);
+            here = std::string(tcg_kernel_name(p.dt, false, true, cls)) + "_grad";
+        } else {
+            GemmCall c = logits_call(p, b, N, wv);
+            c.A = ws + b.xz;
+            c.C = ws + b.l;
+            if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &here, err)) != TC_OK) return st;
+            CeGradArgs ga;
+            ga.l = reinterpret_cast<float *>(ws + b.l);
+            ga.ld = b.pitch;
+            ga.T = (int32_t)p.T;
+            ga.N = (int32_t)N;
+            ga.first = (int32_t)v0;
+            ga.scale = d.scale;
+            ga.rows = rows;
+            ga.g = ws + b.g;
+            ga.pitch = b.pitch;
+            ga.plane = plane;
+            ga.dtype = p.dt;
+            ga.parts = b.parts;
+            e = tcg_launch_ce_grad(ga, s->stream);
+            if (e != hipSuccess) return launch_failed(err, e);
+            here += "+ce_grad";
+        }
+        ctx->dispatches += 1;
+        for (int k = 0; k < b.parts; ++k) {
+            const void *gk = ws + b.g + k * plane * p.es;
+            std::string part;
+            if (k < b.dx_parts) {
+                GemmCall c = dx_call(p, b, g, d.scale, N, v0 > 0 || k > 0 ? 1.f : 0.f, wv);
+                c.A = gk;
+                c.C = sums;
+                if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
+                here += "+" + part;
+            }
+            part.clear();
+            if (k < b.dw_parts) {
+                GemmCall c = dw_call(p, b, g, d.scale, N, k > 0 ? 1.f : g.beta);
+                c.A = gk;
+                c.B = ws + b.xz;
+                c.C = static_cast<char *>(g.dw) + v0 * (g.lddw == 0 ? p.H : g.lddw) * dt_size(g.dw_dtype);
+                c.col_scale = unscale;
+                if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
+                here += "+" + part;
+            }
+        }
+        if (v0 == 0) *name += "+" + here;
+    }
+    if (g.dx) {
+        CeFinishArgs f;
+        f.src = sums;
+        f.ld_src = b.own_dx || g.lddx == 0 ? p.H : g.lddx;
+        f.dst = g.dx;
+        f.ld_dst = g.lddx == 0 ? p.H : g.lddx;
+        f.T = (int32_t)p.T;
+        f.H = (int32_t)p.H;
+        f.dtype = g.dx_dtype;
+        f.rows = rows;
+        f.unscale = unscale;
+        e = tcg_launch_ce_finish(f, s->stream);
+        if (e != hipSuccess) return launch_failed(err, e);
+        ctx->dispatches += 1;
+        *name += "+ce_finish";
+    }
+    return TC_OK;
+}
+
+tc_status_t check_targets(const tc_ce_desc &d, const void *targets, std::string *err) {
+    if (!targets || (uintptr_t)targets % (d.targets64 ? 8 : 4) != 0)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "targets must be non-NULL and aligned to their elements");
+    return TC_OK;
+}
+
+tc_status_t check_space(const void *workspace, int64_t given, int64_t need, std::string *err) {
+    if (!workspace || (uintptr_t)workspace % 16 != 0 || given < need)
+        return fail(err, TC_ERR_INVALID_ARGUMENT,
+                    "the workspace must be 16-byte aligned and hold %lld bytes (%lld given)", (long long)need,
+                    (long long)given);
+    return TC_OK;
+}
+
+}  // namespace
+}  // namespace tcg
+
+using namespace tcg;
+
+extern "C" {
+
+tc_status_t tc_cross_entropy_workspace(const tc_ce_desc *d, const void *x, const void *w, int64_t *bytes) {
+    if (!bytes) return TC_ERR_INVALID_ARGUMENT;
+    CeProblem p;
+    ForwardSpace f;
+    tc_status_t st = check_ce(d, x, w, &p, nullptr);
+    if (st == TC_OK) st = plan_forward(p, x, w, &f, nullptr);
+    if (st == TC_OK) *bytes = f.bytes;
+    return st;
+}
+
+tc_status_t tc_cross_entropy_async(tc_context *ctx, const tc_ce_desc *d, const void *x, const void *w,
+                                   const void *targets, float *loss, float *lse, void *workspace,
+                                   int64_t workspace_bytes, tc_stream *s) {
+    if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
+    ctx->last_error.clear();
+    std::string *err = &ctx->last_error;
+    CeProblem p;
+    ForwardSpace f;
+    tc_status_t st;
+    if ((st = check_ce(d, x, w, &p, err)) != TC_OK) return st;
+    if (!x || !w || !loss || !lse || !s)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "x, w, loss, lse and the stream must be non-NULL");
+    if ((st = check_targets(*d, targets, err)) != TC_OK) return st;
+    if (((uintptr_t)loss | (uintptr_t)lse) % 4 != 0)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "loss and lse must be aligned to their elements");
+    if ((st = plan_forward(p, x, w, &f, err)) != TC_OK) return st;
+    if ((st = check_space(workspace, workspace_bytes, f.bytes, err)) != TC_OK) return st;
+    const Range r[] = {{"loss", loss, p.T * 4},
+                       {"lse", lse, p.T * 4},
+                       {"workspace", workspace, f.bytes},
+                       {"x", x, span(p.T, p.H, p.ldx) * p.es},
+                       {"w", w, span(p.V, p.H, p.ldw) * p.es},
+                       {"targets", targets, p.T * (d->targets64 ? 8 : 4)}};
+    if ((st = check_ranges(r, 6, 3, false, err)) != TC_OK) return st;
+    const DeviceScope dev(ctx);
+    if (dev.status != TC_OK) return dev.status;
+    if ((st = check_ranges(r, 6, 3, true, err)) != TC_OK) return st;
+    std::string name;
+    st = run_forward(ctx, s, *d, p, f, x, w, targets, loss, lse, static_cast<char *>(workspace), &name, err);
+    if (st == TC_OK) ctx->last_kernel = name;
+    return st;
+}
+
+tc_status_t tc_cross_entropy_backward_workspace(const tc_ce_desc *d, const tc_ce_grads *g, const void *x,
+                                                const void *w, int64_t *bytes) {
+    if (!bytes) return TC_ERR_INVALID_ARGUMENT;
+    CeProblem p;
+    BackwardSpace b;
+    tc_status_t st = check_ce(d, x, w, &p, nullptr);
+    if (st == TC_OK) st = check_grads(g, p, nullptr);
+    if (st == TC_OK) st = plan_backward(p, *g, d->scale, w, &b, nullptr);
+    if (st == TC_OK) *bytes = b.bytes;
+    return st;
+}
+
+tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d, const tc_ce_grads *g,
+                                            const void *x, const void *w, const void *targets,
+                                            const float *lse, void *workspace, int64_t workspace_bytes,
+                                            tc_stream *s) {
+    if (!ctx) return TC_ERR_INVALID_ARGUMENT;
+    const Turn turn(ctx);
+    ctx->last_error.clear();
+    std::string *err = &ctx->last_error;
+    CeProblem p;
+    BackwardSpace b;
+    tc_status_t st;
+    if ((st = check_ce(d, x, w, &p, err)) != TC_OK) return st;
+    if (!x || !w || !lse || !s)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "x, w, lse and the stream must be non-NULL");
+    if ((st = check_targets(*d, targets, err)) != TC_OK) return st;
+    if ((uintptr_t)lse % 4 != 0)
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "lse must be aligned to its elements");
+    if ((st = check_grads(g, p, err)) != TC_OK) return st;
+    if ((st = plan_backward(p, *g, d->scale, w, &b, err)) != TC_OK) return st;
+    if ((st = check_space(workspace, workspace_bytes, b.bytes, err)) != TC_OK) return st;
+    const Range r[] = {
+        {"workspace", workspace, b.bytes},
+        {"dx", g->dx, g->dx ? span(p.T, p.H, g->lddx == 0 ? p.H : g->lddx) * dt_size(g->dx_dtype) : 0},
+        {"dw", g->dw, g->dw ? span(p.V, p.H, g->lddw == 0 ? p.H : g->lddw) * dt_size(g->dw_dtype) : 0},
+        {"x", x, span(p.T, p.H, p.ldx) * p.es},
+        {"w", w, span(p.V, p.H, p.ldw) * p.es},
+        {"targets", targets, p.T * (d->targets64 ? 8 : 4)},
+        {"lse", lse, p.T * 4},
+        {"grad", g->grad, ((p.T - 1) * g->grad_stride + 1) * 4}};
+    if ((st = check_ranges(r, 8, 3, false, err)) != TC_OK) return st;
+    const DeviceScope dev(ctx);
+    if (dev.status != TC_OK) return dev.status;
+    if ((st = check_ranges(r, 8, 3, true, err)) != TC_OK) return st;
+    std::string name;
+    st = run_backward(ctx, s, *d, p, *g, b, x, w, targets, lse, static_cast<char *>(workspace), &name, err);
+    if (st == TC_OK) ctx->last_kernel = name;
+    return st;
+}
+
+}  // extern "C"

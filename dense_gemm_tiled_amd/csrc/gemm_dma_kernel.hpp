@@ -422,6 +422,13 @@ struct RingSrc {
 // (unsigned arithmetic: an out-of-range offset stays out of range).
 __device__ inline int group_voff(int off, int j) { return (int)((uint32_t)off - (uint32_t)(j * 1024)); }
 
+// Row m's target, -1 where it is outside [0, N).
+__device__ inline int ce_load_target(const GemmArgs &args, int64_t m) {
+    const int64_t t = args.ce_targets64 ? static_cast<const int64_t *>(args.ce_targets)[m]
+                                        : (int64_t)static_cast<const int32_t *>(args.ce_targets)[m];
+    return t >= 0 && t < args.N ? (int)t : -1;
+}
+
 // Epilogue variants of the kernel: beta == 0 and no fused epilogue; beta != 0
 // (16-bit C tiles staged through LDS); the fused epilogue (bias and
 // activation, any beta, C_old read per block).  The last one is a separate
@@ -444,13 +451,16 @@ constexpr int EPI_PLAIN = 0, EPI_BETA = 1, EPI_FUSED = 2;
 // just left).  So both sub-steps issue half of a tile's loads -- with two
 // stages all of them go out in sub-step 1 -- still with one barrier per
 // K-tile, and tile t+2 has from then to the middle of tile t+1 to land.
-template <int DT, bool TA, bool TB, int OUT, int BM, int BN, int NW, int OCC, bool KMASK,
+template <int DT, bool TA, bool TB, int OUTSEL, int BM, int BN, int NW, int OCC, bool KMASK,
           int EPI, int NST, int MS>
 __global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64),
                           amdgpu_waves_per_eu(NW / 4 * OCC, NW / 4 * OCC)))
 void gemm_dma_kernel(const GemmArgs args) {
     constexpr int ES = dt_size(DT);
     static_assert(ES == 2 || ES == 1, "direct-to-LDS kernel: 16-bit and int8 inputs");
+    // the cross entropy's epilogues (the code after them is never reached)
+    constexpr bool CE_STAT = OUTSEL == OUT_CE_STAT, CE_GRAD = OUTSEL == OUT_CE_GRAD;
+    constexpr int OUT = CE_STAT || CE_GRAD ? DT : OUTSEL;
     static_assert(NW == 4 || NW == 8, "4 or 8 waves");
     constexpr int BK = kLdsRowBytes / ES;
     constexpr bool A_MC = TA, B_MC = !TB;
@@ -647,6 +657,14 @@ void gemm_dma_kernel(const GemmArgs args) {
     if constexpr (EPI_LDS > 1) {
         if (tid < BN)
             load_epi1<OUT>(make_epi<OUT>(args, z, N), n0 + tid, N, epi_b, epi_s);
+    }
+    // cross entropy: the row of this thread's number waits in registers, too
+    [[maybe_unused]] int ce_target = -1;
+    [[maybe_unused]] u32x4 ce_row{};
+    if constexpr (CE_STAT) {
+        if (tid < BM && m0 + tid < M) ce_target = ce_load_target(args, m0 + tid);
+    } else if constexpr (CE_GRAD) {
+        if (tid < BM && m0 + tid < M) ce_row = *reinterpret_cast<const u32x4 *>(args.ce_rows + m0 + tid);
     }
     // beta != 0 with a 16-bit C tile inside C: the epilogue reads C_old from
     // an LDS image of the tile (below).  On the ring with at least two
@@ -868,6 +886,146 @@ void gemm_dma_kernel(const GemmArgs args) {
         return wn * WTN + j * MS + (MS == 16 ? 4 * (lane >> 4) : 8 * q + 4 * (lane >> 5));
     };
     constexpr int CES = dt_size(OUT == OUT_PARTIAL ? DT_F32 : OUT);
+    if constexpr (CE_STAT) {
+        // The softmax of the tile's rows over this wave's columns, from the
+        // accumulators: per row the largest value m (in the accumulator's
+        // units; clamped, so that a row of -inf sums to 0 and one with +inf to
+        // inf) and sum_n exp2((v_n - m) a2), written once.  The difference is
+        // formed first (v a2 - m a2 in one step, 1 instruction less of 6,
+        // would be off by the rounding of m a2).  Each row is spread over 4
+        // lanes (16 columns of 4 apart).
+        static_assert(MS == 16 && DT != DT_I8, "16 x 16 blocks of float sums");
+        asm volatile("s_barrier" ::: "memory");
+        int *tgt = reinterpret_cast<int *>(smem);
+        if (tid < BM) tgt[tid] = ce_target;
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (args.alpha < 0.f) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    acc[i][j] = -acc[i][j];
+                    asm volatile("" : "+a"(acc[i][j]));
+                }
+        }
+        if (n0 + BN > N) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n0 + nl_of(j, 0) + e >= N) acc[i][j][e] = -INFINITY;
+                    asm volatile("" : "+a"(acc[i][j]));
+                }
+        }
+        const float a2 = __builtin_fabsf(args.alpha) * kLog2E, limit = ce_limit(a2);
+        float2 *part = static_cast<float2 *>(args.ws) + (int64_t)(tn * WNW + wn) * M + m0;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int ml = ml_of(i);
+            const bool row_in = m0 + ml < M;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, acc[i][j][e]);
+            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
+            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+            mx = __builtin_fminf(__builtin_fmaxf(mx, -limit), limit);
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s += __builtin_amdgcn_exp2f((acc[i][j][e] - mx) * a2);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (lane < 16 && row_in) part[ml] = make_float2(mx, s);
+            // the target's product, from the lane that holds it
+            const int d = tgt[ml] - (n0 + nl_of(0, 0));
+            const bool hit = row_in && d >= 0 && d < WTN && (d & 12) == 0;
+            if (__any(hit)) {
+                float v = 0.f;
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v = d == 16 * j + e ? acc[i][j][e] : v;
+                if (hit) args.ce_logit[m0 + ml] = v;
+            }
+        }
+        return;
+    }
+    if constexpr (CE_GRAD) {
+        // grad (exp(alpha v - lse) - [n is the target]) in 16 bits.  The
+        // waves' tiles go out along rows through LDS, as the plain epilogue's
+        // do; the target's value, expm1 of its own difference (1 taken off a
+        // rounded exponential would leave nothing near 1), replaces the one
+        // staged for it.
+        static_assert(MS == 16 && DT != DT_I8, "16 x 16 blocks of float sums");
+        constexpr int RB = BM * (int)sizeof(CeRow);
+        constexpr int PITCH = (WTN + 16) * 2, REGION = (LDS_BYTES - RB) / NW / 16 * 16;
+        constexpr int BAND = WTM * PITCH <= REGION ? WTM : WTM / 2;
+        static_assert(BAND * PITCH <= REGION && BAND % MS == 0, "staging band fits");
+        asm volatile("s_barrier" ::: "memory");
+        TCG_LDS char *rows = (TCG_LDS char *)(size_t)lds;
+        if (tid < BM) *(TCG_LDS u32x4 *)(rows + tid * 16) = ce_row;
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        TCG_LDS char *reg = (TCG_LDS char *)(size_t)(lds + RB + wave * REGION);
+        const int64_t org = (int64_t)m0 * args.ldc + n0;
+        const __amdgpu_buffer_rsrc_t rg =
+            make_rsrc(static_cast<char *>(args.C) + org * 2, args.c_extent - org * 2);
+        const bool whole = n0 + BN <= N;
+        const float alpha = args.alpha;
+#pragma unroll
+        for (int c0 = 0; c0 < WTM; c0 += BAND) {
+#pragma unroll
+            for (int ib = 0; ib < BAND / MS; ++ib) {
+                const int i = c0 / MS + ib, ml = ml_of(i);
+                const u32x4 q = *(const TCG_LDS u32x4 *)(rows + ml * 16);
+                const float lse = as_f32(q[0]), g = as_f32(q[1]);
+                TCG_LDS char *row = reg + (ml - wm * WTM - c0) * PITCH;
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = g * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], alpha, -lse) * kLog2E);
+                        if (!whole && n0 + nl_of(j, 0) + e >= N) v[e] = 0.f;
+                    }
+                    *(TCG_LDS u32x2 *)(row + (nl_of(j, 0) - wn * WTN) * 2) =
+                        u32x2{pack2_16<OUT>(v[0], v[1]), pack2_16<OUT>(v[2], v[3])};
+                }
+                const int d = (int)q[2] - args.ce_first - (n0 + nl_of(0, 0));
+                const bool hit = (int)q[2] >= 0 && d >= 0 && d < WTN && (d & 12) == 0;
+                if (__any(hit)) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v = d == 16 * j + e ? acc[i][j][e] : v;
+                    v = g * expm1f(__builtin_fmaf(v, alpha, -lse));
+                    if (hit)
+                        *(TCG_LDS unsigned short *)(row + (4 * (lane >> 4) + d) * 2) =
+                            (unsigned short)pack2_16<OUT>(v, 0.f);
+                }
+            }
+            // (the LDS runs one wave's accesses in order)
+            constexpr int LPR = WTN / 8, RPI = 64 / LPR;   // lanes per row, rows per read
+            const int ch = lane % LPR;
+#pragma unroll
+            for (int t = 0; t < BAND / RPI; ++t) {
+                const int row = t * RPI + lane / LPR;
+                const u32x4 v = *(const TCG_LDS u32x4 *)(reg + row * PITCH + ch * 16);
+                // (rows past M start past the store range; a row's 16-byte
+                // pieces are whole)
+                if (n0 + wn * WTN + ch * 8 < args.ldc)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        v, rg, (wm * WTM + c0 + row) * args.ldc * 2 + wn * WTN * 2 + ch * 16, 0, 0);
+            }
+        }
+        return;
+    }
     // Interior tiles whose output rows are whole 16-byte chunks store through
     // LDS (C, or the split-K partial sums, rows ld values apart, at r):
     // each wave writes its tile, SCH rows at a time, into a region of its own

@@ -17,6 +17,9 @@ namespace {
 // classes only for 16-bit and int8 inputs.
 constexpr bool out_ok(int cls, int out) {
     if (is_dma_class(cls) && TCG_DT == DT_F32) return false;
+    if (out == OUT_CE_STAT || out == OUT_CE_GRAD)
+        return TCG_TA == 0 && TCG_TB == 1 && (TCG_DT == DT_F16 || TCG_DT == DT_BF16) &&
+               (cls == TILE_256_DMA || cls == TILE_128_DMA || cls == TILE_128_DMA4);
     if (out == OUT_PARTIAL)
         return cls == TILE_64 || cls == TILE_128 || cls == TILE_128_DMA || cls == TILE_128_DMA4 ||
                cls == TILE_256_DMA;
@@ -101,6 +104,8 @@ hipError_t launch_cls(int out, const GemmArgs &args, int64_t grid, hipStream_t s
     case DT_BF16: return launch_one<CLS, DT_BF16>(args, grid, stream);
     case DT_I32: return launch_one<CLS, DT_I32>(args, grid, stream);
     case OUT_PARTIAL: return launch_one<CLS, OUT_PARTIAL>(args, grid, stream);
+    case OUT_CE_STAT: return launch_one<CLS, OUT_CE_STAT>(args, grid, stream);
+    case OUT_CE_GRAD: return launch_one<CLS, OUT_CE_GRAD>(args, grid, stream);
     default: return hipErrorInvalidValue;
     }
 }

@@ -2,8 +2,7 @@
 // check everything before anything is enqueued and allocate nothing: the
 // layer's scratch memory is the caller's.
 
-#include "moe_args.h"
-#include "qweight.h"
+#include "moe_host.h"
 
 #include <cmath>
 #include <cstring>
@@ -12,6 +11,8 @@ namespace tcg {
 namespace {
 
 int64_t up_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+}  // namespace
 
 tc_status_t check_route(const tc_route_desc *r, RouteArgs *a, int64_t *bytes, std::string *err) {
     if (!r) return fail(err, TC_ERR_INVALID_ARGUMENT, "routing descriptor is NULL");
@@ -40,6 +41,8 @@ tc_status_t check_route(const tc_route_desc *r, RouteArgs *a, int64_t *bytes, st
     *bytes = span(r->T, r->E, a->ld) * dt_size(r->dtype);
     return TC_OK;
 }
+
+namespace {
 
 // The layer's workspace: offsets of its parts.
 struct MoeSpace {

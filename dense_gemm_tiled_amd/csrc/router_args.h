@@ -1,0 +1,37 @@
+// router_args.h -- what the host hands to the kernels of a router's balance
+// loss and gradient.  Not part of the public ABI.
+#pragma once
+
+#include "moe_args.h"
+
+namespace tcg {
+
+constexpr int kBalanceGroups = 256;       // workgroups whose sums are joined, at most
+
+struct BalanceArgs {
+    RouteArgs route;           // logits, sizes, ids
+    float coef;
+    float *loss;
+    int32_t *counts;           // [E]
+    float *slope;              // [E]
+    // workspace: per workgroup the sums of p, the counts and the tokens
+    float *part_p;             // [groups][E]
+    int32_t *part_count;       // [groups][E]
+    int32_t *part_tokens;      // [groups]
+};
+
+struct RouteGradArgs {
+    RouteArgs route;
+    const float *dweights;     // [T, top_k], or null
+    const float *slope, *dloss;   // [E], [1], or both null
+    void *dlogits;
+    int64_t ldd;               // elements
+    int32_t d_dtype;
+};
+
+}  // namespace tcg
+
+// workgroups a balance loss is spread over (1: one launch, no workspace used)
+int tcg_balance_groups(const tcg::RouteArgs &a);
+hipError_t tcg_launch_balance(const tcg::BalanceArgs &a, int *launches, hipStream_t s);
+hipError_t tcg_launch_route_grad(const tcg::RouteGradArgs &a, hipStream_t s);

@@ -1,0 +1,469 @@
+// router_kernels.hip -- the balance loss of a router and the gradient of its
+// logits.  A token's logits are spread over L lanes of a wave (64 / L tokens a
+// wave), V neighbours at a time: expert (s L + lane) V + i is value i of the
+// lane's s-th load.
+#include "gemm_kernel.hpp"
+
+#include "router_args.h"
+
+namespace tcg {
+namespace {
+
+constexpr float kMaxFloat = 3.4028235e38f;
+
+// Sum and maximum over the L lanes of a token, in all of them: rotations
+// inside rows of 16 lanes, then exchanges of rows and of halves, all on the
+// vector ALU (reads across lanes through LDS would take as long as the loads).
+template <int CTRL>
+__device__ inline float ror(float x) {
+    return as_f32((u32)__builtin_amdgcn_update_dpp(0, (int)as_u32(x), CTRL, 0xF, 0xF, false));
+}
+template <int L, class F>
+__device__ inline float over_token(float x, F f) {
+    x = f(x, ror<0x128>(x));   // row_ror 8, 4, 2, 1
+    x = f(x, ror<0x124>(x));
+    x = f(x, ror<0x122>(x));
+    x = f(x, ror<0x121>(x));
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(as_u32(x), as_u32(x), false, false);
+        x = f(as_f32((u32)r[0]), as_f32((u32)r[1]));
+    }
+    if constexpr (L >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(as_u32(x), as_u32(x), false, false);
+        x = f(as_f32((u32)r[0]), as_f32((u32)r[1]));
+    }
+    return x;
+}
+template <int L>
+__device__ inline float sum_token(float x) {
+    return over_token<L>(x, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ inline float max_token(float x) {
+    return over_token<L>(x, [](float a, float b) { return fmaxf(a, b); });
+}
+
+__device__ inline float decode16(u32 h, int dtype) {
+    return dtype == DT_F16 ? from_f16_bits(h) : from_bf16_bits(h);
+}
+
+// V neighbouring logits from element i on; those from E on have no part.
+template <int V>
+__device__ inline void load_logits(const RouteArgs &a, int64_t row, int e, float (&v)[V]) {
+    if constexpr (V == 4) {
+        // (E is a multiple of 4, rows and base whole pieces of 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = -INFINITY;
+        if (e >= a.E) return;
+        if (a.dtype == DT_F32) {
+            const f32x4 w = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.logits) + row + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = w[i];
+        } else {
+            const u32x2 w =
+                *reinterpret_cast<const u32x2 *>(static_cast<const unsigned short *>(a.logits) + row + e);
+            v[0] = decode16(w.x & 0xFFFFu, a.dtype);
+            v[1] = decode16(w.x >> 16, a.dtype);
+            v[2] = decode16(w.y & 0xFFFFu, a.dtype);
+            v[3] = decode16(w.y >> 16, a.dtype);
+        }
+    } else {
+        v[0] = -INFINITY;
+        if (e >= a.E) return;
+        v[0] = a.dtype == DT_F32 ? static_cast<const float *>(a.logits)[row + e]
+                                 : decode16(static_cast<const unsigned short *>(a.logits)[row + e], a.dtype);
+    }
+}
+
+// -inf and NaN have no part, +inf counts as the largest finite number.
+__device__ inline float clean(float v) { return v > -INFINITY ? fminf(v, kMaxFloat) : -INFINITY; }
+
+// v := the softmax of a token's logits (all 0 where none has a part).
+template <int V, int L, int S>
+__device__ inline void softmax_token(float (&v)[S][V]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[s][i] = clean(v[s][i]);
+            m = fmaxf(m, v[s][i]);
+        }
+    m = fmaxf(max_token<L>(m), -kMaxFloat);
+    float z = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[s][i] = v[s][i] > -INFINITY ? expf(v[s][i] - m) : 0.f;
+            z += v[s][i];
+        }
+    z = sum_token<L>(z);
+    const float r = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[s][i] *= r;
+}
+
+// The loss, the counts and the slopes from the sums, by one workgroup of 1024:
+// thread e (and 512 threads at most) holds expert e's.
+__device__ inline void balance_result(const BalanceArgs &a, int tid, double p, int count, int tokens) {
+    __shared__ double dot[16];
+    __shared__ int64_t tot[16];
+    double d = p * count;
+    int64_t c = count;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        d += __shfl_xor(d, o);
+        c += __shfl_xor((long long)c, o);
+    }
+    if ((tid & 63) == 0) {
+        dot[tid >> 6] = d;
+        tot[tid >> 6] = c;
+    }
+    __syncthreads();
+    d = 0.0;
+    c = 0;
+    for (int w = 0; w < 16; ++w) {
+        d += dot[w];
+        c += tot[w];
+    }
+    const int E = a.route.E;
+    const double scale = c > 0 ? (double)a.coef / ((double)c * tokens) : 0.0;
+    if (tid < E) {
+        a.counts[tid] = count;
+        a.slope[tid] = (float)(scale * (double)((int64_t)E * count - c));
+    }
+    if (tid == 0) a.loss[0] = (float)(scale * E * d);
+}
+
+// Each workgroup's share of the tokens: sums of p in registers (a lane has the
+// same experts for every token), the next token's logits on the way while one
+// is taken.  Bound by those loads and by the cross-lane steps of the softmax.
+// ONE: the only workgroup goes on to the result.
+template <int V, int L, int S, bool ONE>
+__global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
+    constexpr int TOK = 1024 / L;                 // tokens at a time
+    __shared__ float sums[16 * kMaxExperts];      // [TOK][L S V]
+    __shared__ int count[kMaxExperts];
+    __shared__ int tokens;
+    static_assert(TOK * L * S * V <= 16 * kMaxExperts, "the tokens' sums fit");
+    const RouteArgs &r = a.route;
+    const int tid = threadIdx.x, l = tid % L, g = tid / L;
+    for (int e = tid; e < kMaxExperts; e += 1024) count[e] = 0;
+    if (tid == 0) tokens = 0;
+    __syncthreads();
+    float p[S][V] = {}, v[S][V], next[S][V];
+    int id = -1, next_id = -1, mine = 0;
+    const int64_t step = (int64_t)gridDim.x * TOK;
+    auto load = [&](int64_t t, float (&to)[S][V], int &to_id) {
+        to_id = -1;
+        if (t < r.T) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) load_logits<V>(r, t * r.ld, (s * L + l) * V, to[s]);
+            if (l < r.top_k) to_id = r.ids[t * r.top_k + l];
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i) to[s][i] = -INFINITY;
+        }
+    };
+    int64_t t = (int64_t)blockIdx.x * TOK + g;
+    load(t, v, id);
+    // (every lane of a wave stays until the last of its tokens is done)
+    for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < r.T; t0 += step, t += step) {
+        load(t + step, next, next_id);
+        const bool inside = id >= 0 && id < r.E;
+        if (inside) atomicAdd(&count[id], 1);
+        const bool alive = max_token<L>(inside ? 1.f : 0.f) > 0.f;
+        softmax_token<V, L, S>(v);
+        if (alive) {
+            mine += 1;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i) p[s][i] += v[s][i];
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[s][i] = next[s][i];
+        id = next_id;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sums[g * (L * S * V) + (s * L + l) * V + i] = p[s][i];
+    if (l == 0 && mine) atomicAdd(&tokens, mine);
+    __syncthreads();
+    double total = 0.0;
+    if (tid < r.E) {
+#pragma unroll 4
+        for (int k = 0; k < TOK; ++k) total += sums[k * (L * S * V) + tid];
+    }
+    if constexpr (ONE) {
+        balance_result(a, tid, total, tid < r.E ? count[tid] : 0, tokens);
+    } else {
+        if (tid < r.E) {
+            a.part_p[(int64_t)blockIdx.x * r.E + tid] = (float)total;
+            a.part_count[(int64_t)blockIdx.x * r.E + tid] = count[tid];
+        }
+        if (tid == 0) a.part_tokens[blockIdx.x] = tokens;
+    }
+}
+
+// The workgroups' sums joined, E to a slice of the threads.
+__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int groups) {
+    __shared__ double sum[1024];
+    __shared__ int cnt[1024];
+    __shared__ int tokens;
+    const int E = a.route.E, tid = threadIdx.x;
+    const int slices = 1024 / E, slice = tid / E, e = tid - slice * E;
+    if (tid == 0) tokens = 0;
+    __syncthreads();
+    double p = 0.0;
+    int c = 0;
+    if (slice < slices) {
+#pragma unroll 8
+        for (int w = slice; w < groups; w += slices) {
+            p += a.part_p[(int64_t)w * E + e];
+            c += a.part_count[(int64_t)w * E + e];
+        }
+    }
+    if (tid < groups) atomicAdd(&tokens, a.part_tokens[tid]);
+    sum[tid] = p;
+    cnt[tid] = c;
+    __syncthreads();
+    p = 0.0;
+    c = 0;
+    if (tid < E) {
+        for (int k = 0; k < slices; ++k) {
+            p += sum[k * E + tid];
+            c += cnt[k * E + tid];
+        }
+    }
+    __syncthreads();
+    balance_result(a, tid, p, c, tokens);
+}
+
+// One token to L lanes.  Through the weights: with q the softmax over the
+// chosen, w = scale q, dl_j = w_j dw_j - q_j sum_i w_i dw_i; with weights over
+// all experts the second term goes by p, for every e.  Through the loss:
+// dloss p_e (slope_e - sum_i p_i slope_i).  Bound by reading and writing the
+// logits.
+template <int V, int L, int S>
+__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
+    constexpr int TOK = 256 / L;
+    __shared__ int at[TOK][kMaxTopK];
+    __shared__ float add[TOK][kMaxTopK];
+    const RouteArgs &r = a.route;
+    const int tid = threadIdx.x, l = tid % L, g = tid / L;
+    const int64_t t = (int64_t)blockIdx.x * TOK + g;
+    const bool there = t < r.T;
+    float v[S][V];
+    int id = -1;
+    float dw = 0.f, chosen = -INFINITY;
+    if (there) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) load_logits<V>(r, t * r.ld, (s * L + l) * V, v[s]);
+        if (l < r.top_k) {
+            id = r.ids[t * r.top_k + l];
+            if (a.dweights) dw = a.dweights[t * r.top_k + l];
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[s][i] = -INFINITY;
+    }
+    const bool inside = id >= 0 && id < r.E;
+    if (inside && a.dweights) {
+        float one[1];
+        load_logits<1>(r, t * r.ld, id, one);
+        chosen = clean(one[0]);
+    }
+    const bool alive = max_token<L>(inside ? 1.f : 0.f) > 0.f;
+    float top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[s][i] = clean(v[s][i]);
+            top = fmaxf(top, v[s][i]);
+        }
+    top = fmaxf(max_token<L>(top), -kMaxFloat);
+    float z = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[s][i] = v[s][i] > -INFINITY ? expf(v[s][i] - top) : 0.f;
+            z += v[s][i];
+        }
+    z = sum_token<L>(z);
+    const float rz = z > 0.f ? 1.f / z : 0.f;
+    float all = 0.f;               // what every p is multiplied by, and taken off
+    if (a.dweights) {
+        // (a place whose logit has no part has weight 0 whatever dweights holds)
+        const bool part = chosen > -INFINITY;
+        float q;
+        if (r.renormalize) {
+            const float m = fmaxf(max_token<L>(chosen), -kMaxFloat);
+            q = part ? expf(chosen - m) : 0.f;
+            const float zq = sum_token<L>(q);
+            q = zq > 0.f ? q / zq : 0.f;
+        } else {
+            q = part ? expf(chosen - top) * rz : 0.f;
+        }
+        const float wd = part ? r.scale * q * dw : 0.f;
+        const float sum = sum_token<L>(wd);
+        if (l < r.top_k) {
+            at[g][l] = part ? id : -1;
+            add[g][l] = r.renormalize ? wd - q * sum : wd;
+        }
+        if (!r.renormalize) all = sum;
+    }
+    float slope[S][V];
+    if (a.slope) {
+        const float dloss = a.dloss[0];
+        float mean = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = (s * L + l) * V + i;
+                slope[s][i] = e < r.E ? a.slope[e] : 0.f;
+                mean += v[s][i] * slope[s][i];
+            }
+        mean = sum_token<L>(mean) * rz;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) slope[s][i] = dloss * (slope[s][i] - mean);
+    }
+    float d[S][V];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float f = (a.slope ? slope[s][i] : 0.f) - all;
+            // (a logit that has no part gets 0 also where f is no number)
+            d[s][i] = v[s][i] > 0.f ? v[s][i] * rz * f : 0.f;
+        }
+    if (a.dweights) {
+        __syncthreads();
+        for (int j = 0; j < r.top_k; ++j) {
+            const int e = at[g][j];
+            const float x = add[g][j];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[s][i] += e == (s * L + l) * V + i ? x : 0.f;
+        }
+    }
+    if (!there) return;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int e = (s * L + l) * V;
+        if (e >= r.E) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[s][i] = alive ? d[s][i] : 0.f;
+        const int64_t o = t * a.ldd + e;
+        if (a.d_dtype == DT_F32) {
+            float *to = static_cast<float *>(a.dlogits) + o;
+            if constexpr (V == 4) *reinterpret_cast<f32x4 *>(to) = f32x4{d[s][0], d[s][1], d[s][2], d[s][3]};
+            else *to = d[s][0];
+        } else {
+            unsigned short *to = static_cast<unsigned short *>(a.dlogits) + o;
+            const bool f16 = a.d_dtype == DT_F16;
+            if constexpr (V == 4) {
+                const u32x2 w = f16 ? u32x2{pack2_16<DT_F16>(d[s][0], d[s][1]), pack2_16<DT_F16>(d[s][2], d[s][3])}
+                                    : u32x2{pack2_16<DT_BF16>(d[s][0], d[s][1]), pack2_16<DT_BF16>(d[s][2], d[s][3])};
+                *reinterpret_cast<u32x2 *>(to) = w;
+            } else {
+                *to = (unsigned short)(f16 ? to_f16_bits(d[s][0]) : to_bf16_bits(d[s][0]));
+            }
+        }
+    }
+}
+
+// Whether rows can be taken 4 logits at a time, and the lanes of a token.
+bool four_at_a_time(const RouteArgs &a) {
+    return a.E % 4 == 0 && a.ld % 4 == 0 && (uintptr_t)a.logits % (4 * dt_size(a.dtype)) == 0;
+}
+int lanes_of(const RouteArgs &a, bool four) {
+    if (four) return a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
+    return a.E <= 16 ? 16 : a.E <= 32 ? 32 : 64;
+}
+
+// CALL<V, L, S> for the sizes of a
+#define ROUTER_SIZES(a, four, CALL)                    \
+    do {                                               \
+        if (four) {                                    \
+            if ((a).E <= 64) CALL(4, 16, 1);           \
+            else if ((a).E <= 128) CALL(4, 32, 1);     \
+            else if ((a).E <= 256) CALL(4, 64, 1);     \
+            else CALL(4, 64, 2);                       \
+        } else {                                       \
+            if ((a).E <= 16) CALL(1, 16, 1);           \
+            else if ((a).E <= 32) CALL(1, 32, 1);      \
+            else if ((a).E <= 64) CALL(1, 64, 1);      \
+            else if ((a).E <= 128) CALL(1, 64, 2);     \
+            else if ((a).E <= 256) CALL(1, 64, 4);     \
+            else CALL(1, 64, 8);                       \
+        }                                              \
+    } while (0)
+
+bool sizes_ok(const RouteArgs &a) {
+    return a.T >= 1 && a.E >= 1 && a.E <= kMaxExperts && a.top_k >= 1 && a.top_k <= kMaxTopK;
+}
+
+}  // namespace
+}  // namespace tcg
+
+using namespace tcg;
+
+int tcg_balance_groups(const RouteArgs &a) {
+    const int64_t tok = 1024 / lanes_of(a, four_at_a_time(a));
+    const int64_t passes = (a.T + tok - 1) / tok;
+    // Up to 4 passes a single workgroup ends before a second launch would begin.
+    if (passes <= 4) return 1;
+    return passes < kBalanceGroups ? (int)passes : kBalanceGroups;
+}
+
+hipError_t tcg_launch_balance(const BalanceArgs &a, int *launches, hipStream_t s) {
+    const RouteArgs &r = a.route;
+    if (!sizes_ok(r)) return hipErrorInvalidValue;
+    const bool four = four_at_a_time(r);
+    const int groups = tcg_balance_groups(r);
+#define BALANCE(V, L, S)                                                                                  \
+    do {                                                                                                  \
+        if (groups == 1) hipLaunchKernelGGL((balance_kernel<V, L, S, true>), dim3(1), dim3(1024), 0, s, a); \
+        else hipLaunchKernelGGL((balance_kernel<V, L, S, false>), dim3(groups), dim3(1024), 0, s, a);      \
+    } while (0)
+    ROUTER_SIZES(r, four, BALANCE);
+#undef BALANCE
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    *launches += 1;
+    if (groups == 1) return e;
+    hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, s, a, groups);
+    e = hipGetLastError();
+    if (e == hipSuccess) *launches += 1;
+    return e;
+}
+
+hipError_t tcg_launch_route_grad(const RouteGradArgs &a, hipStream_t s) {
+    const RouteArgs &r = a.route;
+    if (!sizes_ok(r)) return hipErrorInvalidValue;
+    const bool four = four_at_a_time(r) && a.ldd % 4 == 0 && (uintptr_t)a.dlogits % (4 * dt_size(a.d_dtype)) == 0;
+    const int64_t tok = 256 / lanes_of(r, four), blocks = (r.T + tok - 1) / tok;
+    if (blocks >= (1 << 24)) return hipErrorInvalidValue;
+#define ROUTE_GRAD(V, L, S) \
+    hipLaunchKernelGGL((route_grad_kernel<V, L, S>), dim3((unsigned)blocks), dim3(256), 0, s, a)
+    ROUTER_SIZES(r, four, ROUTE_GRAD);
+#undef ROUTE_GRAD
+    return hipGetLastError();
+}

@@ -84,6 +84,24 @@ constexpr int kMaxDevices = 64;
 // sums of one split-K slice (fp32, or int32 for int8 inputs).
 constexpr int OUT_PARTIAL = 5;
 
+// Output selectors of the cross entropy of a linear layer (16-bit inputs, NT,
+// direct-to-LDS classes): per row and wave's share of a tile's columns the
+// maximum and sum of a softmax, and its gradient in the inputs' type.
+constexpr int OUT_CE_STAT = 6, OUT_CE_GRAD = 7;
+
+// Softmax maxima (of products, a2 = |scale| log2 e to a power of two) are kept
+// within +-ce_limit, so that they and their differences stay finite times a2.
+constexpr float kLog2E = 1.44269504f;
+__host__ __device__ inline float ce_limit(float a2) { return 8.5070592e37f / (a2 > 1.f ? a2 : 1.f); }
+
+// One token of the cross entropy's backward pass.
+struct CeRow {
+    float lse;
+    float grad;        // what its gradient is multiplied by; 0: it adds nothing
+    int32_t target;    // or -1
+    int32_t pad;
+};
+
 // Fused-epilogue activations (tessl "Architecture", "Fused Epilogue").
 constexpr int ACT_NONE = 0, ACT_RELU = 1, ACT_GELU_TANH = 2;
 
@@ -115,6 +133,16 @@ struct GemmArgs {
     // thin kernel only: output (r, c) of this problem is C[c * ldc + r] (the
     // transposed product of a small-M GEMM); bias and scales then go by r
     int32_t c_trans;
+    // cross entropy only.  OUT_CE_STAT: ws holds float2 [2 tiles_n][M] of
+    // (maximum, sum) and ce_logit [M] receives the targets' products, both in
+    // units of the accumulator (negated where alpha < 0); targets are int32
+    // or int64.  OUT_CE_GRAD: C's row length is ldc (columns N .. ldc are
+    // written 0), ce_rows [M], column n is word ce_first + n.
+    const void *ce_targets;
+    int32_t ce_targets64;
+    int32_t ce_first;
+    float *ce_logit;
+    const CeRow *ce_rows;
 };
 
 // Arguments of the split-K reduction and of the alpha == 0 scaling kernel.

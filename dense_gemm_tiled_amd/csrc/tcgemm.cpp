@@ -8,6 +8,7 @@
 // returns before anything is enqueued, so a refused call leaves the dispatch
 // count unchanged (same page, "The Kernel Library and the nn Boundary").
 
+#include "gemm_call.h"
 #include "tc_host.h"
 
 #include <cmath>
@@ -53,6 +54,8 @@ struct Problem {
     // the transposed form of a small-M GEMM: this problem's output (r, c) is
     // C[c*ldc + r] of the caller's
     bool c_trans = false;
+    // operand w's rows are stored in whole 16-byte pieces, zeros past them
+    bool whole[2] = {false, false};
 };
 
 struct Plan {
@@ -231,7 +234,7 @@ bool operand_dma_ready(const Problem &p, int w, bool aligned) {
     const int64_t ld = w == 0 ? p.lda : p.ldb, stride = w == 0 ? p.stride_a : p.stride_b;
     int64_t rows, cols;
     operand_shape(p, w, &rows, &cols);
-    if ((cols * es) % 16 != 0) return false;
+    if ((cols * es) % 16 != 0 && !p.whole[w]) return false;
     return !pack_unaligned() || ((ld * es) % 16 == 0 && (stride * es) % 16 == 0 && aligned);
 }
 
@@ -313,6 +316,8 @@ Problem transposed_problem(const Problem &p) {
     q.b_ext = p.a_ext;
     q.a_total = p.b_total;
     q.b_total = p.a_total;
+    q.whole[0] = p.whole[1];
+    q.whole[1] = p.whole[0];
     q.c_trans = true;
     return q;
 }
@@ -864,6 +869,13 @@ tc_status_t enqueue(tc_context *ctx, tc_stream *s, const Problem &p, const Plan 
         const void *src[2] = {A, B};
         int64_t ld[2] = {p.lda, p.ldb}, stride[2] = {p.stride_a, p.stride_b};
         int64_t extent[2] = {p.a_ext * es, p.b_ext * es};
+        for (int w = 0; w < 2; ++w) {
+            if (!p.whole[w]) continue;
+            // (the last row's last 16-byte piece is there to be read)
+            int64_t rows, cols;
+            operand_shape(p, w, &rows, &cols);
+            extent[w] = align_up(((rows - 1) * ld[w] + cols) * es, 16);
+        }
         bool tb = p.tb;
         for (int w = 0; w < 2 && e == hipSuccess; ++w) {
             if (!pl.pack[w]) continue;
@@ -1297,6 +1309,60 @@ void note(tc_context *ctx, const char *text) {
 }
 
 }  // namespace
+
+namespace tcg {
+
+namespace {
+
+tc_status_t plan_call(const GemmCall &c, Problem *p, Plan *pl, Epilogue *epi, std::string *err) {
+    const tc_gemm_batched_desc bd = single(&c.d);
+    const tc_status_t st = validate(&bd, p, err, c.col_scale != nullptr);
+    if (st != TC_OK) return st;
+    p->whole[0] = c.whole[0];
+    p->whole[1] = c.whole[1];
+    epi->scale = c.col_scale;
+    make_plan(*p, pl);
+    return TC_OK;
+}
+
+}  // namespace
+
+tc_status_t gemm_call_workspace(const GemmCall &c, int64_t *bytes, std::string *err) {
+    const KnobScope knobs;
+    Problem p;
+    Plan pl;
+    Epilogue epi;
+    const tc_status_t st = plan_call(c, &p, &pl, &epi, err);
+    if (st != TC_OK) return st;
+    StripBt sb;
+    *bytes = call_workspace(p, pl, c.A, c.B, &sb);
+    return TC_OK;
+}
+
+tc_status_t gemm_call_enqueue(tc_context *ctx, tc_stream *s, const GemmCall &c, void *workspace,
+                              int64_t workspace_bytes, std::string *names, std::string *err) {
+    const KnobScope knobs;
+    Problem p;
+    Plan pl;
+    Epilogue epi;
+    const tc_status_t st = plan_call(c, &p, &pl, &epi, err);
+    if (st != TC_OK) return st;
+    StripBt sb;
+    const int64_t need = call_workspace(p, pl, c.A, c.B, &sb);
+    if (need > workspace_bytes || (need > 0 && !workspace))
+        return fail(err, TC_ERR_INVALID_ARGUMENT, "a product needs %lld bytes of workspace, %lld given",
+                    (long long)need, (long long)workspace_bytes);
+    // (an armed measurement waits for a GEMM call of the user's)
+    hipEvent_t armed[2] = {ctx->time_ev[0], ctx->time_ev[1]};
+    ctx->time_ev[0] = ctx->time_ev[1] = nullptr;
+    const tc_status_t done =
+        enqueue_call(ctx, s, p, pl, c.A, c.B, c.C, epi, names, err, need > 0 ? workspace : nullptr);
+    ctx->time_ev[0] = armed[0];
+    ctx->time_ev[1] = armed[1];
+    return done;
+}
+
+}  // namespace tcg
 
 extern "C" {
 

@@ -373,6 +373,104 @@ tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
                          const float *weights, const tc_qweight *gate_up, const tc_qweight *down,
                          void *y, void *workspace, int64_t workspace_bytes, tc_stream *s);
 
+/* ---------------------------------------------------------------------------
+ * Losses of a training step, with their gradients
+ * ------------------------------------------------------------------------- */
+
+/* The softmax cross entropy of a linear layer over a vocabulary: with
+ * l[t, v] = scale * <x[t], w[v]> (x [T, H] and w [V, H], f32, f16 or bf16, rows
+ * ldx and ldw apart, 0 = H; scale finite, not 0),
+ *     lse[t]  = log sum_v exp(l[t, v]),
+ *     loss[t] = lse[t] - l[t, targets[t]],  0 where the target is outside [0, V)
+ * (such a token is ignored), both fp32 [T].  The products are summed in fp32
+ * and not stored (f32 inputs, and rows, pitches or addresses that are no whole
+ * 16-byte pieces: 2^26 at a time).  targets: int32, or int64 with targets64,
+ * contiguous.  A row of x or w that holds NaN or infinity gives the losses
+ * that it takes part in as NaN or infinity; no other token's.
+ * workspace: tc_cross_entropy_workspace bytes of device memory for the same x
+ * and w (of which only the addresses' alignment counts), 16-byte aligned, the
+ * caller's until the work on s has ended; nothing is kept in it. */
+typedef struct {
+    int32_t T, V, H;
+    tc_dtype_t dtype;             /* of x and w */
+    int32_t ldx, ldw;             /* elements; 0 = contiguous */
+    bool targets64;
+    float scale;
+} tc_ce_desc;
+
+tc_status_t tc_cross_entropy_workspace(const tc_ce_desc *d, const void *x, const void *w,
+                                       int64_t *bytes);
+
+tc_status_t tc_cross_entropy_async(tc_context *ctx, const tc_ce_desc *d, const void *x, const void *w,
+                                   const void *targets, float *loss, float *lse, void *workspace,
+                                   int64_t workspace_bytes, tc_stream *s);
+
+/* Its gradients, from lse and grad[t] = dL/dloss[t] (fp32, grad_stride elements
+ * apart; 0 = one for all tokens): with
+ *     G[t, v] = grad[t] * (exp(l[t, v] - lse[t]) - [v = targets[t]]),
+ *     dx = scale * G @ w,    dw = scale * G^T @ x + beta * dw.
+ * A token that is ignored, or whose grad is 0, adds nothing to dw and has dx =
+ * 0, whatever its row of x holds.  dx and dw: x's type or f32, each written
+ * once per word or token (dw read only when beta != 0); one of them may be
+ * NULL.  G is computed from the products again, many words at a time, and
+ * rounded: for a result of x's type once to that type (relative to the largest
+ * grad, f16 keeps numbers down to 2^-39), for an f32 result from 16-bit inputs
+ * to the sum of three bf16 or two f16 numbers, which takes two products as
+ * many times.  lse has to be the one that belongs to x, w and scale. */
+typedef struct {
+    const float *grad;
+    int64_t grad_stride;          /* elements */
+    void *dx;
+    tc_dtype_t dx_dtype;
+    int32_t lddx;                 /* elements; 0 = contiguous */
+    void *dw;
+    tc_dtype_t dw_dtype;
+    int32_t lddw;
+    float beta;
+} tc_ce_grads;
+
+tc_status_t tc_cross_entropy_backward_workspace(const tc_ce_desc *d, const tc_ce_grads *g,
+                                                const void *x, const void *w, int64_t *bytes);
+
+tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d,
+                                            const tc_ce_grads *g, const void *x, const void *w,
+                                            const void *targets, const float *lse, void *workspace,
+                                            int64_t workspace_bytes, tc_stream *s);
+
+/* The balance loss of a router, and the tokens of each expert.  logits [T, E]
+ * as in tc_route_desc (r->top_k columns of ids; renormalize and scale do not
+ * count), ids [T, top_k] as tc_moe_route_async gives them.  A token counts
+ * where one of its ids is inside [0, E); p is the softmax of its logits, where
+ * -inf and NaN have no part and +inf counts as the largest finite number.
+ *     counts[e] = places of ids that hold e,  total = their sum,
+ *     n         = the tokens that count,
+ *     loss      = coef * E * sum_e (counts[e] / total) * (sum_t p[t, e] / n),
+ *     slope[e]  = coef * (E * counts[e] - total) / (total * n),
+ * 0 where no token counts.  loss [1], slope [E] fp32, counts [E] int32.  slope is
+ * what the gradient needs: dloss / d sum_t p[t, e], less what is the same for
+ * every e (the p of a token sum to 1).  Sums do not depend on the order in
+ * which the GPU runs the workgroups.  workspace as above. */
+tc_status_t tc_moe_balance_workspace(const tc_route_desc *r, int64_t *bytes);
+
+tc_status_t tc_moe_balance_async(tc_context *ctx, const tc_route_desc *r, const void *logits,
+                                 const int32_t *ids, float coef, float *loss, int32_t *counts,
+                                 float *slope, void *workspace, int64_t workspace_bytes, tc_stream *s);
+
+/* The gradient of a router's logits, written once:
+ *     dlogits[t] = (d weights[t] / d logits[t])^T dweights[t]
+ *                + dloss * p[t] * (slope - sum_e p[t, e] * slope[e])
+ * with weights[t, j] as *r says (tc_moe_route_async's formula for the experts
+ * that ids names) and p, slope and the tokens that count as above.  dweights
+ * fp32 [T, top_k], or NULL: the first line is 0.  slope [E] and dloss [1]
+ * fp32, or both NULL: the second line is 0.  dlogits [T, E] of the logits'
+ * type or f32, rows ldd apart (0 = E); 0 for tokens that do not count and for
+ * logits that have no part.  A place whose id is outside [0, E) counts for
+ * nothing.  No workspace. */
+tc_status_t tc_moe_route_backward_async(tc_context *ctx, const tc_route_desc *r, const void *logits,
+                                        const int32_t *ids, const float *dweights, const float *slope,
+                                        const float *dloss, void *dlogits, tc_dtype_t d_dtype,
+                                        int32_t ldd, tc_stream *s);
+
 /* First-call autotuning (the tile-class choice the pages leave to a
  * measured cache; tessl "Architecture", "GEMM Pipeline & Kernel Selection").
  * With it on, the first call of each problem (types, layout, M, N, K, batch,

@@ -51,10 +51,11 @@ struct CePrepArgs {
     CeRow *rows;
     void *xz;
     int64_t xz_pitch;          // elements
-    // f16: the gradients are scaled by a power of two that brings the largest
-    // to 2^14 .. 2^15; its reciprocal, H times (null: no scaling)
+    // 16-bit types: the gradients are scaled so that the largest grad becomes
+    // 2^14; the reciprocal of that factor, H times (null: no scaling)
     float *unscale;
 };
+constexpr int kCeScanTokens = 4096;   // up to these every workgroup looks for the largest itself
 
 // The gradient of stored products: g = grad (exp(scale l - lse) - [target]),
 // fp32 over l itself, or the sum of `parts` 16-bit numbers, plane after plane.
@@ -67,10 +68,14 @@ struct CeGradArgs {
     void *g;
     int64_t pitch, plane;      // elements of g; columns N .. pitch are written 0
     int32_t dtype, parts;
+    float *lost;               // [T], what the sum of the first lost_parts of a target's value lacks
+    int32_t lost_parts;
 };
 
-// dx from its sums: times the reciprocal of the scale, 0 for tokens that add
-// nothing, rounded once.  src may be dst.
+// dx from its sums: what the rounding of a token's largest value lost is put
+// back (scale * lost[t] times the target's row of w), then times the reciprocal
+// of the gradients' scaling, 0 for tokens that add nothing, rounded once.  src
+// may be dst.
 struct CeFinishArgs {
     const float *src;
     int64_t ld_src;            // elements
@@ -80,11 +85,32 @@ struct CeFinishArgs {
     int32_t dtype;             // of dst
     const CeRow *rows;
     const float *unscale;      // or null
+    const float *lost;         // or null
+    float scale;
+    const void *w;
+    int64_t ldw;               // elements
+    int32_t w_dtype;
+};
+
+// Partial softmaxes of the products of a few tokens, from x and w: parts
+// [ceil(V / kCeRowWords)][T] and logit as in CeStatArgs.
+constexpr int kCeRowWords = 64, kCeRowTokens = 32;
+struct CeRowsArgs {
+    const void *x, *w;
+    int64_t ldx, ldw;          // elements
+    int32_t T, V, H;
+    int32_t dtype;
+    float scale;
+    const void *targets;
+    int32_t targets64;
+    float2 *parts;
+    float *logit;
 };
 
 }  // namespace tcg
 
 hipError_t tcg_launch_ce_join(const tcg::CeJoinArgs &a, hipStream_t s);
+hipError_t tcg_launch_ce_rows(const tcg::CeRowsArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_stat(const tcg::CeStatArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_prep(const tcg::CePrepArgs &a, int *launches, hipStream_t s);
 hipError_t tcg_launch_ce_grad(const tcg::CeGradArgs &a, hipStream_t s);

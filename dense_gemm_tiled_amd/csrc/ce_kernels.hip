@@ -27,26 +27,35 @@ __device__ inline void join(float &m, float &s, float m2, float s2, float a2) {
     m = top;
 }
 
-// 16 tokens a workgroup, 64 threads each: thread q takes shares q, q + 64, ..
+// TOK tokens a workgroup, 1024 / TOK threads each: thread q takes shares q, q +
+// 1024 / TOK, ..; 8 of them on the way at once (the shares of 64 tokens by
+// 131072 words: 4 tokens a workgroup 5.x us, 16 tokens 9.2).
+template <int TOK>
 __global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
+    constexpr int Q = 1024 / TOK;
     __shared__ float sm[1024], ss[1024];
-    const int tid = threadIdx.x, tok = tid & 15, q = tid >> 4;
-    const int64_t t = (int64_t)blockIdx.x * 16 + tok;
-    const float scale = fabsf(a.scale), a2 = scale * kLog2E;
-    float m = -ce_limit(a2), s = 0.f;
+    const int tid = threadIdx.x, tok = tid % TOK, q = tid / TOK;
+    const int64_t t = (int64_t)blockIdx.x * TOK + tok;
+    const float scale = fabsf(a.scale), a2 = scale * kLog2E, least = -ce_limit(a2);
+    float m = least, s = 0.f;
     if (t < a.T) {
-#pragma unroll 4
-        for (int p = q; p < a.num; p += 64) {
-            const float2 v = a.parts[(int64_t)p * a.T + t];
-            join(m, s, v.x, v.y, a2);
+        for (int p = q; p < a.num; p += 8 * Q) {
+            float2 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int at = p + k * Q;
+                v[k] = at < a.num ? a.parts[(int64_t)at * a.T + t] : make_float2(least, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) join(m, s, v[k].x, v[k].y, a2);
         }
     }
     sm[tid] = m;
     ss[tid] = s;
-    for (int h = 32; h > 0; h >>= 1) {
+    for (int h = Q / 2; h > 0; h >>= 1) {
         __syncthreads();
         if (q < h) {
-            join(m, s, sm[tid + 16 * h], ss[tid + 16 * h], a2);
+            join(m, s, sm[tid + TOK * h], ss[tid + TOK * h], a2);
             sm[tid] = m;
             ss[tid] = s;
         }
@@ -56,6 +65,113 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
         a.lse[t] = __builtin_fmaf(scale, m, rest);
         const bool counts = target_of(a.targets, a.targets64, t, a.V) >= 0;
         a.loss[t] = counts ? __builtin_fmaf(scale, m - a.logit[t], rest) : 0.f;
+    }
+}
+
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8v __attribute__((ext_vector_type(8)));
+template <int DT>
+__device__ inline f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, a),
+                                                       __builtin_bit_cast(bf16x8v, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8v, a),
+                                                      __builtin_bit_cast(f16x8v, b), c, 0, 0, 0);
+}
+
+// Few tokens: bound by reading w, so nothing but loads should take time.  A
+// workgroup takes 64 words for all tokens (TB blocks of 16), its 8 waves every
+// 8th group of 64 k each (whole 128-byte lines of every row), straight from
+// memory into the operands' registers, the next group on the way while one is
+// multiplied; the waves' sums meet in LDS and leave as one share of the
+// softmax per token.  1 token by 32768 x 2048 bf16: see the table of measured
+// times.
+template <int DT, int TB>
+__global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
+    constexpr int W = kCeRowWords, PITCH = W + 4;
+    __shared__ float sums[8][TB * 16][PITCH];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4;
+    const int64_t v0 = (int64_t)blockIdx.x * W;
+    const char *wb = static_cast<const char *>(a.w) + v0 * a.ldw * 2;
+    const __amdgpu_buffer_rsrc_t rw =
+        make_rsrc(wb, ((int64_t)(a.V - 1) * a.ldw + a.H - v0 * a.ldw) * 2);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, ((int64_t)(a.T - 1) * a.ldx + a.H) * 2);
+    const int wrow = r * (int)a.ldw * 2, xrow = r * (int)a.ldx * 2;
+    const int wstep = 16 * (int)a.ldw * 2, xstep = 16 * (int)a.ldx * 2;
+    f32x4 acc[TB][4];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 wf[2][2][4], xf[2][2][TB];
+    // group g: k = 64 g + 32 h + 8 c .. + 7 for half h; past H nothing is read
+    auto load = [&](int g, u32x4 (&wt)[2][4], u32x4 (&xt)[2][TB]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = g * 64 + h * 32 + c * 8;
+            const bool in = k < a.H;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) wt[h][b] = ld128(rw, in ? wrow + b * wstep + k * 2 : -16);
+#pragma unroll
+            for (int t = 0; t < TB; ++t) xt[h][t] = ld128(rx, in ? xrow + t * xstep + k * 2 : -16);
+        }
+    };
+    auto multiply = [&](const u32x4 (&wt)[2][4], const u32x4 (&xt)[2][TB]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) acc[t][b] = mma<DT>(wt[h][b], xt[h][t], acc[t][b]);
+    };
+    const int groups = (a.H + 63) / 64;
+    load(wave, wf[0], xf[0]);
+    for (int g = wave; g < groups; g += 16) {
+        load(g + 8, wf[1], xf[1]);
+        multiply(wf[0], xf[0]);
+        load(g + 16, wf[0], xf[0]);
+        multiply(wf[1], xf[1]);
+    }
+    // (the last products are read behind the loop's branch: their wait is here)
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) asm volatile("s_nop 7" : "+v"(acc[t][b]));
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            *reinterpret_cast<f32x4 *>(&sums[wave][t * 16 + r][b * 16 + c * 4]) = acc[t][b];
+    __syncthreads();
+    // 32 lanes to a token, 2 words each
+    const float a2 = fabsf(a.scale) * kLog2E, limit = ce_limit(a2);
+    const u32 flip = a.scale < 0.f ? 0x80000000u : 0u;
+    const int n = (tid & 31) * 2;
+#pragma unroll
+    for (int p = 0; p < TB; ++p) {
+        const int t = p * 16 + (tid >> 5);
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) x += sums[w][t][n + e];
+            v[e] = v0 + n + e < a.V ? as_f32(as_u32(x) ^ flip) : -INFINITY;
+        }
+        float m = fmaxf(v[0], v[1]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+        m = fminf(fmaxf(m, -limit), limit);
+        float s = __builtin_amdgcn_exp2f((v[0] - m) * a2) + __builtin_amdgcn_exp2f((v[1] - m) * a2);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) s += __shfl_xor(s, o);
+        if (t < a.T) {
+            if ((tid & 31) == 0) a.parts[(int64_t)blockIdx.x * a.T + t] = make_float2(m, s);
+            const int64_t d = target_of(a.targets, a.targets64, t, a.V) - v0 - n;
+            if (d == 0 || d == 1) a.logit[t] = d ? v[1] : v[0];
+        }
     }
 }
 
@@ -104,29 +220,33 @@ __global__ __launch_bounds__(256) void ce_stat_kernel(CeStatArgs a) {
     }
 }
 
-// The power of two that brings the largest |grad| of a counted token to 2^14
-// .. 2^15, so that f16 holds gradients down to 2^-39 of it; its reciprocal H
-// times, the columns' factors of the weight's gradient.
-__global__ __launch_bounds__(1024) void ce_unscale_kernel(CePrepArgs a) {
-    __shared__ float top[16];
-    const int tid = threadIdx.x;
+// The largest |grad| of a counted token, by a workgroup of NT threads; kept
+// where its reciprocal and 2^14 times it are ordinary numbers.
+template <int NT>
+__device__ inline float largest_grad(const CePrepArgs &a, int tid) {
+    __shared__ float top[NT / 64];
     float m = 0.f;
-    for (int64_t t = tid; t < a.T; t += 1024) {
+    for (int64_t t = tid; t < a.T; t += NT) {
         const float g = fabsf(a.grad[t * a.grad_stride]);
-        if (target_of(a.targets, a.targets64, t, a.V) >= 0 && g < INFINITY) m = fmaxf(m, g);
+        if (g < INFINITY && target_of(a.targets, a.targets64, t, a.V) >= 0) m = fmaxf(m, g);
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
     if ((tid & 63) == 0) top[tid >> 6] = m;
     __syncthreads();
-    for (int w = 0; w < 16; ++w) m = fmaxf(m, top[w]);
-    int e = 0;
-    if (m > 0.f) {
-        (void)frexpf(m, &e);       // m = f 2^e, 1/2 <= f < 1
-        e = max(min(e - 15, 100), -100);
-    }
-    const float v = ldexpf(1.f, e);
-    for (int h = tid; h < a.H; h += 1024) a.unscale[h] = v;
+    for (int w = 0; w < NT / 64; ++w) m = fmaxf(m, top[w]);
+    return m > 0.f ? fminf(fmaxf(m, 0x1p-100f), 0x1p+100f) : 1.f;
+}
+
+// The scaling of 16-bit gradients.  Both types: a token's value at its target
+// is -grad (1 - p), for most tokens close to -grad, and the numbers just below
+// a power of two are rounded by half as much of themselves as those just
+// above: with grads that are alike the rounding of G costs the result a third
+// of what its own rounding does.  f16: numbers down to 2^-39 of the largest
+// remain.  (More tokens than each workgroup of ce_prep_kernel looks through.)
+__global__ __launch_bounds__(1024) void ce_unscale_kernel(CePrepArgs a) {
+    const float v = largest_grad<1024>(a, threadIdx.x) * 0x1p-14f;
+    for (int h = threadIdx.x; h < a.H; h += 1024) a.unscale[h] = v;
 }
 
 // A wave to a token.
@@ -134,10 +254,18 @@ template <int ES, bool VEC>
 __global__ __launch_bounds__(256) void ce_prep_kernel(CePrepArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    float unscale = 1.f;
+    if (a.unscale && a.T <= kCeScanTokens) {
+        unscale = largest_grad<256>(a, threadIdx.x) * 0x1p-14f;
+        if (blockIdx.x == 0)
+            for (int h = threadIdx.x; h < a.H; h += 256) a.unscale[h] = unscale;
+    } else if (a.unscale) {
+        unscale = a.unscale[0];
+    }
     if (t >= a.T) return;
     const int target = target_of(a.targets, a.targets64, t, a.V);
     float g = target >= 0 ? a.grad[t * a.grad_stride] : 0.f;
-    if (a.unscale) g /= a.unscale[0];
+    g /= unscale;
     if (lane == 0) {
         CeRow r;
         r.lse = g != 0.f ? a.lse[t] : 0.f;
@@ -177,6 +305,7 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(CeGradArgs a) {
         const int n = c * kCeStatCols + k * 1024 + threadIdx.x * 4;
         if (n >= a.pitch) continue;
         float v[4];
+        int at = -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[e] = 0.f;
@@ -184,6 +313,7 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(CeGradArgs a) {
                 const float z = __builtin_fmaf(row[n + e], a.scale, -r.lse);
                 const bool hit = r.target >= 0 && n + e == r.target - a.first;
                 v[e] = r.grad * (hit ? expm1f(z) : __builtin_amdgcn_exp2f(z * kLog2E));
+                if (hit) at = e;
             }
         }
         if constexpr (DT == DT_F32) {
@@ -199,23 +329,37 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(CeGradArgs a) {
                 for (int e = 0; e < 4; ++e) {
                     const u32 h = (e < 2 ? w.x : w.y) >> (16 * (e & 1)) & 0xFFFFu;
                     v[e] -= DT == DT_BF16 ? from_bf16_bits(h) : from_f16_bits(h);
+                    if (e == at && p + 1 == a.lost_parts) a.lost[t] = v[e];
                 }
             }
         }
     }
 }
 
+__device__ inline float decode(u32 h, int dtype) { return dtype == DT_F16 ? from_f16_bits(h) : from_bf16_bits(h); }
+
 // A row to a workgroup.
 template <int DT, bool VEC>
 __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
     const int64_t t = blockIdx.x;
-    const bool live = a.rows[t].grad != 0.f;
+    const CeRow row = a.rows[t];
+    const bool live = row.grad != 0.f;
     const float f = a.unscale ? a.unscale[0] : 1.f;
     const float *src = a.src + t * a.ld_src;
-    if (DT == DT_F32 && src == a.dst && live && f == 1.f) return;
+    const bool more = a.lost && live;
+    if (DT == DT_F32 && src == a.dst && live && f == 1.f && !more) return;
+    const float lost = more ? a.scale * a.lost[t] : 0.f;
+    const unsigned short *w = static_cast<const unsigned short *>(a.w) + (more ? row.target * a.ldw : 0);
     if constexpr (VEC) {
         for (int h = threadIdx.x * 4; h < a.H; h += 1024) {
             f32x4 v = *reinterpret_cast<const f32x4 *>(src + h);
+            if (more) {
+                const u32x2 k = *reinterpret_cast<const u32x2 *>(w + h);
+                v[0] = __builtin_fmaf(lost, decode(k.x & 0xFFFFu, a.w_dtype), v[0]);
+                v[1] = __builtin_fmaf(lost, decode(k.x >> 16, a.w_dtype), v[1]);
+                v[2] = __builtin_fmaf(lost, decode(k.y & 0xFFFFu, a.w_dtype), v[2]);
+                v[3] = __builtin_fmaf(lost, decode(k.y >> 16, a.w_dtype), v[3]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = live ? v[e] * f : 0.f;
             if constexpr (DT == DT_F32)
@@ -226,7 +370,9 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
         }
     } else {
         for (int h = threadIdx.x; h < a.H; h += 256) {
-            const float v = live ? src[h] * f : 0.f;
+            float v = src[h];
+            if (more) v = __builtin_fmaf(lost, decode(w[h], a.w_dtype), v);
+            v = live ? v * f : 0.f;
             if constexpr (DT == DT_F32) static_cast<float *>(a.dst)[t * a.ld_dst + h] = v;
             else
                 static_cast<unsigned short *>(a.dst)[t * a.ld_dst + h] = (unsigned short)pack2_16<DT>(v, 0.f);
@@ -242,9 +388,27 @@ constexpr int64_t kMaxBlocks = 1 << 24;   // of 256 threads: a launch's threads 
 using namespace tcg;
 
 hipError_t tcg_launch_ce_join(const CeJoinArgs &a, hipStream_t s) {
-    const int64_t blocks = ((int64_t)a.T + 15) / 16;
+    // few tokens: more threads for each
+    const int tok = a.T <= 1024 ? 4 : 16;
+    const int64_t blocks = ((int64_t)a.T + tok - 1) / tok;
     if (a.T < 1 || a.num < 1 || blocks >= kMaxBlocks / 4) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, a);
+    if (tok == 4) hipLaunchKernelGGL(ce_join_kernel<4>, dim3((unsigned)blocks), dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL(ce_join_kernel<16>, dim3((unsigned)blocks), dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t tcg_launch_ce_rows(const CeRowsArgs &a, hipStream_t s) {
+    const int64_t blocks = ((int64_t)a.V + kCeRowWords - 1) / kCeRowWords;
+    if (a.T < 1 || a.T > kCeRowTokens || blocks >= kMaxBlocks / 2) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks), b(512);
+    const bool one = a.T <= 16;
+    if (a.dtype == DT_F16) {
+        if (one) hipLaunchKernelGGL((ce_rows_kernel<DT_F16, 1>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((ce_rows_kernel<DT_F16, 2>), g, b, 0, s, a);
+    } else {
+        if (one) hipLaunchKernelGGL((ce_rows_kernel<DT_BF16, 1>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((ce_rows_kernel<DT_BF16, 2>), g, b, 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -258,7 +422,7 @@ hipError_t tcg_launch_ce_stat(const CeStatArgs &a, hipStream_t s) {
 hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s) {
     const int es = dt_size(a.dtype);
     if (a.T < 1 || a.T > kMaxBlocks || (a.xz_pitch * es) % 16 != 0 || a.xz_pitch < a.H) return hipErrorInvalidValue;
-    if (a.unscale) {
+    if (a.unscale && a.T > kCeScanTokens) {
         hipLaunchKernelGGL(ce_unscale_kernel, dim3(1), dim3(1024), 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -289,7 +453,8 @@ hipError_t tcg_launch_ce_finish(const CeFinishArgs &a, hipStream_t s) {
     if (a.T < 1 || a.T >= kMaxBlocks) return hipErrorInvalidValue;
     const int es = dt_size(a.dtype);
     const bool vec = a.H % 4 == 0 && a.ld_src % 4 == 0 && a.ld_dst % 4 == 0 && (uintptr_t)a.src % 16 == 0 &&
-                     (uintptr_t)a.dst % (4 * es) == 0;
+                     (uintptr_t)a.dst % (4 * es) == 0 &&
+                     (!a.lost || (a.ldw % 4 == 0 && (uintptr_t)a.w % 8 == 0));
     const dim3 g((unsigned)a.T), b(256);
 #define CE_FINISH(DT)                                                                     \
     do {                                                                                  \

@@ -61,10 +61,26 @@ tc_status_t check_ce(const tc_ce_desc *d, const void *x, const void *w, CeProble
 // 256 tiles (one a CU) counts 1, of 128 x 128 tiles (two a CU) 0.625, as for
 // the plain product; 128 x 128 tiles that leave every CU at most one take the
 // variant with more loads in flight.
+double rounds(int64_t T, int64_t N, int tile) {
+    const int64_t n = ceil_div(T, tile) * ceil_div(N, tile);
+    return tile == 256 ? (double)ceil_div(n, 256) : 0.625 * (double)ceil_div(n, 512);
+}
 int ce_class(int64_t T, int64_t N) {
-    const int64_t t256 = ceil_div(T, 256) * ceil_div(N, 256), t128 = ceil_div(T, 128) * ceil_div(N, 128);
-    if ((double)ceil_div(t256, 256) <= 0.625 * (double)ceil_div(t128, 512)) return TILE_256_DMA;
-    return t128 <= 256 ? TILE_128_DMA4 : TILE_128_DMA;
+    if (rounds(T, N, 256) <= rounds(T, N, 128)) return TILE_256_DMA;
+    return ceil_div(T, 128) * ceil_div(N, 128) <= 256 ? TILE_128_DMA4 : TILE_128_DMA;
+}
+
+// How many of N words (whole tile columns) go first, in full rounds of 256 x
+// 256 tiles, when the rest then takes less as a launch of its own (0.05 for
+// it) than the last round costs; N: all in one launch.  1021 tokens by 50021
+// words of 2056, fp16 (784 tiles, three rounds and 16 tiles): loss RAGGED_LOSS.
+int64_t first_words(int64_t T, int64_t N) {
+    const int64_t tm = ceil_div(T, 256), tiles = tm * ceil_div(N, 256);
+    const double whole = rounds(T, N, 256) < rounds(T, N, 128) ? rounds(T, N, 256) : rounds(T, N, 128);
+    const int64_t n = tiles / 256 * 256 / tm * 256;
+    if (tiles <= 256 || n < 256 || n >= N) return N;
+    const double rest = rounds(T, N - n, 256) < rounds(T, N - n, 128) ? rounds(T, N - n, 256) : rounds(T, N - n, 128);
+    return rounds(T, n, 256) + rest + 0.05 < whole ? n : N;
 }
 
 // Arguments of the products x W^T with an epilogue of their own.
@@ -116,21 +132,26 @@ tc_gemm_desc gemm_desc(int64_t M, int64_t N, int64_t K, int dt, int cdt, bool ta
 // Tokens are taken Tc at a time (bounds the partial softmaxes), and where the
 // products are stored, N words at a time.
 struct ForwardSpace {
-    bool fused;
+    bool fused, few;                   // few: one launch takes all tokens
     int64_t Tc, N, pitch, num;         // num: shares of the words
     int64_t parts, logit, l, gemm, gemm_bytes, bytes;
 };
 
 tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, ForwardSpace *f, std::string *err) {
     f->fused = p.whole && p.ldx % 8 == 0 && (uintptr_t)x % 16 == 0;
+    f->few = f->fused && p.T <= kCeRowTokens && ceil_div(p.V, kCeRowWords) < kMaxGroups / 2;
     f->Tc = p.T < 16384 ? p.T : 16384;
     f->l = f->gemm = f->gemm_bytes = 0;
-    if (f->fused) {
-        f->N = p.V;
-        const int bn = tile_shape(ce_class(f->Tc, p.V)).bn, last = (int)(p.T % f->Tc);
-        f->num = 2 * ceil_div(p.V, bn);
-        if (last) {                    // (another class may take the last tokens)
-            const int64_t n = 2 * ceil_div(p.V, tile_shape(ce_class(last, p.V)).bn);
+    if (f->few) {
+        f->num = ceil_div(p.V, kCeRowWords);
+    } else if (f->fused) {
+        f->num = 0;
+        for (const int64_t T : {f->Tc, p.T % f->Tc}) {
+            if (T == 0) continue;
+            const int64_t first = first_words(T, p.V);
+            int64_t n = 0;
+            for (const int64_t N : {first, p.V - first})
+                if (N > 0) n += 2 * ceil_div(N, tile_shape(ce_class(T, N)).bn);
             if (n > f->num) f->num = n;
         }
     } else {
@@ -186,19 +207,45 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
         std::string here;
         hipError_t e;
         int64_t num = 0;
-        if (f.fused) {
-            const int cls = ce_class(T, p.V);
-            int64_t grid;
-            GemmArgs a = product_args(p, xt, p.ldx, T, w, p.V, d.scale, cls, &grid);
-            a.ws = ws + f.parts;
-            a.ce_targets = tt;
-            a.ce_targets64 = d.targets64;
-            a.ce_logit = reinterpret_cast<float *>(ws + f.logit);
-            num = 2 * a.tiles_n;
-            e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_STAT, a, grid, s->stream);
+        if (f.few) {
+            CeRowsArgs a;
+            a.x = x;
+            a.w = w;
+            a.ldx = p.ldx;
+            a.ldw = p.ldw;
+            a.T = (int32_t)p.T;
+            a.V = (int32_t)p.V;
+            a.H = (int32_t)p.H;
+            a.dtype = p.dt;
+            a.scale = d.scale;
+            a.targets = targets;
+            a.targets64 = d.targets64;
+            a.parts = reinterpret_cast<float2 *>(ws + f.parts);
+            a.logit = reinterpret_cast<float *>(ws + f.logit);
+            num = f.num;
+            e = tcg_launch_ce_rows(a, s->stream);
             if (e != hipSuccess) return launch_failed(err, e);
             ctx->dispatches += 1;
-            here = std::string(tcg_kernel_name(p.dt, false, true, cls)) + "_softmax";
+            here = "ce_rows";
+        } else if (f.fused) {
+            const int64_t first = first_words(T, p.V);
+            for (int64_t v0 = 0; v0 < p.V; v0 += first) {
+                const int64_t N = v0 == 0 ? first : p.V - v0;
+                const int cls = ce_class(T, N);
+                int64_t grid;
+                GemmArgs a = product_args(p, xt, p.ldx, T, at(w, v0 * p.ldw * p.es), N, d.scale, cls, &grid);
+                a.ws = reinterpret_cast<float2 *>(ws + f.parts) + num * T;
+                a.ce_targets = tt;
+                a.ce_targets64 = d.targets64;
+                a.ce_first = (int32_t)v0;
+                a.ce_logit = reinterpret_cast<float *>(ws + f.logit);
+                num += 2 * a.tiles_n;
+                e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_STAT, a, grid, s->stream);
+                if (e != hipSuccess) return launch_failed(err, e);
+                ctx->dispatches += 1;
+                here += std::string(v0 ? "|" : "") + tcg_kernel_name(p.dt, false, true, cls) + "_softmax";
+                if (v0) break;
+            }
         } else {
             for (int64_t v0 = 0; v0 < p.V; v0 += f.N) {
                 const int64_t N = p.V - v0 < f.N ? p.V - v0 : f.N;
@@ -258,7 +305,7 @@ struct BackwardSpace {
     bool own_dx;                       // dx is summed in the workspace
     int parts, dx_parts, dw_parts;
     int64_t N, pitch, xz_pitch;
-    int64_t rows, unscale, xz, acc, g, l, gemm, gemm_bytes, bytes;
+    int64_t rows, lost, unscale, xz, acc, g, l, gemm, gemm_bytes, bytes;
 };
 
 GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
@@ -326,7 +373,8 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     // A gradient in fp32 from 16-bit inputs: the products' gradient as the sum
     // of as many numbers as fp32 shows (24 bits: three of bf16; two of f16
     // have 22).  One in the inputs' type takes one: that rounding is as large
-    // as the result's own.
+    // as the result's own, and dx gets most of it back (a token's value at its
+    // target, all but certain tokens' largest by far).
     const int wide = p.dt == TC_BF16 ? 3 : p.dt == TC_F16 ? 2 : 1;
     b->dx_parts = !g.dx ? 0 : g.dx_dtype == TC_F32 ? wide : 1;
     b->dw_parts = !g.dw ? 0 : g.dw_dtype == TC_F32 ? wide : 1;
@@ -351,10 +399,11 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     b->N = N < p.V ? N : p.V;
     b->pitch = up_to(b->N, 8);
     if (p.T * b->pitch > kMaxIndex) return fail(err, TC_ERR_OVERFLOW, "T=%lld is too large", (long long)p.T);
-    const bool f16 = p.dt == TC_F16;
     b->rows = 0;
-    b->unscale = f16 ? up_to(p.T * (int64_t)sizeof(CeRow), 256) : -1;
-    b->xz = up_to(p.T * (int64_t)sizeof(CeRow), 256) + (f16 ? up_to(p.H * 4, 256) : 0);
+    b->lost = up_to(p.T * (int64_t)sizeof(CeRow), 256);
+    const int64_t after = up_to(b->lost + p.T * 4, 256);
+    b->unscale = p.es == 2 ? after : -1;
+    b->xz = after + (p.es == 2 ? up_to(p.H * 4, 256) : 0);
     b->acc = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
     b->g = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
     b->l = up_to(b->g + p.T * b->pitch * p.es * b->parts, 256);
@@ -398,6 +447,7 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
                          std::string *err) {
     const CeRow *rows = reinterpret_cast<const CeRow *>(ws + b.rows);
     float *unscale = b.unscale >= 0 ? reinterpret_cast<float *>(ws + b.unscale) : nullptr;
+    float *const lost = reinterpret_cast<float *>(ws + b.lost);
     CePrepArgs pa;
     pa.x = x;
     pa.ldx = p.ldx;
@@ -427,17 +477,27 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
         const void *wv = at(w, v0 * p.ldw * p.es);
         std::string here;
         if (b.fused) {
-            const int cls = ce_class(p.T, N);
-            int64_t grid;
-            GemmArgs a = product_args(p, ws + b.xz, b.xz_pitch, p.T, wv, N, d.scale, cls, &grid);
-            a.C = ws + b.g;
-            a.ldc = (int32_t)b.pitch;
-            a.c_extent = p.T * b.pitch * 2;
-            a.ce_first = (int32_t)v0;
-            a.ce_rows = rows;
-            e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_GRAD, a, grid, s->stream);
-            if (e != hipSuccess) return launch_failed(err, e);
-            here = std::string(tcg_kernel_name(p.dt, false, true, cls)) + "_grad";
+            const int64_t first = first_words(p.T, N);
+            for (int64_t n0 = 0; n0 < N; n0 += first) {
+                const int64_t n = n0 == 0 ? first : N - n0;
+                const int cls = ce_class(p.T, n);
+                int64_t grid;
+                GemmArgs a = product_args(p, ws + b.xz, b.xz_pitch, p.T, at(wv, n0 * p.ldw * p.es), n, d.scale, cls,
+                                          &grid);
+                // (the last piece's columns up to the pitch are zeros)
+                a.C = ws + b.g + n0 * 2;
+                a.ldc = (int32_t)b.pitch;
+                a.c_extent = (p.T * b.pitch - n0) * 2;
+                a.ce_cols = (int32_t)(n0 + n < N ? n : up_to(n, 8));
+                a.ce_first = (int32_t)(v0 + n0);
+                a.ce_rows = rows;
+                a.ce_lost = lost;
+                e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_GRAD, a, grid, s->stream);
+                if (e != hipSuccess) return launch_failed(err, e);
+                ctx->dispatches += 1;
+                here += std::string(n0 ? "|" : "") + tcg_kernel_name(p.dt, false, true, cls) + "_grad";
+                if (n0) break;
+            }
         } else {
             GemmCall c = logits_call(p, b, N, wv);
             c.A = ws + b.xz;
@@ -456,11 +516,13 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
             ga.plane = plane;
             ga.dtype = p.dt;
             ga.parts = b.parts;
+            ga.lost = lost;
+            ga.lost_parts = b.dx_parts;
             e = tcg_launch_ce_grad(ga, s->stream);
             if (e != hipSuccess) return launch_failed(err, e);
+            ctx->dispatches += 1;
             here += "+ce_grad";
         }
-        ctx->dispatches += 1;
         for (int k = 0; k < b.parts; ++k) {
             const void *gk = ws + b.g + k * plane * p.es;
             std::string part;
@@ -495,6 +557,12 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
         f.dtype = g.dx_dtype;
         f.rows = rows;
         f.unscale = unscale;
+        // (with several numbers to a value there is nothing left to put back)
+        f.lost = p.es == 2 && b.dx_parts == 1 ? lost : nullptr;
+        f.scale = d.scale;
+        f.w = w;
+        f.ldw = p.ldw;
+        f.w_dtype = p.dt;
         e = tcg_launch_ce_finish(f, s->stream);
         if (e != hipSuccess) return launch_failed(err, e);
         ctx->dispatches += 1;

@@ -422,11 +422,11 @@ struct RingSrc {
 // (unsigned arithmetic: an out-of-range offset stays out of range).
 __device__ inline int group_voff(int off, int j) { return (int)((uint32_t)off - (uint32_t)(j * 1024)); }
 
-// Row m's target, -1 where it is outside [0, N).
+// Row m's target as a column of the product, -1 where it is none.
 __device__ inline int ce_load_target(const GemmArgs &args, int64_t m) {
     const int64_t t = args.ce_targets64 ? static_cast<const int64_t *>(args.ce_targets)[m]
                                         : (int64_t)static_cast<const int32_t *>(args.ce_targets)[m];
-    return t >= 0 && t < args.N ? (int)t : -1;
+    return t >= args.ce_first && t < (int64_t)args.ce_first + args.N ? (int)(t - args.ce_first) : -1;
 }
 
 // Epilogue variants of the kernel: beta == 0 and no fused epilogue; beta != 0
@@ -660,7 +660,7 @@ void gemm_dma_kernel(const GemmArgs args) {
     }
     // cross entropy: the row of this thread's number waits in registers, too
     [[maybe_unused]] int ce_target = -1;
-    [[maybe_unused]] u32x4 ce_row{};
+    [[maybe_unused]] u32x4 ce_row{0u, 0u, 0xFFFFFFFFu, 0u};   // (past M: no target)
     if constexpr (CE_STAT) {
         if (tid < BM && m0 + tid < M) ce_target = ce_load_target(args, m0 + tid);
     } else if constexpr (CE_GRAD) {
@@ -961,7 +961,7 @@ void gemm_dma_kernel(const GemmArgs args) {
         // waves' tiles go out along rows through LDS, as the plain epilogue's
         // do; the target's value, expm1 of its own difference (1 taken off a
         // rounded exponential would leave nothing near 1), replaces the one
-        // staged for it.
+        // staged for it; what its rounding loses is kept for dx.
         static_assert(MS == 16 && DT != DT_I8, "16 x 16 blocks of float sums");
         constexpr int RB = BM * (int)sizeof(CeRow);
         constexpr int PITCH = (WTN + 16) * 2, REGION = (LDS_BYTES - RB) / NW / 16 * 16;
@@ -1005,9 +1005,11 @@ void gemm_dma_kernel(const GemmArgs args) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v = d == 16 * j + e ? acc[i][j][e] : v;
                     v = g * expm1f(__builtin_fmaf(v, alpha, -lse));
-                    if (hit)
-                        *(TCG_LDS unsigned short *)(row + (4 * (lane >> 4) + d) * 2) =
-                            (unsigned short)pack2_16<OUT>(v, 0.f);
+                    if (hit) {
+                        const u32 h = pack2_16<OUT>(v, 0.f) & 0xFFFFu;
+                        *(TCG_LDS unsigned short *)(row + (4 * (lane >> 4) + d) * 2) = (unsigned short)h;
+                        args.ce_lost[m0 + ml] = v - (OUT == DT_BF16 ? from_bf16_bits(h) : from_f16_bits(h));
+                    }
                 }
             }
             // (the LDS runs one wave's accesses in order)
@@ -1019,7 +1021,7 @@ void gemm_dma_kernel(const GemmArgs args) {
                 const u32x4 v = *(const TCG_LDS u32x4 *)(reg + row * PITCH + ch * 16);
                 // (rows past M start past the store range; a row's 16-byte
                 // pieces are whole)
-                if (n0 + wn * WTN + ch * 8 < args.ldc)
+                if (n0 + wn * WTN + ch * 8 < args.ce_cols)
                     __builtin_amdgcn_raw_buffer_store_b128(
                         v, rg, (wm * WTM + c0 + row) * args.ldc * 2 + wn * WTN * 2 + ch * 16, 0, 0);
             }

@@ -136,13 +136,14 @@ struct GemmArgs {
     // cross entropy only.  OUT_CE_STAT: ws holds float2 [2 tiles_n][M] of
     // (maximum, sum) and ce_logit [M] receives the targets' products, both in
     // units of the accumulator (negated where alpha < 0); targets are int32
-    // or int64.  OUT_CE_GRAD: C's row length is ldc (columns N .. ldc are
-    // written 0), ce_rows [M], column n is word ce_first + n.
+    // or int64.  OUT_CE_GRAD: columns N .. ce_cols of C are written 0, ce_rows
+    // [M].  Both: column n is word ce_first + n.
     const void *ce_targets;
     int32_t ce_targets64;
-    int32_t ce_first;
+    int32_t ce_first, ce_cols;
     float *ce_logit;
     const CeRow *ce_rows;
+    float *ce_lost;            // OUT_CE_GRAD: [M], what the rounding of a target's value lost
 };
 
 // Arguments of the split-K reduction and of the alpha == 0 scaling kernel.

@@ -71,7 +71,8 @@ def backward(x, w, targets, grad, scale=1.0, dx="own", dw="own", beta=0.0, lse=N
 
 SHAPES = [(1, 1, 1), (1, 2, 8), (2, 1, 16), (1, 257, 64), (3, 128, 72), (16, 300, 128), (17, 1000, 64),
           (64, 4099, 192), (129, 513, 136), (256, 256, 64), (257, 769, 520), (300, 4099, 1032),
-          (5, 300, 7), (64, 1025, 100), (33, 129, 65), (1021, 5003, 264)]
+          (5, 300, 7), (64, 1025, 100), (33, 129, 65), (1021, 5003, 264),
+          (7, 130, 2056), (32, 65, 40), (31, 1000, 72), (300, 33101, 64)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])

@@ -33,7 +33,7 @@ __device__ inline void join(float &m, float &s, float m2, float s2, float a2) {
 template <int TOK>
 __global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
     constexpr int Q = 1024 / TOK;
-    __shared__ float sm[1024], ss[1024];
+    __shared__ float sm[16][TOK], ss[16][TOK];
     const int tid = threadIdx.x, tok = tid % TOK, q = tid / TOK;
     const int64_t t = (int64_t)blockIdx.x * TOK + tok;
     const float scale = fabsf(a.scale), a2 = scale * kLog2E, least = -ce_limit(a2);
@@ -50,16 +50,16 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
             for (int k = 0; k < 8; ++k) join(m, s, v[k].x, v[k].y, a2);
         }
     }
-    sm[tid] = m;
-    ss[tid] = s;
-    for (int h = Q / 2; h > 0; h >>= 1) {
-        __syncthreads();
-        if (q < h) {
-            join(m, s, sm[tid + TOK * h], ss[tid + TOK * h], a2);
-            sm[tid] = m;
-            ss[tid] = s;
-        }
+    // over the wave's threads of a token, then over the waves
+#pragma unroll
+    for (int o = TOK; o < 64; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o), a2);
+    if ((tid & 63) < TOK) {
+        sm[tid >> 6][tok] = m;
+        ss[tid >> 6][tok] = s;
     }
+    __syncthreads();
+    if (q == 0)
+        for (int w = 1; w < 16; ++w) join(m, s, sm[w][tok], ss[w][tok], a2);
     if (q == 0 && t < a.T) {
         const float rest = logf(s);
         a.lse[t] = __builtin_fmaf(scale, m, rest);

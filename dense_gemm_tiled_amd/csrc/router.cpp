@@ -19,7 +19,7 @@ struct BalanceSpace {
 };
 BalanceSpace balance_space(const tc_route_desc &r) {
     BalanceSpace b;
-    b.count = up_to((int64_t)kBalanceGroups * r.E * 4, 256);
+    b.count = up_to((int64_t)kBalanceGroups * up_to(r.E, 4) * 4, 256);
     b.tokens = 2 * b.count;
     b.bytes = b.tokens + kBalanceGroups * 4;
     return b;
@@ -91,6 +91,7 @@ tc_status_t tc_moe_balance_async(tc_context *ctx, const tc_route_desc *r, const 
     a.loss = loss;
     a.counts = counts;
     a.slope = slope;
+    a.pitch = (int32_t)up_to(r->E, 4);
     a.part_p = reinterpret_cast<float *>(ws);
     a.part_count = reinterpret_cast<int32_t *>(ws + sp.count);
     a.part_tokens = reinterpret_cast<int32_t *>(ws + sp.tokens);

@@ -15,8 +15,9 @@ struct BalanceArgs {
     int32_t *counts;           // [E]
     float *slope;              // [E]
     // workspace: per workgroup the sums of p, the counts and the tokens
-    float *part_p;             // [groups][E]
-    int32_t *part_count;       // [groups][E]
+    int32_t pitch;             // E rounded up to 4
+    float *part_p;             // [groups][pitch]
+    int32_t *part_count;       // [groups][pitch]
     int32_t *part_tokens;      // [groups]
 };
 

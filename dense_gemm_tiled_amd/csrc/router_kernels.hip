@@ -78,10 +78,11 @@ __device__ inline void load_logits(const RouteArgs &a, int64_t row, int e, float
 // -inf and NaN have no part, +inf counts as the largest finite number.
 __device__ inline float clean(float v) { return v > -INFINITY ? fminf(v, kMaxFloat) : -INFINITY; }
 
-// v := the softmax of a token's logits (all 0 where none has a part).
+// v := exp(v - the token's largest logit), 0 for what has no part; the sum.
+// The argument's rounding is at most 2^-24 of it (exponents below -126 give 0).
 template <int V, int L, int S>
-__device__ inline void softmax_token(float (&v)[S][V]) {
-    float m = -INFINITY;
+__device__ inline float exp_token(float (&v)[S][V], float &m) {
+    m = -INFINITY;
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -95,15 +96,11 @@ __device__ inline void softmax_token(float (&v)[S][V]) {
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            v[s][i] = v[s][i] > -INFINITY ? expf(v[s][i] - m) : 0.f;
+            // (-inf less a finite number: 0)
+            v[s][i] = __builtin_amdgcn_exp2f((v[s][i] - m) * kLog2E);
             z += v[s][i];
         }
-    z = sum_token<L>(z);
-    const float r = z > 0.f ? 1.f / z : 0.f;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[s][i] *= r;
+    return sum_token<L>(z);
 }
 
 // The loss, the counts and the slopes from the sums, by one workgroup of 1024:
@@ -139,58 +136,66 @@ __device__ inline void balance_result(const BalanceArgs &a, int tid, double p, i
 }
 
 // Each workgroup's share of the tokens: sums of p in registers (a lane has the
-// same experts for every token), the next token's logits on the way while one
-// is taken.  Bound by those loads and by the cross-lane steps of the softmax.
-// ONE: the only workgroup goes on to the result.
+// same experts for every token), U tokens a group of lanes at a time, the next
+// U on the way meanwhile (one at a time: 16.4 us for 32768 x 256 f32 against
+// BAL_MAIN).  Bound by those loads.  ONE: the only workgroup goes on to the
+// result.
 template <int V, int L, int S, bool ONE>
 __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
-    constexpr int TOK = 1024 / L;                 // tokens at a time
-    __shared__ float sums[16 * kMaxExperts];      // [TOK][L S V]
+    constexpr int GROUPS = 1024 / L;
+    constexpr int U = ONE ? 1 : S * V <= 4 ? 4 : 2;
+    __shared__ float sums[16 * kMaxExperts];      // [GROUPS][L S V]
     __shared__ int count[kMaxExperts];
     __shared__ int tokens;
-    static_assert(TOK * L * S * V <= 16 * kMaxExperts, "the tokens' sums fit");
+    static_assert(GROUPS * L * S * V <= 16 * kMaxExperts, "the groups' sums fit");
     const RouteArgs &r = a.route;
     const int tid = threadIdx.x, l = tid % L, g = tid / L;
     for (int e = tid; e < kMaxExperts; e += 1024) count[e] = 0;
     if (tid == 0) tokens = 0;
     __syncthreads();
-    float p[S][V] = {}, v[S][V], next[S][V];
-    int id = -1, next_id = -1, mine = 0;
-    const int64_t step = (int64_t)gridDim.x * TOK;
-    auto load = [&](int64_t t, float (&to)[S][V], int &to_id) {
-        to_id = -1;
-        if (t < r.T) {
+    float p[S][V] = {}, v[U][S][V], next[U][S][V];
+    int id[U], next_id[U], mine = 0;
+    const int64_t step = (int64_t)gridDim.x * GROUPS * U;
+    // token u of a group's U is GROUPS further on
+    auto load = [&](int64_t t, float (&to)[U][S][V], int (&to_id)[U]) {
 #pragma unroll
-            for (int s = 0; s < S; ++s) load_logits<V>(r, t * r.ld, (s * L + l) * V, to[s]);
-            if (l < r.top_k) to_id = r.ids[t * r.top_k + l];
-        } else {
+        for (int u = 0; u < U; ++u, t += GROUPS) {
+            to_id[u] = -1;
+            const bool there = t < r.T;
+            // (past the last token: its row again, and no id)
+            const int64_t row = (there ? t : r.T - 1) * r.ld;
 #pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int i = 0; i < V; ++i) to[s][i] = -INFINITY;
+            for (int s = 0; s < S; ++s) load_logits<V>(r, row, (s * L + l) * V, to[u][s]);
+            if (there && l < r.top_k) to_id[u] = r.ids[t * r.top_k + l];
         }
     };
-    int64_t t = (int64_t)blockIdx.x * TOK + g;
+    int64_t t = (int64_t)blockIdx.x * GROUPS * U + g;
     load(t, v, id);
     // (every lane of a wave stays until the last of its tokens is done)
-    for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < r.T; t0 += step, t += step) {
-        load(t + step, next, next_id);
-        const bool inside = id >= 0 && id < r.E;
-        if (inside) atomicAdd(&count[id], 1);
-        const bool alive = max_token<L>(inside ? 1.f : 0.f) > 0.f;
-        softmax_token<V, L, S>(v);
-        if (alive) {
-            mine += 1;
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * U; t0 < r.T; t0 += step, t += step) {
+        if (t0 + step < r.T) load(t + step, next, next_id);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool inside = id[u] >= 0 && id[u] < r.E;
+            if (inside) atomicAdd(&count[id[u]], 1);
+            const bool alive = max_token<L>(inside ? 1.f : 0.f) > 0.f;
+            float m;
+            const float z = exp_token<V, L, S>(v[u], m);
+            const float f = alive && z > 0.f ? 1.f / z : 0.f;
+            mine += alive;
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int i = 0; i < V; ++i) p[s][i] += v[s][i];
+                for (int i = 0; i < V; ++i) p[s][i] = __builtin_fmaf(v[u][s][i], f, p[s][i]);
         }
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int u = 0; u < U; ++u) {
+            id[u] = next_id[u];
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[s][i] = next[s][i];
-        id = next_id;
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[u][s][i] = next[u][s][i];
+        }
     }
 #pragma unroll
     for (int s = 0; s < S; ++s)
@@ -201,189 +206,207 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
     double total = 0.0;
     if (tid < r.E) {
 #pragma unroll 4
-        for (int k = 0; k < TOK; ++k) total += sums[k * (L * S * V) + tid];
+        for (int k = 0; k < GROUPS; ++k) total += sums[k * (L * S * V) + tid];
     }
     if constexpr (ONE) {
         balance_result(a, tid, total, tid < r.E ? count[tid] : 0, tokens);
     } else {
         if (tid < r.E) {
-            a.part_p[(int64_t)blockIdx.x * r.E + tid] = (float)total;
-            a.part_count[(int64_t)blockIdx.x * r.E + tid] = count[tid];
+            a.part_p[(int64_t)blockIdx.x * a.pitch + tid] = (float)total;
+            a.part_count[(int64_t)blockIdx.x * a.pitch + tid] = count[tid];
         }
         if (tid == 0) a.part_tokens[blockIdx.x] = tokens;
     }
 }
 
-// The workgroups' sums joined, E to a slice of the threads.
+// The workgroups' sums joined, 4 experts to a thread, 4096 / pitch slices; 8
+// sums and 8 counts of a thread on the way at once.
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int groups) {
-    __shared__ double sum[1024];
-    __shared__ int cnt[1024];
+    __shared__ double sum[4096];
+    __shared__ int cnt[4096];
     __shared__ int tokens;
-    const int E = a.route.E, tid = threadIdx.x;
-    const int slices = 1024 / E, slice = tid / E, e = tid - slice * E;
+    const int E = a.route.E, tid = threadIdx.x, four = a.pitch / 4;
+    const int slices = 1024 / four, slice = tid / four, e = (tid - slice * four) * 4;
     if (tid == 0) tokens = 0;
     __syncthreads();
-    double p = 0.0;
-    int c = 0;
+    double p[4] = {};
+    i32x4 c = {0, 0, 0, 0};
     if (slice < slices) {
-#pragma unroll 8
-        for (int w = slice; w < groups; w += slices) {
-            p += a.part_p[(int64_t)w * E + e];
-            c += a.part_count[(int64_t)w * E + e];
+        for (int w = slice; w < groups; w += 8 * slices) {
+            f32x4 x[8];
+            i32x4 y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int at = w + k * slices;
+                x[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+                y[k] = i32x4{0, 0, 0, 0};
+                if (at < groups) {
+                    x[k] = *reinterpret_cast<const f32x4 *>(a.part_p + (int64_t)at * a.pitch + e);
+                    y[k] = *reinterpret_cast<const i32x4 *>(a.part_count + (int64_t)at * a.pitch + e);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                c += y[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] += (double)x[k][i];
+            }
+        }
+        // (sums and counts past E are never looked at)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum[slice * a.pitch + e + i] = p[i];
+            cnt[slice * a.pitch + e + i] = c[i];
         }
     }
     if (tid < groups) atomicAdd(&tokens, a.part_tokens[tid]);
-    sum[tid] = p;
-    cnt[tid] = c;
     __syncthreads();
-    p = 0.0;
-    c = 0;
+    double total = 0.0;
+    int n = 0;
     if (tid < E) {
         for (int k = 0; k < slices; ++k) {
-            p += sum[k * E + tid];
-            c += cnt[k * E + tid];
+            total += sum[k * a.pitch + tid];
+            n += cnt[k * a.pitch + tid];
         }
     }
-    __syncthreads();
-    balance_result(a, tid, p, c, tokens);
+    balance_result(a, tid, total, n, tokens);
 }
 
-// One token to L lanes.  Through the weights: with q the softmax over the
+// U tokens to L lanes.  Through the weights: with q the softmax over the
 // chosen, w = scale q, dl_j = w_j dw_j - q_j sum_i w_i dw_i; with weights over
 // all experts the second term goes by p, for every e.  Through the loss:
-// dloss p_e (slope_e - sum_i p_i slope_i).  Bound by reading and writing the
-// logits.
+// dloss p_e (slope_e - sum_i p_i slope_i).  The chosen logits are read back from
+// LDS, not from memory (a load that waits for the ids' load).  Bound by reading
+// and writing the logits.
 template <int V, int L, int S>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
-    constexpr int TOK = 256 / L;
-    __shared__ int at[TOK][kMaxTopK];
-    __shared__ float add[TOK][kMaxTopK];
+    constexpr int GROUPS = 256 / L, U = S * V <= 4 ? 2 : 1;
+    __shared__ float own[GROUPS][U][L * S * V];
+    __shared__ int at[GROUPS][U][kMaxTopK];
+    __shared__ float add[GROUPS][U][kMaxTopK];
     const RouteArgs &r = a.route;
     const int tid = threadIdx.x, l = tid % L, g = tid / L;
-    const int64_t t = (int64_t)blockIdx.x * TOK + g;
-    const bool there = t < r.T;
-    float v[S][V];
-    int id = -1;
-    float dw = 0.f, chosen = -INFINITY;
-    if (there) {
+    const int64_t t0 = (int64_t)blockIdx.x * GROUPS * U + g;
+    float v[U][S][V], dw[U], slope[S][V], dloss = 0.f;
+    int id[U];
 #pragma unroll
-        for (int s = 0; s < S; ++s) load_logits<V>(r, t * r.ld, (s * L + l) * V, v[s]);
-        if (l < r.top_k) {
-            id = r.ids[t * r.top_k + l];
-            if (a.dweights) dw = a.dweights[t * r.top_k + l];
+    for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * GROUPS;
+        const bool there = t < r.T;
+        id[u] = -1;
+        dw[u] = 0.f;
+        const int64_t row = (there ? t : r.T - 1) * r.ld;
+#pragma unroll
+        for (int s = 0; s < S; ++s) load_logits<V>(r, row, (s * L + l) * V, v[u][s]);
+        if (there && l < r.top_k) {
+            id[u] = r.ids[t * r.top_k + l];
+            if (a.dweights) dw[u] = a.dweights[t * r.top_k + l];
         }
-    } else {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[s][i] = -INFINITY;
     }
-    const bool inside = id >= 0 && id < r.E;
-    if (inside && a.dweights) {
-        float one[1];
-        load_logits<1>(r, t * r.ld, id, one);
-        chosen = clean(one[0]);
-    }
-    const bool alive = max_token<L>(inside ? 1.f : 0.f) > 0.f;
-    float top = -INFINITY;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[s][i] = clean(v[s][i]);
-            top = fmaxf(top, v[s][i]);
-        }
-    top = fmaxf(max_token<L>(top), -kMaxFloat);
-    float z = 0.f;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[s][i] = v[s][i] > -INFINITY ? expf(v[s][i] - top) : 0.f;
-            z += v[s][i];
-        }
-    z = sum_token<L>(z);
-    const float rz = z > 0.f ? 1.f / z : 0.f;
-    float all = 0.f;               // what every p is multiplied by, and taken off
-    if (a.dweights) {
-        // (a place whose logit has no part has weight 0 whatever dweights holds)
-        const bool part = chosen > -INFINITY;
-        float q;
-        if (r.renormalize) {
-            const float m = fmaxf(max_token<L>(chosen), -kMaxFloat);
-            q = part ? expf(chosen - m) : 0.f;
-            const float zq = sum_token<L>(q);
-            q = zq > 0.f ? q / zq : 0.f;
-        } else {
-            q = part ? expf(chosen - top) * rz : 0.f;
-        }
-        const float wd = part ? r.scale * q * dw : 0.f;
-        const float sum = sum_token<L>(wd);
-        if (l < r.top_k) {
-            at[g][l] = part ? id : -1;
-            add[g][l] = r.renormalize ? wd - q * sum : wd;
-        }
-        if (!r.renormalize) all = sum;
-    }
-    float slope[S][V];
     if (a.slope) {
-        const float dloss = a.dloss[0];
-        float mean = 0.f;
+        dloss = a.dloss[0];
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = (s * L + l) * V + i;
                 slope[s][i] = e < r.E ? a.slope[e] : 0.f;
-                mean += v[s][i] * slope[s][i];
             }
-        mean = sum_token<L>(mean) * rz;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int i = 0; i < V; ++i) slope[s][i] = dloss * (slope[s][i] - mean);
     }
-    float d[S][V];
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float f = (a.slope ? slope[s][i] : 0.f) - all;
-            // (a logit that has no part gets 0 also where f is no number)
-            d[s][i] = v[s][i] > 0.f ? v[s][i] * rz * f : 0.f;
-        }
     if (a.dweights) {
-        __syncthreads();
-        for (int j = 0; j < r.top_k; ++j) {
-            const int e = at[g][j];
-            const float x = add[g][j];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int i = 0; i < V; ++i) d[s][i] += e == (s * L + l) * V + i ? x : 0.f;
+                for (int i = 0; i < V; ++i) own[g][u][(s * L + l) * V + i] = v[u][s][i];
+        __syncthreads();
+    }
+    float all[U], rz[U], mean[U];
+    bool alive[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool inside = id[u] >= 0 && id[u] < r.E;
+        alive[u] = max_token<L>(inside ? 1.f : 0.f) > 0.f;
+        float top;
+        const float z = exp_token<V, L, S>(v[u], top);
+        rz[u] = z > 0.f ? 1.f / z : 0.f;
+        all[u] = 0.f;              // what every p is multiplied by, and taken off
+        if (a.dweights) {
+            // (a place whose logit has no part has weight 0 whatever dweights holds)
+            const float chosen = inside ? clean(own[g][u][id[u]]) : -INFINITY;
+            const bool part = chosen > -INFINITY;
+            float q;
+            if (r.renormalize) {
+                const float m = fmaxf(max_token<L>(chosen), -kMaxFloat);
+                q = __builtin_amdgcn_exp2f((chosen - m) * kLog2E);
+                const float zq = sum_token<L>(q);
+                q = zq > 0.f ? q / zq : 0.f;
+            } else {
+                q = __builtin_amdgcn_exp2f((chosen - top) * kLog2E) * rz[u];
+            }
+            const float wd = part ? r.scale * q * dw[u] : 0.f;
+            const float sum = sum_token<L>(wd);
+            if (l < r.top_k) {
+                at[g][u][l] = part ? id[u] : -1;
+                add[g][u][l] = r.renormalize ? wd - q * sum : wd;
+            }
+            if (!r.renormalize) all[u] = sum;
+        }
+        mean[u] = 0.f;
+        if (a.slope) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i) mean[u] += v[u][s][i] * slope[s][i];
+            mean[u] = sum_token<L>(mean[u]) * rz[u];
         }
     }
-    if (!there) return;
+    if (a.dweights) __syncthreads();
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int e = (s * L + l) * V;
-        if (e >= r.E) continue;
+    for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * GROUPS;
+        float d[S][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[s][i] = alive ? d[s][i] : 0.f;
-        const int64_t o = t * a.ldd + e;
-        if (a.d_dtype == DT_F32) {
-            float *to = static_cast<float *>(a.dlogits) + o;
-            if constexpr (V == 4) *reinterpret_cast<f32x4 *>(to) = f32x4{d[s][0], d[s][1], d[s][2], d[s][3]};
-            else *to = d[s][0];
-        } else {
-            unsigned short *to = static_cast<unsigned short *>(a.dlogits) + o;
-            const bool f16 = a.d_dtype == DT_F16;
-            if constexpr (V == 4) {
-                const u32x2 w = f16 ? u32x2{pack2_16<DT_F16>(d[s][0], d[s][1]), pack2_16<DT_F16>(d[s][2], d[s][3])}
-                                    : u32x2{pack2_16<DT_BF16>(d[s][0], d[s][1]), pack2_16<DT_BF16>(d[s][2], d[s][3])};
-                *reinterpret_cast<u32x2 *>(to) = w;
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float f = (a.slope ? dloss * (slope[s][i] - mean[u]) : 0.f) - all[u];
+                // (a logit that has no part gets 0 also where f is no number)
+                d[s][i] = v[u][s][i] > 0.f ? v[u][s][i] * rz[u] * f : 0.f;
+            }
+        if (a.dweights) {
+            for (int j = 0; j < r.top_k; ++j) {
+                const int e = at[g][u][j];
+                const float x = add[g][u][j];
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) d[s][i] += e == (s * L + l) * V + i ? x : 0.f;
+            }
+        }
+        if (t >= r.T) continue;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int e = (s * L + l) * V;
+            if (e >= r.E) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[s][i] = alive[u] ? d[s][i] : 0.f;
+            const int64_t o = t * a.ldd + e;
+            if (a.d_dtype == DT_F32) {
+                float *to = static_cast<float *>(a.dlogits) + o;
+                if constexpr (V == 4) *reinterpret_cast<f32x4 *>(to) = f32x4{d[s][0], d[s][1], d[s][2], d[s][3]};
+                else *to = d[s][0];
             } else {
-                *to = (unsigned short)(f16 ? to_f16_bits(d[s][0]) : to_bf16_bits(d[s][0]));
+                unsigned short *to = static_cast<unsigned short *>(a.dlogits) + o;
+                const bool f16 = a.d_dtype == DT_F16;
+                if constexpr (V == 4) {
+                    const u32x2 w = f16 ? u32x2{pack2_16<DT_F16>(d[s][0], d[s][1]), pack2_16<DT_F16>(d[s][2], d[s][3])}
+                                        : u32x2{pack2_16<DT_BF16>(d[s][0], d[s][1]), pack2_16<DT_BF16>(d[s][2], d[s][3])};
+                    *reinterpret_cast<u32x2 *>(to) = w;
+                } else {
+                    *to = (unsigned short)(f16 ? to_f16_bits(d[s][0]) : to_bf16_bits(d[s][0]));
+                }
             }
         }
     }
@@ -428,9 +451,12 @@ using namespace tcg;
 int tcg_balance_groups(const RouteArgs &a) {
     const int64_t tok = 1024 / lanes_of(a, four_at_a_time(a));
     const int64_t passes = (a.T + tok - 1) / tok;
-    // Up to 4 passes a single workgroup ends before a second launch would begin.
+    // Up to 4 passes a single workgroup ends before a second launch would
+    // begin; else workgroups that look at 2 to 4 tokens a group of lanes at a
+    // time.
     if (passes <= 4) return 1;
-    return passes < kBalanceGroups ? (int)passes : kBalanceGroups;
+    const int64_t groups = (passes + 3) / 4;
+    return groups < kBalanceGroups ? (int)groups : kBalanceGroups;
 }
 
 hipError_t tcg_launch_balance(const BalanceArgs &a, int *launches, hipStream_t s) {
@@ -459,7 +485,9 @@ hipError_t tcg_launch_route_grad(const RouteGradArgs &a, hipStream_t s) {
     const RouteArgs &r = a.route;
     if (!sizes_ok(r)) return hipErrorInvalidValue;
     const bool four = four_at_a_time(r) && a.ldd % 4 == 0 && (uintptr_t)a.dlogits % (4 * dt_size(a.d_dtype)) == 0;
-    const int64_t tok = 256 / lanes_of(r, four), blocks = (r.T + tok - 1) / tok;
+    // (2 tokens to a group of lanes where the logits of both fit 8 registers)
+    const int64_t tok = 256 / lanes_of(r, four) * (r.E <= 256 ? 2 : 1);
+    const int64_t blocks = (r.T + tok - 1) / tok;
     if (blocks >= (1 << 24)) return hipErrorInvalidValue;
 #define ROUTE_GRAD(V, L, S) \
     hipLaunchKernelGGL((route_grad_kernel<V, L, S>), dim3((unsigned)blocks), dim3(256), 0, s, a)

@@ -11,11 +11,19 @@ namespace tcg {
 
 constexpr int kCeStatCols = 2048;   // columns a workgroup of ce_stat_kernel takes
 
-// Tokens' losses from the partial softmaxes of their products: parts
-// [num][T] of (maximum, sum) and the targets' products, in units of the
-// products (negated where scale < 0).
+// Where the (maximum, sum) of share p of token t's words is: at p sp + t st.
+// Up to kCeRowsOfParts tokens a token's shares lie side by side (a workgroup
+// joins them), from there on a share's tokens do (the products write them so).
+constexpr int kCeRowsOfParts = 1024;
+struct CeParts {
+    float2 *at;
+    int64_t sp, st;
+};
+
+// Tokens' losses from the partial softmaxes of their products and the
+// targets' products, in units of the products (negated where scale < 0).
 struct CeJoinArgs {
-    const float2 *parts;
+    CeParts parts;
     const float *logit;        // [T]; read where the target is inside [0, V)
     const void *targets;
     int32_t targets64;
@@ -33,7 +41,7 @@ struct CeStatArgs {
     float scale;
     const void *targets;
     int32_t targets64;
-    float2 *parts;             // [ceil(N / kCeStatCols)][T]
+    CeParts parts;             // share: kCeStatCols words
     float *logit;
 };
 
@@ -54,6 +62,8 @@ struct CePrepArgs {
     // 16-bit types: the gradients are scaled so that the largest grad becomes
     // 2^14; the reciprocal of that factor, H times (null: no scaling)
     float *unscale;
+    void *xt;                  // few tokens only: [H][tp], or null
+    int32_t tp;
 };
 constexpr int kCeScanTokens = 4096;   // up to these every workgroup looks for the largest itself
 
@@ -92,8 +102,8 @@ struct CeFinishArgs {
     int32_t w_dtype;
 };
 
-// Partial softmaxes of the products of a few tokens, from x and w: parts
-// [ceil(V / kCeRowWords)][T] and logit as in CeStatArgs.
+// Partial softmaxes of the products of a few tokens, from x and w: a share is
+// kCeRowWords words.
 constexpr int kCeRowWords = 64, kCeRowTokens = 32;
 struct CeRowsArgs {
     const void *x, *w;
@@ -103,8 +113,25 @@ struct CeRowsArgs {
     float scale;
     const void *targets;
     int32_t targets64;
-    float2 *parts;
+    CeParts parts;
     float *logit;
+};
+
+// Few tokens' backward pass: the tokens as CePrepArgs has them, and x again
+// transposed, xt [H][tp], tp = 32 or 64 >= T, zeros past T; and dw [N, H] =
+// scale * unscale * g^T x + beta * dw from it, g [T, pitch].
+constexpr int kCeFewTokens = 64;
+struct CeOuterArgs {
+    const void *g;
+    int64_t pitch;
+    const void *xt;
+    int32_t tp;
+    int32_t T, N, H;
+    int32_t dtype;
+    float scale, beta;
+    const float *unscale;
+    void *dw;
+    int64_t lddw;              // elements
 };
 
 }  // namespace tcg
@@ -113,5 +140,6 @@ hipError_t tcg_launch_ce_join(const tcg::CeJoinArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_rows(const tcg::CeRowsArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_stat(const tcg::CeStatArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_prep(const tcg::CePrepArgs &a, int *launches, hipStream_t s);
+hipError_t tcg_launch_ce_outer(const tcg::CeOuterArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_grad(const tcg::CeGradArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_finish(const tcg::CeFinishArgs &a, hipStream_t s);

@@ -27,45 +27,74 @@ __device__ inline void join(float &m, float &s, float m2, float s2, float a2) {
     m = top;
 }
 
-// TOK tokens a workgroup, 1024 / TOK threads each: thread q takes shares q, q +
-// 1024 / TOK, ..; 8 of them on the way at once (the shares of 64 tokens by
-// 131072 words: 4 tokens a workgroup 5.x us, 16 tokens 9.2).
-template <int TOK>
-__global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
-    constexpr int Q = 1024 / TOK;
-    __shared__ float sm[16][TOK], ss[16][TOK];
-    const int tid = threadIdx.x, tok = tid % TOK, q = tid / TOK;
-    const int64_t t = (int64_t)blockIdx.x * TOK + tok;
-    const float scale = fabsf(a.scale), a2 = scale * kLog2E, least = -ce_limit(a2);
-    float m = least, s = 0.f;
-    if (t < a.T) {
-        for (int p = q; p < a.num; p += 8 * Q) {
-            float2 v[8];
+// A token's result from its joined shares.
+__device__ inline void finish_token(const CeJoinArgs &a, int64_t t, float m, float s, float scale) {
+    const float rest = logf(s);
+    a.lse[t] = __builtin_fmaf(scale, m, rest);
+    const bool counts = target_of(a.targets, a.targets64, t, a.V) >= 0;
+    a.loss[t] = counts ? __builtin_fmaf(scale, m - a.logit[t], rest) : 0.f;
+}
+
+// Thread q of Q joins shares q, q + Q, .. of token t, 8 of them on the way at
+// once.
+template <int Q>
+__device__ inline void join_shares(const CeJoinArgs &a, int64_t t, int q, float a2, float &m, float &s) {
+    const float least = -ce_limit(a2);
+    m = least;
+    s = 0.f;
+    const float2 *row = a.parts.at + t * a.parts.st;
+    for (int p = q; p < a.num; p += 8 * Q) {
+        float2 v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int at = p + k * Q;
-                v[k] = at < a.num ? a.parts[(int64_t)at * a.T + t] : make_float2(least, 0.f);
-            }
+        for (int k = 0; k < 8; ++k)
+            v[k] = p + k * Q < a.num ? row[(p + k * Q) * a.parts.sp] : make_float2(least, 0.f);
+        float top = m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) join(m, s, v[k].x, v[k].y, a2);
-        }
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, v[k].x);
+        s *= __builtin_amdgcn_exp2f((m - top) * a2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k].y * __builtin_amdgcn_exp2f((v[k].x - top) * a2);
+        m = top;
     }
-    // over the wave's threads of a token, then over the waves
+}
+
+// A token to a workgroup, its shares side by side.
+__global__ __launch_bounds__(256) void ce_join_token_kernel(CeJoinArgs a) {
+    __shared__ float sm[4], ss[4];
+    const int tid = threadIdx.x;
+    const float scale = fabsf(a.scale), a2 = scale * kLog2E;
+    float m, s;
+    join_shares<256>(a, blockIdx.x, tid, a2, m, s);
 #pragma unroll
-    for (int o = TOK; o < 64; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o), a2);
-    if ((tid & 63) < TOK) {
+    for (int o = 1; o < 64; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o), a2);
+    if ((tid & 63) == 0) {
+        sm[tid >> 6] = m;
+        ss[tid >> 6] = s;
+    }
+    __syncthreads();
+    if (tid > 0) return;
+    for (int w = 1; w < 4; ++w) join(m, s, sm[w], ss[w], a2);
+    finish_token(a, blockIdx.x, m, s, scale);
+}
+
+// 16 tokens to a workgroup, side by side in every share.
+__global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
+    __shared__ float sm[16][16], ss[16][16];
+    const int tid = threadIdx.x, tok = tid % 16, q = tid / 16;
+    const int64_t t = (int64_t)blockIdx.x * 16 + tok;
+    const float scale = fabsf(a.scale), a2 = scale * kLog2E;
+    float m = -ce_limit(a2), s = 0.f;
+    if (t < a.T) join_shares<64>(a, t, q, a2, m, s);
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o), a2);
+    if ((tid & 63) < 16) {
         sm[tid >> 6][tok] = m;
         ss[tid >> 6][tok] = s;
     }
     __syncthreads();
-    if (q == 0)
-        for (int w = 1; w < 16; ++w) join(m, s, sm[w][tok], ss[w][tok], a2);
-    if (q == 0 && t < a.T) {
-        const float rest = logf(s);
-        a.lse[t] = __builtin_fmaf(scale, m, rest);
-        const bool counts = target_of(a.targets, a.targets64, t, a.V) >= 0;
-        a.loss[t] = counts ? __builtin_fmaf(scale, m - a.logit[t], rest) : 0.f;
-    }
+    if (tid >= 16 || t >= a.T) return;
+    for (int w = 1; w < 16; ++w) join(m, s, sm[w][tok], ss[w][tok], a2);
+    finish_token(a, t, m, s, scale);
 }
 
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
@@ -168,7 +197,7 @@ __global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) s += __shfl_xor(s, o);
         if (t < a.T) {
-            if ((tid & 31) == 0) a.parts[(int64_t)blockIdx.x * a.T + t] = make_float2(m, s);
+            if ((tid & 31) == 0) a.parts.at[blockIdx.x * a.parts.sp + t * a.parts.st] = make_float2(m, s);
             const int64_t d = target_of(a.targets, a.targets64, t, a.V) - v0 - n;
             if (d == 0 || d == 1) a.logit[t] = d ? v[1] : v[0];
         }
@@ -216,7 +245,7 @@ __global__ __launch_bounds__(256) void ce_stat_kernel(CeStatArgs a) {
     __syncthreads();
     if (tid == 0) {
         for (int w = 1; w < 4; ++w) join(m, s, sm[w], ss[w], a2);
-        a.parts[(int64_t)c * a.T + t] = make_float2(m, s);
+        a.parts.at[c * a.parts.sp + t * a.parts.st] = make_float2(m, s);
     }
 }
 
@@ -288,6 +317,141 @@ __global__ __launch_bounds__(256) void ce_prep_kernel(CePrepArgs a) {
     } else {
         for (int64_t i = lane; i < a.xz_pitch; i += 64)
             reinterpret_cast<float *>(dst)[i] = live && i < a.H ? reinterpret_cast<const float *>(src)[i] : 0.f;
+    }
+}
+
+// Few tokens (16-bit): 64 columns of x for all of them to a workgroup, which
+// finds the largest grad itself; x goes out again as it is (zeros for tokens
+// that add nothing) and transposed.
+__global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
+    __shared__ unsigned short tile[kCeFewTokens][64 + 2];
+    __shared__ float grads[kCeFewTokens];
+    const int tid = threadIdx.x, c = tid & 63, h = blockIdx.x * 64 + c;
+    const float unscale = largest_grad<256>(a, tid) * 0x1p-14f;
+    if (tid < a.tp) {
+        const int t = tid;
+        const int target = t < a.T ? target_of(a.targets, a.targets64, t, a.V) : -1;
+        const float g = target >= 0 ? a.grad[t * a.grad_stride] / unscale : 0.f;
+        grads[t] = g;
+        if (blockIdx.x == 0 && t < a.T) {
+            CeRow r;
+            r.lse = g != 0.f ? a.lse[t] : 0.f;
+            r.grad = g;
+            r.target = g != 0.f ? target : -1;
+            r.pad = 0;
+            a.rows[t] = r;
+        }
+    }
+    if (tid < 64 && h < a.H) a.unscale[h] = unscale;
+    __syncthreads();
+    const unsigned short *x = static_cast<const unsigned short *>(a.x);
+    unsigned short *xz = static_cast<unsigned short *>(a.xz), *xt = static_cast<unsigned short *>(a.xt);
+#pragma unroll 4
+    for (int t = tid >> 6; t < a.tp; t += 4) {
+        const bool there = t < a.T && h < a.H;
+        const unsigned short v = there && grads[t] != 0.f ? x[t * a.ldx + h] : (unsigned short)0;
+        tile[t][c] = v;
+        if (there) xz[t * a.xz_pitch + h] = v;
+    }
+    __syncthreads();
+    // (tp is 32 or 64: lane t of a row)
+    const int t = tid & (a.tp - 1), rows = 256 / a.tp;
+    for (int k = tid / a.tp; k < 64; k += rows)
+        if (blockIdx.x * 64 + k < a.H) xt[(int64_t)(blockIdx.x * 64 + k) * a.tp + t] = tile[t][k];
+}
+
+// dw for few tokens: 2 or 4 bytes of dw to a byte of everything else, so the
+// stores should never wait.  A wave holds the gradients of 64 words (gathered
+// once: a word's tokens side by side) and runs along h, 32 columns at a time:
+// rows of xt straight into the operands' registers, the next 32 on the way,
+// each lane's 8 results of a word as one 16-byte store (64 bytes of a word to
+// 4 lanes; row 4 c + e of block j is column 32 (j / 2) + 8 c + 4 (j % 2) + e).
+// No LDS, no barriers.
+template <int DT, int KS, bool BETA>
+__global__ __launch_bounds__(256) void ce_outer_kernel(CeOuterArgs a, int per) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, c = lane >> 4;
+    const int slices = (a.H + per - 1) / per;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
+    const int64_t n0 = unit / slices * 64;
+    const int h0 = (int)(unit % slices) * per, h1 = min(a.H, h0 + per);
+    if (n0 >= a.N) return;
+    const unsigned short *g = static_cast<const unsigned short *>(a.g);
+    u32x4 gf[KS][4];
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int64_t n = n0 + 16 * b + r;
+            u32 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32 v[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int t = 32 * k + 8 * c + 2 * i + q;
+                    v[q] = t < a.T && n < a.N ? g[t * a.pitch + n] : 0u;
+                }
+                w[i] = v[0] | v[1] << 16;
+            }
+            gf[k][b] = u32x4{w[0], w[1], w[2], w[3]};
+        }
+    const float alpha = a.scale * a.unscale[0];
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xt, (int64_t)a.H * a.tp * 2);
+    const int64_t org = n0 * a.lddw;
+    const __amdgpu_buffer_rsrc_t rd =
+        make_rsrc(static_cast<unsigned short *>(a.dw) + org, ((a.N - 1 - n0) * a.lddw + a.H) * 2);
+    // (A row r of block j: column h + 32 j' ..; past H reads zeros)
+    const int xrow = 8 * (r >> 2) + (r & 3);
+    u32x4 xf[2][KS][2];
+    auto load = [&](int h, u32x4 (&to)[KS][2]) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                to[k][j] = ld128(rx, h < h1 ? ((h + xrow + 4 * j) * a.tp + 32 * k + 8 * c) * 2 : -16);
+    };
+    auto step = [&](int h, const u32x4 (&x)[KS][2]) {
+        f32x4 acc[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                acc[j][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) acc[j][b] = mma<DT>(x[k][j], gf[k][b], acc[j][b]);
+            }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            // (a store past N or H is dropped: whole pieces of 8, H a multiple of it)
+            const int64_t n = n0 + 16 * b + r;
+            const int col = h + 8 * c;
+            const int off = n < a.N && col < h1 ? ((16 * b + r) * (int)a.lddw + col) * 2 : -16;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = alpha * acc[0][b][e];
+                v[4 + e] = alpha * acc[1][b][e];
+            }
+            if constexpr (BETA) {
+                const u32x4 old = ld128(rd, off);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const u32 o = old[e / 2] >> (16 * (e & 1)) & 0xFFFFu;
+                    v[e] = __builtin_fmaf(a.beta, DT == DT_BF16 ? from_bf16_bits(o) : from_f16_bits(o), v[e]);
+                }
+            }
+            const u32x4 w = {pack2_16<DT>(v[0], v[1]), pack2_16<DT>(v[2], v[3]), pack2_16<DT>(v[4], v[5]),
+                             pack2_16<DT>(v[6], v[7])};
+            __builtin_amdgcn_raw_buffer_store_b128(w, rd, off, 0, 0);
+        }
+    };
+    load(h0, xf[0]);
+    for (int h = h0; h < h1; h += 64) {
+        load(h + 32, xf[1]);
+        step(h, xf[0]);
+        load(h + 64, xf[0]);
+        if (h + 32 < h1) step(h + 32, xf[1]);
     }
 }
 
@@ -388,12 +552,14 @@ constexpr int64_t kMaxBlocks = 1 << 24;   // of 256 threads: a launch's threads 
 using namespace tcg;
 
 hipError_t tcg_launch_ce_join(const CeJoinArgs &a, hipStream_t s) {
-    // few tokens: more threads for each
-    const int tok = a.T <= 1024 ? 4 : 16;
-    const int64_t blocks = ((int64_t)a.T + tok - 1) / tok;
-    if (a.T < 1 || a.num < 1 || blocks >= kMaxBlocks / 4) return hipErrorInvalidValue;
-    if (tok == 4) hipLaunchKernelGGL(ce_join_kernel<4>, dim3((unsigned)blocks), dim3(1024), 0, s, a);
-    else hipLaunchKernelGGL(ce_join_kernel<16>, dim3((unsigned)blocks), dim3(1024), 0, s, a);
+    if (a.T < 1 || a.num < 1) return hipErrorInvalidValue;
+    if (a.T <= kCeRowsOfParts) {
+        hipLaunchKernelGGL(ce_join_token_kernel, dim3((unsigned)a.T), dim3(256), 0, s, a);
+    } else {
+        const int64_t blocks = ((int64_t)a.T + 15) / 16;
+        if (blocks >= kMaxBlocks / 4) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -422,6 +588,13 @@ hipError_t tcg_launch_ce_stat(const CeStatArgs &a, hipStream_t s) {
 hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s) {
     const int es = dt_size(a.dtype);
     if (a.T < 1 || a.T > kMaxBlocks || (a.xz_pitch * es) % 16 != 0 || a.xz_pitch < a.H) return hipErrorInvalidValue;
+    if (a.xt) {
+        if (es != 2 || !a.unscale || (a.tp != 32 && a.tp != 64) || a.T > a.tp || a.xz_pitch != a.H)
+            return hipErrorInvalidValue;
+        hipLaunchKernelGGL(ce_prep_few_kernel, dim3((unsigned)((a.H + 63) / 64)), dim3(256), 0, s, a);
+        *launches += 1;
+        return hipGetLastError();
+    }
     if (a.unscale && a.T > kCeScanTokens) {
         hipLaunchKernelGGL(ce_unscale_kernel, dim3(1), dim3(1024), 0, s, a);
         const hipError_t e = hipGetLastError();
@@ -435,6 +608,30 @@ hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s)
     else if (vec) hipLaunchKernelGGL((ce_prep_kernel<2, true>), g, b, 0, s, a);
     else hipLaunchKernelGGL((ce_prep_kernel<2, false>), g, b, 0, s, a);
     *launches += 1;
+    return hipGetLastError();
+}
+
+hipError_t tcg_launch_ce_outer(const CeOuterArgs &a, hipStream_t s) {
+    if (a.T < 1 || a.T > a.tp || (a.tp != 32 && a.tp != 64) || a.N < 1 || a.H < 8 || a.H % 8 != 0)
+        return hipErrorInvalidValue;
+    // columns to a wave: 1024 (the gradients' gathers are then a tenth of its
+    // loads), fewer where that leaves less than 8 waves a CU
+    const int64_t words = ((int64_t)a.N + 63) / 64;
+    int per = 1024;
+    while (per > 128 && words * ((a.H + per - 1) / per) < 2048) per /= 2;
+    const int64_t blocks = (words * ((a.H + per - 1) / per) + 3) / 4;
+    if (blocks >= kMaxBlocks) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks), b(256);
+#define CE_OUTER(DT)                                                                                          \
+    do {                                                                                                      \
+        if (a.tp == 32 && a.beta == 0.f) hipLaunchKernelGGL((ce_outer_kernel<DT, 1, false>), g, b, 0, s, a, per); \
+        else if (a.tp == 32) hipLaunchKernelGGL((ce_outer_kernel<DT, 1, true>), g, b, 0, s, a, per);          \
+        else if (a.beta == 0.f) hipLaunchKernelGGL((ce_outer_kernel<DT, 2, false>), g, b, 0, s, a, per);      \
+        else hipLaunchKernelGGL((ce_outer_kernel<DT, 2, true>), g, b, 0, s, a, per);                          \
+    } while (0)
+    if (a.dtype == DT_F16) CE_OUTER(DT_F16);
+    else CE_OUTER(DT_BF16);
+#undef CE_OUTER
     return hipGetLastError();
 }
 

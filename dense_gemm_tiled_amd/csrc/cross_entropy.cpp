@@ -192,6 +192,15 @@ tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, Forwa
 
 const void *at(const void *p, int64_t bytes) { return static_cast<const char *>(p) + bytes; }
 
+// Where T tokens' shares go from share `first` on, num in all.
+CeParts parts_at(char *ws, int64_t T, int64_t num, int64_t first) {
+    CeParts p;
+    p.sp = T <= kCeRowsOfParts ? 1 : T;
+    p.st = T <= kCeRowsOfParts ? num : 1;
+    p.at = reinterpret_cast<float2 *>(ws) + first * p.sp;
+    return p;
+}
+
 tc_status_t launch_failed(std::string *err, hipError_t e) {
     (void)hipGetLastError();
     return fail(err, TC_ERR_DEVICE, "kernel launch failed: %s", hipGetErrorString(e));
@@ -220,7 +229,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
             a.scale = d.scale;
             a.targets = targets;
             a.targets64 = d.targets64;
-            a.parts = reinterpret_cast<float2 *>(ws + f.parts);
+            a.parts = parts_at(ws + f.parts, T, f.num, 0);
             a.logit = reinterpret_cast<float *>(ws + f.logit);
             num = f.num;
             e = tcg_launch_ce_rows(a, s->stream);
@@ -234,7 +243,10 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
                 const int cls = ce_class(T, N);
                 int64_t grid;
                 GemmArgs a = product_args(p, xt, p.ldx, T, at(w, v0 * p.ldw * p.es), N, d.scale, cls, &grid);
-                a.ws = reinterpret_cast<float2 *>(ws + f.parts) + num * T;
+                const CeParts parts = parts_at(ws + f.parts, T, f.num, num);
+                a.ws = parts.at;
+                a.ce_sp = parts.sp;
+                a.ce_sm = parts.st;
                 a.ce_targets = tt;
                 a.ce_targets64 = d.targets64;
                 a.ce_first = (int32_t)v0;
@@ -269,7 +281,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
                 a.scale = d.scale;
                 a.targets = tt;
                 a.targets64 = d.targets64;
-                a.parts = reinterpret_cast<float2 *>(ws + f.parts) + num * T;
+                a.parts = parts_at(ws + f.parts, T, f.num, num);
                 a.logit = reinterpret_cast<float *>(ws + f.logit);
                 e = tcg_launch_ce_stat(a, s->stream);
                 if (e != hipSuccess) return launch_failed(err, e);
@@ -279,7 +291,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
             }
         }
         CeJoinArgs j;
-        j.parts = reinterpret_cast<const float2 *>(ws + f.parts);
+        j.parts = parts_at(ws + f.parts, T, f.num, 0);
         j.logit = reinterpret_cast<const float *>(ws + f.logit);
         j.targets = tt;
         j.targets64 = d.targets64;
@@ -302,10 +314,12 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
 // the inputs' type (parts times), then its two products.
 struct BackwardSpace {
     bool fused;
+    bool outer;                        // dw of few tokens by a kernel of its own
+    int tp;                            // its tokens, rounded up
     bool own_dx;                       // dx is summed in the workspace
     int parts, dx_parts, dw_parts;
     int64_t N, pitch, xz_pitch;
-    int64_t rows, lost, unscale, xz, acc, g, l, gemm, gemm_bytes, bytes;
+    int64_t rows, lost, unscale, xz, xt, acc, g, l, gemm, gemm_bytes, bytes;
 };
 
 GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
@@ -380,6 +394,9 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     b->dw_parts = !g.dw ? 0 : g.dw_dtype == TC_F32 ? wide : 1;
     b->parts = b->dx_parts > b->dw_parts ? b->dx_parts : b->dw_parts;
     b->fused = p.whole && b->parts == 1;
+    // few tokens, whole pieces of 8 columns: dw is all stores
+    b->outer = b->fused && g.dw && p.T <= kCeFewTokens;
+    b->tp = p.T <= 32 ? 32 : 64;
     b->own_dx = g.dx && g.dx_dtype != TC_F32;
     b->xz_pitch = up_to(p.H, 16 / p.es);
     // Words at a time: 512 MiB of gradients, at least 8192 words (each piece
@@ -404,7 +421,8 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     const int64_t after = up_to(b->lost + p.T * 4, 256);
     b->unscale = p.es == 2 ? after : -1;
     b->xz = after + (p.es == 2 ? up_to(p.H * 4, 256) : 0);
-    b->acc = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
+    b->xt = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
+    b->acc = up_to(b->xt + (b->outer ? p.H * b->tp * 2 : 0), 256);
     b->g = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
     b->l = up_to(b->g + p.T * b->pitch * p.es * b->parts, 256);
     // (fp32: the gradient takes the place of its products)
@@ -432,7 +450,7 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
         for (const float beta : {g.beta, 1.f}) {
-            if (!g.dw) continue;
+            if (!g.dw || b->outer) continue;
             if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, n, beta), &bytes, err)) != TC_OK) return st;
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
@@ -464,6 +482,8 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
     pa.xz = ws + b.xz;
     pa.xz_pitch = b.xz_pitch;
     pa.unscale = unscale;
+    pa.xt = b.outer ? ws + b.xt : nullptr;
+    pa.tp = b.tp;
     int launches = 0;
     hipError_t e = tcg_launch_ce_prep(pa, &launches, s->stream);
     ctx->dispatches += launches;
@@ -534,7 +554,26 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
                 here += "+" + part;
             }
             part.clear();
-            if (k < b.dw_parts) {
+            if (b.outer) {
+                CeOuterArgs oa;
+                oa.g = gk;
+                oa.pitch = b.pitch;
+                oa.xt = ws + b.xt;
+                oa.tp = b.tp;
+                oa.T = (int32_t)p.T;
+                oa.N = (int32_t)N;
+                oa.H = (int32_t)p.H;
+                oa.dtype = p.dt;
+                oa.scale = d.scale;
+                oa.beta = g.beta;
+                oa.unscale = unscale;
+                oa.lddw = g.lddw == 0 ? p.H : g.lddw;
+                oa.dw = static_cast<char *>(g.dw) + v0 * oa.lddw * 2;
+                e = tcg_launch_ce_outer(oa, s->stream);
+                if (e != hipSuccess) return launch_failed(err, e);
+                ctx->dispatches += 1;
+                here += "+ce_outer";
+            } else if (k < b.dw_parts) {
                 GemmCall c = dw_call(p, b, g, d.scale, N, k > 0 ? 1.f : g.beta);
                 c.A = gk;
                 c.B = ws + b.xz;

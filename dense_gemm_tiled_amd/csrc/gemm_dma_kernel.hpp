@@ -920,7 +920,7 @@ void gemm_dma_kernel(const GemmArgs args) {
                 }
         }
         const float a2 = __builtin_fabsf(args.alpha) * kLog2E, limit = ce_limit(a2);
-        float2 *part = static_cast<float2 *>(args.ws) + (int64_t)(tn * WNW + wn) * M + m0;
+        float2 *part = static_cast<float2 *>(args.ws) + (tn * WNW + wn) * args.ce_sp + m0 * args.ce_sm;
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int ml = ml_of(i);
@@ -941,7 +941,7 @@ void gemm_dma_kernel(const GemmArgs args) {
                     s += __builtin_amdgcn_exp2f((acc[i][j][e] - mx) * a2);
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
-            if (lane < 16 && row_in) part[ml] = make_float2(mx, s);
+            if (lane < 16 && row_in) part[ml * args.ce_sm] = make_float2(mx, s);
             // the target's product, from the lane that holds it
             const int d = tgt[ml] - (n0 + nl_of(0, 0));
             const bool hit = row_in && d >= 0 && d < WTN && (d & 12) == 0;

@@ -15,13 +15,15 @@ int64_t up_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 // The workspace of a balance loss (as if spread over as many workgroups as
 // there may be: how many there are depends on the logits' address, too).
 struct BalanceSpace {
-    int64_t count, tokens, bytes;
+    int64_t count, tokens, dot, joined, bytes;
 };
 BalanceSpace balance_space(const tc_route_desc &r) {
     BalanceSpace b;
     b.count = up_to((int64_t)kBalanceGroups * up_to(r.E, 4) * 4, 256);
     b.tokens = 2 * b.count;
-    b.bytes = b.tokens + kBalanceGroups * 4;
+    b.dot = b.tokens + kBalanceGroups * 8;
+    b.joined = b.dot + kMaxExperts / 16 * 8;
+    b.bytes = b.joined + 4;
     return b;
 }
 
@@ -94,7 +96,9 @@ tc_status_t tc_moe_balance_async(tc_context *ctx, const tc_route_desc *r, const 
     a.pitch = (int32_t)up_to(r->E, 4);
     a.part_p = reinterpret_cast<float *>(ws);
     a.part_count = reinterpret_cast<int32_t *>(ws + sp.count);
-    a.part_tokens = reinterpret_cast<int32_t *>(ws + sp.tokens);
+    a.part_tokens = reinterpret_cast<int2 *>(ws + sp.tokens);
+    a.part_dot = reinterpret_cast<double *>(ws + sp.dot);
+    a.joined = reinterpret_cast<int32_t *>(ws + sp.joined);
     int launches = 0;
     const hipError_t e = tcg_launch_balance(a, &launches, s->stream);
     ctx->dispatches += launches;

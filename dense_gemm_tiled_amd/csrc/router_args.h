@@ -18,7 +18,9 @@ struct BalanceArgs {
     int32_t pitch;             // E rounded up to 4
     float *part_p;             // [groups][pitch]
     int32_t *part_count;       // [groups][pitch]
-    int32_t *part_tokens;      // [groups]
+    int2 *part_tokens;         // [groups] tokens that count, places
+    double *part_dot;          // [kMaxExperts / 16] joined workgroups' shares of the loss
+    int32_t *joined;           // how many of them have ended
 };
 
 struct RouteGradArgs {

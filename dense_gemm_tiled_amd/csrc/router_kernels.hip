@@ -16,7 +16,7 @@ constexpr float kMaxFloat = 3.4028235e38f;
 // vector ALU (reads across lanes through LDS would take as long as the loads).
 template <int CTRL>
 __device__ inline float ror(float x) {
-    return as_f32((u32)__builtin_amdgcn_update_dpp(0, (int)as_u32(x), CTRL, 0xF, 0xF, false));
+    return as_f32((u32)__builtin_amdgcn_update_dpp(0, (int)as_u32(x), CTRL, 0xF, 0xF, true));
 }
 template <int L, class F>
 __device__ inline float over_token(float x, F f) {
@@ -75,8 +75,20 @@ __device__ inline void load_logits(const RouteArgs &a, int64_t row, int e, float
     }
 }
 
-// -inf and NaN have no part, +inf counts as the largest finite number.
-__device__ inline float clean(float v) { return v > -INFINITY ? fminf(v, kMaxFloat) : -INFINITY; }
+// -inf and NaN (which a maximum passes over) have no part, +inf counts as the
+// largest finite number.
+__device__ inline float clean(float v) { return __builtin_fminf(__builtin_fmaxf(v, -INFINITY), kMaxFloat); }
+
+// Whether the condition holds in one of a token's lanes.
+template <int L>
+__device__ inline bool any_of_token(bool c) {
+    const uint64_t set = __ballot(c);
+    if constexpr (L == 64) return set != 0;
+    return (set >> ((threadIdx.x & 63) / L * L) & ((1ull << L) - 1)) != 0;
+}
+
+// Keeps LDS accesses of one wave (whose order the LDS keeps) in program order.
+__device__ inline void in_order() { asm volatile("" ::: "memory"); }
 
 // v := exp(v - the token's largest logit), 0 for what has no part; the sum.
 // The argument's rounding is at most 2^-24 of it (exponents below -126 give 0).
@@ -103,36 +115,37 @@ __device__ inline float exp_token(float (&v)[S][V], float &m) {
     return sum_token<L>(z);
 }
 
-// The loss, the counts and the slopes from the sums, by one workgroup of 1024:
-// thread e (and 512 threads at most) holds expert e's.
-__device__ inline void balance_result(const BalanceArgs &a, int tid, double p, int count, int tokens) {
-    __shared__ double dot[16];
-    __shared__ int64_t tot[16];
-    double d = p * count;
-    int64_t c = count;
+// What a workgroup of NT threads knows of its experts (thread e of expert e)
+// summed: the places over all experts, and the sum of places times p.
+template <int NT>
+__device__ inline void balance_sums(int tid, double &dot, int64_t &places) {
+    __shared__ double d[NT / 64];
+    __shared__ int64_t n[NT / 64];
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        d += __shfl_xor(d, o);
-        c += __shfl_xor((long long)c, o);
+        dot += __shfl_xor(dot, o);
+        places += __shfl_xor((long long)places, o);
     }
     if ((tid & 63) == 0) {
-        dot[tid >> 6] = d;
-        tot[tid >> 6] = c;
+        d[tid >> 6] = dot;
+        n[tid >> 6] = places;
     }
     __syncthreads();
-    d = 0.0;
-    c = 0;
-    for (int w = 0; w < 16; ++w) {
-        d += dot[w];
-        c += tot[w];
+    dot = 0.0;
+    places = 0;
+    for (int w = 0; w < NT / 64; ++w) {
+        dot += d[w];
+        places += n[w];
     }
-    const int E = a.route.E;
-    const double scale = c > 0 ? (double)a.coef / ((double)c * tokens) : 0.0;
-    if (tid < E) {
-        a.counts[tid] = count;
-        a.slope[tid] = (float)(scale * (double)((int64_t)E * count - c));
-    }
-    if (tid == 0) a.loss[0] = (float)(scale * E * d);
+}
+
+// coef / (total n), 0 where no token counts
+__device__ inline double balance_scale(const BalanceArgs &a, int64_t total, int tokens) {
+    return total > 0 ? (double)a.coef / ((double)total * tokens) : 0.0;
+}
+__device__ inline void balance_expert(const BalanceArgs &a, int e, int count, int64_t total, double scale) {
+    a.counts[e] = count;
+    a.slope[e] = (float)(scale * (double)((int64_t)a.route.E * count - total));
 }
 
 // Each workgroup's share of the tokens: sums of p in registers (a lane has the
@@ -150,9 +163,6 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
     static_assert(GROUPS * L * S * V <= 16 * kMaxExperts, "the groups' sums fit");
     const RouteArgs &r = a.route;
     const int tid = threadIdx.x, l = tid % L, g = tid / L;
-    for (int e = tid; e < kMaxExperts; e += 1024) count[e] = 0;
-    if (tid == 0) tokens = 0;
-    __syncthreads();
     float p[S][V] = {}, v[U][S][V], next[U][S][V];
     int id[U], next_id[U], mine = 0;
     const int64_t step = (int64_t)gridDim.x * GROUPS * U;
@@ -171,6 +181,9 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
     };
     int64_t t = (int64_t)blockIdx.x * GROUPS * U + g;
     load(t, v, id);
+    for (int e = tid; e < kMaxExperts; e += 1024) count[e] = 0;
+    if (tid == 0) tokens = 0;
+    __syncthreads();
     // (every lane of a wave stays until the last of its tokens is done)
     for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * U; t0 < r.T; t0 += step, t += step) {
         if (t0 + step < r.T) load(t + step, next, next_id);
@@ -178,7 +191,7 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
         for (int u = 0; u < U; ++u) {
             const bool inside = id[u] >= 0 && id[u] < r.E;
             if (inside) atomicAdd(&count[id[u]], 1);
-            const bool alive = max_token<L>(inside ? 1.f : 0.f) > 0.f;
+            const bool alive = any_of_token<L>(inside);
             float m;
             const float z = exp_token<V, L, S>(v[u], m);
             const float f = alive && z > 0.f ? 1.f / z : 0.f;
@@ -208,68 +221,102 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
 #pragma unroll 4
         for (int k = 0; k < GROUPS; ++k) total += sums[k * (L * S * V) + tid];
     }
+    const int own = tid < r.E ? count[tid] : 0;
     if constexpr (ONE) {
-        balance_result(a, tid, total, tid < r.E ? count[tid] : 0, tokens);
+        double dot = total * own;
+        int64_t places = own;
+        balance_sums<1024>(tid, dot, places);
+        const double scale = balance_scale(a, places, tokens);
+        if (tid < r.E) balance_expert(a, tid, own, places, scale);
+        if (tid == 0) a.loss[0] = (float)(scale * r.E * dot);
     } else {
+        double none = 0.0;
+        int64_t places = own;
+        balance_sums<1024>(tid, none, places);
         if (tid < r.E) {
             a.part_p[(int64_t)blockIdx.x * a.pitch + tid] = (float)total;
-            a.part_count[(int64_t)blockIdx.x * a.pitch + tid] = count[tid];
+            a.part_count[(int64_t)blockIdx.x * a.pitch + tid] = own;
         }
-        if (tid == 0) a.part_tokens[blockIdx.x] = tokens;
+        if (tid == 0) a.part_tokens[blockIdx.x] = make_int2(tokens, (int)places);
+        if (tid == 0 && blockIdx.x == 0) *a.joined = 0;
     }
 }
 
-// The workgroups' sums joined, 4 experts to a thread, 4096 / pitch slices; 8
-// sums and 8 counts of a thread on the way at once.
+// The workgroups' sums joined: 16 experts to a workgroup (one alone would read
+// for 4 us: a CU gets some 130 GB/s), 4 threads to a share.  The last workgroup
+// to end adds up what the others left of the loss, in their order.
+constexpr int kJoinExperts = 16;
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int groups) {
-    __shared__ double sum[4096];
-    __shared__ int cnt[4096];
-    __shared__ int tokens;
-    const int E = a.route.E, tid = threadIdx.x, four = a.pitch / 4;
-    const int slices = 1024 / four, slice = tid / four, e = (tid - slice * four) * 4;
-    if (tid == 0) tokens = 0;
-    __syncthreads();
-    double p[4] = {};
+    __shared__ double sum[256][kJoinExperts + 1];
+    __shared__ int cnt[256][kJoinExperts + 1];
+    __shared__ int64_t total;
+    __shared__ int tokens, last;
+    const int E = a.route.E, tid = threadIdx.x, slice = tid / 4, i4 = tid % 4 * 4;
+    const int e0 = blockIdx.x * kJoinExperts;
+    // (kBalanceGroups shares at most, one to every 4 threads)
+    const bool there = slice < groups && e0 + i4 < E;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
     i32x4 c = {0, 0, 0, 0};
-    if (slice < slices) {
-        for (int w = slice; w < groups; w += 8 * slices) {
-            f32x4 x[8];
-            i32x4 y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int at = w + k * slices;
-                x[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-                y[k] = i32x4{0, 0, 0, 0};
-                if (at < groups) {
-                    x[k] = *reinterpret_cast<const f32x4 *>(a.part_p + (int64_t)at * a.pitch + e);
-                    y[k] = *reinterpret_cast<const i32x4 *>(a.part_count + (int64_t)at * a.pitch + e);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                c += y[k];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] += (double)x[k][i];
-            }
-        }
-        // (sums and counts past E are never looked at)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sum[slice * a.pitch + e + i] = p[i];
-            cnt[slice * a.pitch + e + i] = c[i];
-        }
+    if (there) {
+        x = *reinterpret_cast<const f32x4 *>(a.part_p + (int64_t)slice * a.pitch + e0 + i4);
+        c = *reinterpret_cast<const i32x4 *>(a.part_count + (int64_t)slice * a.pitch + e0 + i4);
     }
-    if (tid < groups) atomicAdd(&tokens, a.part_tokens[tid]);
+    int2 n = make_int2(0, 0);
+    if (tid < groups) n = a.part_tokens[tid];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum[slice][i4 + i] = (double)x[i];
+        cnt[slice][i4 + i] = c[i];
+    }
+    if (tid == 0) {
+        total = 0;
+        tokens = 0;
+    }
     __syncthreads();
-    double total = 0.0;
-    int n = 0;
-    if (tid < E) {
-        for (int k = 0; k < slices; ++k) {
-            total += sum[k * a.pitch + tid];
-            n += cnt[k * a.pitch + tid];
+    // whole numbers, in any order
+    int64_t places = n.y;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        places += __shfl_xor((long long)places, o);
+        n.x += __shfl_xor(n.x, o);
+    }
+    if ((tid & 63) == 0 && tid < groups) {
+        atomicAdd((unsigned long long *)&total, (unsigned long long)places);
+        atomicAdd(&tokens, n.x);
+    }
+    // expert i of the workgroup's: 64 lanes of wave i, 4 shares each
+    const int i = tid >> 6, lane = tid & 63;
+    double p = 0.0;
+    int k = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        p += sum[lane * 4 + q][i];
+        k += cnt[lane * 4 + q][i];
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        p += __shfl_xor(p, o);
+        k += __shfl_xor(k, o);
+    }
+    __syncthreads();
+    if (lane == 0) sum[0][i] = e0 + i < E ? p * k : 0.0;
+    const double scale = balance_scale(a, total, tokens);
+    if (lane == 0 && e0 + i < E) balance_expert(a, e0 + i, k, total, scale);
+    __syncthreads();
+    if (tid == 0) {
+        double dot = 0.0;
+        for (int q = 0; q < kJoinExperts; ++q) dot += sum[0][q];
+        a.part_dot[blockIdx.x] = dot;
+        __threadfence();
+        last = atomicAdd(a.joined, 1) == (int)gridDim.x - 1;
+        if (last) {
+            __threadfence();
+            dot = 0.0;
+            for (unsigned w = 0; w < gridDim.x; ++w)
+                dot += __hip_atomic_load(a.part_dot + w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            a.loss[0] = (float)(scale * E * dot);
         }
     }
-    balance_result(a, tid, total, n, tokens);
 }
 
 // U tokens to L lanes.  Through the weights: with q the softmax over the
@@ -281,9 +328,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int g
 template <int V, int L, int S>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
     constexpr int GROUPS = 256 / L, U = S * V <= 4 ? 2 : 1;
-    __shared__ float own[GROUPS][U][L * S * V];
-    __shared__ int at[GROUPS][U][kMaxTopK];
-    __shared__ float add[GROUPS][U][kMaxTopK];
+    __shared__ __attribute__((aligned(16))) float own[GROUPS][U][L * S * V];
     const RouteArgs &r = a.route;
     const int tid = threadIdx.x, l = tid % L, g = tid / L;
     const int64_t t0 = (int64_t)blockIdx.x * GROUPS * U + g;
@@ -320,18 +365,19 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int i = 0; i < V; ++i) own[g][u][(s * L + l) * V + i] = v[u][s][i];
-        __syncthreads();
+        in_order();
     }
-    float all[U], rz[U], mean[U];
+    float all[U], rz[U], mean[U], add[U];
     bool alive[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const bool inside = id[u] >= 0 && id[u] < r.E;
-        alive[u] = max_token<L>(inside ? 1.f : 0.f) > 0.f;
+        alive[u] = any_of_token<L>(inside);
         float top;
         const float z = exp_token<V, L, S>(v[u], top);
         rz[u] = z > 0.f ? 1.f / z : 0.f;
         all[u] = 0.f;              // what every p is multiplied by, and taken off
+        add[u] = 0.f;              // what the lane's own place adds to its logit
         if (a.dweights) {
             // (a place whose logit has no part has weight 0 whatever dweights holds)
             const float chosen = inside ? clean(own[g][u][id[u]]) : -INFINITY;
@@ -347,10 +393,8 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
             }
             const float wd = part ? r.scale * q * dw[u] : 0.f;
             const float sum = sum_token<L>(wd);
-            if (l < r.top_k) {
-                at[g][u][l] = part ? id[u] : -1;
-                add[g][u][l] = r.renormalize ? wd - q * sum : wd;
-            }
+            add[u] = r.renormalize ? wd - q * sum : wd;
+            if (!part) id[u] = -1;
             if (!r.renormalize) all[u] = sum;
         }
         mean[u] = 0.f;
@@ -362,29 +406,56 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
             mean[u] = sum_token<L>(mean[u]) * rz[u];
         }
     }
-    if (a.dweights) __syncthreads();
+    // The places' shares go to their logits' lanes through the token's row in
+    // LDS: zeros, then each place's own.  Where two places name one logit (the
+    // number of the last to write it is not the other's) they add one by one.
+    if (a.dweights) {
+        in_order();
+        bool twice = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float *row = own[g][u];
+            const bool place = id[u] >= 0 && id[u] < r.E;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i) row[(s * L + l) * V + i] = 0.f;
+            in_order();
+            if (place) row[id[u]] = as_f32((u32)l);
+            in_order();
+            if (place) twice = twice || as_u32(row[id[u]]) != (u32)l;
+            in_order();
+            if (place) row[id[u]] = add[u];
+        }
+        if (__any(twice)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float *row = own[g][u];
+                const bool place = id[u] >= 0 && id[u] < r.E;
+                in_order();
+                if (place) row[id[u]] = 0.f;
+                for (int j = 0; j < r.top_k; ++j) {
+                    in_order();
+                    if (place && l == j) row[id[u]] += add[u];
+                }
+            }
+        }
+        in_order();
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t t = t0 + u * GROUPS;
+        const float c1 = dloss * rz[u], c0 = all[u] * rz[u];
         float d[S][V];
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float f = (a.slope ? dloss * (slope[s][i] - mean[u]) : 0.f) - all[u];
+                const float f = a.slope ? __builtin_fmaf(slope[s][i] - mean[u], c1, -c0) : -c0;
                 // (a logit that has no part gets 0 also where f is no number)
-                d[s][i] = v[u][s][i] > 0.f ? v[u][s][i] * rz[u] * f : 0.f;
+                d[s][i] = v[u][s][i] > 0.f ? v[u][s][i] * f : 0.f;
+                if (a.dweights) d[s][i] += own[g][u][(s * L + l) * V + i];
             }
-        if (a.dweights) {
-            for (int j = 0; j < r.top_k; ++j) {
-                const int e = at[g][u][j];
-                const float x = add[g][u][j];
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) d[s][i] += e == (s * L + l) * V + i ? x : 0.f;
-            }
-        }
         if (t >= r.T) continue;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -475,7 +546,7 @@ hipError_t tcg_launch_balance(const BalanceArgs &a, int *launches, hipStream_t s
     if (e != hipSuccess) return e;
     *launches += 1;
     if (groups == 1) return e;
-    hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, s, a, groups);
+    hipLaunchKernelGGL(balance_join_kernel, dim3((r.E + kJoinExperts - 1) / kJoinExperts), dim3(1024), 0, s, a, groups);
     e = hipGetLastError();
     if (e == hipSuccess) *launches += 1;
     return e;

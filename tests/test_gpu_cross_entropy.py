@@ -98,6 +98,17 @@ def test_scale(dtype, scale):
     backward(x, w, targets, torch.rand(70, device="cuda", generator=g), scale)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("beta", [0.0, 1.0])
+@pytest.mark.parametrize("T,V,H,pad", [(1, 65, 8, 0), (31, 1000, 1032, 0), (32, 130, 136, 8), (33, 63, 2056, 3),
+                                       (64, 5000, 72, 0), (50, 30000, 200, 5)])
+def test_gradients_of_few_tokens(T, V, H, pad, beta, dtype):
+    x, w, targets, g = case(T, V, H, dtype, seed=T + V + 2)
+    old = torch.randn(V, H, device="cuda", generator=g)
+    backward(x, w, targets, torch.rand(T, device="cuda", generator=g) + 0.1, beta=beta, old=old, pads=(pad, pad))
+    backward(x, w, targets, torch.rand(T, device="cuda", generator=g) + 0.1, dx=None, beta=beta, old=old)
+
+
 @pytest.mark.parametrize("T,V,H,dtype", [(33000, 17000, 64, "bf16"), (5000, 20000, 16, "f32"),
                                          (4100, 40003, 24, "f16"), (4100, 40003, 23, "bf16")])
 def test_many_pieces(T, V, H, dtype):

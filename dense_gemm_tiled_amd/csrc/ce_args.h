@@ -104,7 +104,7 @@ struct CeFinishArgs {
 
 // Partial softmaxes of the products of a few tokens, from x and w: a share is
 // kCeRowWords words.
-constexpr int kCeRowWords = 64, kCeRowTokens = 32;
+constexpr int kCeRowWords = 64, kCeRowTokens = 32;    // (gradients: kCeFewTokens)
 struct CeRowsArgs {
     const void *x, *w;
     int64_t ldx, ldw;          // elements
@@ -115,11 +115,18 @@ struct CeRowsArgs {
     int32_t targets64;
     CeParts parts;
     float *logit;
+    // or their gradients: g [T, pitch] (columns V .. pitch written 0) of words
+    // first .. first + V, as CeGradArgs has them
+    const CeRow *rows;
+    void *g;
+    int64_t pitch;
+    int32_t first;
+    float *lost;
 };
 
-// Few tokens' backward pass: the tokens as CePrepArgs has them, and x again
-// transposed, xt [H][tp], tp = 32 or 64 >= T, zeros past T; and dw [N, H] =
-// scale * unscale * g^T x + beta * dw from it, g [T, pitch].
+// Few tokens' backward pass: the tokens as CePrepArgs has them, x transposed, xt
+// [H][tp], tp = 32 or 64 >= T, zeros past T and for tokens that add nothing; and
+// dw [N, H] = scale * unscale * g^T x + beta * dw from it, g [T, pitch].
 constexpr int kCeFewTokens = 64;
 struct CeOuterArgs {
     const void *g;
@@ -137,7 +144,7 @@ struct CeOuterArgs {
 }  // namespace tcg
 
 hipError_t tcg_launch_ce_join(const tcg::CeJoinArgs &a, hipStream_t s);
-hipError_t tcg_launch_ce_rows(const tcg::CeRowsArgs &a, hipStream_t s);
+hipError_t tcg_launch_ce_rows(const tcg::CeRowsArgs &a, bool grad, hipStream_t s);
 hipError_t tcg_launch_ce_stat(const tcg::CeStatArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_prep(const tcg::CePrepArgs &a, int *launches, hipStream_t s);
 hipError_t tcg_launch_ce_outer(const tcg::CeOuterArgs &a, hipStream_t s);

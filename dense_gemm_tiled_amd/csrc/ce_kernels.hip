@@ -114,9 +114,8 @@ __device__ inline f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // 8th group of 64 k each (whole 128-byte lines of every row), straight from
 // memory into the operands' registers, the next group on the way while one is
 // multiplied; the waves' sums meet in LDS and leave as one share of the
-// softmax per token.  1 token by 32768 x 2048 bf16: see the table of measured
-// times.
-template <int DT, int TB>
+// softmax per token, or (GRAD) as the gradients of its products.
+template <int DT, int TB, bool GRAD>
 __global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
     constexpr int W = kCeRowWords, PITCH = W + 4;
     __shared__ float sums[8][TB * 16][PITCH];
@@ -135,12 +134,17 @@ __global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     u32x4 wf[2][2][4], xf[2][2][TB];
+    const int groups = (a.H + 63) / 64;
+    // (a workgroup of an XCD begins 1 KiB behind the one before: rows of a power
+    // of two bytes would keep all of them on the same few memory channels; 1
+    // token by 65536 x 4096 130 -> 99 us)
+    const int rot = (int)((blockIdx.x / 8 * 8) % (unsigned)groups);
     // group g: k = 64 g + 32 h + 8 c .. + 7 for half h; past H nothing is read
     auto load = [&](int g, u32x4 (&wt)[2][4], u32x4 (&xt)[2][TB]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int k = g * 64 + h * 32 + c * 8;
-            const bool in = k < a.H;
+            const int k = (g + rot < groups ? g + rot : g + rot - groups) * 64 + h * 32 + c * 8;
+            const bool in = g < groups && k < a.H;
 #pragma unroll
             for (int b = 0; b < 4; ++b) wt[h][b] = ld128(rw, in ? wrow + b * wstep + k * 2 : -16);
 #pragma unroll
@@ -155,7 +159,6 @@ __global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b) acc[t][b] = mma<DT>(wt[h][b], xt[h][t], acc[t][b]);
     };
-    const int groups = (a.H + 63) / 64;
     load(wave, wf[0], xf[0]);
     for (int g = wave; g < groups; g += 16) {
         load(g + 8, wf[1], xf[1]);
@@ -175,6 +178,37 @@ __global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
             *reinterpret_cast<f32x4 *>(&sums[wave][t * 16 + r][b * 16 + c * 4]) = acc[t][b];
     __syncthreads();
     // 32 lanes to a token, 2 words each
+    if constexpr (GRAD) {
+        const int64_t n = v0 + (tid & 31) * 2;
+#pragma unroll
+        for (int p = 0; p < TB; ++p) {
+            const int t = p * 16 + (tid >> 5);
+            if (t >= a.T) continue;
+            const CeRow row = a.rows[t];
+            float v[2];
+            int at = -1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) x += sums[w][t][(tid & 31) * 2 + e];
+                const float z = __builtin_fmaf(x, a.scale, -row.lse);
+                const bool hit = row.target >= 0 && n + e == row.target - a.first;
+                v[e] = row.grad * (hit ? expm1f(z) : __builtin_amdgcn_exp2f(z * kLog2E));
+                // (a token that adds nothing, whatever its products are)
+                if (row.grad == 0.f || n + e >= a.V) v[e] = 0.f;
+                if (hit) at = e;
+            }
+            const u32 w = pack2_16<DT>(v[0], v[1]);
+            if (n < a.pitch)
+                *reinterpret_cast<u32 *>(static_cast<unsigned short *>(a.g) + t * a.pitch + n) = w;
+            if (at >= 0) {
+                const u32 h = at ? w >> 16 : w & 0xFFFFu;
+                a.lost[t] = (at ? v[1] : v[0]) - (DT == DT_BF16 ? from_bf16_bits(h) : from_f16_bits(h));
+            }
+        }
+        return;
+    }
     const float a2 = fabsf(a.scale) * kLog2E, limit = ce_limit(a2);
     const u32 flip = a.scale < 0.f ? 0x80000000u : 0u;
     const int n = (tid & 31) * 2;
@@ -321,12 +355,30 @@ __global__ __launch_bounds__(256) void ce_prep_kernel(CePrepArgs a) {
 }
 
 // Few tokens (16-bit): 64 columns of x for all of them to a workgroup, which
-// finds the largest grad itself; x goes out again as it is (zeros for tokens
-// that add nothing) and transposed.
+// finds the largest grad itself and writes x transposed.
+template <bool VEC>
 __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
-    __shared__ unsigned short tile[kCeFewTokens][64 + 2];
+    __shared__ __attribute__((aligned(16))) unsigned short tile[kCeFewTokens][72];
     __shared__ float grads[kCeFewTokens];
-    const int tid = threadIdx.x, c = tid & 63, h = blockIdx.x * 64 + c;
+    const int tid = threadIdx.x, h0 = blockIdx.x * 64;
+    const unsigned short *x = static_cast<const unsigned short *>(a.x);
+    // 8 threads to a token's 64 columns, two tokens to a thread
+    const int t8 = tid >> 3, c8 = tid & 7;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int t = t8 + 32 * p;
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (t < a.T && h0 + c8 * 8 < a.H) {
+            const unsigned short *from = x + t * a.ldx + h0 + c8 * 8;
+            if constexpr (VEC) {
+                v = *reinterpret_cast<const u32x4 *>(from);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = from[2 * e] | (u32)from[2 * e + 1] << 16;
+            }
+        }
+        *reinterpret_cast<u32x4 *>(&tile[t][c8 * 8]) = v;
+    }
     const float unscale = largest_grad<256>(a, tid) * 0x1p-14f;
     if (tid < a.tp) {
         const int t = tid;
@@ -342,40 +394,56 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
             a.rows[t] = r;
         }
     }
-    if (tid < 64 && h < a.H) a.unscale[h] = unscale;
+    if (tid < 64 && h0 + tid < a.H) a.unscale[h0 + tid] = unscale;
     __syncthreads();
-    const unsigned short *x = static_cast<const unsigned short *>(a.x);
-    unsigned short *xz = static_cast<unsigned short *>(a.xz), *xt = static_cast<unsigned short *>(a.xt);
-#pragma unroll 4
-    for (int t = tid >> 6; t < a.tp; t += 4) {
-        const bool there = t < a.T && h < a.H;
-        const unsigned short v = there && grads[t] != 0.f ? x[t * a.ldx + h] : (unsigned short)0;
-        tile[t][c] = v;
-        if (there) xz[t * a.xz_pitch + h] = v;
+    // (tp is 32 or 64: 8 tokens of a column to a thread)
+    unsigned short *xt = static_cast<unsigned short *>(a.xt);
+    const int per = a.tp / 8;
+    for (int i = tid; i < 64 * per; i += 256) {
+        const int k = i / per, t = i % per * 8;
+        if (h0 + k >= a.H) continue;
+        u32 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const u32 lo = grads[t + 2 * e] != 0.f ? tile[t + 2 * e][k] : 0u;
+            const u32 hi = grads[t + 2 * e + 1] != 0.f ? tile[t + 2 * e + 1][k] : 0u;
+            w[e] = lo | hi << 16;
+        }
+        *reinterpret_cast<u32x4 *>(xt + (int64_t)(h0 + k) * a.tp + t) = u32x4{w[0], w[1], w[2], w[3]};
     }
-    __syncthreads();
-    // (tp is 32 or 64: lane t of a row)
-    const int t = tid & (a.tp - 1), rows = 256 / a.tp;
-    for (int k = tid / a.tp; k < 64; k += rows)
-        if (blockIdx.x * 64 + k < a.H) xt[(int64_t)(blockIdx.x * 64 + k) * a.tp + t] = tile[t][k];
+    if (!a.xz) return;
+    unsigned short *xz = static_cast<unsigned short *>(a.xz);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int t = t8 + 32 * p;
+        if (t < a.T && h0 + c8 * 8 < a.H)
+            *reinterpret_cast<u32x4 *>(xz + t * a.xz_pitch + h0 + c8 * 8) =
+                grads[t] != 0.f ? *reinterpret_cast<const u32x4 *>(&tile[t][c8 * 8]) : u32x4{0u, 0u, 0u, 0u};
+    }
 }
 
-// dw for few tokens: 2 or 4 bytes of dw to a byte of everything else, so the
-// stores should never wait.  A wave holds the gradients of 64 words (gathered
-// once: a word's tokens side by side) and runs along h, 32 columns at a time:
-// rows of xt straight into the operands' registers, the next 32 on the way,
-// each lane's 8 results of a word as one 16-byte store (64 bytes of a word to
-// 4 lanes; row 4 c + e of block j is column 32 (j / 2) + 8 c + 4 (j % 2) + e).
-// No LDS, no barriers.
+// dw for few tokens: one byte read for many stored, so the stores should never
+// wait.  A workgroup keeps `per` columns of xt in LDS, each of its waves the
+// gradients of 64 words in registers (gathered once: a word's tokens side by
+// side); then it runs along the columns, 32 at a time: operands from LDS, whose
+// reads a wave can wait for without its stores, each lane's 8 results of a
+// word as one 16-byte store (64 bytes of a word to 4 lanes; row 4 c + e of block
+// j is column 32 (j / 2) + 8 c + 4 (j % 2) + e).
+constexpr int kOuterWaves = 8;
 template <int DT, int KS, bool BETA>
-__global__ __launch_bounds__(256) void ce_outer_kernel(CeOuterArgs a, int per) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(kOuterWaves * 64) void ce_outer_kernel(CeOuterArgs a, int per) {
+    constexpr int ROW = KS * 64 + 16;                 // bytes; 16 rows hit different banks
+    constexpr int COLS = 512;
+    __shared__ __attribute__((aligned(16))) char xs[COLS * ROW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
     const int slices = (a.H + per - 1) / per;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-    const int64_t n0 = unit / slices * 64;
-    const int h0 = (int)(unit % slices) * per, h1 = min(a.H, h0 + per);
-    if (n0 >= a.N) return;
+    const int64_t n0 = ((int64_t)(blockIdx.x / slices) * kOuterWaves + wave) * 64;
+    const int h0 = (int)(blockIdx.x % slices) * per, h1 = min(a.H, h0 + per);
+    const char *xt = static_cast<const char *>(a.xt) + (int64_t)h0 * KS * 64;
+    for (int i = tid; i < (h1 - h0) * KS * 4; i += kOuterWaves * 64)
+        *reinterpret_cast<u32x4 *>(xs + i / (KS * 4) * ROW + i % (KS * 4) * 16) =
+            *reinterpret_cast<const u32x4 *>(xt + (int64_t)i * 16);
     const unsigned short *g = static_cast<const unsigned short *>(a.g);
     u32x4 gf[KS][4];
 #pragma unroll
@@ -397,36 +465,42 @@ __global__ __launch_bounds__(256) void ce_outer_kernel(CeOuterArgs a, int per) {
             gf[k][b] = u32x4{w[0], w[1], w[2], w[3]};
         }
     const float alpha = a.scale * a.unscale[0];
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xt, (int64_t)a.H * a.tp * 2);
-    const int64_t org = n0 * a.lddw;
+    __syncthreads();
+    if (n0 >= a.N) return;
+    const int64_t org = n0 * a.lddw + h0;
     const __amdgpu_buffer_rsrc_t rd =
-        make_rsrc(static_cast<unsigned short *>(a.dw) + org, ((a.N - 1 - n0) * a.lddw + a.H) * 2);
-    // (A row r of block j: column h + 32 j' ..; past H reads zeros)
-    const int xrow = 8 * (r >> 2) + (r & 3);
-    u32x4 xf[2][KS][2];
-    auto load = [&](int h, u32x4 (&to)[KS][2]) {
+        make_rsrc(static_cast<unsigned short *>(a.dw) + org, ((a.N - 1 - n0) * a.lddw + a.H - h0) * 2);
+    const char *row = xs + (8 * (r >> 2) + (r & 3)) * ROW + c * 16;
+    int off[4];
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                to[k][j] = ld128(rx, h < h1 ? ((h + xrow + 4 * j) * a.tp + 32 * k + 8 * c) * 2 : -16);
-    };
-    auto step = [&](int h, const u32x4 (&x)[KS][2]) {
+    for (int b = 0; b < 4; ++b)
+        off[b] = n0 + 16 * b + r < a.N ? ((16 * b + r) * (int)a.lddw + 8 * c) * 2 : INT32_MIN;
+    // (each wave's words begin 64 bytes behind the last one's: as for the loads,
+    // rows of a power of two bytes would all go to the same memory channels)
+    const int span = (h1 - h0 + 31) / 32;
+    int at = (int)((n0 / 64) % span);
+    for (int i = 0; i < span; ++i) {
+        const int h = at * 32;
+        at = at + 1 == span ? 0 : at + 1;
         f32x4 acc[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                acc[j][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int b = 0; b < 4; ++b) acc[j][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) acc[j][b] = mma<DT>(x[k][j], gf[k][b], acc[j][b]);
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // (rows past the slice: what the LDS holds, for columns not stored)
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(row + (h + 4 * j) * ROW + k * 64);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) acc[j][b] = mma<DT>(x, gf[k][b], acc[j][b]);
             }
+        // (whole pieces of 8 columns; a store past N or the slice is dropped)
+        const bool in = h + 8 * c < h1 - h0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            // (a store past N or H is dropped: whole pieces of 8, H a multiple of it)
-            const int64_t n = n0 + 16 * b + r;
-            const int col = h + 8 * c;
-            const int off = n < a.N && col < h1 ? ((16 * b + r) * (int)a.lddw + col) * 2 : -16;
+            const int to = in ? off[b] + 2 * h : INT32_MIN;
             float v[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -434,7 +508,7 @@ __global__ __launch_bounds__(256) void ce_outer_kernel(CeOuterArgs a, int per) {
                 v[4 + e] = alpha * acc[1][b][e];
             }
             if constexpr (BETA) {
-                const u32x4 old = ld128(rd, off);
+                const u32x4 old = ld128(rd, to);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const u32 o = old[e / 2] >> (16 * (e & 1)) & 0xFFFFu;
@@ -443,15 +517,8 @@ __global__ __launch_bounds__(256) void ce_outer_kernel(CeOuterArgs a, int per) {
             }
             const u32x4 w = {pack2_16<DT>(v[0], v[1]), pack2_16<DT>(v[2], v[3]), pack2_16<DT>(v[4], v[5]),
                              pack2_16<DT>(v[6], v[7])};
-            __builtin_amdgcn_raw_buffer_store_b128(w, rd, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(w, rd, to, 0, 0);
         }
-    };
-    load(h0, xf[0]);
-    for (int h = h0; h < h1; h += 64) {
-        load(h + 32, xf[1]);
-        step(h, xf[0]);
-        load(h + 64, xf[0]);
-        if (h + 32 < h1) step(h + 32, xf[1]);
     }
 }
 
@@ -563,18 +630,22 @@ hipError_t tcg_launch_ce_join(const CeJoinArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t tcg_launch_ce_rows(const CeRowsArgs &a, hipStream_t s) {
+hipError_t tcg_launch_ce_rows(const CeRowsArgs &a, bool grad, hipStream_t s) {
     const int64_t blocks = ((int64_t)a.V + kCeRowWords - 1) / kCeRowWords;
-    if (a.T < 1 || a.T > kCeRowTokens || blocks >= kMaxBlocks / 2) return hipErrorInvalidValue;
+    if (a.T < 1 || a.T > (grad ? kCeFewTokens : kCeRowTokens) || blocks >= kMaxBlocks / 2)
+        return hipErrorInvalidValue;
     const dim3 g((unsigned)blocks), b(512);
-    const bool one = a.T <= 16;
-    if (a.dtype == DT_F16) {
-        if (one) hipLaunchKernelGGL((ce_rows_kernel<DT_F16, 1>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((ce_rows_kernel<DT_F16, 2>), g, b, 0, s, a);
-    } else {
-        if (one) hipLaunchKernelGGL((ce_rows_kernel<DT_BF16, 1>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((ce_rows_kernel<DT_BF16, 2>), g, b, 0, s, a);
-    }
+#define CE_ROWS(DT)                                                                              \
+    do {                                                                                         \
+        if (!grad && a.T <= 16) hipLaunchKernelGGL((ce_rows_kernel<DT, 1, false>), g, b, 0, s, a); \
+        else if (!grad) hipLaunchKernelGGL((ce_rows_kernel<DT, 2, false>), g, b, 0, s, a);        \
+        else if (a.T <= 16) hipLaunchKernelGGL((ce_rows_kernel<DT, 1, true>), g, b, 0, s, a);     \
+        else if (a.T <= 32) hipLaunchKernelGGL((ce_rows_kernel<DT, 2, true>), g, b, 0, s, a);     \
+        else hipLaunchKernelGGL((ce_rows_kernel<DT, 4, true>), g, b, 0, s, a);                    \
+    } while (0)
+    if (a.dtype == DT_F16) CE_ROWS(DT_F16);
+    else CE_ROWS(DT_BF16);
+#undef CE_ROWS
     return hipGetLastError();
 }
 
@@ -589,9 +660,13 @@ hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s)
     const int es = dt_size(a.dtype);
     if (a.T < 1 || a.T > kMaxBlocks || (a.xz_pitch * es) % 16 != 0 || a.xz_pitch < a.H) return hipErrorInvalidValue;
     if (a.xt) {
-        if (es != 2 || !a.unscale || (a.tp != 32 && a.tp != 64) || a.T > a.tp || a.xz_pitch != a.H)
+        if (es != 2 || !a.unscale || (a.tp != 32 && a.tp != 64) || a.T > a.tp || a.H % 8 != 0)
             return hipErrorInvalidValue;
-        hipLaunchKernelGGL(ce_prep_few_kernel, dim3((unsigned)((a.H + 63) / 64)), dim3(256), 0, s, a);
+        const dim3 g((unsigned)((a.H + 63) / 64)), b(256);
+        if (a.ldx % 8 == 0 && (uintptr_t)a.x % 16 == 0)
+            hipLaunchKernelGGL(ce_prep_few_kernel<true>, g, b, 0, s, a);
+        else
+            hipLaunchKernelGGL(ce_prep_few_kernel<false>, g, b, 0, s, a);
         *launches += 1;
         return hipGetLastError();
     }
@@ -614,14 +689,14 @@ hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s)
 hipError_t tcg_launch_ce_outer(const CeOuterArgs &a, hipStream_t s) {
     if (a.T < 1 || a.T > a.tp || (a.tp != 32 && a.tp != 64) || a.N < 1 || a.H < 8 || a.H % 8 != 0)
         return hipErrorInvalidValue;
-    // columns to a wave: 1024 (the gradients' gathers are then a tenth of its
-    // loads), fewer where that leaves less than 8 waves a CU
-    const int64_t words = ((int64_t)a.N + 63) / 64;
-    int per = 1024;
-    while (per > 128 && words * ((a.H + per - 1) / per) < 2048) per /= 2;
-    const int64_t blocks = (words * ((a.H + per - 1) / per) + 3) / 4;
-    if (blocks >= kMaxBlocks) return hipErrorInvalidValue;
-    const dim3 g((unsigned)blocks), b(256);
+    // columns to a workgroup: 512, fewer where that leaves less than two
+    // workgroups a CU
+    const int64_t words = ((int64_t)a.N + 64 * kOuterWaves - 1) / (64 * kOuterWaves);
+    int per = 512;
+    while (per > 64 && words * ((a.H + per - 1) / per) < 512) per /= 2;
+    const int64_t blocks = words * ((a.H + per - 1) / per);
+    if (blocks >= kMaxBlocks / 2) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks), b(kOuterWaves * 64);
 #define CE_OUTER(DT)                                                                                          \
     do {                                                                                                      \
         if (a.tp == 32 && a.beta == 0.f) hipLaunchKernelGGL((ce_outer_kernel<DT, 1, false>), g, b, 0, s, a, per); \

@@ -83,6 +83,16 @@ int64_t first_words(int64_t T, int64_t N) {
     return rounds(T, n, 256) + rest + 0.05 < whole ? n : N;
 }
 
+// Whether few tokens' products with N words go by ce_rows_kernel: where the
+// 128 x 128 tiles would leave half the CUs idle, and for very few tokens over
+// little memory, where its smaller shares end closer together.  us, loss, rows
+// / tiles: 1 token by 8192 x 1024 12.6 / 15.1, 4096 x 4096 24.0 / 36.3, 32768 x
+// 2048 31.1 / 35.9, 32768 x 4096 53.8 / 51.5, 131072 x 4096 197 / 183; 32
+// tokens 8192 x 1024 13.0 / 15.5, 32768 x 2048 37.8 / 33.6.
+bool takes_rows(int64_t T, int64_t N, int64_t H) {
+    return T <= kCeRowTokens && (N <= 16384 || (T <= 8 && N * H <= (80 << 20)));
+}
+
 // Arguments of the products x W^T with an epilogue of their own.
 GemmArgs product_args(const CeProblem &p, const void *x, int64_t ldx, int64_t T, const void *w, int64_t N,
                       float scale, int cls, int64_t *grid) {
@@ -105,6 +115,7 @@ GemmArgs product_args(const CeProblem &p, const void *x, int64_t ldx, int64_t T,
     a.k_per_split = (int32_t)up_to(p.H, kLdsRowBytes / p.es);
     a.groups = 1;
     a.band = 8;
+    a.ce_rotate = a.tiles_m <= 4;
     *grid = (int64_t)a.tiles_m * a.tiles_n;
     return a;
 }
@@ -139,7 +150,7 @@ struct ForwardSpace {
 
 tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, ForwardSpace *f, std::string *err) {
     f->fused = p.whole && p.ldx % 8 == 0 && (uintptr_t)x % 16 == 0;
-    f->few = f->fused && p.T <= kCeRowTokens && ceil_div(p.V, kCeRowWords) < kMaxGroups / 2;
+    f->few = f->fused && takes_rows(p.T, p.V, p.H);
     f->Tc = p.T < 16384 ? p.T : 16384;
     f->l = f->gemm = f->gemm_bytes = 0;
     if (f->few) {
@@ -218,6 +229,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
         int64_t num = 0;
         if (f.few) {
             CeRowsArgs a;
+            memset(&a, 0, sizeof a);
             a.x = x;
             a.w = w;
             a.ldx = p.ldx;
@@ -232,7 +244,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
             a.parts = parts_at(ws + f.parts, T, f.num, 0);
             a.logit = reinterpret_cast<float *>(ws + f.logit);
             num = f.num;
-            e = tcg_launch_ce_rows(a, s->stream);
+            e = tcg_launch_ce_rows(a, false, s->stream);
             if (e != hipSuccess) return launch_failed(err, e);
             ctx->dispatches += 1;
             here = "ce_rows";
@@ -314,8 +326,8 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
 // the inputs' type (parts times), then its two products.
 struct BackwardSpace {
     bool fused;
-    bool outer;                        // dw of few tokens by a kernel of its own
-    int tp;                            // its tokens, rounded up
+    bool few;                          // few tokens: kernels of their own, no copy of x
+    int tp;                            // their number, rounded up
     bool own_dx;                       // dx is summed in the workspace
     int parts, dx_parts, dw_parts;
     int64_t N, pitch, xz_pitch;
@@ -330,6 +342,15 @@ GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &
     c.d = gemm_desc(p.T, p.H, N, p.dt, TC_F32, false, false, scale, beta, b.pitch, p.ldw, ld);
     c.B = w;
     c.whole[0] = true;
+    // one row of tiles over a long K: as many slices of it as CUs (the planner's
+    // choice for under 128 rows and from 8192 columns on is the 64 x 64 tile
+    // unsliced: 64 tokens, 32768 words by 8192 947 us against DX_SLICED)
+    const int64_t tiles = ceil_div(p.H, 128), ktiles = ceil_div(N, 64);
+    if (p.whole && p.T <= 128 && p.H >= 256 && ktiles >= 32 && tiles <= 256) {
+        int64_t s = 256 / tiles;
+        if (s > ktiles / 4) s = ktiles / 4;
+        c.slices = (int32_t)(s > 32 ? 32 : s);
+    }
     return c;
 }
 
@@ -382,8 +403,9 @@ tc_status_t check_grads(const tc_ce_grads *g, const CeProblem &p, std::string *e
     return TC_OK;
 }
 
-tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale, const void *w,
+tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale, const void *x, const void *w,
                           BackwardSpace *b, std::string *err) {
+    const bool x_whole = p.ldx % 8 == 0 && (uintptr_t)x % 16 == 0;
     // A gradient in fp32 from 16-bit inputs: the products' gradient as the sum
     // of as many numbers as fp32 shows (24 bits: three of bf16; two of f16
     // have 22).  One in the inputs' type takes one: that rounding is as large
@@ -394,8 +416,7 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     b->dw_parts = !g.dw ? 0 : g.dw_dtype == TC_F32 ? wide : 1;
     b->parts = b->dx_parts > b->dw_parts ? b->dx_parts : b->dw_parts;
     b->fused = p.whole && b->parts == 1;
-    // few tokens, whole pieces of 8 columns: dw is all stores
-    b->outer = b->fused && g.dw && p.T <= kCeFewTokens;
+    b->few = b->fused && x_whole && p.T <= kCeFewTokens;
     b->tp = p.T <= 32 ? 32 : 64;
     b->own_dx = g.dx && g.dx_dtype != TC_F32;
     b->xz_pitch = up_to(p.H, 16 / p.es);
@@ -422,7 +443,7 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     b->unscale = p.es == 2 ? after : -1;
     b->xz = after + (p.es == 2 ? up_to(p.H * 4, 256) : 0);
     b->xt = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
-    b->acc = up_to(b->xt + (b->outer ? p.H * b->tp * 2 : 0), 256);
+    b->acc = up_to(b->xt + (b->few ? p.H * b->tp * 2 : 0), 256);
     b->g = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
     b->l = up_to(b->g + p.T * b->pitch * p.es * b->parts, 256);
     // (fp32: the gradient takes the place of its products)
@@ -450,7 +471,7 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
         for (const float beta : {g.beta, 1.f}) {
-            if (!g.dw || b->outer) continue;
+            if (!g.dw || b->few) continue;
             if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, n, beta), &bytes, err)) != TC_OK) return st;
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
@@ -482,7 +503,7 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
     pa.xz = ws + b.xz;
     pa.xz_pitch = b.xz_pitch;
     pa.unscale = unscale;
-    pa.xt = b.outer ? ws + b.xt : nullptr;
+    pa.xt = b.few ? ws + b.xt : nullptr;
     pa.tp = b.tp;
     int launches = 0;
     hipError_t e = tcg_launch_ce_prep(pa, &launches, s->stream);
@@ -496,7 +517,28 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
         const int64_t N = p.V - v0 < b.N ? p.V - v0 : b.N;
         const void *wv = at(w, v0 * p.ldw * p.es);
         std::string here;
-        if (b.fused) {
+        if (b.few && takes_rows(p.T, N, p.H)) {
+            CeRowsArgs a;
+            memset(&a, 0, sizeof a);
+            a.x = x;
+            a.w = wv;
+            a.ldx = p.ldx;
+            a.ldw = p.ldw;
+            a.T = (int32_t)p.T;
+            a.V = (int32_t)N;
+            a.H = (int32_t)p.H;
+            a.dtype = p.dt;
+            a.scale = d.scale;
+            a.rows = rows;
+            a.g = ws + b.g;
+            a.pitch = b.pitch;
+            a.first = (int32_t)v0;
+            a.lost = lost;
+            e = tcg_launch_ce_rows(a, true, s->stream);
+            if (e != hipSuccess) return launch_failed(err, e);
+            ctx->dispatches += 1;
+            here = "ce_rows_grad";
+        } else if (b.fused) {
             const int64_t first = first_words(p.T, N);
             for (int64_t n0 = 0; n0 < N; n0 += first) {
                 const int64_t n = n0 == 0 ? first : N - n0;
@@ -554,7 +596,7 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
                 here += "+" + part;
             }
             part.clear();
-            if (b.outer) {
+            if (b.few && g.dw) {
                 CeOuterArgs oa;
                 oa.g = gk;
                 oa.pitch = b.pitch;
@@ -682,7 +724,7 @@ tc_status_t tc_cross_entropy_backward_workspace(const tc_ce_desc *d, const tc_ce
     BackwardSpace b;
     tc_status_t st = check_ce(d, x, w, &p, nullptr);
     if (st == TC_OK) st = check_grads(g, p, nullptr);
-    if (st == TC_OK) st = plan_backward(p, *g, d->scale, w, &b, nullptr);
+    if (st == TC_OK) st = plan_backward(p, *g, d->scale, x, w, &b, nullptr);
     if (st == TC_OK) *bytes = b.bytes;
     return st;
 }
@@ -705,7 +747,7 @@ tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d
     if ((uintptr_t)lse % 4 != 0)
         return fail(err, TC_ERR_INVALID_ARGUMENT, "lse must be aligned to its elements");
     if ((st = check_grads(g, p, err)) != TC_OK) return st;
-    if ((st = plan_backward(p, *g, d->scale, w, &b, err)) != TC_OK) return st;
+    if ((st = plan_backward(p, *g, d->scale, x, w, &b, err)) != TC_OK) return st;
     if ((st = check_space(workspace, workspace_bytes, b.bytes, err)) != TC_OK) return st;
     const Range r[] = {
         {"workspace", workspace, b.bytes},

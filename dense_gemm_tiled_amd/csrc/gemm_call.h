@@ -14,6 +14,8 @@ struct GemmCall {
     const float *col_scale;    // N per-column factors, or null
     bool whole[2];             // A's, B's rows are stored in whole 16-byte
                                // pieces, what lies past them zeros
+    int32_t slices;            // 0: the planner's choice; else the 4-stage 128 x
+                               // 128 tile with so many slices of K
 };
 
 // Bytes of scratch memory the call needs.

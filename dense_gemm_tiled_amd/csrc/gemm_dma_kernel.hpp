@@ -416,6 +416,11 @@ struct RingSrc {
         base += step;
         rem -= step;
     }
+    // back by n K-tiles
+    __device__ inline void rewind(int n) {
+        base -= n * step;
+        rem += n * step;
+    }
 };
 
 // Buffer offset of load j of a group, whose immediate offset adds j KiB
@@ -524,6 +529,17 @@ void gemm_dma_kernel(const GemmArgs args) {
     fa.init(lane, wm * WTM);
     fb.init(lane, wn * WTN);
 
+    // Cross entropy with one row of tiles: all the tiles in flight would read
+    // the same 128 bytes of every 8 KiB at the same time (rows of a power of
+    // two bytes), a few memory channels' share.  So tile column tn begins at
+    // K-tile tn and wraps around (loss of 64
+    // tokens by 65536 words of 4096: 128 -> 97 us, of 256 tokens 143 -> 108).
+    constexpr bool CE = CE_STAT || CE_GRAD;
+    const int rot = CE && args.ce_rotate ? tn % nkt : 0;
+    auto k_at = [&](int t) {
+        if constexpr (!CE) return t;
+        return t >= nkt || t + rot < nkt ? t + (t < nkt ? rot : 0) : t + rot - nkt;
+    };
     // Buffer resources of tile kt, based at its origin; a tile past the end
     // of the K slice gets empty ranges (its loads fetch nothing and read
     // zeros, into a stage nobody reads).
@@ -679,7 +695,7 @@ void gemm_dma_kernel(const GemmArgs args) {
     if constexpr (RING) {
       if (nkt > 0) {
         // items 0 .. 3 (tiles 0 and 1) into slots 0 .. 3
-        const TileSrc s0 = tile_src(0), s1 = tile_src(1);
+        const TileSrc s0 = tile_src(k_at(0)), s1 = tile_src(k_at(1));
 #pragma unroll
         for (int d = 0; d < LPA; ++d) dma_a(s0, lds, d);
 #pragma unroll
@@ -695,8 +711,9 @@ void gemm_dma_kernel(const GemmArgs args) {
         // Sources of the loaded tiles from tile 2 on, advanced one K-tile per
         // iteration; only tiles inside the K slice are loaded (the last two
         // iterations load nothing).
-        RingSrc ga = ring_src(2, Ab, args.a_extent, A_MC, args.lda, m0);
-        RingSrc gb = ring_src(2, Bb, args.b_extent, B_MC, args.ldb, n0);
+        [[maybe_unused]] int ld = k_at(2);    // (CE: the K-tile they are at)
+        RingSrc ga = ring_src(ld, Ab, args.a_extent, A_MC, args.lda, m0);
+        RingSrc gb = ring_src(ld, Bb, args.b_extent, B_MC, args.ldb, n0);
         // M0 offsets of this wave's load groups inside a slot
         const uint32_t wofs_a = dwave * LPA * 1024, wofs_b = dwave * LPB * 1024;
         // slot addresses of items 2kt .. 2kt+4, advanced by 2 (mod 5) per tile
@@ -727,7 +744,7 @@ void gemm_dma_kernel(const GemmArgs args) {
             static_assert(CPH == 0 || (!WL && NW == 4 && NDW == NW && LPA == 8 && LPB == 8 && BN == 256),
                           "C quarters: 8 loads per wave, every wave loading");
             const uint32_t a_at = s_a, b_at = s_b, an_at = s_an, bn_at = s_bn, ld_at = s_ld;
-            const int kv = min(BK, k_hi - (k_lo + (kt + 2) * BK));
+            const int kv = min(BK, k_hi - (k_lo + (CE ? ld : kt + 2) * BK));
             // sub-step 0: reads of sub-step 1 from tile kt, A of tile kt+2 (or C
             // quarter 0 into the slot tile kt+2's A would have taken)
             {
@@ -770,6 +787,13 @@ void gemm_dma_kernel(const GemmArgs args) {
                          });
             }
             if constexpr (WL) gb.advance();
+            if constexpr (WL && CE) {
+                if (++ld == nkt) {
+                    ld = 0;
+                    ga.rewind(nkt);
+                    gb.rewind(nkt);
+                }
+            }
             if constexpr (CPH == 1) {
                 cq0 = ld_at;
                 cq1 = a_at;
@@ -801,7 +825,7 @@ void gemm_dma_kernel(const GemmArgs args) {
     } else if (nkt > 0) {
 #pragma unroll
         for (int t = 0; t < NST; ++t) {
-            const TileSrc st = tile_src(t);
+            const TileSrc st = tile_src(k_at(t));
 #pragma unroll
             for (int d = 0; d < ND; ++d) dma(st, lds + t * STAGE, d);
         }
@@ -818,8 +842,9 @@ void gemm_dma_kernel(const GemmArgs args) {
         for (int r = 0; r < NR; ++r) read(lds, 0, r, a0, b0);
         // sources of tile NST on, advanced one K-tile per iteration (tiles
         // past the K slice: empty ranges)
-        RingSrc ga = ring_src(NST, Ab, args.a_extent, A_MC, args.lda, m0);
-        RingSrc gb = ring_src(NST, Bb, args.b_extent, B_MC, args.ldb, n0);
+        [[maybe_unused]] int ld = k_at(NST);
+        RingSrc ga = ring_src(ld, Ab, args.a_extent, A_MC, args.lda, m0);
+        RingSrc gb = ring_src(ld, Bb, args.b_extent, B_MC, args.ldb, n0);
         // M0 offsets of this wave's load groups inside a stage
         static_assert(LPA % kLoadGroup == 0 && LPB % kLoadGroup == 0, "whole load groups per operand");
         const uint32_t wofs_a = dwave * LPA * 1024, wofs_b = A_BYTES + dwave * LPB * 1024;
@@ -834,7 +859,7 @@ void gemm_dma_kernel(const GemmArgs args) {
             // sub-step 0 and the loads of tile kt+NST into `cur` (A, then B),
             // a group of loads per M0 write
             const bool inside = kt + NST < nkt;
-            const int kv = min(BK, k_hi - (k_lo + (kt + NST) * BK));
+            const int kv = min(BK, k_hi - (k_lo + (CE ? ld : kt + NST) * BK));
             const i32x4 ra = ga.rsrc(inside), rb = gb.rsrc(inside);
             ring_sub(std::integral_constant<int, ND>{}, a1, b1,
                      [&](int r) { read(nxt, 0, r, a0, b0); },
@@ -854,6 +879,13 @@ void gemm_dma_kernel(const GemmArgs args) {
                      });
             ga.advance();
             gb.advance();
+            if constexpr (CE) {
+                if (++ld == nkt) {
+                    ld = 0;
+                    ga.rewind(nkt);
+                    gb.rewind(nkt);
+                }
+            }
         }
         // no load may still be writing LDS when the workgroup ends, and the
         // last MFMA results need wait states before the accumulators are read

@@ -141,6 +141,7 @@ struct GemmArgs {
     const void *ce_targets;
     int32_t ce_targets64;
     int32_t ce_first, ce_cols;
+    int32_t ce_rotate;         // tile column tn starts at K-tile tn (see the kernel)
     int64_t ce_sp, ce_sm;
     float *ce_logit;
     const CeRow *ce_rows;

@@ -104,7 +104,7 @@ struct CeFinishArgs {
 
 // Partial softmaxes of the products of a few tokens, from x and w: a share is
 // kCeRowWords words.
-constexpr int kCeRowWords = 64, kCeRowTokens = 32;    // (gradients: kCeFewTokens)
+constexpr int kCeRowWords = 64, kCeRowTokens = 32;
 struct CeRowsArgs {
     const void *x, *w;
     int64_t ldx, ldw;          // elements
@@ -124,8 +124,8 @@ struct CeRowsArgs {
     float *lost;
 };
 
-// Few tokens' backward pass: the tokens as CePrepArgs has them, x transposed, xt
-// [H][tp], tp = 32 or 64 >= T, zeros past T and for tokens that add nothing; and
+// Few tokens' backward pass: the tokens as CePrepArgs has them, x transposed,
+// xt [H][tp], tp = 32 or 64 >= T, zeros for tokens that add nothing; and
 // dw [N, H] = scale * unscale * g^T x + beta * dw from it, g [T, pitch].
 constexpr int kCeFewTokens = 64;
 struct CeOuterArgs {

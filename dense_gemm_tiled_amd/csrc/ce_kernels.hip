@@ -362,10 +362,10 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
     __shared__ float grads[kCeFewTokens];
     const int tid = threadIdx.x, h0 = blockIdx.x * 64;
     const unsigned short *x = static_cast<const unsigned short *>(a.x);
-    // 8 threads to a token's 64 columns, two tokens to a thread
+    // 8 threads to a token's 64 columns, up to 4 tokens to a thread
     const int t8 = tid >> 3, c8 = tid & 7;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < kCeFewTokens / 32; ++p) {
         const int t = t8 + 32 * p;
         u32x4 v = {0u, 0u, 0u, 0u};
         if (t < a.T && h0 + c8 * 8 < a.H) {
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
     }
     if (tid < 64 && h0 + tid < a.H) a.unscale[h0 + tid] = unscale;
     __syncthreads();
-    // (tp is 32 or 64: 8 tokens of a column to a thread)
+    // (8 tokens of a column to a thread)
     unsigned short *xt = static_cast<unsigned short *>(a.xt);
     const int per = a.tp / 8;
     for (int i = tid; i < 64 * per; i += 256) {
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
     if (!a.xz) return;
     unsigned short *xz = static_cast<unsigned short *>(a.xz);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < kCeFewTokens / 32; ++p) {
         const int t = t8 + 32 * p;
         if (t < a.T && h0 + c8 * 8 < a.H)
             *reinterpret_cast<u32x4 *>(xz + t * a.xz_pitch + h0 + c8 * 8) =
@@ -425,15 +425,27 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
 // dw for few tokens: one byte read for many stored, so the stores should never
 // wait.  A workgroup keeps `per` columns of xt in LDS, each of its waves the
 // gradients of 64 words in registers (gathered once: a word's tokens side by
-// side); then it runs along the columns, 32 at a time: operands from LDS, whose
-// reads a wave can wait for without its stores, each lane's 8 results of a
-// word as one 16-byte store (64 bytes of a word to 4 lanes; row 4 c + e of block
-// j is column 32 (j / 2) + 8 c + 4 (j % 2) + e).
+// side); then it runs along the columns, 64 at a time: operands from LDS, whose
+// reads a wave can wait for without its stores, 8 results of a word
+// to a 16-byte store (row 4 c + e of block j is column 32 (j / 2) + 8 c + 4 (j %
+// 2) + e).
 constexpr int kOuterWaves = 8;
-template <int DT, int KS, bool BETA>
+// The value of the lane 8 further on in the row of 16.
+__device__ inline u32 swap8(u32 x) {
+    return (u32)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true);
+}
+// LINES: dw's rows are whole 128-byte lines.  What is stored is not read again
+// here, so then non-temporal stores keep it out of the memory-side cache, which
+// would write it back while the next kernel reads w.  Gradients of 64 tokens by
+// 65536 x 4096 bf16: 409 us with half lines, 384 with whole ones, 345 with
+// these; 8 tokens by 131072 x 4096 686 / 623 / 598.  (Rows of 2056: 190 us with
+// ordinary stores, 262 with these.)
+constexpr int kNonTemporal = 2;
+constexpr int kOuterColumns = 512;            // of xt: two workgroups of a CU can keep them
+template <int DT, int KS, bool BETA, bool LINES>
 __global__ __launch_bounds__(kOuterWaves * 64) void ce_outer_kernel(CeOuterArgs a, int per) {
     constexpr int ROW = KS * 64 + 16;                 // bytes; 16 rows hit different banks
-    constexpr int COLS = 512;
+    constexpr int COLS = kOuterColumns, AUX = LINES ? kNonTemporal : 0;
     __shared__ __attribute__((aligned(16))) char xs[COLS * ROW];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
@@ -471,53 +483,89 @@ __global__ __launch_bounds__(kOuterWaves * 64) void ce_outer_kernel(CeOuterArgs 
     const __amdgpu_buffer_rsrc_t rd =
         make_rsrc(static_cast<unsigned short *>(a.dw) + org, ((a.N - 1 - n0) * a.lddw + a.H - h0) * 2);
     const char *row = xs + (8 * (r >> 2) + (r & 3)) * ROW + c * 16;
-    int off[4];
+    // A store's lanes: words 0 .. 7 of a block, then 8 .. 15; 8 lanes have a
+    // word's 64 columns, a whole line (lanes r and r + 8 exchange the halves that
+    // are the other's).
+    const bool low = r < 8;
+    const int half = low ? 0 : 32;
+    int off[4][2];
 #pragma unroll
     for (int b = 0; b < 4; ++b)
-        off[b] = n0 + 16 * b + r < a.N ? ((16 * b + r) * (int)a.lddw + 8 * c) * 2 : INT32_MIN;
-    // (each wave's words begin 64 bytes behind the last one's: as for the loads,
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int n = 16 * b + 8 * q + (r & 7);
+            off[b][q] = n0 + n < a.N ? (n * (int)a.lddw + half + 8 * c) * 2 : INT32_MIN;
+        }
+    // (each wave's words begin a line behind the last one's: as for the loads,
     // rows of a power of two bytes would all go to the same memory channels)
-    const int span = (h1 - h0 + 31) / 32;
+    const int span = (h1 - h0 + 63) / 64;
     int at = (int)((n0 / 64) % span);
     for (int i = 0; i < span; ++i) {
-        const int h = at * 32;
+        const int h = at * 64;
         at = at + 1 == span ? 0 : at + 1;
-        f32x4 acc[2][4];
+        f32x4 acc[4][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int b = 0; b < 4; ++b) acc[j][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 // (rows past the slice: what the LDS holds, for columns not stored)
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(row + (h + 4 * j) * ROW + k * 64);
+                const u32x4 x =
+                    *reinterpret_cast<const u32x4 *>(row + (h + 32 * (j >> 1) + 4 * (j & 1)) * ROW + k * 64);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) acc[j][b] = mma<DT>(x, gf[k][b], acc[j][b]);
             }
         // (whole pieces of 8 columns; a store past N or the slice is dropped)
-        const bool in = h + 8 * c < h1 - h0;
+        const bool in = h + half + 8 * c < h1 - h0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int to = in ? off[b] + 2 * h : INT32_MIN;
-            float v[8];
+            int to[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = alpha * acc[0][b][e];
-                v[4 + e] = alpha * acc[1][b][e];
-            }
-            if constexpr (BETA) {
-                const u32x4 old = ld128(rd, to);
+            for (int q = 0; q < 2; ++q) to[q] = in ? off[b][q] + 2 * h : INT32_MIN;
+            if constexpr (!BETA) {
+                // rounded, then exchanged
+                u32 x[2][4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const u32 o = old[e / 2] >> (16 * (e & 1)) & 0xFFFFu;
-                    v[e] = __builtin_fmaf(a.beta, DT == DT_BF16 ? from_bf16_bits(o) : from_f16_bits(o), v[e]);
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4 v = acc[2 * q + e / 2][b];
+                        x[q][e] = pack2_16<DT>(alpha * v[2 * (e & 1)], alpha * v[2 * (e & 1) + 1]);
+                    }
+                u32x4 w[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const u32 other = swap8(low ? x[1][e] : x[0][e]);
+                    w[0][e] = low ? x[0][e] : other;
+                    w[1][e] = low ? other : x[1][e];
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) __builtin_amdgcn_raw_buffer_store_b128(w[q], rd, to[q], 0, AUX);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const u32x4 old = ld128(rd, to[q]);
+                    u32x4 w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v[2];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const int f = 2 * (e & 1) + m;
+                            const float x0 = alpha * acc[e / 2][b][f], x1 = alpha * acc[2 + e / 2][b][f];
+                            const float other = as_f32(swap8(as_u32(low ? x1 : x0)));
+                            const u32 o = old[e] >> (16 * m) & 0xFFFFu;
+                            v[m] = __builtin_fmaf(a.beta, DT == DT_BF16 ? from_bf16_bits(o) : from_f16_bits(o),
+                                                  q == 0 ? (low ? x0 : other) : (low ? other : x1));
+                        }
+                        w[e] = pack2_16<DT>(v[0], v[1]);
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(w, rd, to[q], 0, AUX);
                 }
             }
-            const u32x4 w = {pack2_16<DT>(v[0], v[1]), pack2_16<DT>(v[2], v[3]), pack2_16<DT>(v[4], v[5]),
-                             pack2_16<DT>(v[6], v[7])};
-            __builtin_amdgcn_raw_buffer_store_b128(w, rd, to, 0, 0);
         }
     }
 }
@@ -632,7 +680,7 @@ hipError_t tcg_launch_ce_join(const CeJoinArgs &a, hipStream_t s) {
 
 hipError_t tcg_launch_ce_rows(const CeRowsArgs &a, bool grad, hipStream_t s) {
     const int64_t blocks = ((int64_t)a.V + kCeRowWords - 1) / kCeRowWords;
-    if (a.T < 1 || a.T > (grad ? kCeFewTokens : kCeRowTokens) || blocks >= kMaxBlocks / 2)
+    if (a.T < 1 || a.T > kCeRowTokens || blocks >= kMaxBlocks / 2)
         return hipErrorInvalidValue;
     const dim3 g((unsigned)blocks), b(512);
 #define CE_ROWS(DT)                                                                              \
@@ -640,8 +688,7 @@ hipError_t tcg_launch_ce_rows(const CeRowsArgs &a, bool grad, hipStream_t s) {
         if (!grad && a.T <= 16) hipLaunchKernelGGL((ce_rows_kernel<DT, 1, false>), g, b, 0, s, a); \
         else if (!grad) hipLaunchKernelGGL((ce_rows_kernel<DT, 2, false>), g, b, 0, s, a);        \
         else if (a.T <= 16) hipLaunchKernelGGL((ce_rows_kernel<DT, 1, true>), g, b, 0, s, a);     \
-        else if (a.T <= 32) hipLaunchKernelGGL((ce_rows_kernel<DT, 2, true>), g, b, 0, s, a);     \
-        else hipLaunchKernelGGL((ce_rows_kernel<DT, 4, true>), g, b, 0, s, a);                    \
+        else hipLaunchKernelGGL((ce_rows_kernel<DT, 2, true>), g, b, 0, s, a);                    \
     } while (0)
     if (a.dtype == DT_F16) CE_ROWS(DT_F16);
     else CE_ROWS(DT_BF16);
@@ -689,24 +736,31 @@ hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s)
 hipError_t tcg_launch_ce_outer(const CeOuterArgs &a, hipStream_t s) {
     if (a.T < 1 || a.T > a.tp || (a.tp != 32 && a.tp != 64) || a.N < 1 || a.H < 8 || a.H % 8 != 0)
         return hipErrorInvalidValue;
-    // columns to a workgroup: 512, fewer where that leaves less than two
+    // fewer columns to a workgroup where they would leave less than two
     // workgroups a CU
     const int64_t words = ((int64_t)a.N + 64 * kOuterWaves - 1) / (64 * kOuterWaves);
-    int per = 512;
+    int per = kOuterColumns;
     while (per > 64 && words * ((a.H + per - 1) / per) < 512) per /= 2;
     const int64_t blocks = words * ((a.H + per - 1) / per);
     if (blocks >= kMaxBlocks / 2) return hipErrorInvalidValue;
     const dim3 g((unsigned)blocks), b(kOuterWaves * 64);
-#define CE_OUTER(DT)                                                                                          \
+    const bool lines = a.lddw % 64 == 0 && (uintptr_t)a.dw % 128 == 0;
+#define CE_OUTER_KS(DT, KS)                                                                                   \
     do {                                                                                                      \
-        if (a.tp == 32 && a.beta == 0.f) hipLaunchKernelGGL((ce_outer_kernel<DT, 1, false>), g, b, 0, s, a, per); \
-        else if (a.tp == 32) hipLaunchKernelGGL((ce_outer_kernel<DT, 1, true>), g, b, 0, s, a, per);          \
-        else if (a.beta == 0.f) hipLaunchKernelGGL((ce_outer_kernel<DT, 2, false>), g, b, 0, s, a, per);      \
-        else hipLaunchKernelGGL((ce_outer_kernel<DT, 2, true>), g, b, 0, s, a, per);                          \
+        if (a.beta == 0.f && lines) hipLaunchKernelGGL((ce_outer_kernel<DT, KS, false, true>), g, b, 0, s, a, per); \
+        else if (a.beta == 0.f) hipLaunchKernelGGL((ce_outer_kernel<DT, KS, false, false>), g, b, 0, s, a, per);    \
+        else if (lines) hipLaunchKernelGGL((ce_outer_kernel<DT, KS, true, true>), g, b, 0, s, a, per);        \
+        else hipLaunchKernelGGL((ce_outer_kernel<DT, KS, true, false>), g, b, 0, s, a, per);                  \
+    } while (0)
+#define CE_OUTER(DT)                        \
+    do {                                    \
+        if (a.tp == 32) CE_OUTER_KS(DT, 1); \
+        else CE_OUTER_KS(DT, 2);            \
     } while (0)
     if (a.dtype == DT_F16) CE_OUTER(DT_F16);
     else CE_OUTER(DT_BF16);
 #undef CE_OUTER
+#undef CE_OUTER_KS
     return hipGetLastError();
 }
 

@@ -101,7 +101,8 @@ def test_scale(dtype, scale):
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("beta", [0.0, 1.0])
 @pytest.mark.parametrize("T,V,H,pad", [(1, 65, 8, 0), (31, 1000, 1032, 0), (32, 130, 136, 8), (33, 63, 2056, 3),
-                                       (64, 5000, 72, 0), (50, 30000, 200, 5)])
+                                       (64, 5000, 72, 0), (50, 30000, 200, 5), (65, 700, 520, 0),
+                                       (128, 1025, 264, 8), (100, 9000, 1288, 0)])
 def test_gradients_of_few_tokens(T, V, H, pad, beta, dtype):
     x, w, targets, g = case(T, V, H, dtype, seed=T + V + 2)
     old = torch.randn(V, H, device="cuda", generator=g)

@@ -13,6 +13,7 @@ namespace tcg {
 namespace {
 
 constexpr int64_t kMaxIndex = 0x7FFFFFFF;
+constexpr int64_t kFewOdd = 128;           // tokens up to which W is read in place whatever its rows
 constexpr int64_t kMaxWords = 1 << 20;     // at a time: 256 rows of fp32 products stay below 2^31 bytes
 
 int64_t up_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -22,7 +23,7 @@ bool is_float(int dt) { return dt == TC_F32 || dt == TC_F16 || dt == TC_BF16; }
 struct CeProblem {
     int64_t T, V, H, ldx, ldw;
     int dt, es;
-    bool whole;        // x and W can be read by the direct-to-LDS loads as they are
+    bool whole;        // W can be read by the direct-to-LDS loads as it is
 };
 
 tc_status_t check_ce(const tc_ce_desc *d, const void *x, const void *w, CeProblem *p, std::string *err) {
@@ -73,7 +74,8 @@ int ce_class(int64_t T, int64_t N) {
 // How many of N words (whole tile columns) go first, in full rounds of 256 x
 // 256 tiles, when the rest then takes less as a launch of its own (0.05 for
 // it) than the last round costs; N: all in one launch.  1021 tokens by 50021
-// words of 2056, fp16 (784 tiles, three rounds and 16 tiles): loss RAGGED_LOSS.
+// words of 2056, fp16 (784 tiles, three rounds and 16 tiles): 231 us
+// in one launch, 215 so.
 int64_t first_words(int64_t T, int64_t N) {
     const int64_t tm = ceil_div(T, 256), tiles = tm * ceil_div(N, 256);
     const double whole = rounds(T, N, 256) < rounds(T, N, 128) ? rounds(T, N, 256) : rounds(T, N, 128);
@@ -100,8 +102,8 @@ GemmArgs product_args(const CeProblem &p, const void *x, int64_t ldx, int64_t T,
     memset(&a, 0, sizeof a);
     a.A = x;
     a.B = w;
-    a.a_extent = ((T - 1) * ldx + p.H) * p.es;
-    a.b_extent = ((N - 1) * p.ldw + p.H) * p.es;
+    a.a_extent = ((T - 1) * ldx + up_to(p.H, 8)) * p.es;
+    a.b_extent = ((N - 1) * p.ldw + up_to(p.H, 8)) * p.es;
     a.M = (int32_t)T;
     a.N = (int32_t)N;
     a.K = (int32_t)p.H;
@@ -139,18 +141,89 @@ tc_gemm_desc gemm_desc(int64_t M, int64_t N, int64_t K, int dt, int cdt, bool ta
     return d;
 }
 
+// The product x W^T of T tokens and N words, stored in fp32.
+GemmCall logits_call(const CeProblem &p, int64_t T, int64_t N, int64_t ldx, int64_t pitch, const void *x,
+                     const void *w) {
+    GemmCall c;
+    memset(&c, 0, sizeof c);
+    c.d = gemm_desc(T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, ldx, p.ldw, pitch);
+    c.A = x;
+    c.B = w;
+    const int64_t tiles = ceil_div(T, 128) * ceil_div(N, 128);
+    if (p.es == 4) {
+        // f32 from 256 tiles of 128 x 128 on, where the planner takes those or
+        // 256 x 256: 64 x 64 ones, four and more a CU, unless the larger ones
+        // fill their rounds.  us, 128 / 64: 10007 words by 1024, 512 tokens (316
+        // tiles) 147 / 111, 8000 by 4096, 700 tokens 570 / 454, 32768 by 1024,
+        // 300 tokens 275 / 207, 512 (1024 tiles) 271 / 286.
+        c.chosen = T > 64 && tiles >= 256;
+        c.cls = (double)T * N > 0.95 * 128 * 128 * 256 * ceil_div(tiles, 256) ? TILE_128 : TILE_64;
+    } else if (!p.whole) {
+        // 16 bits, W's rows not whole 16-byte pieces: the classes that read them
+        // as they are (a copy of W costs more than these few tokens' product).
+        // us, the planner's choice / so, 65536 words by 4095: 16 tokens 279 /
+        // 127, 128 tokens 351 / 180; 20000 by 1501: 16 tokens 40 / 30, 128
+        // tokens 49 / 35 (64 x 64; 43 in 128 x 128).
+        c.chosen = T >= 4 && T <= kFewOdd;
+        c.cls = T <= 64 || tiles < 256 ? TILE_64 : TILE_128;
+    }
+    return c;
+}
+
+// Words at a time where W's rows are copied to whole 16-byte pieces: 512 MiB.
+int64_t copied_words(const CeProblem &p) {
+    const int64_t n = (1 << 28) / up_to(p.H, 8) / 256 * 256;
+    return n < 256 ? 256 : n;
+}
+
+// The launches of T tokens' products with V words, `most` at a time: f(first
+// word, words).
+template <class F>
+void each_launch(int64_t T, int64_t V, int64_t most, F f) {
+    for (int64_t v0 = 0; v0 < V; v0 += most) {
+        const int64_t N = V - v0 < most ? V - v0 : most, first = first_words(T, N);
+        f(v0, first);
+        if (first < N) f(v0 + first, N - first);
+    }
+}
+
+tc_status_t launch_failed(std::string *err, hipError_t e) {
+    (void)hipGetLastError();
+    return fail(err, TC_ERR_DEVICE, "kernel launch failed: %s", hipGetErrorString(e));
+}
+
+// n rows of H values, ld apart, copied to rows of whole 16-byte pieces.
+hipError_t copy_rows(tc_context *ctx, tc_stream *s, const CeProblem &p, const void *src, int64_t ld, int64_t n,
+                     void *dst) {
+    PackArgs a;
+    memset(&a, 0, sizeof a);
+    a.src = src;
+    a.dst = dst;
+    a.src_pitch = ld * p.es;
+    a.dst_pitch = up_to(p.H, 8) * p.es;
+    a.rows = (int32_t)n;
+    a.row_bytes = (int32_t)(p.H * p.es);
+    a.batch = 1;
+    const hipError_t e = tcg_launch_pack_rows(a, s->stream);
+    if (e == hipSuccess) ctx->dispatches += 1;
+    return e;
+}
+
 // ------------------------------------------------------------------ loss
 // Tokens are taken Tc at a time (bounds the partial softmaxes), and where the
 // products are stored, N words at a time.
 struct ForwardSpace {
     bool fused, few;                   // few: one launch takes all tokens
+    bool copy_x, copy_w;               // fused: rows copied to whole 16-byte pieces
     int64_t Tc, N, pitch, num;         // num: shares of the words
-    int64_t parts, logit, l, gemm, gemm_bytes, bytes;
+    int64_t parts, logit, x, w, l, gemm, gemm_bytes, bytes;
 };
 
 tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, ForwardSpace *f, std::string *err) {
-    f->fused = p.whole && p.ldx % 8 == 0 && (uintptr_t)x % 16 == 0;
-    f->few = f->fused && takes_rows(p.T, p.V, p.H);
+    f->fused = p.es == 2 && (p.whole || p.T > kFewOdd);
+    f->copy_w = f->fused && !p.whole;
+    f->copy_x = f->fused && (p.ldx % 8 != 0 || p.H % 8 != 0 || (uintptr_t)x % 16 != 0);
+    f->few = f->fused && !f->copy_x && takes_rows(p.T, p.V, p.H);
     f->Tc = p.T < 16384 ? p.T : 16384;
     f->l = f->gemm = f->gemm_bytes = 0;
     if (f->few) {
@@ -159,10 +232,9 @@ tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, Forwa
         f->num = 0;
         for (const int64_t T : {f->Tc, p.T % f->Tc}) {
             if (T == 0) continue;
-            const int64_t first = first_words(T, p.V);
             int64_t n = 0;
-            for (const int64_t N : {first, p.V - first})
-                if (N > 0) n += 2 * ceil_div(N, tile_shape(ce_class(T, N)).bn);
+            each_launch(T, p.V, f->copy_w ? copied_words(p) : p.V,
+                        [&](int64_t, int64_t N) { n += 2 * ceil_div(N, tile_shape(ce_class(T, N)).bn); });
             if (n > f->num) f->num = n;
         }
     } else {
@@ -179,11 +251,7 @@ tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, Forwa
         for (const int64_t T : {f->Tc, p.T % f->Tc})
             for (const int64_t N : {f->N, p.V % f->N}) {
                 if (T == 0 || N == 0) continue;
-                GemmCall c;
-                memset(&c, 0, sizeof c);
-                c.d = gemm_desc(T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, p.ldx, p.ldw, f->pitch);
-                c.A = x;
-                c.B = w;
+                GemmCall c = logits_call(p, T, N, p.ldx, f->pitch, x, w);
                 int64_t bytes = 0;
                 const tc_status_t st = gemm_call_workspace(c, &bytes, err);
                 if (st != TC_OK) return st;
@@ -195,7 +263,10 @@ tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, Forwa
     }
     f->parts = 0;
     f->logit = up_to(f->num * f->Tc * 8, 256);
-    f->l = up_to(f->logit + f->Tc * 4, 256);
+    f->x = up_to(f->logit + f->Tc * 4, 256);
+    f->w = up_to(f->x + (f->copy_x ? f->Tc * up_to(p.H, 8) * 2 : 0), 256);
+    const int64_t words = p.V < copied_words(p) ? p.V : copied_words(p);
+    f->l = up_to(f->w + (f->copy_w ? words * up_to(p.H, 8) * 2 : 0), 256);
     f->gemm = f->fused ? f->l : up_to(f->l + f->Tc * f->pitch * 4, 256);
     f->bytes = f->gemm + f->gemm_bytes;
     return TC_OK;
@@ -210,11 +281,6 @@ CeParts parts_at(char *ws, int64_t T, int64_t num, int64_t first) {
     p.st = T <= kCeRowsOfParts ? num : 1;
     p.at = reinterpret_cast<float2 *>(ws) + first * p.sp;
     return p;
-}
-
-tc_status_t launch_failed(std::string *err, hipError_t e) {
-    (void)hipGetLastError();
-    return fail(err, TC_ERR_DEVICE, "kernel launch failed: %s", hipGetErrorString(e));
 }
 
 tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, const CeProblem &p,
@@ -249,12 +315,26 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
             ctx->dispatches += 1;
             here = "ce_rows";
         } else if (f.fused) {
-            const int64_t first = first_words(T, p.V);
-            for (int64_t v0 = 0; v0 < p.V; v0 += first) {
-                const int64_t N = v0 == 0 ? first : p.V - v0;
+            const int64_t most = f.copy_w ? copied_words(p) : p.V;
+            CeProblem q = p;
+            e = hipSuccess;
+            if (f.copy_x) {
+                e = copy_rows(ctx, s, p, xt, p.ldx, T, ws + f.x);
+                xt = ws + f.x;
+                here = "pack_rows";
+            }
+            const int64_t ldx = f.copy_x ? up_to(p.H, 8) : p.ldx;
+            if (f.copy_w) q.ldw = up_to(p.H, 8);
+            each_launch(T, p.V, most, [&](int64_t v0, int64_t N) {
+                const int64_t at0 = v0 / most * most;
+                if (e == hipSuccess && f.copy_w && v0 == at0)
+                    e = copy_rows(ctx, s, p, at(w, v0 * p.ldw * p.es), p.ldw, p.V - v0 < most ? p.V - v0 : most,
+                                  ws + f.w);
+                if (e != hipSuccess) return;
+                const void *wv = f.copy_w ? at(ws + f.w, (v0 - at0) * q.ldw * p.es) : at(w, v0 * p.ldw * p.es);
                 const int cls = ce_class(T, N);
                 int64_t grid;
-                GemmArgs a = product_args(p, xt, p.ldx, T, at(w, v0 * p.ldw * p.es), N, d.scale, cls, &grid);
+                GemmArgs a = product_args(q, xt, ldx, T, wv, N, d.scale, cls, &grid);
                 const CeParts parts = parts_at(ws + f.parts, T, f.num, num);
                 a.ws = parts.at;
                 a.ce_sp = parts.sp;
@@ -265,19 +345,17 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
                 a.ce_logit = reinterpret_cast<float *>(ws + f.logit);
                 num += 2 * a.tiles_n;
                 e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_STAT, a, grid, s->stream);
-                if (e != hipSuccess) return launch_failed(err, e);
+                if (e != hipSuccess) return;
                 ctx->dispatches += 1;
-                here += std::string(v0 ? "|" : "") + tcg_kernel_name(p.dt, false, true, cls) + "_softmax";
-                if (v0) break;
-            }
+                if (v0 < most)
+                    here += std::string(v0 ? "|" : f.copy_x ? "+" : "") + tcg_kernel_name(p.dt, false, true, cls) +
+                            "_softmax";
+            });
+            if (e != hipSuccess) return launch_failed(err, e);
         } else {
             for (int64_t v0 = 0; v0 < p.V; v0 += f.N) {
                 const int64_t N = p.V - v0 < f.N ? p.V - v0 : f.N;
-                GemmCall c;
-                memset(&c, 0, sizeof c);
-                c.d = gemm_desc(T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, p.ldx, p.ldw, f.pitch);
-                c.A = xt;
-                c.B = at(w, v0 * p.ldw * p.es);
+                GemmCall c = logits_call(p, T, N, p.ldx, f.pitch, xt, at(w, v0 * p.ldw * p.es));
                 c.C = ws + f.l;
                 std::string part;
                 const tc_status_t st =
@@ -329,9 +407,10 @@ struct BackwardSpace {
     bool few;                          // few tokens: kernels of their own, no copy of x
     int tp;                            // their number, rounded up
     bool own_dx;                       // dx is summed in the workspace
+    bool copy_w;                       // W's rows are copied to whole 16-byte pieces
     int parts, dx_parts, dw_parts;
     int64_t N, pitch, xz_pitch;
-    int64_t rows, lost, unscale, xz, xt, acc, g, l, gemm, gemm_bytes, bytes;
+    int64_t rows, lost, unscale, xz, xt, w, acc, g, l, gemm, gemm_bytes, bytes;
 };
 
 GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
@@ -342,13 +421,23 @@ GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &
     c.d = gemm_desc(p.T, p.H, N, p.dt, TC_F32, false, false, scale, beta, b.pitch, p.ldw, ld);
     c.B = w;
     c.whole[0] = true;
+    c.whole[1] = b.copy_w;
     // one row of tiles over a long K: as many slices of it as CUs (the planner's
     // choice for under 128 rows and from 8192 columns on is the 64 x 64 tile
     // unsliced: 64 tokens, 32768 words by 8192: 935 us with it, 207 so)
-    const int64_t tiles = ceil_div(p.H, 128), ktiles = ceil_div(N, 64);
-    if (p.whole && p.T <= 128 && p.H >= 256 && ktiles >= 32 && tiles <= 256) {
-        int64_t s = 256 / tiles;
-        if (s > ktiles / 4) s = ktiles / 4;
+    // f32, 8 to 256 tiles of 128 x 128: two workgroups a CU (the planner takes
+    // 64 x 64 tiles there, from 128 of them on unsliced.  10007 words by 1024,
+    // us, the planner's / so: 128 tokens 42 / 37, 255 tokens 77 / 65, 512 368 /
+    // 107, 1024 372 / 190; by 4096, 64 tokens 77 / 105, 128 367 / 109, 1024 757
+    // / 675; by 256, 255 tokens (4 tiles) 30 / 40)
+    const int64_t tiles = ceil_div(p.T, 128) * ceil_div(p.H, 128), ktiles = ceil_div(N * p.es, 128);
+    const bool few = p.whole && p.T <= 128 && p.H >= 256 && ktiles >= 32 && tiles <= 256;
+    const bool f32 = p.dt == TC_F32 && p.T > 64 && tiles >= 8 && tiles <= 256;
+    if (few || f32) {
+        int64_t s = (f32 ? 512 : 256) / tiles;
+        if (s > ktiles / (f32 ? 8 : 4)) s = ktiles / (f32 ? 8 : 4);
+        c.chosen = few || s >= 2;
+        c.cls = f32 ? TILE_128 : TILE_128_DMA4;
         c.slices = (int32_t)(s > 32 ? 32 : s);
     }
     return c;
@@ -361,17 +450,14 @@ GemmCall dw_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &
     const int64_t ld = g.lddw == 0 ? p.H : g.lddw;
     c.d = gemm_desc(N, p.H, p.T, p.dt, g.dw_dtype, true, false, scale, beta, b.pitch, b.xz_pitch, ld);
     c.whole[0] = c.whole[1] = true;
+    // (f32, 16384 words by 700 of 255 tokens: 73 us, 100 on the 256 x 256 tiles
+    // that the planner takes there; 65536 by 2048, 1024 tokens: 2181, 2318)
+    if (p.dt == TC_F32 && ceil_div(N, 128) * ceil_div(p.H, 128) >= 256) {
+        c.chosen = true;
+        c.cls = TILE_128;
+    }
     // (present or not is all that counts for the workspace)
     c.col_scale = b.unscale >= 0 ? reinterpret_cast<const float *>(16) : nullptr;
-    return c;
-}
-
-GemmCall logits_call(const CeProblem &p, const BackwardSpace &b, int64_t N, const void *w) {
-    GemmCall c;
-    memset(&c, 0, sizeof c);
-    c.d = gemm_desc(p.T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, b.xz_pitch, p.ldw, b.pitch);
-    c.B = w;
-    c.whole[0] = true;
     return c;
 }
 
@@ -403,9 +489,18 @@ tc_status_t check_grads(const tc_ce_grads *g, const CeProblem &p, std::string *e
     return TC_OK;
 }
 
-tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale, const void *x, const void *w,
-                          BackwardSpace *b, std::string *err) {
-    const bool x_whole = p.ldx % 8 == 0 && (uintptr_t)x % 16 == 0;
+// *q: the problem as its products see it.
+tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float scale, const void *x, const void *w,
+                          CeProblem *q, BackwardSpace *b, std::string *err) {
+    // dx would copy W in any case
+    b->copy_w = problem.es == 2 && !problem.whole && (g.dx || problem.T > kFewOdd);
+    *q = problem;
+    if (b->copy_w) {
+        q->ldw = up_to(problem.H, 8);
+        q->whole = true;
+    }
+    const CeProblem &p = *q;
+    const bool x_whole = p.ldx % 8 == 0 && p.H % 8 == 0 && (uintptr_t)x % 16 == 0;
     // A gradient in fp32 from 16-bit inputs: the products' gradient as the sum
     // of as many numbers as fp32 shows (24 bits: three of bf16; two of f16
     // have 22).  One in the inputs' type takes one: that rounding is as large
@@ -428,6 +523,7 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     if (N > kMaxWords) N = kMaxWords;
     if (N > kMaxIndex / p.T) N = kMaxIndex / p.T;
     if (N > kMaxIndex / rows_w) N = kMaxIndex / rows_w;
+    if (b->copy_w && N > copied_words(p)) N = copied_words(p);
     if (N < 256)
         return fail(err, TC_ERR_OVERFLOW, "T=%lld tokens or rows %lld apart leave less than 256 words at a time",
                     (long long)p.T, (long long)rows_w);
@@ -443,7 +539,8 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     b->unscale = p.es == 2 ? after : -1;
     b->xz = after + (p.es == 2 ? up_to(p.H * 4, 256) : 0);
     b->xt = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
-    b->acc = up_to(b->xt + (b->few ? p.H * b->tp * 2 : 0), 256);
+    b->w = up_to(b->xt + (b->few ? p.H * b->tp * 2 : 0), 256);
+    b->acc = up_to(b->w + (b->copy_w ? b->N * p.ldw * 2 : 0), 256);
     b->g = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
     b->l = up_to(b->g + p.T * b->pitch * p.es * b->parts, 256);
     // (fp32: the gradient takes the place of its products)
@@ -456,9 +553,12 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
         GemmCall c[6];
         int k = 0;
         // (a later piece of W may start off 16-byte boundaries)
-        for (const void *at : {w, odd}) {
+        for (const void *at : {b->copy_w ? reinterpret_cast<const void *>(16) : w, odd}) {
             if (at == odd && p.whole) continue;
-            if (!b->fused) c[k++] = logits_call(p, *b, n, at);
+            if (!b->fused) {
+                c[k] = logits_call(p, p.T, n, b->xz_pitch, b->pitch, nullptr, at);
+                c[k++].whole[0] = true;
+            }
             if (g.dx) {
                 c[k++] = dx_call(p, *b, g, scale, n, 0.f, at);
                 c[k++] = dx_call(p, *b, g, scale, n, 1.f, at);
@@ -480,8 +580,9 @@ tc_status_t plan_backward(const CeProblem &p, const tc_ce_grads &g, float scale,
     return TC_OK;
 }
 
-tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, const CeProblem &p,
-                         const tc_ce_grads &g, const BackwardSpace &b, const void *x, const void *w,
+// problem: the call's; p: as its products see it (plan_backward).
+tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, const CeProblem &problem,
+                         const CeProblem &p, const tc_ce_grads &g, const BackwardSpace &b, const void *x, const void *w,
                          const void *targets, const float *lse, char *ws, std::string *name,
                          std::string *err) {
     const CeRow *rows = reinterpret_cast<const CeRow *>(ws + b.rows);
@@ -515,8 +616,14 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
     tc_status_t st;
     for (int64_t v0 = 0; v0 < p.V; v0 += b.N) {
         const int64_t N = p.V - v0 < b.N ? p.V - v0 : b.N;
-        const void *wv = at(w, v0 * p.ldw * p.es);
+        const void *wv = at(w, v0 * problem.ldw * p.es);
         std::string here;
+        if (b.copy_w) {
+            e = copy_rows(ctx, s, p, wv, problem.ldw, N, ws + b.w);
+            if (e != hipSuccess) return launch_failed(err, e);
+            wv = ws + b.w;
+            here = "pack_rows+";
+        }
         if (b.few && takes_rows(p.T, N, p.H)) {
             CeRowsArgs a;
             memset(&a, 0, sizeof a);
@@ -537,7 +644,7 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
             e = tcg_launch_ce_rows(a, true, s->stream);
             if (e != hipSuccess) return launch_failed(err, e);
             ctx->dispatches += 1;
-            here = "ce_rows_grad";
+            here += "ce_rows_grad";
         } else if (b.fused) {
             const int64_t first = first_words(p.T, N);
             for (int64_t n0 = 0; n0 < N; n0 += first) {
@@ -561,10 +668,12 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
                 if (n0) break;
             }
         } else {
-            GemmCall c = logits_call(p, b, N, wv);
-            c.A = ws + b.xz;
+            GemmCall c = logits_call(p, p.T, N, b.xz_pitch, b.pitch, ws + b.xz, wv);
+            c.whole[0] = true;
             c.C = ws + b.l;
-            if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &here, err)) != TC_OK) return st;
+            std::string part;
+            if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
+            here += part;
             CeGradArgs ga;
             ga.l = reinterpret_cast<float *>(ws + b.l);
             ga.ld = b.pitch;
@@ -642,7 +751,7 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
         f.lost = p.es == 2 && b.dx_parts == 1 ? lost : nullptr;
         f.scale = d.scale;
         f.w = w;
-        f.ldw = p.ldw;
+        f.ldw = problem.ldw;
         f.w_dtype = p.dt;
         e = tcg_launch_ce_finish(f, s->stream);
         if (e != hipSuccess) return launch_failed(err, e);
@@ -720,11 +829,11 @@ tc_status_t tc_cross_entropy_async(tc_context *ctx, const tc_ce_desc *d, const v
 tc_status_t tc_cross_entropy_backward_workspace(const tc_ce_desc *d, const tc_ce_grads *g, const void *x,
                                                 const void *w, int64_t *bytes) {
     if (!bytes) return TC_ERR_INVALID_ARGUMENT;
-    CeProblem p;
+    CeProblem p, q;
     BackwardSpace b;
     tc_status_t st = check_ce(d, x, w, &p, nullptr);
     if (st == TC_OK) st = check_grads(g, p, nullptr);
-    if (st == TC_OK) st = plan_backward(p, *g, d->scale, x, w, &b, nullptr);
+    if (st == TC_OK) st = plan_backward(p, *g, d->scale, x, w, &q, &b, nullptr);
     if (st == TC_OK) *bytes = b.bytes;
     return st;
 }
@@ -737,7 +846,7 @@ tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d
     const Turn turn(ctx);
     ctx->last_error.clear();
     std::string *err = &ctx->last_error;
-    CeProblem p;
+    CeProblem p, q;
     BackwardSpace b;
     tc_status_t st;
     if ((st = check_ce(d, x, w, &p, err)) != TC_OK) return st;
@@ -747,7 +856,7 @@ tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d
     if ((uintptr_t)lse % 4 != 0)
         return fail(err, TC_ERR_INVALID_ARGUMENT, "lse must be aligned to its elements");
     if ((st = check_grads(g, p, err)) != TC_OK) return st;
-    if ((st = plan_backward(p, *g, d->scale, x, w, &b, err)) != TC_OK) return st;
+    if ((st = plan_backward(p, *g, d->scale, x, w, &q, &b, err)) != TC_OK) return st;
     if ((st = check_space(workspace, workspace_bytes, b.bytes, err)) != TC_OK) return st;
     const Range r[] = {
         {"workspace", workspace, b.bytes},
@@ -763,7 +872,7 @@ tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d
     if (dev.status != TC_OK) return dev.status;
     if ((st = check_ranges(r, 8, 3, true, err)) != TC_OK) return st;
     std::string name;
-    st = run_backward(ctx, s, *d, p, *g, b, x, w, targets, lse, static_cast<char *>(workspace), &name, err);
+    st = run_backward(ctx, s, *d, p, q, *g, b, x, w, targets, lse, static_cast<char *>(workspace), &name, err);
     if (st == TC_OK) ctx->last_kernel = name;
     return st;
 }

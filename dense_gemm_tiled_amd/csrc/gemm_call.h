@@ -14,8 +14,8 @@ struct GemmCall {
     const float *col_scale;    // N per-column factors, or null
     bool whole[2];             // A's, B's rows are stored in whole 16-byte
                                // pieces, what lies past them zeros
-    int32_t slices;            // 0: the planner's choice; else the 4-stage 128 x
-                               // 128 tile with so many slices of K
+    bool chosen;               // not the planner's tile class and slices of K, but
+    int32_t cls, slices;       // these (0 or 1: the whole)
 };
 
 // Bytes of scratch memory the call needs.

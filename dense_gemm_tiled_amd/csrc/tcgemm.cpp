@@ -1321,8 +1321,8 @@ tc_status_t plan_call(const GemmCall &c, Problem *p, Plan *pl, Epilogue *epi, st
     p->whole[0] = c.whole[0];
     p->whole[1] = c.whole[1];
     epi->scale = c.col_scale;
-    const Choice ch{TILE_128_DMA4, c.slices, 0};
-    make_plan(*p, pl, true, c.slices > 0 ? &ch : nullptr);
+    const Choice ch{c.cls, c.slices, 0};
+    make_plan(*p, pl, true, c.chosen ? &ch : nullptr);
     return TC_OK;
 }
 

@@ -141,8 +141,42 @@ struct CeOuterArgs {
     int64_t lddw;              // elements
 };
 
+// Few tokens in fp32: dst [T, H] = scale * g w (+ dst), w [N, H], and dw [N, H]
+// = scale * g^T x + beta * dw, x [T, x_pitch].
+constexpr int kCeFewF32 = 16;
+struct CeFewArgs {
+    const float *g;
+    int64_t pitch;             // elements
+    int32_t T, N, H;
+    float scale;
+    // dx
+    const float *w;
+    int64_t ldw;               // elements
+    float *part;               // ce_few_parts() of them, T x H each
+    float *dst;
+    int64_t ld_dst;
+    bool add;
+    // dw
+    const float *x;
+    int64_t x_pitch;
+    float beta;
+    float *dw;
+    int64_t lddw;              // elements
+};
+// Shares of N words (in whole kCeFewWords) of the dx product.
+constexpr int kCeFewCols = 256, kCeFewWords = 64;
+inline int64_t ce_few_share(int64_t N, int64_t H) {
+    const int64_t shares = (1024 + (H + kCeFewCols - 1) / kCeFewCols - 1) / ((H + kCeFewCols - 1) / kCeFewCols);
+    return ((N + shares - 1) / shares + kCeFewWords - 1) / kCeFewWords * kCeFewWords;
+}
+inline int64_t ce_few_parts(int64_t N, int64_t H) {
+    return (N + ce_few_share(N, H) - 1) / ce_few_share(N, H);
+}
+
 }  // namespace tcg
 
+hipError_t tcg_launch_ce_few_dx(const tcg::CeFewArgs &a, int *launches, hipStream_t s);
+hipError_t tcg_launch_ce_few_dw(const tcg::CeFewArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_join(const tcg::CeJoinArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_rows(const tcg::CeRowsArgs &a, bool grad, hipStream_t s);
 hipError_t tcg_launch_ce_stat(const tcg::CeStatArgs &a, hipStream_t s);

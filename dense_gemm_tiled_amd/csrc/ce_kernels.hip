@@ -661,6 +661,144 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
 
 constexpr int64_t kMaxBlocks = 1 << 24;   // of 256 threads: a launch's threads fit 32 bits
 
+// Few tokens in fp32.  Both products read or write V x H numbers once and have
+// 2 KT operations for each, KT (T rounded up) at most 16: a tile's rows would be
+// mostly padding, and the vector units keep up with the memory.  Both
+// gradients, us, with tiles / so: 8 tokens by 32000 x 4096 560 / 363 (3.2 TB/s
+// of w read twice and dw written), 16 tokens 599 / 439, 32 tokens 659 / 720; 8
+// tokens by 10007 x 1024 69 / 45, by 65536 x 4095 1906 / 840.  A lane has 4 columns, 64 apart (rows may start anywhere: each access of a wave
+// is 256 bytes in a row), a wave 16 of every kCeFewWords words; the gradient is
+// read from LDS, a word's tokens side by side, every lane the same ones.
+//
+// The gradients of words n .. n + kCeFewWords, zeros from word n1 and token T on.
+template <int KT>
+__device__ inline void few_gradients(const CeFewArgs &a, int64_t n, int64_t n1, float *gs) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < KT * kCeFewWords; i += 256) {
+        const int t = i / kCeFewWords, v = i % kCeFewWords;
+        gs[v * KT + t] = t < a.T && n + v < n1 ? a.g[t * a.pitch + n + v] : 0.f;
+    }
+    __syncthreads();
+}
+
+// One share (`per` words) of dx's sums over 256 columns; the waves' are joined
+// through LDS.
+template <int KT>
+__global__ __launch_bounds__(256) void ce_few_dx_kernel(CeFewArgs a, int per, int groups) {
+    constexpr int U = 8;                              // words on the way at once
+    __shared__ __attribute__((aligned(16))) float gs[kCeFewWords * KT];
+    __shared__ float sums[4][4][kCeFewCols];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int share = blockIdx.x / groups, h0 = blockIdx.x % groups * kCeFewCols;
+    const int64_t n0 = (int64_t)share * per, n1 = min((int64_t)a.N, n0 + per);
+    int col[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) col[j] = min(h0 + 64 * j + lane, a.H - 1);
+    float acc[KT][4] = {};
+    for (int64_t n = n0; n < n1; n += kCeFewWords) {
+        few_gradients<KT>(a, n, n1, gs);
+#pragma unroll 1
+        for (int u0 = 0; u0 < kCeFewWords / 4; u0 += U) {
+            const int v0 = wave * (kCeFewWords / 4) + u0;
+            if (n + v0 >= n1) break;
+            float w[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float *row = a.w + min(n + v0 + u, n1 - 1) * a.ldw;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[u][j] = row[col[j]];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (n + v0 + u >= n1) break;          // (not 0 times what a row before holds)
+                const f32x4 *g = reinterpret_cast<const f32x4 *>(gs + (v0 + u) * KT);
+#pragma unroll
+                for (int t = 0; t < KT; t += 4) {
+                    const f32x4 q = g[t / 4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[t + e][j] = __builtin_fmaf(q[e], w[u][j], acc[t + e][j]);
+                }
+            }
+        }
+    }
+    float *part = a.part + (int64_t)share * a.T * a.H;
+#pragma unroll
+    for (int t = 0; t < KT; t += 4) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sums[wave][e][64 * j + lane] = acc[t + e][j];
+        __syncthreads();
+        if (h0 + tid < a.H)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t + e < a.T)
+                    part[(int64_t)(t + e) * a.H + h0 + tid] =
+                        (sums[0][e][tid] + sums[1][e][tid]) + (sums[2][e][tid] + sums[3][e][tid]);
+    }
+}
+
+// The shares' sum: 64 columns of a token, 16 threads for each.
+__global__ __launch_bounds__(1024) void ce_few_join_kernel(CeFewArgs a, int num) {
+    __shared__ float sums[16][64];
+    const int c = threadIdx.x & 63, q = threadIdx.x >> 6, t = blockIdx.y, h = blockIdx.x * 64 + c;
+    float s = 0.f;
+    if (h < a.H)
+#pragma unroll 8
+        for (int p = q; p < num; p += 16) s += a.part[((int64_t)p * a.T + t) * a.H + h];
+    sums[q][c] = s;
+    __syncthreads();
+    if (q == 0 && h < a.H) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += sums[k][c];
+        float *d = a.dst + (int64_t)t * a.ld_dst + h;
+        *d = a.add ? __builtin_fmaf(a.scale, s, *d) : a.scale * s;
+    }
+}
+
+template <int KT, bool BETA>
+__global__ __launch_bounds__(256) void ce_few_dw_kernel(CeFewArgs a, int per, int groups) {
+    __shared__ __attribute__((aligned(16))) float gs[kCeFewWords * KT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h0 = blockIdx.x % groups * kCeFewCols;
+    const int64_t n0 = (int64_t)(blockIdx.x / groups) * per, n1 = min((int64_t)a.N, n0 + per);
+    float x[KT][4];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int h = h0 + 64 * j + lane;
+            x[t][j] = t < a.T && h < a.H ? a.x[(int64_t)t * a.x_pitch + h] : 0.f;
+        }
+    for (int64_t n = n0; n < n1; n += kCeFewWords) {
+        few_gradients<KT>(a, n, n1, gs);
+#pragma unroll 2
+        for (int u = 0; u < kCeFewWords / 4; ++u) {
+            const int v = wave * (kCeFewWords / 4) + u;
+            if (n + v >= n1) break;
+            float *row = a.dw + (n + v) * a.lddw;
+            float s[4] = {};
+            const f32x4 *g = reinterpret_cast<const f32x4 *>(gs + v * KT);
+#pragma unroll
+            for (int t = 0; t < KT; t += 4) {
+                const f32x4 q = g[t / 4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(q[e], x[t + e][j], s[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int h = h0 + 64 * j + lane;
+                if (h < a.H) row[h] = BETA ? __builtin_fmaf(a.scale, s[j], a.beta * row[h]) : a.scale * s[j];
+            }
+        }
+    }
+}
+
 }  // namespace
 }  // namespace tcg
 
@@ -761,6 +899,47 @@ hipError_t tcg_launch_ce_outer(const CeOuterArgs &a, hipStream_t s) {
     else CE_OUTER(DT_BF16);
 #undef CE_OUTER
 #undef CE_OUTER_KS
+    return hipGetLastError();
+}
+
+hipError_t tcg_launch_ce_few_dx(const CeFewArgs &a, int *launches, hipStream_t s) {
+    if (a.T < 1 || a.T > kCeFewF32 || a.N < 1 || a.H < 1) return hipErrorInvalidValue;
+    const int64_t groups = ((int64_t)a.H + kCeFewCols - 1) / kCeFewCols, num = ce_few_parts(a.N, a.H);
+    if (groups * num >= kMaxBlocks / 2) return hipErrorInvalidValue;
+    const int per = (int)ce_few_share(a.N, a.H);
+    const dim3 g((unsigned)(groups * num)), b(256);
+    if (a.T <= 4) hipLaunchKernelGGL(ce_few_dx_kernel<4>, g, b, 0, s, a, per, (int)groups);
+    else if (a.T <= 8) hipLaunchKernelGGL(ce_few_dx_kernel<8>, g, b, 0, s, a, per, (int)groups);
+    else hipLaunchKernelGGL(ce_few_dx_kernel<16>, g, b, 0, s, a, per, (int)groups);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    *launches += 1;
+    hipLaunchKernelGGL(ce_few_join_kernel, dim3((unsigned)((a.H + 63) / 64), (unsigned)a.T), dim3(1024), 0, s, a,
+                       (int)num);
+    e = hipGetLastError();
+    if (e == hipSuccess) *launches += 1;
+    return e;
+}
+
+hipError_t tcg_launch_ce_few_dw(const CeFewArgs &a, hipStream_t s) {
+    if (a.T < 1 || a.T > kCeFewF32 || a.N < 1 || a.H < 1) return hipErrorInvalidValue;
+    // 256 words to a workgroup (x is read once for them), fewer where they
+    // would leave less than four workgroups a CU
+    const int64_t groups = ((int64_t)a.H + kCeFewCols - 1) / kCeFewCols;
+    int per = 4 * kCeFewWords;
+    while (per > kCeFewWords && groups * (((int64_t)a.N + per - 1) / per) < 1024) per -= kCeFewWords;
+    const int64_t blocks = groups * (((int64_t)a.N + per - 1) / per);
+    if (blocks >= kMaxBlocks / 2) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks), b(256);
+#define CE_FEW_DW(KT)                                                                                        \
+    do {                                                                                                     \
+        if (a.beta == 0.f) hipLaunchKernelGGL((ce_few_dw_kernel<KT, false>), g, b, 0, s, a, per, (int)groups); \
+        else hipLaunchKernelGGL((ce_few_dw_kernel<KT, true>), g, b, 0, s, a, per, (int)groups);               \
+    } while (0)
+    if (a.T <= 4) CE_FEW_DW(4);
+    else if (a.T <= 8) CE_FEW_DW(8);
+    else CE_FEW_DW(16);
+#undef CE_FEW_DW
     return hipGetLastError();
 }
 

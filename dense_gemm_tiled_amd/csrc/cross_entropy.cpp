@@ -405,6 +405,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
 struct BackwardSpace {
     bool fused;
     bool few;                          // few tokens: kernels of their own, no copy of x
+    bool few32;                        // few tokens in fp32: both products by kernels of their own
     int tp;                            // their number, rounded up
     bool own_dx;                       // dx is summed in the workspace
     bool copy_w;                       // W's rows are copied to whole 16-byte pieces
@@ -512,6 +513,7 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     b->parts = b->dx_parts > b->dw_parts ? b->dx_parts : b->dw_parts;
     b->fused = p.whole && b->parts == 1;
     b->few = b->fused && x_whole && p.T <= kCeFewTokens;
+    b->few32 = p.es == 4 && p.T <= kCeFewF32;
     b->tp = p.T <= 32 ? 32 : 64;
     b->own_dx = g.dx && g.dx_dtype != TC_F32;
     b->xz_pitch = up_to(p.H, 16 / p.es);
@@ -559,7 +561,7 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
                 c[k] = logits_call(p, p.T, n, b->xz_pitch, b->pitch, nullptr, at);
                 c[k++].whole[0] = true;
             }
-            if (g.dx) {
+            if (g.dx && !b->few32) {
                 c[k++] = dx_call(p, *b, g, scale, n, 0.f, at);
                 c[k++] = dx_call(p, *b, g, scale, n, 1.f, at);
             }
@@ -571,10 +573,15 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
         for (const float beta : {g.beta, 1.f}) {
-            if (!g.dw || b->few) continue;
+            if (!g.dw || b->few || b->few32) continue;
             if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, n, beta), &bytes, err)) != TC_OK) return st;
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
+    }
+    for (const int64_t n : {b->N, p.V % b->N}) {
+        if (n == 0 || !b->few32 || !g.dx) continue;
+        const int64_t bytes = ce_few_parts(n, p.H) * p.T * p.H * 4;
+        if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
     }
     b->bytes = b->gemm + b->gemm_bytes;
     return TC_OK;
@@ -694,7 +701,37 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
             ctx->dispatches += 1;
             here += "+ce_grad";
         }
-        for (int k = 0; k < b.parts; ++k) {
+        if (b.few32) {
+            CeFewArgs fa;
+            memset(&fa, 0, sizeof fa);
+            fa.g = reinterpret_cast<const float *>(ws + b.g);
+            fa.pitch = b.pitch;
+            fa.T = (int32_t)p.T;
+            fa.N = (int32_t)N;
+            fa.H = (int32_t)p.H;
+            fa.scale = d.scale;
+            fa.w = static_cast<const float *>(wv);
+            fa.ldw = p.ldw;
+            fa.part = reinterpret_cast<float *>(ws + b.gemm);
+            fa.dst = sums;
+            fa.ld_dst = g.lddx == 0 ? p.H : g.lddx;
+            fa.add = v0 > 0;
+            fa.x = reinterpret_cast<const float *>(ws + b.xz);
+            fa.x_pitch = b.xz_pitch;
+            fa.beta = g.beta;
+            fa.lddw = g.lddw == 0 ? p.H : g.lddw;
+            fa.dw = static_cast<float *>(g.dw) + (g.dw ? v0 * fa.lddw : 0);
+            int n = 0;
+            if (g.dx) e = tcg_launch_ce_few_dx(fa, &n, s->stream);
+            if (e == hipSuccess && g.dw) {
+                e = tcg_launch_ce_few_dw(fa, s->stream);
+                if (e == hipSuccess) n += 1;
+            }
+            ctx->dispatches += n;
+            if (e != hipSuccess) return launch_failed(err, e);
+            here += std::string(g.dx ? "+ce_few_dx" : "") + (g.dw ? "+ce_few_dw" : "");
+        }
+        for (int k = 0; k < b.parts && !b.few32; ++k) {
             const void *gk = ws + b.g + k * plane * p.es;
             std::string part;
             if (k < b.dx_parts) {

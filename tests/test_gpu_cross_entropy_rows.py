@@ -88,3 +88,22 @@ def test_captured():
         torch.cuda.synchronize()
         for a, b in ((got[0], want[0]), (got[1], want[1]), (dx2, dx), (dw2, dw)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("beta", [0.0, 0.5])
+@pytest.mark.parametrize("T", [1, 4, 5, 8, 9, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("V,H", [(1, 1), (63, 255), (64, 256), (65, 257), (20011, 64), (70000, 300), (300, 5000)])
+def test_few_tokens_in_fp32(V, H, T, beta):
+    """Shares of words that end inside a wave's, columns that end inside one."""
+    x, w, targets, g = case(T, V, H, "f32", seed=T + V, pad=(3, 1))
+    old = torch.randn(V, H, device="cuda", generator=g)
+    grad = torch.rand(T, device="cuda", generator=g) + 0.1
+    backward(x, w, targets, grad, scale=-0.5, beta=beta, old=old, pads=(2, 5))
+
+
+def test_few_tokens_in_fp32_over_pieces():
+    """More words than a piece holds: dx goes on from the sums before."""
+    T, V, H = 3, (1 << 20) + 65, 5
+    x, w, targets, g = case(T, V, H, "f32")
+    targets[:] = torch.tensor([0, 1 << 20, V - 1], device="cuda")
+    backward(x, w, targets, torch.rand(T, device="cuda", generator=g) + 0.1)

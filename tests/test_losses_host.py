@@ -47,6 +47,17 @@ def gsize(lib, d, g, x=X, w=W):
     return st, n.value
 
 
+@pytest.mark.parametrize("dtype", [tg.BF16, tg.F16])
+@pytest.mark.parametrize("T,V,H", [(1, 1000, 77), (200, 65536, 4095), (300, 500, 1)])
+def test_room_for_copied_rows(lib, T, V, H, dtype):
+    """Rows that are not whole 16-byte pieces: the copy of W (all of it at these
+    sizes) fits beside the gradient of its products."""
+    st, odd = gsize(lib, cdesc(T, V, H, dtype), cgrads(dxt=dtype, dwt=dtype))
+    assert st == 0 and odd >= (V * ((H + 7) // 8 * 8) + T * V) * 2
+    st, odd = size(lib, cdesc(max(T, 129), V, H, dtype))
+    assert st == 0 and odd >= (V + max(T, 129)) * ((H + 7) // 8 * 8) * 2
+
+
 def test_workspaces(lib):
     assert size(lib, cdesc(1, 1, 1))[0] == 0
     st, n = size(lib, cdesc(4096, 131072, 4096))

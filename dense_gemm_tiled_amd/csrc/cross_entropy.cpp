@@ -66,7 +66,7 @@ double rounds(int64_t T, int64_t N, int tile) {
     const int64_t n = ceil_div(T, tile) * ceil_div(N, tile);
     return tile == 256 ? (double)ceil_div(n, 256) : 0.625 * (double)ceil_div(n, 512);
 }
-int ce_class(int64_t T, int64_t N) {
+int dma_class(int64_t T, int64_t N) {
     if (rounds(T, N, 256) <= rounds(T, N, 128)) return TILE_256_DMA;
     return ceil_div(T, 128) * ceil_div(N, 128) <= 256 ? TILE_128_DMA4 : TILE_128_DMA;
 }
@@ -95,6 +95,26 @@ bool takes_rows(int64_t T, int64_t N, int64_t H) {
     return T <= kCeRowTokens && (N <= 16384 || (T <= 8 && N * H <= (80 << 20)));
 }
 
+// f32, and 16 bits where W's rows are not whole 16-byte pieces: the classes that
+// stage such rows through registers.  Up to 16 f32 tokens (3 of 16 bits) and
+// under 128 tiles of 64 x 64 their products are stored (a GEMM's own choices for
+// such shapes are better).
+bool staged(const CeProblem &p, int64_t T, int64_t N) {
+    return T >= (p.es == 4 ? 17 : 4) && ceil_div(T, 64) * ceil_div(N, 64) >= 128;
+}
+// f32: 64 x 64, four and more a CU, unless 128 x 128 tiles fill their rounds.
+// Products alone, us, 128 / 64: 10007 words by 1024, 512 tokens (316 tiles) 147 /
+// 111, 8000 by 4096, 700 tokens 570 / 454, 32768 by 1024, 300 tokens 275 / 207,
+// 512 (1024 tiles) 271 / 286.  16 bits: bound by W's loads, so as few rows of
+// tiles as can be: 65536 by 4095, 128 tokens 180 / 289, 64 tokens 179 / 184;
+// 20000 by 1501 (157 tiles), 128 tokens 43 / 35.
+int staged_class(const CeProblem &p, int64_t T, int64_t N) {
+    const int64_t tiles = ceil_div(T, 128) * ceil_div(N, 128);
+    if (ceil_div(T, 64) * ceil_div(N, 64) > kMaxGroups) return TILE_128;
+    if (tiles < 256 || T <= 64) return TILE_64;
+    return p.es == 2 || (double)T * N > 0.95 * 128 * 128 * 256 * ceil_div(tiles, 256) ? TILE_128 : TILE_64;
+}
+
 // Arguments of the products x W^T with an epilogue of their own.
 GemmArgs product_args(const CeProblem &p, const void *x, int64_t ldx, int64_t T, const void *w, int64_t N,
                       float scale, int cls, int64_t *grid) {
@@ -102,8 +122,10 @@ GemmArgs product_args(const CeProblem &p, const void *x, int64_t ldx, int64_t T,
     memset(&a, 0, sizeof a);
     a.A = x;
     a.B = w;
-    a.a_extent = ((T - 1) * ldx + up_to(p.H, 8)) * p.es;
-    a.b_extent = ((N - 1) * p.ldw + up_to(p.H, 8)) * p.es;
+    // (the direct loads take whole 16-byte pieces)
+    const int64_t H = is_dma_class(cls) ? up_to(p.H, 8) : p.H;
+    a.a_extent = ((T - 1) * ldx + H) * p.es;
+    a.b_extent = ((N - 1) * p.ldw + H) * p.es;
     a.M = (int32_t)T;
     a.N = (int32_t)N;
     a.K = (int32_t)p.H;
@@ -149,24 +171,9 @@ GemmCall logits_call(const CeProblem &p, int64_t T, int64_t N, int64_t ldx, int6
     c.d = gemm_desc(T, N, p.H, p.dt, TC_F32, false, true, 1.f, 0.f, ldx, p.ldw, pitch);
     c.A = x;
     c.B = w;
-    const int64_t tiles = ceil_div(T, 128) * ceil_div(N, 128);
-    if (p.es == 4) {
-        // f32 from 256 tiles of 128 x 128 on, where the planner takes those or
-        // 256 x 256: 64 x 64 ones, four and more a CU, unless the larger ones
-        // fill their rounds.  us, 128 / 64: 10007 words by 1024, 512 tokens (316
-        // tiles) 147 / 111, 8000 by 4096, 700 tokens 570 / 454, 32768 by 1024,
-        // 300 tokens 275 / 207, 512 (1024 tiles) 271 / 286.
-        c.chosen = T > 64 && tiles >= 256;
-        c.cls = (double)T * N > 0.95 * 128 * 128 * 256 * ceil_div(tiles, 256) ? TILE_128 : TILE_64;
-    } else if (!p.whole) {
-        // 16 bits, W's rows not whole 16-byte pieces: the classes that read them
-        // as they are (a copy of W costs more than these few tokens' product).
-        // us, the planner's choice / so, 65536 words by 4095: 16 tokens 279 /
-        // 127, 128 tokens 351 / 180; 20000 by 1501: 16 tokens 40 / 30, 128
-        // tokens 49 / 35 (64 x 64; 43 in 128 x 128).
-        c.chosen = T >= 4 && T <= kFewOdd;
-        c.cls = T <= 64 || tiles < 256 ? TILE_64 : TILE_128;
-    }
+    // (where the planner would copy W first)
+    c.chosen = p.es == 2 && !p.whole && staged(p, T, N);
+    c.cls = staged_class(p, T, N);
     return c;
 }
 
@@ -177,13 +184,13 @@ int64_t copied_words(const CeProblem &p) {
 }
 
 // The launches of T tokens' products with V words, `most` at a time: f(first
-// word, words).
+// word, words, tile class).
 template <class F>
-void each_launch(int64_t T, int64_t V, int64_t most, F f) {
+void each_launch(const CeProblem &p, bool dma, int64_t T, int64_t V, int64_t most, F f) {
     for (int64_t v0 = 0; v0 < V; v0 += most) {
-        const int64_t N = V - v0 < most ? V - v0 : most, first = first_words(T, N);
-        f(v0, first);
-        if (first < N) f(v0 + first, N - first);
+        const int64_t N = V - v0 < most ? V - v0 : most, first = dma ? first_words(T, N) : N;
+        f(v0, first, dma ? dma_class(T, first) : staged_class(p, T, N));
+        if (first < N) f(v0 + first, N - first, dma_class(T, N - first));
     }
 }
 
@@ -213,17 +220,18 @@ hipError_t copy_rows(tc_context *ctx, tc_stream *s, const CeProblem &p, const vo
 // Tokens are taken Tc at a time (bounds the partial softmaxes), and where the
 // products are stored, N words at a time.
 struct ForwardSpace {
-    bool fused, few;                   // few: one launch takes all tokens
-    bool copy_x, copy_w;               // fused: rows copied to whole 16-byte pieces
+    bool dma, fused, few;              // few: one launch takes all tokens
+    bool copy_x, copy_w;               // dma: rows copied to whole 16-byte pieces
     int64_t Tc, N, pitch, num;         // num: shares of the words
     int64_t parts, logit, x, w, l, gemm, gemm_bytes, bytes;
 };
 
 tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, ForwardSpace *f, std::string *err) {
-    f->fused = p.es == 2 && (p.whole || p.T > kFewOdd);
-    f->copy_w = f->fused && !p.whole;
-    f->copy_x = f->fused && (p.ldx % 8 != 0 || p.H % 8 != 0 || (uintptr_t)x % 16 != 0);
-    f->few = f->fused && !f->copy_x && takes_rows(p.T, p.V, p.H);
+    f->dma = p.es == 2 && (p.whole || p.T > kFewOdd);
+    f->fused = f->dma || staged(p, p.T, p.V);
+    f->copy_w = f->dma && !p.whole;
+    f->copy_x = f->dma && (p.ldx % 8 != 0 || p.H % 8 != 0 || (uintptr_t)x % 16 != 0);
+    f->few = f->dma && !f->copy_x && takes_rows(p.T, p.V, p.H);
     f->Tc = p.T < 16384 ? p.T : 16384;
     f->l = f->gemm = f->gemm_bytes = 0;
     if (f->few) {
@@ -233,8 +241,8 @@ tc_status_t plan_forward(const CeProblem &p, const void *x, const void *w, Forwa
         for (const int64_t T : {f->Tc, p.T % f->Tc}) {
             if (T == 0) continue;
             int64_t n = 0;
-            each_launch(T, p.V, f->copy_w ? copied_words(p) : p.V,
-                        [&](int64_t, int64_t N) { n += 2 * ceil_div(N, tile_shape(ce_class(T, N)).bn); });
+            each_launch(p, f->dma, T, p.V, f->copy_w ? copied_words(p) : p.V,
+                        [&](int64_t, int64_t N, int cls) { n += 2 * ceil_div(N, tile_shape(cls).bn); });
             if (n > f->num) f->num = n;
         }
     } else {
@@ -325,14 +333,13 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
             }
             const int64_t ldx = f.copy_x ? up_to(p.H, 8) : p.ldx;
             if (f.copy_w) q.ldw = up_to(p.H, 8);
-            each_launch(T, p.V, most, [&](int64_t v0, int64_t N) {
+            each_launch(p, f.dma, T, p.V, most, [&](int64_t v0, int64_t N, int cls) {
                 const int64_t at0 = v0 / most * most;
                 if (e == hipSuccess && f.copy_w && v0 == at0)
                     e = copy_rows(ctx, s, p, at(w, v0 * p.ldw * p.es), p.ldw, p.V - v0 < most ? p.V - v0 : most,
                                   ws + f.w);
                 if (e != hipSuccess) return;
                 const void *wv = f.copy_w ? at(ws + f.w, (v0 - at0) * q.ldw * p.es) : at(w, v0 * p.ldw * p.es);
-                const int cls = ce_class(T, N);
                 int64_t grid;
                 GemmArgs a = product_args(q, xt, ldx, T, wv, N, d.scale, cls, &grid);
                 const CeParts parts = parts_at(ws + f.parts, T, f.num, num);
@@ -403,7 +410,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
 // The gradient of N words' products at a time, all tokens: T x N numbers of
 // the inputs' type (parts times), then its two products.
 struct BackwardSpace {
-    bool fused;
+    bool dma, fused;
     bool few;                          // few tokens: kernels of their own, no copy of x
     bool few32;                        // few tokens in fp32: both products by kernels of their own
     int tp;                            // their number, rounded up
@@ -511,8 +518,8 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     b->dx_parts = !g.dx ? 0 : g.dx_dtype == TC_F32 ? wide : 1;
     b->dw_parts = !g.dw ? 0 : g.dw_dtype == TC_F32 ? wide : 1;
     b->parts = b->dx_parts > b->dw_parts ? b->dx_parts : b->dw_parts;
-    b->fused = p.whole && b->parts == 1;
-    b->few = b->fused && x_whole && p.T <= kCeFewTokens;
+    b->dma = p.whole && b->parts == 1;
+    b->few = b->dma && x_whole && p.T <= kCeFewTokens;
     b->few32 = p.es == 4 && p.T <= kCeFewF32;
     b->tp = p.T <= 32 ? 32 : 64;
     b->own_dx = g.dx && g.dx_dtype != TC_F32;
@@ -534,6 +541,7 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     N = even < N ? even : N / 256 * 256;
     b->N = N < p.V ? N : p.V;
     b->pitch = up_to(b->N, 8);
+    b->fused = b->dma || (p.es == 4 && staged(p, p.T, b->N));
     if (p.T * b->pitch > kMaxIndex) return fail(err, TC_ERR_OVERFLOW, "T=%lld is too large", (long long)p.T);
     b->rows = 0;
     b->lost = up_to(p.T * (int64_t)sizeof(CeRow), 256);
@@ -653,27 +661,26 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
             ctx->dispatches += 1;
             here += "ce_rows_grad";
         } else if (b.fused) {
-            const int64_t first = first_words(p.T, N);
-            for (int64_t n0 = 0; n0 < N; n0 += first) {
-                const int64_t n = n0 == 0 ? first : N - n0;
-                const int cls = ce_class(p.T, n);
+            e = hipSuccess;
+            each_launch(p, b.dma, p.T, N, N, [&](int64_t n0, int64_t n, int cls) {
+                if (e != hipSuccess) return;
                 int64_t grid;
                 GemmArgs a = product_args(p, ws + b.xz, b.xz_pitch, p.T, at(wv, n0 * p.ldw * p.es), n, d.scale, cls,
                                           &grid);
                 // (the last piece's columns up to the pitch are zeros)
-                a.C = ws + b.g + n0 * 2;
+                a.C = ws + b.g + n0 * p.es;
                 a.ldc = (int32_t)b.pitch;
-                a.c_extent = (p.T * b.pitch - n0) * 2;
+                a.c_extent = (p.T * b.pitch - n0) * p.es;
                 a.ce_cols = (int32_t)(n0 + n < N ? n : up_to(n, 8));
                 a.ce_first = (int32_t)(v0 + n0);
                 a.ce_rows = rows;
                 a.ce_lost = lost;
                 e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_GRAD, a, grid, s->stream);
-                if (e != hipSuccess) return launch_failed(err, e);
+                if (e != hipSuccess) return;
                 ctx->dispatches += 1;
                 here += std::string(n0 ? "|" : "") + tcg_kernel_name(p.dt, false, true, cls) + "_grad";
-                if (n0) break;
-            }
+            });
+            if (e != hipSuccess) return launch_failed(err, e);
         } else {
             GemmCall c = logits_call(p, p.T, N, b.xz_pitch, b.pitch, ws + b.xz, wv);
             c.whole[0] = true;

@@ -427,13 +427,6 @@ struct RingSrc {
 // (unsigned arithmetic: an out-of-range offset stays out of range).
 __device__ inline int group_voff(int off, int j) { return (int)((uint32_t)off - (uint32_t)(j * 1024)); }
 
-// Row m's target as a column of the product, -1 where it is none.
-__device__ inline int ce_load_target(const GemmArgs &args, int64_t m) {
-    const int64_t t = args.ce_targets64 ? static_cast<const int64_t *>(args.ce_targets)[m]
-                                        : (int64_t)static_cast<const int32_t *>(args.ce_targets)[m];
-    return t >= args.ce_first && t < (int64_t)args.ce_first + args.N ? (int)(t - args.ce_first) : -1;
-}
-
 // Epilogue variants of the kernel: beta == 0 and no fused epilogue; beta != 0
 // (16-bit C tiles staged through LDS); the fused epilogue (bias and
 // activation, any beta, C_old read per block).  The last one is a separate

@@ -17,9 +17,11 @@ namespace {
 // classes only for 16-bit and int8 inputs.
 constexpr bool out_ok(int cls, int out) {
     if (is_dma_class(cls) && TCG_DT == DT_F32) return false;
-    if (out == OUT_CE_STAT || out == OUT_CE_GRAD)
-        return TCG_TA == 0 && TCG_TB == 1 && (TCG_DT == DT_F16 || TCG_DT == DT_BF16) &&
-               (cls == TILE_256_DMA || cls == TILE_128_DMA || cls == TILE_128_DMA4);
+    if (out == OUT_CE_STAT || out == OUT_CE_GRAD) {
+        if (TCG_TA != 0 || TCG_TB != 1 || TCG_DT == DT_I8) return false;
+        if (cls == TILE_64 || cls == TILE_128) return out == OUT_CE_STAT || TCG_DT == DT_F32;
+        return cls == TILE_256_DMA || cls == TILE_128_DMA || cls == TILE_128_DMA4;
+    }
     if (out == OUT_PARTIAL)
         return cls == TILE_64 || cls == TILE_128 || cls == TILE_128_DMA || cls == TILE_128_DMA4 ||
                cls == TILE_256_DMA;

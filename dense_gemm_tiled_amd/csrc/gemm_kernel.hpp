@@ -613,8 +613,16 @@ struct Occupancy {
     static constexpr int value = CLS == TILE_256 ? 1 : 2;
 };
 
+// Row m's target as a column of the product, -1 where it is none.
+__device__ inline int ce_load_target(const GemmArgs &args, int64_t m) {
+    const int64_t t = args.ce_targets64 ? static_cast<const int64_t *>(args.ce_targets)[m]
+                                        : (int64_t)static_cast<const int32_t *>(args.ce_targets)[m];
+    return t >= args.ce_first && t < (int64_t)args.ce_first + args.N ? (int)(t - args.ce_first) : -1;
+}
+
 // OUT is the output element type (DT_F32 / DT_F16 / DT_BF16 / DT_I32), or
-// OUT_PARTIAL to write raw split-K partial sums to the workspace.
+// OUT_PARTIAL to write raw split-K partial sums to the workspace, or one of the
+// cross entropy's epilogues.
 template <int DT, bool TA, bool TB, int CLS, int OUT>
 __global__ __launch_bounds__(256, Occupancy<CLS>::value) void gemm_kernel(const GemmArgs args) {
     constexpr TileShape TS = tile_shape(CLS);
@@ -736,7 +744,86 @@ __global__ __launch_bounds__(256, Occupancy<CLS>::value) void gemm_kernel(const 
     // ---- epilogue: lane holds C[m][n .. n+3] of each 16x16 block
     const int ml0 = wm * WTM + (lane & 15);
     const int nl0 = wn * WTN + 4 * (lane >> 4);
-    if constexpr (OUT == OUT_PARTIAL) {
+    if constexpr (OUT == OUT_CE_STAT) {
+        // The softmax of the tile's rows over this wave's columns: the largest
+        // value m (clamped, so that a row of -inf sums to 0) and sum exp2((v -
+        // m) a2), in units of the accumulator; each row is spread over 4 lanes.
+        static_assert(DT != DT_I8 && WN == 2, "float sums, two shares of a tile's columns");
+        const float sign = args.alpha < 0.f ? -1.f : 1.f;
+        const float a2 = __builtin_fabsf(args.alpha) * kLog2E, limit = ce_limit(a2);
+        float2 *part = static_cast<float2 *>(args.ws) + (tn * WN + wn) * args.ce_sp + m0 * args.ce_sm;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int ml = ml0 + i * 16;
+            const bool row_in = m0 + ml < M;
+            float v[FN][4], mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[j][e] = n0 + nl0 + j * 16 + e < N ? sign * acc[i][j][e] : -INFINITY;
+                    mx = __builtin_fmaxf(mx, v[j][e]);
+                }
+            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
+            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+            mx = __builtin_fminf(__builtin_fmaxf(mx, -limit), limit);
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f((v[j][e] - mx) * a2);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (!row_in) continue;
+            if (lane < 16) part[ml * args.ce_sm] = make_float2(mx, s);
+            // the target's product, from the lane that holds it
+            const int target = ce_load_target(args, m0 + ml);
+            const int d = target - (n0 + nl0);
+            if (target >= 0 && d >= 0 && d < WTN && (d & 12) == 0) {
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x = d == 16 * j + e ? v[j][e] : x;
+                args.ce_logit[m0 + ml] = x;
+            }
+        }
+    } else if constexpr (OUT == OUT_CE_GRAD) {
+        // grad (exp(alpha v - lse) - [n is the target]); the target's by expm1
+        // (1 taken off a rounded exponential would leave nothing near 1)
+        static_assert(DT == DT_F32, "gradients in fp32");
+        const int64_t org = ((int64_t)m0 * args.ldc + n0) * 4;
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(static_cast<char *>(args.C) + org, args.c_extent - org);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int ml = ml0 + i * 16;
+            if (m0 + ml >= M) continue;
+            const CeRow r = args.ce_rows[m0 + ml];
+            int d = r.target - args.ce_first - (n0 + nl0);
+            d = r.target >= 0 && d >= 0 && d < WTN && (d & 12) == 0 ? d : -1;
+            float at = 0.f;
+            if (d >= 0) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) at = d == 16 * j + e ? acc[i][j][e] : at;
+                at = r.grad * expm1f(__builtin_fmaf(at, args.alpha, -r.lse));
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int n = n0 + nl0 + j * 16;
+                int v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = __builtin_fmaf(acc[i][j][e], args.alpha, -r.lse);
+                    const float g = d == 16 * j + e ? at : r.grad * __builtin_amdgcn_exp2f(x * kLog2E);
+                    v[e] = n + e < N ? as_i32(g) : 0;
+                }
+                // (rows are whole 16-byte pieces)
+                if (n < args.ce_cols) store_i4(rc, (ml * args.ldc + nl0 + j * 16) * 4, 4, true, v);
+            }
+        }
+    } else if constexpr (OUT == OUT_PARTIAL) {
         // raw fp32 / int32 partial sums of this K slice: workspace plane g
         char *wsb = static_cast<char *>(args.ws) +
                     ((int64_t)g * M * N + (int64_t)m0 * N + n0) * 4;

@@ -424,8 +424,8 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
 
 // dw for few tokens: one byte read for many stored, so the stores should never
 // wait.  A workgroup keeps `per` columns of xt in LDS, each of its waves the
-// gradients of 64 words in registers (gathered once: a word's tokens side by
-// side); then it runs along the columns, 64 at a time: operands from LDS, whose
+// gradients of 64 words in registers (loaded once, a word's tokens then brought
+// side by side); then it runs along the columns, 64 at a time: operands from LDS, whose
 // reads a wave can wait for without its stores, 8 results of a word
 // to a 16-byte store (row 4 c + e of block j is column 32 (j / 2) + 8 c + 4 (j %
 // 2) + e).
@@ -433,6 +433,35 @@ constexpr int kOuterWaves = 8;
 // The value of the lane 8 further on in the row of 16.
 __device__ inline u32 swap8(u32 x) {
     return (u32)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true);
+}
+// 8 lanes' rows of 8 16-bit numbers transposed: lane i of them has row i, then
+// column i (halves, quarters and single numbers exchanged with the lanes 4, 2
+// and 1 away).
+template <int CTRL>
+__device__ inline u32 dpp(u32 x) {
+    return (u32)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+__device__ inline u32x4 transpose8(u32x4 v, int lane) {
+    const bool b4 = lane & 4, b2 = lane & 2, b1 = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        // (the lane 4 away: the half row mirrored, then each 4 mirrored back)
+        const u32 other = dpp<0x1B>(dpp<0x141>(b4 ? v[i] : v[2 + i]));
+        if (b4) v[i] = other;
+        else v[2 + i] = other;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const u32 other = dpp<0x4E>(b2 ? v[i] : v[i + 1]);
+        if (b2) v[i] = other;
+        else v[i + 1] = other;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const u32 other = dpp<0xB1>(v[i]);
+        v[i] = b1 ? other >> 16 | (v[i] & 0xFFFF0000u) : (v[i] & 0xFFFFu) | other << 16;
+    }
+    return v;
 }
 // LINES: dw's rows are whole 128-byte lines.  What is stored is not read again
 // here, so then non-temporal stores keep it out of the memory-side cache, which
@@ -453,29 +482,25 @@ __global__ __launch_bounds__(kOuterWaves * 64) void ce_outer_kernel(CeOuterArgs 
     const int64_t n0 = ((int64_t)(blockIdx.x / slices) * kOuterWaves + wave) * 64;
     const int h0 = (int)(blockIdx.x % slices) * per, h1 = min(a.H, h0 + per);
     const char *xt = static_cast<const char *>(a.xt) + (int64_t)h0 * KS * 64;
-    for (int i = tid; i < (h1 - h0) * KS * 4; i += kOuterWaves * 64)
-        *reinterpret_cast<u32x4 *>(xs + i / (KS * 4) * ROW + i % (KS * 4) * 16) =
-            *reinterpret_cast<const u32x4 *>(xt + (int64_t)i * 16);
+    // (8 words of a token to a lane; rows of g are whole 16-byte pieces)
     const unsigned short *g = static_cast<const unsigned short *>(a.g);
     u32x4 gf[KS][4];
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int64_t n = n0 + 16 * b + r;
-            u32 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u32 v[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int t = 32 * k + 8 * c + 2 * i + q;
-                    v[q] = t < a.T && n < a.N ? g[t * a.pitch + n] : 0u;
-                }
-                w[i] = v[0] | v[1] << 16;
-            }
-            gf[k][b] = u32x4{w[0], w[1], w[2], w[3]};
+            const int64_t n = n0 + 16 * b + (r & 8);
+            const int t = 32 * k + 8 * c + (r & 7);
+            gf[k][b] = t < a.T && n < a.pitch ? *reinterpret_cast<const u32x4 *>(g + t * a.pitch + n)
+                                              : u32x4{0u, 0u, 0u, 0u};
         }
+    for (int i = tid; i < (h1 - h0) * KS * 4; i += kOuterWaves * 64)
+        *reinterpret_cast<u32x4 *>(xs + i / (KS * 4) * ROW + i % (KS * 4) * 16) =
+            *reinterpret_cast<const u32x4 *>(xt + (int64_t)i * 16);
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) gf[k][b] = transpose8(gf[k][b], lane);
     const float alpha = a.scale * a.unscale[0];
     __syncthreads();
     if (n0 >= a.N) return;
@@ -626,7 +651,7 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
     const float f = a.unscale ? a.unscale[0] : 1.f;
     const float *src = a.src + t * a.ld_src;
     const bool more = a.lost && live;
-    if (DT == DT_F32 && src == a.dst && live && f == 1.f && !more) return;
+    if (DT == DT_F32 && a.src == a.dst && live && f == 1.f && !more) return;
     const float lost = more ? a.scale * a.lost[t] : 0.f;
     const unsigned short *w = static_cast<const unsigned short *>(a.w) + (more ? row.target * a.ldw : 0);
     if constexpr (VEC) {
@@ -872,7 +897,7 @@ hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s)
 }
 
 hipError_t tcg_launch_ce_outer(const CeOuterArgs &a, hipStream_t s) {
-    if (a.T < 1 || a.T > a.tp || (a.tp != 32 && a.tp != 64) || a.N < 1 || a.H < 8 || a.H % 8 != 0)
+    if (a.T < 1 || a.T > a.tp || (a.tp != 32 && a.tp != 64) || a.N < 1 || a.H < 8 || a.H % 8 != 0 || a.pitch % 8 != 0)
         return hipErrorInvalidValue;
     // fewer columns to a workgroup where they would leave less than two
     // workgroups a CU

@@ -151,7 +151,7 @@ __device__ inline void balance_expert(const BalanceArgs &a, int e, int count, in
 // Each workgroup's share of the tokens: sums of p in registers (a lane has the
 // same experts for every token), U tokens a group of lanes at a time, the next
 // U on the way meanwhile (one at a time: 16.4 us for 32768 x 256 f32 against
-// BAL_MAIN).  Bound by those loads.  ONE: the only workgroup goes on to the
+// 10.6).  Bound by those loads.  ONE: the only workgroup goes on to the
 // result.
 template <int V, int L, int S, bool ONE>
 __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {

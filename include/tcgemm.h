@@ -383,8 +383,9 @@ tc_status_t tc_moe_async(tc_context *ctx, const tc_moe_desc *d, const void *x,
  *     lse[t]  = log sum_v exp(l[t, v]),
  *     loss[t] = lse[t] - l[t, targets[t]],  0 where the target is outside [0, V)
  * (such a token is ignored), both fp32 [T].  The products are summed in fp32
- * and not stored (f32 inputs, and rows, pitches or addresses that are no whole
- * 16-byte pieces: 2^26 at a time).  targets: int32, or int64 with targets64,
+ * and not stored (few tokens of f32, or of rows of w that are no whole 16-byte
+ * pieces: 2^26 at a time; such rows of 16-bit types are copied to whole pieces
+ * where there are more tokens, 512 MiB at a time).  targets: int32, or int64 with targets64,
  * contiguous.  A row of x or w that holds NaN or infinity gives the losses
  * that it takes part in as NaN or infinity; no other token's.
  * workspace: tc_cross_entropy_workspace bytes of device memory for the same x

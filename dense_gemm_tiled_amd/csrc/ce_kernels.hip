@@ -429,7 +429,6 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
 // reads a wave can wait for without its stores, 8 results of a word
 // to a 16-byte store (row 4 c + e of block j is column 32 (j / 2) + 8 c + 4 (j %
 // 2) + e).
-constexpr int kOuterWaves = 8;
 // The value of the lane 8 further on in the row of 16.
 __device__ inline u32 swap8(u32 x) {
     return (u32)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true);
@@ -467,19 +466,25 @@ __device__ inline u32x4 transpose8(u32x4 v, int lane) {
 // here, so then non-temporal stores keep it out of the memory-side cache, which
 // would write it back while the next kernel reads w.  Gradients of 64 tokens by
 // 65536 x 4096 bf16: 409 us with half lines, 384 with whole ones, 345 with
-// these; 8 tokens by 131072 x 4096 686 / 623 / 598.  (Rows of 2056: 190 us with
+// these (337 now); 8 tokens by 131072 x 4096 686 / 623 / 598 (571 now).  (Rows of 2056: 190 us with
 // ordinary stores, 262 with these.)
 constexpr int kNonTemporal = 2;
-constexpr int kOuterColumns = 512;            // of xt: two workgroups of a CU can keep them
+// Waves, and columns of xt: two workgroups of a CU can keep 512 of 64 tokens.
+// Both gradients, us, 8 waves by 512 columns / 4 by 128: 64 tokens by 65536 x 4096
+// 337 / 356, 8 tokens 306 / 283, 8 by 131072 x 4096 606 / 571, 30 by 10007 x
+// 1024 38 / 37.
+constexpr int outer_waves(int ks) { return ks == 1 ? 4 : 8; }
+constexpr int outer_columns(int ks) { return ks == 1 ? 128 : 512; }
 template <int DT, int KS, bool BETA, bool LINES>
-__global__ __launch_bounds__(kOuterWaves * 64) void ce_outer_kernel(CeOuterArgs a, int per) {
+__global__ __launch_bounds__(outer_waves(KS) * 64) void ce_outer_kernel(CeOuterArgs a, int per) {
+    constexpr int WAVES = outer_waves(KS);
     constexpr int ROW = KS * 64 + 16;                 // bytes; 16 rows hit different banks
-    constexpr int COLS = kOuterColumns, AUX = LINES ? kNonTemporal : 0;
+    constexpr int COLS = outer_columns(KS), AUX = LINES ? kNonTemporal : 0;
     __shared__ __attribute__((aligned(16))) char xs[COLS * ROW];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
     const int slices = (a.H + per - 1) / per;
-    const int64_t n0 = ((int64_t)(blockIdx.x / slices) * kOuterWaves + wave) * 64;
+    const int64_t n0 = ((int64_t)(blockIdx.x / slices) * WAVES + wave) * 64;
     const int h0 = (int)(blockIdx.x % slices) * per, h1 = min(a.H, h0 + per);
     const char *xt = static_cast<const char *>(a.xt) + (int64_t)h0 * KS * 64;
     // (8 words of a token to a lane; rows of g are whole 16-byte pieces)
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(kOuterWaves * 64) void ce_outer_kernel(CeOuterArgs 
             gf[k][b] = t < a.T && n < a.pitch ? *reinterpret_cast<const u32x4 *>(g + t * a.pitch + n)
                                               : u32x4{0u, 0u, 0u, 0u};
         }
-    for (int i = tid; i < (h1 - h0) * KS * 4; i += kOuterWaves * 64)
+    for (int i = tid; i < (h1 - h0) * KS * 4; i += WAVES * 64)
         *reinterpret_cast<u32x4 *>(xs + i / (KS * 4) * ROW + i % (KS * 4) * 16) =
             *reinterpret_cast<const u32x4 *>(xt + (int64_t)i * 16);
 #pragma unroll
@@ -901,12 +906,13 @@ hipError_t tcg_launch_ce_outer(const CeOuterArgs &a, hipStream_t s) {
         return hipErrorInvalidValue;
     // fewer columns to a workgroup where they would leave less than two
     // workgroups a CU
-    const int64_t words = ((int64_t)a.N + 64 * kOuterWaves - 1) / (64 * kOuterWaves);
-    int per = kOuterColumns;
+    const int ks = a.tp / 32, waves = outer_waves(ks);
+    const int64_t words = ((int64_t)a.N + 64 * waves - 1) / (64 * waves);
+    int per = outer_columns(ks);
     while (per > 64 && words * ((a.H + per - 1) / per) < 512) per /= 2;
     const int64_t blocks = words * ((a.H + per - 1) / per);
     if (blocks >= kMaxBlocks / 2) return hipErrorInvalidValue;
-    const dim3 g((unsigned)blocks), b(kOuterWaves * 64);
+    const dim3 g((unsigned)blocks), b(waves * 64);
     const bool lines = a.lddw % 64 == 0 && (uintptr_t)a.dw % 128 == 0;
 #define CE_OUTER_KS(DT, KS)                                                                                   \
     do {                                                                                                      \

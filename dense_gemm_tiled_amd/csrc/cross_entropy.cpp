@@ -430,9 +430,9 @@ GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &
     c.B = w;
     c.whole[0] = true;
     c.whole[1] = b.copy_w;
-    // one row of tiles over a long K: as many slices of it as CUs (the planner's
+    // 16 bits, one row of tiles over a long K: as many slices of it as CUs (the planner's
     // choice for under 128 rows and from 8192 columns on is the 64 x 64 tile
-    // unsliced: 64 tokens, 32768 words by 8192: 935 us with it, 207 so)
+    // unsliced: 64 tokens, 32768 words by 8192: 935 us with it, 207 so).
     // f32, 8 to 256 tiles of 128 x 128: two workgroups a CU (the planner takes
     // 64 x 64 tiles there, from 128 of them on unsliced.  10007 words by 1024,
     // us, the planner's / so: 128 tokens 42 / 37, 255 tokens 77 / 65, 512 368 /

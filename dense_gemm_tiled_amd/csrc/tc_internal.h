@@ -134,10 +134,11 @@ struct GemmArgs {
     // transposed product of a small-M GEMM); bias and scales then go by r
     int32_t c_trans;
     // cross entropy only.  OUT_CE_STAT: ws holds float2 (maximum, sum) of share
-    // p = 0 .. 2 tiles_n - 1 of row m at p ce_sp + m ce_sm, and ce_logit [M] receives the targets' products, both in
-    // units of the accumulator (negated where alpha < 0); targets are int32
-    // or int64.  OUT_CE_GRAD: columns N .. ce_cols of C are written 0, ce_rows
-    // [M].  Both: column n is word ce_first + n.
+    // p = 0 .. 2 tiles_n - 1 of row m at p ce_sp + m ce_sm, and ce_logit [M]
+    // receives the targets' products, both in units of the accumulator (negated
+    // where alpha < 0); targets are int32 or int64.  OUT_CE_GRAD: columns N ..
+    // ce_cols of C are written 0, ce_rows [M].  Both: column n is word ce_first
+    // + n.
     const void *ce_targets;
     int32_t ce_targets64;
     int32_t ce_first, ce_cols;

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("T", [1, 3, 4, 17, 64, 65, 128, 129, 300])
+@pytest.mark.parametrize("T", [1, 3, 4, 17, 64, 65, 128, 129, 256, 257, 300])
 @pytest.mark.parametrize("V,H", [(700, 77), (33000, 131)])
 def test_odd_rows(T, V, H, dtype):
     x, w, targets, g = case(T, V, H, dtype, seed=T)
@@ -57,9 +57,10 @@ def test_infinite_rows(T, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_pieces_of_copied_words(dtype):
+@pytest.mark.parametrize("T", [130, 260])
+def test_pieces_of_copied_words(T, dtype):
     """More words than a piece of the copy holds (2^28 elements of whole rows)."""
-    T, V, H = 130, 70001, 4095
+    V, H = 70001, 4095
     x, w, targets, g = case(T, V, H, dtype)
     targets[:4] = torch.tensor([0, 65535, 65536, 70000], device="cuda")
     forward(x, w, targets)

@@ -54,8 +54,8 @@ def test_room_for_copied_rows(lib, T, V, H, dtype):
     sizes) fits beside the gradient of its products."""
     st, odd = gsize(lib, cdesc(T, V, H, dtype), cgrads(dxt=dtype, dwt=dtype))
     assert st == 0 and odd >= (V * ((H + 7) // 8 * 8) + T * V) * 2
-    st, odd = size(lib, cdesc(max(T, 129), V, H, dtype))
-    assert st == 0 and odd >= (V + max(T, 129)) * ((H + 7) // 8 * 8) * 2
+    st, odd = size(lib, cdesc(max(T, 257), V, H, dtype))
+    assert st == 0 and odd >= (V + max(T, 257)) * ((H + 7) // 8 * 8) * 2
 
 
 def test_workspaces(lib):

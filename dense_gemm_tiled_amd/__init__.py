@@ -937,10 +937,11 @@ def _new(shapes, like, device: int, stream):
     """New tensors of the given (shape, dtype)s, made for the stream a call
     runs on."""
     import torch
+    empty, where = torch.empty, like.device
     if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=like.device) for shape, dtype in shapes]
+        return [empty(shape, dtype=dtype, device=where) for shape, dtype in shapes]
     with _on_stream(device, stream):
-        return [torch.empty(shape, dtype=dtype, device=like.device) for shape, dtype in shapes]
+        return [empty(shape, dtype=dtype, device=where) for shape, dtype in shapes]
 
 
 def _make_ce(x, weight, targets, scale):
@@ -989,7 +990,7 @@ def cross_entropy(x, weight, targets, *, scale: float = 1.0, stream=None):
                             lambda: _make_ce_forward(x, weight, targets, scale))
     lib = _lib if _lib is not None else load_library()
     ctx, s = _torch_stream(device, stream)
-    (loss, lse), space = _new([((d.T,), torch.float32)] * 2, x, device, stream), _scratch(need, x, device, stream)
+    (loss, lse), space = _new([(d.T, torch.float32)] * 2, x, device, stream), _scratch(need, x, device, stream)
     st = lib.tc_cross_entropy_async(ctx, dref, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
                                     loss.data_ptr(), lse.data_ptr(), space.data_ptr(), need, s)
     if st != 0:
@@ -1084,10 +1085,11 @@ def moe_balance(logits, ids, *, coef: float = 1.0, stream=None):
                              ids.dtype), lambda: _make_balance(logits, ids))
     lib = _lib if _lib is not None else load_library()
     ctx, s = _torch_stream(device, stream)
-    loss, counts, slope, space = _new([((), torch.float32), ((r.E,), torch.int32), ((r.E,), torch.float32),
-                                       ((need,), torch.uint8)], logits, device, stream)
+    loss, counts, slope = _new([((), torch.float32), (r.E, torch.int32), (r.E, torch.float32)], logits, device,
+                               stream)
+    space = _scratch(need, logits, device, stream) if need else None
     st = lib.tc_moe_balance_async(ctx, rref, logits.data_ptr(), ids.data_ptr(), float(coef), loss.data_ptr(),
-                                  counts.data_ptr(), slope.data_ptr(), space.data_ptr(), need, s)
+                                  counts.data_ptr(), slope.data_ptr(), space.data_ptr() if need else None, need, s)
     if st != 0:
         _check(st, ctx)
     return loss, counts, slope

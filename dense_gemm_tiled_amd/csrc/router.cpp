@@ -12,13 +12,16 @@ namespace {
 
 int64_t up_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// The workspace of a balance loss (as if spread over as many workgroups as
-// there may be: how many there are depends on the logits' address, too).
+// The workspace of a balance loss: none for so few tokens that one workgroup
+// takes them, else as if spread over as many as there may be (how many there are
+// depends on the logits' address, too).
 struct BalanceSpace {
     int64_t count, tokens, dot, joined, bytes;
 };
-BalanceSpace balance_space(const tc_route_desc &r) {
+BalanceSpace balance_space(const tc_route_desc &r, const RouteArgs &a) {
     BalanceSpace b;
+    memset(&b, 0, sizeof b);
+    if (tcg_balance_alone(a)) return b;
     b.count = up_to((int64_t)kBalanceGroups * up_to(r.E, 4) * 4, 256);
     b.tokens = 2 * b.count;
     b.dot = b.tokens + kBalanceGroups * 8;
@@ -52,7 +55,7 @@ tc_status_t tc_moe_balance_workspace(const tc_route_desc *r, int64_t *bytes) {
     RouteArgs a;
     int64_t span_bytes;
     const tc_status_t st = check_route(r, &a, &span_bytes, nullptr);
-    if (st == TC_OK) *bytes = balance_space(*r).bytes;
+    if (st == TC_OK) *bytes = balance_space(*r, a).bytes;
     return st;
 }
 
@@ -73,32 +76,34 @@ tc_status_t tc_moe_balance_async(tc_context *ctx, const tc_route_desc *r, const 
     if (((uintptr_t)loss | (uintptr_t)counts | (uintptr_t)slope) % 4 != 0)
         return fail(err, TC_ERR_INVALID_ARGUMENT, "loss, counts and slope must be aligned to their elements");
     if (!std::isfinite(coef)) return fail(err, TC_ERR_INVALID_ARGUMENT, "coef must be finite");
-    const BalanceSpace sp = balance_space(*r);
-    if (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < sp.bytes)
+    const BalanceSpace sp = balance_space(*r, a.route);
+    if (sp.bytes > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < sp.bytes))
         return fail(err, TC_ERR_INVALID_ARGUMENT,
                     "the workspace must be 16-byte aligned and hold %lld bytes (%lld given)",
                     (long long)sp.bytes, (long long)workspace_bytes);
     const Range g[] = {{"loss", loss, 4},
                        {"counts", counts, (int64_t)r->E * 4},
                        {"slope", slope, (int64_t)r->E * 4},
-                       {"workspace", workspace, sp.bytes},
+                       {"workspace", sp.bytes > 0 ? workspace : nullptr, sp.bytes},
                        {"logits", logits, bytes},
                        {"ids", ids, (int64_t)r->T * r->top_k * 4}};
     if ((st = check_ranges(g, 6, 4, false, err)) != TC_OK) return st;
     const DeviceScope dev(ctx);
     if (dev.status != TC_OK) return dev.status;
     if ((st = check_ranges(g, 6, 4, true, err)) != TC_OK) return st;
-    char *const ws = static_cast<char *>(workspace);
     a.coef = coef;
     a.loss = loss;
     a.counts = counts;
     a.slope = slope;
     a.pitch = (int32_t)up_to(r->E, 4);
-    a.part_p = reinterpret_cast<float *>(ws);
-    a.part_count = reinterpret_cast<int32_t *>(ws + sp.count);
-    a.part_tokens = reinterpret_cast<int2 *>(ws + sp.tokens);
-    a.part_dot = reinterpret_cast<double *>(ws + sp.dot);
-    a.joined = reinterpret_cast<int32_t *>(ws + sp.joined);
+    if (sp.bytes > 0) {
+        char *const ws = static_cast<char *>(workspace);
+        a.part_p = reinterpret_cast<float *>(ws);
+        a.part_count = reinterpret_cast<int32_t *>(ws + sp.count);
+        a.part_tokens = reinterpret_cast<int2 *>(ws + sp.tokens);
+        a.part_dot = reinterpret_cast<double *>(ws + sp.dot);
+        a.joined = reinterpret_cast<int32_t *>(ws + sp.joined);
+    }
     int launches = 0;
     const hipError_t e = tcg_launch_balance(a, &launches, s->stream);
     ctx->dispatches += launches;

@@ -34,6 +34,8 @@ struct RouteGradArgs {
 
 }  // namespace tcg
 
+// whether it is one launch wherever the logits lie
+bool tcg_balance_alone(const tcg::RouteArgs &a);
 // workgroups a balance loss is spread over (1: one launch, no workspace used)
 int tcg_balance_groups(const tcg::RouteArgs &a);
 hipError_t tcg_launch_balance(const tcg::BalanceArgs &a, int *launches, hipStream_t s);

@@ -487,10 +487,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
 bool four_at_a_time(const RouteArgs &a) {
     return a.E % 4 == 0 && a.ld % 4 == 0 && (uintptr_t)a.logits % (4 * dt_size(a.dtype)) == 0;
 }
-int lanes_of(const RouteArgs &a, bool four) {
-    if (four) return a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
-    return a.E <= 16 ? 16 : a.E <= 32 ? 32 : 64;
+int lanes_of(int E, bool four) {
+    if (four) return E <= 64 ? 16 : E <= 128 ? 32 : 64;
+    return E <= 16 ? 16 : E <= 32 ? 32 : 64;
 }
+// Passes of a workgroup of the balance loss over T tokens; up to 4 a single
+// workgroup ends before a second launch would begin.
+int64_t balance_passes(int64_t T, int lanes) { return (T + 1024 / lanes - 1) / (1024 / lanes); }
+constexpr int kAlone = 4;
 
 // CALL<V, L, S> for the sizes of a
 #define ROUTER_SIZES(a, four, CALL)                    \
@@ -519,13 +523,12 @@ bool sizes_ok(const RouteArgs &a) {
 
 using namespace tcg;
 
+bool tcg_balance_alone(const RouteArgs &a) { return balance_passes(a.T, lanes_of(a.E, false)) <= kAlone; }
+
 int tcg_balance_groups(const RouteArgs &a) {
-    const int64_t tok = 1024 / lanes_of(a, four_at_a_time(a));
-    const int64_t passes = (a.T + tok - 1) / tok;
-    // Up to 4 passes a single workgroup ends before a second launch would
-    // begin; else workgroups that look at 2 to 4 tokens a group of lanes at a
-    // time.
-    if (passes <= 4) return 1;
+    const int64_t passes = balance_passes(a.T, lanes_of(a.E, four_at_a_time(a)));
+    // (else workgroups that look at 2 to 4 tokens a group of lanes at a time)
+    if (passes <= kAlone) return 1;
     const int64_t groups = (passes + 3) / 4;
     return groups < kBalanceGroups ? (int)groups : kBalanceGroups;
 }
@@ -557,7 +560,7 @@ hipError_t tcg_launch_route_grad(const RouteGradArgs &a, hipStream_t s) {
     if (!sizes_ok(r)) return hipErrorInvalidValue;
     const bool four = four_at_a_time(r) && a.ldd % 4 == 0 && (uintptr_t)a.dlogits % (4 * dt_size(a.d_dtype)) == 0;
     // (2 tokens to a group of lanes where the logits of both fit 8 registers)
-    const int64_t tok = 256 / lanes_of(r, four) * (r.E <= 256 ? 2 : 1);
+    const int64_t tok = 256 / lanes_of(r.E, four) * (r.E <= 256 ? 2 : 1);
     const int64_t blocks = (r.T + tok - 1) / tok;
     if (blocks >= (1 << 24)) return hipErrorInvalidValue;
 #define ROUTE_GRAD(V, L, S) \

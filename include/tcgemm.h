@@ -450,7 +450,8 @@ tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d
  * 0 where no token counts.  loss [1], slope [E] fp32, counts [E] int32.  slope is
  * what the gradient needs: dloss / d sum_t p[t, e], less what is the same for
  * every e (the p of a token sum to 1).  Sums do not depend on the order in
- * which the GPU runs the workgroups.  workspace as above. */
+ * which the GPU runs the workgroups.  workspace as above (NULL where 0 bytes are
+ * asked for: few tokens). */
 tc_status_t tc_moe_balance_workspace(const tc_route_desc *r, int64_t *bytes);
 
 tc_status_t tc_moe_balance_async(tc_context *ctx, const tc_route_desc *r, const void *logits,

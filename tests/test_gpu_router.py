@@ -241,3 +241,17 @@ def test_refusals_on_the_gpu():
             call()
             pytest.fail("call %d was not refused" % i)
     assert tg.dispatch_count() == before
+
+
+@pytest.mark.parametrize("E", [8, 17, 64, 200, 512])
+@pytest.mark.parametrize("ahead", [0, 1])
+def test_around_one_workgroup(E, ahead):
+    """As many tokens as one workgroup takes without scratch memory, and one
+    more; logits that can and cannot be read 4 at a time."""
+    most = 4 * 1024 // (16 if E <= 16 else 32 if E <= 32 else 64)
+    for T in (most, most + 1):
+        logits, ids, g = case(T, E, 2, "f32", seed=T + E)
+        room = torch.zeros(T * E + 1, device="cuda")
+        there = room[ahead:ahead + T * E].view(T, E)
+        there.copy_(logits)
+        balance(there, ids)

@@ -173,3 +173,10 @@ def test_bad_router_arguments(lib, ctx):
                          (7, tg.I32, 2), (8, 63, 1), (6, X + 128, 4), (6, IDS, 4), (6, GRAD + 400, 4), (6, LSE, 4),
                          (6, LOSS, 4)):
         assert call(*[v if j == i else w for j, w in enumerate(good)]) == status, (i, v)
+
+
+@pytest.mark.parametrize("E,most", [(8, 256), (16, 256), (17, 128), (32, 128), (33, 64), (64, 64), (512, 64)])
+def test_few_tokens_need_no_workspace(lib, E, most):
+    n = ctypes.c_int64(-1)
+    assert lib.tc_moe_balance_workspace(R(rdesc(T=most, E=E)), R(n)) == 0 and n.value == 0
+    assert lib.tc_moe_balance_workspace(R(rdesc(T=most + 1, E=E)), R(n)) == 0 and n.value > 0

@@ -561,6 +561,7 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     if (p.es == 4) b->l = b->g;
     b->gemm_bytes = 0;
     const void *odd = reinterpret_cast<const void *>((uintptr_t)p.es);
+    const bool again = b->N < p.V || b->parts > 1;   // dx goes on from the sums before
     for (const int64_t n : {b->N, p.V % b->N}) {
         if (n == 0) continue;
         GemmCall c[6];
@@ -574,7 +575,7 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
             }
             if (g.dx && !b->few32) {
                 c[k++] = dx_call(p, *b, g, scale, n, 0.f, at);
-                c[k++] = dx_call(p, *b, g, scale, n, 1.f, at);
+                if (again) c[k++] = dx_call(p, *b, g, scale, n, 1.f, at);
             }
         }
         tc_status_t st;
@@ -584,7 +585,7 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }
         for (const float beta : {g.beta, 1.f}) {
-            if (!g.dw || b->few || b->few32) continue;
+            if (!g.dw || b->few || b->few32 || (beta != g.beta && b->parts == 1)) continue;
             if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, n, beta), &bytes, err)) != TC_OK) return st;
             if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
         }

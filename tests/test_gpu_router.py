@@ -255,3 +255,18 @@ def test_around_one_workgroup(E, ahead):
         there = room[ahead:ahead + T * E].view(T, E)
         there.copy_(logits)
         balance(there, ids)
+
+
+@pytest.mark.parametrize("E,k", [(2, 2), (16, 16), (60, 5), (64, 8), (200, 7), (256, 8), (500, 16), (512, 3)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_the_same_expert_again(E, k, renormalize):
+    """Ids drawn with repetition from a few experts, and rows of one alone: the
+    shares of the places add up."""
+    T = 301
+    logits, _, g = case(T, E, k, "f32")
+    ids = torch.randint(0, max(2, min(E, 4)), (T, k), device="cuda", generator=g, dtype=torch.int32)
+    ids[::5] = E - 1
+    ids[::7, 0] = -1
+    dw = torch.randn(T, k, device="cuda", generator=g)
+    balance(logits, ids)
+    gradient(logits, ids, dw, renormalize, 1.5, torch.randn(E, device="cuda"), torch.ones((), device="cuda"))

@@ -58,7 +58,8 @@ __device__ inline void join_shares(const CeJoinArgs &a, int64_t t, int q, float 
     }
 }
 
-// A token to a workgroup, its shares side by side.
+// A token to a workgroup, its shares side by side (1 token of 512 shares 3.8 us,
+// 1021 of 408 5.4: starting up).
 __global__ __launch_bounds__(256) void ce_join_token_kernel(CeJoinArgs a) {
     __shared__ float sm[4], ss[4];
     const int tid = threadIdx.x;
@@ -77,7 +78,8 @@ __global__ __launch_bounds__(256) void ce_join_token_kernel(CeJoinArgs a) {
     finish_token(a, blockIdx.x, m, s, scale);
 }
 
-// 16 tokens to a workgroup, side by side in every share.
+// 16 tokens to a workgroup, side by side in every share: bound by reading them
+// (4096 tokens of 1024 shares, 34 MB, 9.6 us).
 __global__ __launch_bounds__(1024) void ce_join_kernel(CeJoinArgs a) {
     __shared__ float sm[16][16], ss[16][16];
     const int tid = threadIdx.x, tok = tid % 16, q = tid / 16;
@@ -238,7 +240,8 @@ __global__ __launch_bounds__(512) void ce_rows_kernel(CeRowsArgs a) {
     }
 }
 
-// One row's kCeStatCols products to a workgroup, 8 to a thread.
+// One row's kCeStatCols products to a workgroup, 8 to a thread: bound by reading
+// them (1024 x 65536 111 us, 2.4 TB/s; 64 x 65536 9 us).
 __global__ __launch_bounds__(256) void ce_stat_kernel(CeStatArgs a) {
     __shared__ float sm[4], ss[4];
     const int chunks = (a.N + kCeStatCols - 1) / kCeStatCols;
@@ -312,7 +315,8 @@ __global__ __launch_bounds__(1024) void ce_unscale_kernel(CePrepArgs a) {
     for (int h = threadIdx.x; h < a.H; h += 1024) a.unscale[h] = v;
 }
 
-// A wave to a token.
+// A wave to a token: bound by the copy (4096 x 4096 bf16 26 us, with the look
+// for the largest grad).
 template <int ES, bool VEC>
 __global__ __launch_bounds__(256) void ce_prep_kernel(CePrepArgs a) {
     const int lane = threadIdx.x & 63;
@@ -601,7 +605,8 @@ __global__ __launch_bounds__(outer_waves(KS) * 64) void ce_outer_kernel(CeOuterA
 }
 
 // kCeStatCols columns of a row to a workgroup.  16-bit gradients are the sum
-// of `parts` numbers, each the rounding of what those before it left.
+// of `parts` numbers, each the rounding of what those before it left.  Bound by
+// reading and writing (1024 x 65536 to one bf16 115 us, 3.5 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void ce_grad_kernel(CeGradArgs a) {
     const int chunks = (int)((a.pitch + kCeStatCols - 1) / kCeStatCols);
@@ -647,7 +652,8 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(CeGradArgs a) {
 
 __device__ inline float decode(u32 h, int dtype) { return dtype == DT_F16 ? from_f16_bits(h) : from_bf16_bits(h); }
 
-// A row to a workgroup.
+// A row to a workgroup: bound by reading and writing (4096 x 4096 to bf16 28 us,
+// 3.6 TB/s).
 template <int DT, bool VEC>
 __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
     const int64_t t = blockIdx.x;

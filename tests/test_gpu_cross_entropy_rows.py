@@ -37,7 +37,7 @@ def test_one_side(T, pad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("T", [64, 130])
+@pytest.mark.parametrize("T", [2, 64, 130, 300])
 def test_infinite_rows(T, dtype):
     """A word whose row holds infinities next to one that is all but certain:
     the row beside it is not touched by them."""

@@ -102,6 +102,17 @@ struct CeFinishArgs {
     int32_t w_dtype;
 };
 
+// Rows of dw from their sums over all tokens (fp32, contiguous): dst = src +
+// beta * dst, rounded once.
+struct CeStoreArgs {
+    const float *src;
+    int32_t N, H;
+    int32_t dtype;             // of dst: 16-bit
+    float beta;
+    void *dst;
+    int64_t ld;                // elements, of dst
+};
+
 // Partial softmaxes of the products of a few tokens, from x and w: a share is
 // kCeRowWords words.
 constexpr int kCeRowWords = 64, kCeRowTokens = 32;
@@ -184,3 +195,4 @@ hipError_t tcg_launch_ce_prep(const tcg::CePrepArgs &a, int *launches, hipStream
 hipError_t tcg_launch_ce_outer(const tcg::CeOuterArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_grad(const tcg::CeGradArgs &a, hipStream_t s);
 hipError_t tcg_launch_ce_finish(const tcg::CeFinishArgs &a, hipStream_t s);
+hipError_t tcg_launch_ce_store(const tcg::CeStoreArgs &a, hipStream_t s);

@@ -695,6 +695,18 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
     }
 }
 
+// A row to a workgroup (tokens by the 100000: a thousandth of their products).
+template <int DT>
+__global__ __launch_bounds__(256) void ce_store_kernel(CeStoreArgs a) {
+    const int64_t n = blockIdx.x;
+    const float *src = a.src + n * a.H;
+    unsigned short *dst = static_cast<unsigned short *>(a.dst) + n * a.ld;
+    for (int h = threadIdx.x; h < a.H; h += 256) {
+        const float old = a.beta == 0.f ? 0.f : decode(dst[h], DT);
+        dst[h] = (unsigned short)pack2_16<DT>(a.beta == 0.f ? src[h] : __builtin_fmaf(a.beta, old, src[h]), 0.f);
+    }
+}
+
 constexpr int64_t kMaxBlocks = 1 << 24;   // of 256 threads: a launch's threads fit 32 bits
 
 // Few tokens in fp32.  Both products read or write V x H numbers once and have
@@ -1007,5 +1019,14 @@ hipError_t tcg_launch_ce_finish(const CeFinishArgs &a, hipStream_t s) {
     else if (a.dtype == DT_F16) CE_FINISH(DT_F16);
     else CE_FINISH(DT_BF16);
 #undef CE_FINISH
+    return hipGetLastError();
+}
+
+hipError_t tcg_launch_ce_store(const CeStoreArgs &a, hipStream_t s) {
+    if (a.N < 1 || a.N >= kMaxBlocks || a.H < 1 || a.ld < a.H) return hipErrorInvalidValue;
+    const dim3 g((unsigned)a.N), b(256);
+    if (a.dtype == DT_F16) hipLaunchKernelGGL(ce_store_kernel<DT_F16>, g, b, 0, s, a);
+    else if (a.dtype == DT_BF16) hipLaunchKernelGGL(ce_store_kernel<DT_BF16>, g, b, 0, s, a);
+    else return hipErrorInvalidValue;
     return hipGetLastError();
 }

@@ -410,26 +410,30 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
 }
 
 // ------------------------------------------------------------------ gradients
-// The gradient of N words' products at a time, all tokens: T x N numbers of
-// the inputs' type (parts times), then its two products.
+// The gradient of N words' products at a time: T x N numbers of the inputs'
+// type (parts times), then its two products.  All tokens at once, unless x's or
+// dx's rows span more than a GEMM's operand may (2^31 elements): then Tc at a
+// time, every one of them for the same words, so that the words' dw is summed
+// in fp32 over all tokens before it is rounded.
 struct BackwardSpace {
     bool dma, fused;
     bool few;                          // few tokens: kernels of their own, no copy of x
     bool few32;                        // few tokens in fp32: both products by kernels of their own
     int tp;                            // their number, rounded up
     bool own_dx;                       // dx is summed in the workspace
+    bool own_dw;                       // and so are N words of dw
     bool copy_w;                       // W's rows are copied to whole 16-byte pieces
     int parts, dx_parts, dw_parts;
-    int64_t N, pitch, xz_pitch;
-    int64_t rows, lost, unscale, xz, xt, w, acc, g, l, gemm, gemm_bytes, bytes;
+    int64_t Tc, N, pitch, xz_pitch;
+    int64_t rows, lost, unscale, xz, xt, w, acc, dw, g, l, gemm, gemm_bytes, bytes;
 };
 
-GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
-                 float beta, const void *w) {
+GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t T,
+                 int64_t N, float beta, const void *w) {
     GemmCall c;
     memset(&c, 0, sizeof c);
     const int64_t ld = b.own_dx ? p.H : g.lddx == 0 ? p.H : g.lddx;
-    c.d = gemm_desc(p.T, p.H, N, p.dt, TC_F32, false, false, scale, beta, b.pitch, p.ldw, ld);
+    c.d = gemm_desc(T, p.H, N, p.dt, TC_F32, false, false, scale, beta, b.pitch, p.ldw, ld);
     c.B = w;
     c.whole[0] = true;
     c.whole[1] = b.copy_w;
@@ -441,9 +445,9 @@ GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &
     // us, the planner's / so: 128 tokens 42 / 37, 255 tokens 77 / 65, 512 368 /
     // 107, 1024 372 / 190; by 4096, 64 tokens 77 / 105, 128 367 / 109, 1024 757
     // / 675; by 256, 255 tokens (4 tiles) 30 / 40)
-    const int64_t tiles = ceil_div(p.T, 128) * ceil_div(p.H, 128), ktiles = ceil_div(N * p.es, 128);
-    const bool few = p.whole && p.T <= 128 && p.H >= 256 && ktiles >= 32 && tiles <= 256;
-    const bool f32 = p.dt == TC_F32 && p.T > 64 && tiles >= 8 && tiles <= 256;
+    const int64_t tiles = ceil_div(T, 128) * ceil_div(p.H, 128), ktiles = ceil_div(N * p.es, 128);
+    const bool few = p.whole && T <= 128 && p.H >= 256 && ktiles >= 32 && tiles <= 256;
+    const bool f32 = p.dt == TC_F32 && T > 64 && tiles >= 8 && tiles <= 256;
     if (few || f32) {
         int64_t s = (f32 ? 512 : 256) / tiles;
         if (s > ktiles / (f32 ? 8 : 4)) s = ktiles / (f32 ? 8 : 4);
@@ -454,12 +458,14 @@ GemmCall dx_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &
     return c;
 }
 
-GemmCall dw_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t N,
-                 float beta) {
+// Where b.own_dw its C is the workspace's sums.
+GemmCall dw_call(const CeProblem &p, const BackwardSpace &b, const tc_ce_grads &g, float scale, int64_t T,
+                 int64_t N, float beta) {
     GemmCall c;
     memset(&c, 0, sizeof c);
-    const int64_t ld = g.lddw == 0 ? p.H : g.lddw;
-    c.d = gemm_desc(N, p.H, p.T, p.dt, g.dw_dtype, true, false, scale, beta, b.pitch, b.xz_pitch, ld);
+    const int64_t ld = b.own_dw || g.lddw == 0 ? p.H : g.lddw;
+    c.d = gemm_desc(N, p.H, T, p.dt, b.own_dw ? TC_F32 : g.dw_dtype, true, false, scale, beta, b.pitch, b.xz_pitch,
+                    ld);
     c.whole[0] = c.whole[1] = true;
     // (f32, 16384 words by 700 of 255 tokens: 73 us, 100 on the 256 x 256 tiles
     // that the planner takes there; 65536 by 2048, 1024 tokens: 2181, 2318)
@@ -527,25 +533,31 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     b->tp = p.T <= 32 ? 32 : 64;
     b->own_dx = g.dx && g.dx_dtype != TC_F32;
     b->xz_pitch = up_to(p.H, 16 / p.es);
+    // (G of 256 words and all tokens, the smallest piece, spans no more than an
+    // operand may; the same where tokens are taken in parts)
+    if (p.T > kMaxIndex / 256)
+        return fail(err, TC_ERR_OVERFLOW, "T=%lld: gradients take at most %lld tokens", (long long)p.T,
+                    (long long)kMaxIndex / 256);
+    const int64_t rows_dx = b->own_dx || g.lddx == 0 ? p.H : g.lddx;
+    const int64_t longest = g.dx && rows_dx > b->xz_pitch ? rows_dx : b->xz_pitch;
+    const int64_t most = kMaxIndex / longest / 256 * 256;
+    b->Tc = span(p.T, p.H, longest) <= kMaxIndex ? p.T : up_to(ceil_div(p.T, ceil_div(p.T, most)), 256);
+    b->own_dw = b->Tc < p.T && g.dw && g.dw_dtype != TC_F32;
     // Words at a time: 512 MiB of gradients, at least 8192 words (each piece
     // reads and writes the sums of dx once).
-    int64_t N = (int64_t)(512 << 20) / (p.T * p.es * b->parts);
+    int64_t N = (int64_t)(512 << 20) / (b->Tc * p.es * b->parts);
     if (N < 8192) N = 8192;
     const int64_t rows_w = g.dw && g.lddw > p.ldw ? g.lddw : p.ldw;
     if (N > kMaxWords) N = kMaxWords;
-    if (N > kMaxIndex / p.T) N = kMaxIndex / p.T;
+    if (N > kMaxIndex / b->Tc) N = kMaxIndex / b->Tc / 8 * 8;
     if (N > kMaxIndex / rows_w) N = kMaxIndex / rows_w;
     if (b->copy_w && N > copied_words(p)) N = copied_words(p);
-    if (N < 256)
-        return fail(err, TC_ERR_OVERFLOW, "T=%lld tokens or rows %lld apart leave less than 256 words at a time",
-                    (long long)p.T, (long long)rows_w);
     const int64_t pieces = ceil_div(p.V, N);
     const int64_t even = up_to(ceil_div(p.V, pieces), 256);   // pieces of about the same size
     N = even < N ? even : N / 256 * 256;
     b->N = N < p.V ? N : p.V;
     b->pitch = up_to(b->N, 8);
-    b->fused = b->dma || (p.es == 4 && staged(p, p.T, b->N));
-    if (p.T * b->pitch > kMaxIndex) return fail(err, TC_ERR_OVERFLOW, "T=%lld is too large", (long long)p.T);
+    b->fused = b->dma || (p.es == 4 && staged(p, b->Tc, b->N));
     b->rows = 0;
     b->lost = up_to(p.T * (int64_t)sizeof(CeRow), 256);
     const int64_t after = up_to(b->lost + p.T * 4, 256);
@@ -554,42 +566,46 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     b->xt = up_to(b->xz + p.T * b->xz_pitch * p.es, 256);
     b->w = up_to(b->xt + (b->few ? p.H * b->tp * 2 : 0), 256);
     b->acc = up_to(b->w + (b->copy_w ? b->N * p.ldw * 2 : 0), 256);
-    b->g = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
-    b->l = up_to(b->g + p.T * b->pitch * p.es * b->parts, 256);
+    b->dw = up_to(b->acc + (b->own_dx ? p.T * p.H * 4 : 0), 256);
+    b->g = up_to(b->dw + (b->own_dw ? b->N * p.H * 4 : 0), 256);
+    b->l = up_to(b->g + b->Tc * b->pitch * p.es * b->parts, 256);
     // (fp32: the gradient takes the place of its products)
-    b->gemm = b->fused || p.es == 4 ? b->l : up_to(b->l + p.T * b->pitch * 4, 256);
+    b->gemm = b->fused || p.es == 4 ? b->l : up_to(b->l + b->Tc * b->pitch * 4, 256);
     if (p.es == 4) b->l = b->g;
     b->gemm_bytes = 0;
     const void *odd = reinterpret_cast<const void *>((uintptr_t)p.es);
     const bool again = b->N < p.V || b->parts > 1;   // dx goes on from the sums before
-    for (const int64_t n : {b->N, p.V % b->N}) {
-        if (n == 0) continue;
-        GemmCall c[6];
-        int k = 0;
-        // (a later piece of W may start off 16-byte boundaries)
-        for (const void *at : {b->copy_w ? reinterpret_cast<const void *>(16) : w, odd}) {
-            if (at == odd && p.whole) continue;
-            if (!b->fused) {
-                c[k] = logits_call(p, p.T, n, b->xz_pitch, b->pitch, nullptr, at);
-                c[k++].whole[0] = true;
+    for (const int64_t T : {b->Tc, p.T % b->Tc})
+        for (const int64_t n : {b->N, p.V % b->N}) {
+            if (T == 0 || n == 0) continue;
+            GemmCall c[6];
+            int k = 0;
+            // (a later piece of W may start off 16-byte boundaries)
+            for (const void *at : {b->copy_w ? reinterpret_cast<const void *>(16) : w, odd}) {
+                if (at == odd && p.whole) continue;
+                if (!b->fused) {
+                    c[k] = logits_call(p, T, n, b->xz_pitch, b->pitch, nullptr, at);
+                    c[k++].whole[0] = true;
+                }
+                if (g.dx && !b->few32) {
+                    c[k++] = dx_call(p, *b, g, scale, T, n, 0.f, at);
+                    if (again) c[k++] = dx_call(p, *b, g, scale, T, n, 1.f, at);
+                }
             }
-            if (g.dx && !b->few32) {
-                c[k++] = dx_call(p, *b, g, scale, n, 0.f, at);
-                if (again) c[k++] = dx_call(p, *b, g, scale, n, 1.f, at);
+            tc_status_t st;
+            int64_t bytes = 0;
+            for (int i = 0; i < k; ++i) {
+                if ((st = gemm_call_workspace(c[i], &bytes, err)) != TC_OK) return st;
+                if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
+            }
+            // the first sums of dw, and those that go on from them
+            for (const float beta : {b->own_dw ? 0.f : g.beta, 1.f}) {
+                if (!g.dw || b->few || b->few32) continue;
+                if (beta == 1.f && beta != g.beta && b->parts == 1 && b->Tc == p.T) continue;
+                if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, T, n, beta), &bytes, err)) != TC_OK) return st;
+                if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
             }
         }
-        tc_status_t st;
-        int64_t bytes = 0;
-        for (int i = 0; i < k; ++i) {
-            if ((st = gemm_call_workspace(c[i], &bytes, err)) != TC_OK) return st;
-            if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
-        }
-        for (const float beta : {g.beta, 1.f}) {
-            if (!g.dw || b->few || b->few32 || (beta != g.beta && b->parts == 1)) continue;
-            if ((st = gemm_call_workspace(dw_call(p, *b, g, scale, n, beta), &bytes, err)) != TC_OK) return st;
-            if (bytes > b->gemm_bytes) b->gemm_bytes = bytes;
-        }
-    }
     for (const int64_t n : {b->N, p.V % b->N}) {
         if (n == 0 || !b->few32 || !g.dx) continue;
         const int64_t bytes = ce_few_parts(n, p.H) * p.T * p.H * 4;
@@ -631,7 +647,7 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
     if (e != hipSuccess) return launch_failed(err, e);
     *name = "ce_prep";
     float *const sums = reinterpret_cast<float *>(b.own_dx ? ws + b.acc : static_cast<char *>(g.dx));
-    const int64_t plane = p.T * b.pitch;
+    const int64_t plane = b.Tc * b.pitch, lddw = g.lddw == 0 ? p.H : g.lddw;
     tc_status_t st;
     for (int64_t v0 = 0; v0 < p.V; v0 += b.N) {
         const int64_t N = p.V - v0 < b.N ? p.V - v0 : b.N;
@@ -643,146 +659,164 @@ tc_status_t run_backward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, con
             wv = ws + b.w;
             here = "pack_rows+";
         }
-        if (b.few && takes_rows(p.T, N, p.H)) {
-            CeRowsArgs a;
-            memset(&a, 0, sizeof a);
-            a.x = x;
-            a.w = wv;
-            a.ldx = p.ldx;
-            a.ldw = p.ldw;
-            a.T = (int32_t)p.T;
-            a.V = (int32_t)N;
-            a.H = (int32_t)p.H;
-            a.dtype = p.dt;
-            a.scale = d.scale;
-            a.rows = rows;
-            a.g = ws + b.g;
-            a.pitch = b.pitch;
-            a.first = (int32_t)v0;
-            a.lost = lost;
-            e = tcg_launch_ce_rows(a, true, s->stream);
-            if (e != hipSuccess) return launch_failed(err, e);
-            ctx->dispatches += 1;
-            here += "ce_rows_grad";
-        } else if (b.fused) {
-            e = hipSuccess;
-            each_launch(p, b.dma, p.T, N, N, [&](int64_t n0, int64_t n, int cls) {
-                if (e != hipSuccess) return;
-                int64_t grid;
-                GemmArgs a = product_args(p, ws + b.xz, b.xz_pitch, p.T, at(wv, n0 * p.ldw * p.es), n, d.scale, cls,
-                                          &grid);
-                // (the last piece's columns up to the pitch are zeros)
-                a.C = ws + b.g + n0 * p.es;
-                a.ldc = (int32_t)b.pitch;
-                a.c_extent = (p.T * b.pitch - n0) * p.es;
-                a.ce_cols = (int32_t)(n0 + n < N ? n : up_to(n, 8));
-                a.ce_first = (int32_t)(v0 + n0);
-                a.ce_rows = rows;
-                a.ce_lost = lost;
-                e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_GRAD, a, grid, s->stream);
-                if (e != hipSuccess) return;
-                ctx->dispatches += 1;
-                here += std::string(n0 ? "|" : "") + tcg_kernel_name(p.dt, false, true, cls) + "_grad";
-            });
-            if (e != hipSuccess) return launch_failed(err, e);
-        } else {
-            GemmCall c = logits_call(p, p.T, N, b.xz_pitch, b.pitch, ws + b.xz, wv);
-            c.whole[0] = true;
-            c.C = ws + b.l;
-            std::string part;
-            if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
-            here += part;
-            CeGradArgs ga;
-            ga.l = reinterpret_cast<float *>(ws + b.l);
-            ga.ld = b.pitch;
-            ga.T = (int32_t)p.T;
-            ga.N = (int32_t)N;
-            ga.first = (int32_t)v0;
-            ga.scale = d.scale;
-            ga.rows = rows;
-            ga.g = ws + b.g;
-            ga.pitch = b.pitch;
-            ga.plane = plane;
-            ga.dtype = p.dt;
-            ga.parts = b.parts;
-            ga.lost = lost;
-            ga.lost_parts = b.dx_parts;
-            e = tcg_launch_ce_grad(ga, s->stream);
-            if (e != hipSuccess) return launch_failed(err, e);
-            ctx->dispatches += 1;
-            here += "+ce_grad";
-        }
-        if (b.few32) {
-            CeFewArgs fa;
-            memset(&fa, 0, sizeof fa);
-            fa.g = reinterpret_cast<const float *>(ws + b.g);
-            fa.pitch = b.pitch;
-            fa.T = (int32_t)p.T;
-            fa.N = (int32_t)N;
-            fa.H = (int32_t)p.H;
-            fa.scale = d.scale;
-            fa.w = static_cast<const float *>(wv);
-            fa.ldw = p.ldw;
-            fa.part = reinterpret_cast<float *>(ws + b.gemm);
-            fa.dst = sums;
-            fa.ld_dst = g.lddx == 0 ? p.H : g.lddx;
-            fa.add = v0 > 0;
-            fa.x = reinterpret_cast<const float *>(ws + b.xz);
-            fa.x_pitch = b.xz_pitch;
-            fa.beta = g.beta;
-            fa.lddw = g.lddw == 0 ? p.H : g.lddw;
-            fa.dw = static_cast<float *>(g.dw) + (g.dw ? v0 * fa.lddw : 0);
-            int n = 0;
-            if (g.dx) e = tcg_launch_ce_few_dx(fa, &n, s->stream);
-            if (e == hipSuccess && g.dw) {
-                e = tcg_launch_ce_few_dw(fa, s->stream);
-                if (e == hipSuccess) n += 1;
-            }
-            ctx->dispatches += n;
-            if (e != hipSuccess) return launch_failed(err, e);
-            here += std::string(g.dx ? "+ce_few_dx" : "") + (g.dw ? "+ce_few_dw" : "");
-        }
-        for (int k = 0; k < b.parts && !b.few32; ++k) {
-            const void *gk = ws + b.g + k * plane * p.es;
-            std::string part;
-            if (k < b.dx_parts) {
-                GemmCall c = dx_call(p, b, g, d.scale, N, v0 > 0 || k > 0 ? 1.f : 0.f, wv);
-                c.A = gk;
-                c.C = sums;
-                if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
-                here += "+" + part;
-            }
-            part.clear();
-            if (b.few && g.dw) {
-                CeOuterArgs oa;
-                oa.g = gk;
-                oa.pitch = b.pitch;
-                oa.xt = ws + b.xt;
-                oa.tp = b.tp;
-                oa.T = (int32_t)p.T;
-                oa.N = (int32_t)N;
-                oa.H = (int32_t)p.H;
-                oa.dtype = p.dt;
-                oa.scale = d.scale;
-                oa.beta = g.beta;
-                oa.unscale = unscale;
-                oa.lddw = g.lddw == 0 ? p.H : g.lddw;
-                oa.dw = static_cast<char *>(g.dw) + v0 * oa.lddw * 2;
-                e = tcg_launch_ce_outer(oa, s->stream);
+        for (int64_t t0 = 0; t0 < p.T; t0 += b.Tc) {
+            const int64_t T = p.T - t0 < b.Tc ? p.T - t0 : b.Tc;
+            const void *const xz = ws + b.xz + t0 * b.xz_pitch * p.es;
+            if (b.few && takes_rows(p.T, N, p.H)) {
+                CeRowsArgs a;
+                memset(&a, 0, sizeof a);
+                a.x = x;
+                a.w = wv;
+                a.ldx = p.ldx;
+                a.ldw = p.ldw;
+                a.T = (int32_t)p.T;
+                a.V = (int32_t)N;
+                a.H = (int32_t)p.H;
+                a.dtype = p.dt;
+                a.scale = d.scale;
+                a.rows = rows;
+                a.g = ws + b.g;
+                a.pitch = b.pitch;
+                a.first = (int32_t)v0;
+                a.lost = lost;
+                e = tcg_launch_ce_rows(a, true, s->stream);
                 if (e != hipSuccess) return launch_failed(err, e);
                 ctx->dispatches += 1;
-                here += "+ce_outer";
-            } else if (k < b.dw_parts) {
-                GemmCall c = dw_call(p, b, g, d.scale, N, k > 0 ? 1.f : g.beta);
-                c.A = gk;
-                c.B = ws + b.xz;
-                c.C = static_cast<char *>(g.dw) + v0 * (g.lddw == 0 ? p.H : g.lddw) * dt_size(g.dw_dtype);
-                c.col_scale = unscale;
+                here += "ce_rows_grad";
+            } else if (b.fused) {
+                e = hipSuccess;
+                each_launch(p, b.dma, T, N, N, [&](int64_t n0, int64_t n, int cls) {
+                    if (e != hipSuccess) return;
+                    int64_t grid;
+                    GemmArgs a =
+                        product_args(p, xz, b.xz_pitch, T, at(wv, n0 * p.ldw * p.es), n, d.scale, cls, &grid);
+                    // (the last piece's columns up to the pitch are zeros)
+                    a.C = ws + b.g + n0 * p.es;
+                    a.ldc = (int32_t)b.pitch;
+                    a.c_extent = (T * b.pitch - n0) * p.es;
+                    a.ce_cols = (int32_t)(n0 + n < N ? n : up_to(n, 8));
+                    a.ce_first = (int32_t)(v0 + n0);
+                    a.ce_rows = rows + t0;
+                    a.ce_lost = lost + t0;
+                    e = tcg_launch_gemm(p.dt, false, true, cls, OUT_CE_GRAD, a, grid, s->stream);
+                    if (e != hipSuccess) return;
+                    ctx->dispatches += 1;
+                    here += std::string(n0 ? "|" : "") + tcg_kernel_name(p.dt, false, true, cls) + "_grad";
+                });
+                if (e != hipSuccess) return launch_failed(err, e);
+            } else {
+                GemmCall c = logits_call(p, T, N, b.xz_pitch, b.pitch, xz, wv);
+                c.whole[0] = true;
+                c.C = ws + b.l;
+                std::string part;
                 if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
-                here += "+" + part;
+                here += part;
+                CeGradArgs ga;
+                ga.l = reinterpret_cast<float *>(ws + b.l);
+                ga.ld = b.pitch;
+                ga.T = (int32_t)T;
+                ga.N = (int32_t)N;
+                ga.first = (int32_t)v0;
+                ga.scale = d.scale;
+                ga.rows = rows + t0;
+                ga.g = ws + b.g;
+                ga.pitch = b.pitch;
+                ga.plane = plane;
+                ga.dtype = p.dt;
+                ga.parts = b.parts;
+                ga.lost = lost + t0;
+                ga.lost_parts = b.dx_parts;
+                e = tcg_launch_ce_grad(ga, s->stream);
+                if (e != hipSuccess) return launch_failed(err, e);
+                ctx->dispatches += 1;
+                here += "+ce_grad";
             }
+            if (b.few32) {
+                CeFewArgs fa;
+                memset(&fa, 0, sizeof fa);
+                fa.g = reinterpret_cast<const float *>(ws + b.g);
+                fa.pitch = b.pitch;
+                fa.T = (int32_t)p.T;
+                fa.N = (int32_t)N;
+                fa.H = (int32_t)p.H;
+                fa.scale = d.scale;
+                fa.w = static_cast<const float *>(wv);
+                fa.ldw = p.ldw;
+                fa.part = reinterpret_cast<float *>(ws + b.gemm);
+                fa.dst = sums;
+                fa.ld_dst = g.lddx == 0 ? p.H : g.lddx;
+                fa.add = v0 > 0;
+                fa.x = reinterpret_cast<const float *>(ws + b.xz);
+                fa.x_pitch = b.xz_pitch;
+                fa.beta = g.beta;
+                fa.lddw = g.lddw == 0 ? p.H : g.lddw;
+                fa.dw = static_cast<float *>(g.dw) + (g.dw ? v0 * fa.lddw : 0);
+                int n = 0;
+                if (g.dx) e = tcg_launch_ce_few_dx(fa, &n, s->stream);
+                if (e == hipSuccess && g.dw) {
+                    e = tcg_launch_ce_few_dw(fa, s->stream);
+                    if (e == hipSuccess) n += 1;
+                }
+                ctx->dispatches += n;
+                if (e != hipSuccess) return launch_failed(err, e);
+                here += std::string(g.dx ? "+ce_few_dx" : "") + (g.dw ? "+ce_few_dw" : "");
+            }
+            for (int k = 0; k < b.parts && !b.few32; ++k) {
+                const void *gk = ws + b.g + k * plane * p.es;
+                std::string part;
+                if (k < b.dx_parts) {
+                    GemmCall c = dx_call(p, b, g, d.scale, T, N, v0 > 0 || k > 0 ? 1.f : 0.f, wv);
+                    c.A = gk;
+                    c.C = sums + t0 * c.d.ldc;
+                    if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
+                    here += "+" + part;
+                }
+                part.clear();
+                if (b.few && g.dw) {
+                    CeOuterArgs oa;
+                    oa.g = gk;
+                    oa.pitch = b.pitch;
+                    oa.xt = ws + b.xt;
+                    oa.tp = b.tp;
+                    oa.T = (int32_t)p.T;
+                    oa.N = (int32_t)N;
+                    oa.H = (int32_t)p.H;
+                    oa.dtype = p.dt;
+                    oa.scale = d.scale;
+                    oa.beta = g.beta;
+                    oa.unscale = unscale;
+                    oa.lddw = g.lddw == 0 ? p.H : g.lddw;
+                    oa.dw = static_cast<char *>(g.dw) + v0 * oa.lddw * 2;
+                    e = tcg_launch_ce_outer(oa, s->stream);
+                    if (e != hipSuccess) return launch_failed(err, e);
+                    ctx->dispatches += 1;
+                    here += "+ce_outer";
+                } else if (k < b.dw_parts) {
+                    GemmCall c = dw_call(p, b, g, d.scale, T, N, k > 0 || t0 > 0 ? 1.f : b.own_dw ? 0.f : g.beta);
+                    c.A = gk;
+                    c.B = xz;
+                    c.C = b.own_dw ? ws + b.dw : static_cast<char *>(g.dw) + v0 * lddw * dt_size(g.dw_dtype);
+                    c.col_scale = unscale;
+                    if ((st = gemm_call_enqueue(ctx, s, c, ws + b.gemm, b.gemm_bytes, &part, err)) != TC_OK) return st;
+                    here += "+" + part;
+                }
+            }
+            if (v0 == 0 && t0 == 0) *name += "+" + here;
         }
-        if (v0 == 0) *name += "+" + here;
+        if (b.own_dw) {
+            CeStoreArgs sa;
+            sa.src = reinterpret_cast<const float *>(ws + b.dw);
+            sa.N = (int32_t)N;
+            sa.H = (int32_t)p.H;
+            sa.dtype = g.dw_dtype;
+            sa.beta = g.beta;
+            sa.dst = static_cast<char *>(g.dw) + v0 * lddw * 2;
+            sa.ld = lddw;
+            e = tcg_launch_ce_store(sa, s->stream);
+            if (e != hipSuccess) return launch_failed(err, e);
+            ctx->dispatches += 1;
+            if (v0 == 0) *name += "+ce_store";
+        }
     }
     if (g.dx) {
         CeFinishArgs f;

@@ -286,8 +286,10 @@ __global__ __launch_bounds__(256) void ce_stat_kernel(CeStatArgs a) {
     }
 }
 
-// The largest |grad| of a counted token, by a workgroup of NT threads; kept
-// where its reciprocal and 2^14 times it are ordinary numbers.
+// The largest |grad| of a counted token, by a workgroup of NT threads.  f16:
+// 2^-112 where it is less, so that 2^-14 times it is an ordinary number (numbers
+// down to 2^-151 then remain, as in fp32 results).  bf16, whose own range is
+// fp32's: within 2^+-100, which leaves the factor room for the scale.
 template <int NT>
 __device__ inline float largest_grad(const CePrepArgs &a, int tid) {
     __shared__ float top[NT / 64];
@@ -301,7 +303,8 @@ __device__ inline float largest_grad(const CePrepArgs &a, int tid) {
     if ((tid & 63) == 0) top[tid >> 6] = m;
     __syncthreads();
     for (int w = 0; w < NT / 64; ++w) m = fmaxf(m, top[w]);
-    return m > 0.f ? fminf(fmaxf(m, 0x1p-100f), 0x1p+100f) : 1.f;
+    if (m == 0.f) return 1.f;
+    return a.dtype == DT_F16 ? fmaxf(m, 0x1p-112f) : fminf(fmaxf(m, 0x1p-100f), 0x1p+100f);
 }
 
 // The scaling of 16-bit gradients.  Both types: a token's value at its target

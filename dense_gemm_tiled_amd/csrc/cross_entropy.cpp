@@ -17,6 +17,7 @@ constexpr int64_t kMaxIndex = 0x7FFFFFFF;
 // 128 tiles.  us, in place / copied first: 200 tokens by 65536 x 4095 284 / 327,
 // 20000 x 1501 55 / 59, 50021 x 515 44 / 54, 33000 x 777 51 / 53.
 constexpr int64_t kFewOdd = 256;
+constexpr int64_t kMaxRowBytes = (int64_t)kMaxRowElems * 2;   // between the rows of a tile
 constexpr int64_t kMaxWords = 1 << 20;     // at a time: 256 rows of fp32 products stay below 2^31 bytes
 
 int64_t up_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -47,7 +48,7 @@ tc_status_t check_ce(const tc_ce_desc *d, const void *x, const void *w, CeProble
     if (p->ldx < d->H || p->ldw < d->H)
         return fail(err, TC_ERR_INVALID_ARGUMENT, "ldx=%lld or ldw=%lld < H=%d", (long long)p->ldx,
                     (long long)p->ldw, d->H);
-    const int64_t longest = (int64_t)kMaxRowElems * 2 / p->es;
+    const int64_t longest = kMaxRowBytes / p->es;
     if (p->ldx > longest || p->ldw > longest)
         return fail(err, TC_ERR_OVERFLOW, "ldx=%lld or ldw=%lld > %lld", (long long)p->ldx, (long long)p->ldw,
                     (long long)longest);
@@ -497,11 +498,16 @@ tc_status_t check_grads(const tc_ce_grads *g, const CeProblem &p, std::string *e
                         dt_name(dt[i]));
         if (ld[i] != 0 && ld[i] < p.H)
             return fail(err, TC_ERR_INVALID_ARGUMENT, "ld%s=%d < H=%lld", name[i], ld[i], (long long)p.H);
-        if ((int64_t)ld[i] * dt_size(dt[i]) > (int64_t)kMaxRowElems * 2)
-            return fail(err, TC_ERR_OVERFLOW, "rows of %s are %d apart: at most 8 MiB", name[i], ld[i]);
+        const int64_t apart = ld[i] == 0 ? p.H : ld[i];
+        if (apart * dt_size(dt[i]) > kMaxRowBytes)
+            return fail(err, TC_ERR_OVERFLOW, "rows of %s are %lld apart: at most %lld bytes", name[i],
+                        (long long)apart, (long long)kMaxRowBytes);
         if ((uintptr_t)out[i] % dt_size(dt[i]) != 0)
             return fail(err, TC_ERR_INVALID_ARGUMENT, "%s must be aligned to its elements", name[i]);
     }
+    if (g->dx && p.H * 4 > kMaxRowBytes)
+        return fail(err, TC_ERR_OVERFLOW, "H=%lld: dx is summed in fp32, rows of at most %lld bytes", (long long)p.H,
+                    (long long)kMaxRowBytes);
     if (!std::isfinite(g->beta)) return fail(err, TC_ERR_INVALID_ARGUMENT, "beta must be finite");
     return TC_OK;
 }
@@ -543,6 +549,9 @@ tc_status_t plan_backward(const CeProblem &problem, const tc_ce_grads &g, float 
     const int64_t most = kMaxIndex / longest / 256 * 256;
     b->Tc = span(p.T, p.H, longest) <= kMaxIndex ? p.T : up_to(ceil_div(p.T, ceil_div(p.T, most)), 256);
     b->own_dw = b->Tc < p.T && g.dw && g.dw_dtype != TC_F32;
+    if (b->own_dw && p.H * 4 > kMaxRowBytes)
+        return fail(err, TC_ERR_OVERFLOW, "H=%lld: dw of T=%lld tokens is summed in fp32, rows of at most %lld bytes",
+                    (long long)p.H, (long long)p.T, (long long)kMaxRowBytes);
     // Words at a time: 512 MiB of gradients, at least 8192 words (each piece
     // reads and writes the sums of dx once).
     int64_t N = (int64_t)(512 << 20) / (b->Tc * p.es * b->parts);

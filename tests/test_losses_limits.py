@@ -44,3 +44,25 @@ def test_most_tokens(lib, ctx):  # noqa: F811
     d, g = cdesc(1 << 23, 64, 8), cgrads()
     assert lib.tc_cross_entropy_backward_async(ctx, R(d), R(g), X, W, TG, LSE, WS, BIG, S) == 3
     assert b"T=8388608" in lib.tc_last_error(ctx)
+
+
+@pytest.mark.parametrize("dtype", [tg.BF16, tg.F16])
+def test_rows_longer_than_their_fp32_sums_may_be(lib, ctx, dtype):  # noqa: F811
+    """16-bit rows of up to 8 MiB, whose sums in fp32 take twice that."""
+    most = 2097120
+    good = [(most, dict(dxt=dtype, dwt=dtype)), (most, dict(dxt=tg.F32, dwt=tg.F32)), (2 * most, dict(dx=None, dwt=dtype))]
+    bad = [(most + 8, dict(dxt=dtype, dwt=dtype)), (most + 8, dict(dxt=tg.F32, dw=None)), (most + 8, dict(dx=None, dwt=tg.F32))]
+    for H, kw in good:
+        assert gsize(lib, cdesc(8, 500, H, dtype), cgrads(**kw))[0] == 0, (H, kw)
+    for H, kw in bad:
+        d, g = cdesc(8, 500, H, dtype), cgrads(**kw)
+        assert gsize(lib, d, g)[0] == 3, (H, kw)
+        assert lib.tc_cross_entropy_backward_async(ctx, R(d), R(g), X, W, TG, LSE, WS, BIG, S) == 3
+        text = lib.tc_last_error(ctx)
+        assert b"%d" % H in text and (b"dx" in text or b"dw" in text), text
+    # tokens in parts: a 16-bit dw is summed in fp32, too
+    assert gsize(lib, cdesc(1025, 500, most, dtype), cgrads(dx=None, dwt=dtype))[0] == 0
+    d, g = cdesc(1025, 500, most + 8, dtype), cgrads(dx=None, dwt=dtype)
+    assert gsize(lib, d, g)[0] == 3
+    assert lib.tc_cross_entropy_backward_async(ctx, R(d), R(g), X, W, TG, LSE, WS, BIG, S) == 3
+    assert b"T=1025" in lib.tc_last_error(ctx)

@@ -361,29 +361,20 @@ __global__ __launch_bounds__(256) void ce_prep_kernel(CePrepArgs a) {
     }
 }
 
-// Few tokens (16-bit): 64 columns of x for all of them to a workgroup, which
-// finds the largest grad itself and writes x transposed.
-template <bool VEC>
+// Few tokens (16-bit, x in whole 16-byte pieces): 64 columns of x for all of them
+// to a workgroup, which finds the largest grad itself and writes x transposed, too.
 __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
     __shared__ __attribute__((aligned(16))) unsigned short tile[kCeFewTokens][72];
     __shared__ float grads[kCeFewTokens];
     const int tid = threadIdx.x, h0 = blockIdx.x * 64;
     const unsigned short *x = static_cast<const unsigned short *>(a.x);
-    // 8 threads to a token's 64 columns, up to 4 tokens to a thread
+    // 8 threads to a token's 64 columns, up to 2 tokens to a thread
     const int t8 = tid >> 3, c8 = tid & 7;
 #pragma unroll
     for (int p = 0; p < kCeFewTokens / 32; ++p) {
         const int t = t8 + 32 * p;
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (t < a.T && h0 + c8 * 8 < a.H) {
-            const unsigned short *from = x + t * a.ldx + h0 + c8 * 8;
-            if constexpr (VEC) {
-                v = *reinterpret_cast<const u32x4 *>(from);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = from[2 * e] | (u32)from[2 * e + 1] << 16;
-            }
-        }
+        if (t < a.T && h0 + c8 * 8 < a.H) v = *reinterpret_cast<const u32x4 *>(x + t * a.ldx + h0 + c8 * 8);
         *reinterpret_cast<u32x4 *>(&tile[t][c8 * 8]) = v;
     }
     const float unscale = largest_grad<256>(a, tid) * 0x1p-14f;
@@ -418,7 +409,6 @@ __global__ __launch_bounds__(256) void ce_prep_few_kernel(CePrepArgs a) {
         }
         *reinterpret_cast<u32x4 *>(xt + (int64_t)(h0 + k) * a.tp + t) = u32x4{w[0], w[1], w[2], w[3]};
     }
-    if (!a.xz) return;
     unsigned short *xz = static_cast<unsigned short *>(a.xz);
 #pragma unroll
     for (int p = 0; p < kCeFewTokens / 32; ++p) {
@@ -896,13 +886,11 @@ hipError_t tcg_launch_ce_prep(const CePrepArgs &a, int *launches, hipStream_t s)
     const int es = dt_size(a.dtype);
     if (a.T < 1 || a.T > kMaxBlocks || (a.xz_pitch * es) % 16 != 0 || a.xz_pitch < a.H) return hipErrorInvalidValue;
     if (a.xt) {
-        if (es != 2 || !a.unscale || (a.tp != 32 && a.tp != 64) || a.T > a.tp || a.H % 8 != 0)
+        if (es != 2 || !a.unscale || (a.tp != 32 && a.tp != 64) || a.T > a.tp || a.H % 8 != 0 || a.ldx % 8 != 0 ||
+            (uintptr_t)a.x % 16 != 0)
             return hipErrorInvalidValue;
         const dim3 g((unsigned)((a.H + 63) / 64)), b(256);
-        if (a.ldx % 8 == 0 && (uintptr_t)a.x % 16 == 0)
-            hipLaunchKernelGGL(ce_prep_few_kernel<true>, g, b, 0, s, a);
-        else
-            hipLaunchKernelGGL(ce_prep_few_kernel<false>, g, b, 0, s, a);
+        hipLaunchKernelGGL(ce_prep_few_kernel, g, b, 0, s, a);
         *launches += 1;
         return hipGetLastError();
     }

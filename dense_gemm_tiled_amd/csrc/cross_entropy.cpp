@@ -418,7 +418,7 @@ tc_status_t run_forward(tc_context *ctx, tc_stream *s, const tc_ce_desc &d, cons
 // in fp32 over all tokens before it is rounded.
 struct BackwardSpace {
     bool dma, fused;
-    bool few;                          // few tokens: kernels of their own, no copy of x
+    bool few;                          // few tokens: kernels of their own, x transposed, too
     bool few32;                        // few tokens in fp32: both products by kernels of their own
     int tp;                            // their number, rounded up
     bool own_dx;                       // dx is summed in the workspace

@@ -645,8 +645,8 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(CeGradArgs a) {
 
 __device__ inline float decode(u32 h, int dtype) { return dtype == DT_F16 ? from_f16_bits(h) : from_bf16_bits(h); }
 
-// A row to a workgroup: bound by reading and writing (4096 x 4096 to bf16 28 us,
-// 3.6 TB/s).
+// A row to a workgroup: bound by reading and writing (4096 x 4096 to bf16 28 us:
+// with the targets' rows of w 4.8 TB/s).
 template <int DT, bool VEC>
 __global__ __launch_bounds__(256) void ce_finish_kernel(CeFinishArgs a) {
     const int64_t t = blockIdx.x;
@@ -705,11 +705,12 @@ constexpr int64_t kMaxBlocks = 1 << 24;   // of 256 threads: a launch's threads 
 // Few tokens in fp32.  Both products read or write V x H numbers once and have
 // 2 KT operations for each, KT (T rounded up) at most 16: a tile's rows would be
 // mostly padding, and the vector units keep up with the memory.  Both
-// gradients, us, with tiles / so: 8 tokens by 32000 x 4096 560 / 363 (3.2 TB/s
+// gradients, us, with tiles / so: 8 tokens by 32000 x 4096 560 / 363 (4.3 TB/s
 // of w read twice and dw written), 16 tokens 599 / 439, 32 tokens 659 / 720; 8
-// tokens by 10007 x 1024 69 / 45, by 65536 x 4095 1906 / 840.  A lane has 4 columns, 64 apart (rows may start anywhere: each access of a wave
-// is 256 bytes in a row), a wave 16 of every kCeFewWords words; the gradient is
-// read from LDS, a word's tokens side by side, every lane the same ones.
+// tokens by 10007 x 1024 69 / 45, by 65536 x 4095 1906 / 840.  A lane has 4
+// columns, 64 apart (rows may start anywhere: each access of a wave is 256 bytes
+// in a row), a wave 16 of every kCeFewWords words; the gradient is read from LDS,
+// a word's tokens side by side, every lane the same ones.
 //
 // The gradients of words n .. n + kCeFewWords, zeros from word n1 and token T on.
 template <int KT>

@@ -244,8 +244,9 @@ __global__ __launch_bounds__(1024) void balance_kernel(BalanceArgs a) {
 
 // The workgroups' sums joined: 16 experts to a workgroup (one alone would read
 // for 4 us: a CU gets some 130 GB/s), 4 threads to a share; 7.4 us for 256
-// workgroups' sums of 256 experts, most of it starting up and waiting.  The last workgroup
-// to end adds up what the others left of the loss, in their order.
+// workgroups' sums of 256 experts, where the emptiest kernels take 4.3.  One thread
+// of the last workgroup to end adds up what the others left of the loss, in their
+// order: behind two fences, E / 16 loads that each wait for the one before.
 constexpr int kJoinExperts = 16;
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int groups) {
     __shared__ double sum[256][kJoinExperts + 1];

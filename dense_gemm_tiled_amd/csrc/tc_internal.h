@@ -84,9 +84,11 @@ constexpr int kMaxDevices = 64;
 // sums of one split-K slice (fp32, or int32 for int8 inputs).
 constexpr int OUT_PARTIAL = 5;
 
-// Output selectors of the cross entropy of a linear layer (16-bit inputs, NT,
-// direct-to-LDS classes): per row and wave's share of a tile's columns the
-// maximum and sum of a softmax, and its gradient in the inputs' type.
+// Output selectors of the cross entropy of a linear layer (float inputs, NT):
+// per row and wave's share of a tile's columns the maximum and sum of a softmax
+// (16 bits: 256 x 256 and 128 x 128 direct-to-LDS tiles, and like f32 the
+// register-staged 128 x 128 and 64 x 64 ones), and its gradient in the inputs'
+// type (16 bits: the former, f32: the latter).
 constexpr int OUT_CE_STAT = 6, OUT_CE_GRAD = 7;
 
 // Softmax maxima (of products, a2 = |scale| log2 e to a power of two) are kept

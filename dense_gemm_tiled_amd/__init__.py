@@ -765,7 +765,8 @@ def moe_route(logits, top_k: int, *, renormalize: bool = True, scale: float = 1.
     largest of the router's logits [T, E] (f32, f16 or bf16), the largest
     first, ties to the lowest index, and scale times their softmax weights,
     over the chosen ones (renormalize) or over all E.  Experts whose logit is
-    -inf or NaN are never chosen; places left over hold id -1, weight 0."""
+    -inf or NaN are never chosen; places left over hold id -1, weight 0.  Not
+    recorded by autograd: moe_route_backward has the weights' gradient."""
     import torch
     device = _same_device(logits)
     if not (isinstance(top_k, int) and top_k >= 1):
@@ -982,7 +983,9 @@ def cross_entropy(x, weight, targets, *, scale: float = 1.0, stream=None):
     f16 or bf16; targets [T] int32 or int64.  A token whose target is outside
     [0, V), -100 for instance, is ignored: its loss is 0.  The [T, V] products
     are not kept.  Scratch memory comes from torch's allocator, for this call
-    alone."""
+    alone.  Not recorded by autograd: the results never require grad, also where
+    x or the weight does, and the caller passes on what cross_entropy_backward
+    gives."""
     import torch
     device = _same_device(x, weight, targets)
     scale = float(scale)
@@ -1033,8 +1036,9 @@ def cross_entropy_backward(x, weight, targets, lse, grad, dx=None, dweight=None,
     and scale; grad float32: the losses' gradient, [T] of any stride or one
     number for all of them.  Ignored tokens add nothing to dweight and have
     dx = 0.  An f32 gradient from 16-bit inputs is as exact as fp32 sums and
-    takes two or three times the products; one in x's type is rounded like any
-    16-bit result.  Returns (dx, dweight)."""
+    takes two or three times the products, which are stored on the way; one in
+    x's type comes from softmax gradients that are rounded to it.  Returns (dx,
+    dweight)."""
     outs = [t for t in (dx, dweight) if t is not None]
     if not outs:
         raise TcGemmError(1, "dx and dweight must not both be None")
@@ -1078,7 +1082,8 @@ def moe_balance(logits, ids, *, coef: float = 1.0, stream=None):
     probability)[e], the choices of each expert, and what moe_route_backward
     needs for its gradient (tc_moe_balance_async has the formulas).  logits [T,
     E] f32, f16 or bf16; ids int32 [T, top_k] as moe_route gives them; a token
-    with no id inside [0, E), padding for instance, does not count."""
+    with no id inside [0, E), padding for instance, does not count.  Not recorded
+    by autograd: moe_route_backward has the gradient."""
     import torch
     device = _same_device(logits, ids)
     r, rref, need = _cached(("balance", logits.shape, logits.stride(), logits.dtype, ids.shape, ids.stride(),

@@ -447,7 +447,8 @@ tc_status_t tc_cross_entropy_backward_async(tc_context *ctx, const tc_ce_desc *d
  * as in tc_route_desc (r->top_k columns of ids; renormalize and scale do not
  * count), ids [T, top_k] as tc_moe_route_async gives them.  A token counts
  * where one of its ids is inside [0, E); p is the softmax of its logits, where
- * -inf and NaN have no part and +inf counts as the largest finite number.
+ * -inf and NaN have no part and +inf counts as the largest finite number (and
+ * what is below 2^-126 of the largest p of a token as 0).
  *     counts[e] = places of ids that hold e,  total = their sum,
  *     n         = the tokens that count,
  *     loss      = coef * E * sum_e (counts[e] / total) * (sum_t p[t, e] / n),

@@ -419,10 +419,10 @@ tc_status_t tc_cross_entropy_async(tc_context *ctx, const tc_ce_desc *d, const v
  * to the sum of three bf16 or two f16 numbers, which takes two products as
  * many times.  lse has to be the one that belongs to x, w and scale; w has to be
  * finite (0 times infinity is NaN, as in any product).  Rows of dx and dw are at
- * most 8 MiB apart, and so are the fp32 sums of dx (H <= 2097120).  At most
- * 2^23 - 1 tokens; where rows of x, or of an f32 dx, span more than 2^31 - 1
- * elements, tokens are taken in parts for the same words, and a 16-bit dw is
- * summed in fp32 over the parts before it is rounded. */
+ * most 8 MiB apart, and so are those of fp32 sums (H <= 2097120), which dx has.
+ * At most 2^23 - 1 tokens; where rows of x, or of an f32 dx, span more than
+ * 2^31 - 1 elements, tokens are taken in parts for the same words, and a 16-bit
+ * dw has fp32 sums, too, over the parts before it is rounded. */
 typedef struct {
     const float *grad;
     int64_t grad_stride;          /* elements */

@@ -71,3 +71,37 @@ def test_the_same_bits_every_time():
         now = dx.clone(), dw
         assert first is None or all(torch.equal(a, b) for a, b in zip(first, now))
         first = now
+
+
+@pytest.mark.parametrize("rest", [1, 5, 20])
+@pytest.mark.parametrize("dtype,dw", [("f32", "own"), ("bf16", "own"), ("f16", "f32")])
+def test_few_tokens_in_the_last_part(dtype, dw, rest):
+    """Three parts of 1024 tokens, and one of a few."""
+    T, V, H, ld = 3072 + rest, 130, 40, 2097120
+    x, w, targets, g = case(T, V, H, dtype, seed=rest)
+    targets[-rest:] = torch.arange(rest, device="cuda") % V
+    old = torch.randn(V, H, device="cuda", generator=g)
+    grad = torch.rand(T, device="cuda", generator=g) + 0.1
+    backward(x, w, targets, grad, dx="f32", dw=dw, beta=0.5, old=old, pads=(ld - H, 0))
+
+
+def test_captured():
+    """Tokens in parts in a graph, replayed after other work."""
+    T, V, H, ld = 1100, 300, 64, 2097120
+    x, w, targets, g = case(T, V, H, "bf16")
+    grad = torch.rand(T, device="cuda", generator=g)
+    lse = tg.cross_entropy(x, w, targets)[1]
+    dx, dw = torch.zeros(T, ld, device="cuda")[:, :H], torch.zeros_like(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tg.cross_entropy_backward(x, w, targets, lse, grad, dx, dw)
+    for n in range(3):
+        grad.mul_(0.75)
+        dx.fill_(0)
+        dw.fill_(0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = dx.clone(), dw.clone()
+        tg.cross_entropy_backward(x, w, targets, lse, grad, dx, dw)
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw), n

@@ -76,8 +76,8 @@ def test_the_same_bits_every_time():
 @pytest.mark.parametrize("rest", [1, 5, 20])
 @pytest.mark.parametrize("dtype,dw", [("f32", "own"), ("bf16", "own"), ("f16", "f32")])
 def test_few_tokens_in_the_last_part(dtype, dw, rest):
-    """Three parts of 1024 tokens, and one of a few."""
-    T, V, H, ld = 3072 + rest, 130, 40, 2097120
+    """Four parts of 1024 tokens, and one of a few."""
+    T, V, H, ld = 4096 + rest, 130, 40, 2097120
     x, w, targets, g = case(T, V, H, dtype, seed=rest)
     targets[-rest:] = torch.arange(rest, device="cuda") % V
     old = torch.randn(V, H, device="cuda", generator=g)
